@@ -8,6 +8,10 @@ fallback: if the library is missing or fails to load, importing ``lib()`` raises
     import exact_attention_13_gb300 as ea
     o, lse = ea.fwd(q, k, v, causal=True)           # q, k, v: [B, H, N, d] bf16 on cuda
     o, lse = ea.fwd(q8, k8, v8, descale=(dq, dk, dv))  # float8_e4m3fn operands
+
+``kv.py`` adds what stands around attention in training and serving: rotary positions (``rope``),
+pages and slots from request lengths (``page_plan``), a paged 4-bit key/value cache (``kv4_cache``,
+``kv4_append``, ``kv4_read``) and attention over it (``kv4_fwd``).
 """
 from __future__ import annotations
 
@@ -17,6 +21,8 @@ import os
 import threading
 
 from . import _build
+from ._kv_abi import FA_ROPE_INTERLEAVED, FA_ROPE_INVERSE  # noqa: F401
+from ._kv_abi import SIGNATURES as _kv_signatures
 
 FA_OK = 0
 FA_ERR_INVALID_ARG = 1
@@ -65,6 +71,7 @@ SIGNATURES = {
     "fa_version": (_c.c_int, []),
     "fa_debug_exp2": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_longlong, _c.c_int,
                                  _c.c_void_p]),
+    **_kv_signatures,
 }
 
 
@@ -378,3 +385,18 @@ def debug_exp2(x, mode: int):
     _check(lib().fa_debug_exp2(x.data_ptr(), y.data_ptr(), x.numel(), mode, stream),
            "fa_debug_exp2")
     return y
+
+
+# Rotary positions, page planning, the 4-bit cache and attention over it: functions of kv.py, loaded
+# on first use (that module imports torch, this one does not).
+_KV_NAMES = ("rope", "rope_turns", "page_plan", "PagePlan", "kv4_cache", "kv4_append", "kv4_read",
+             "kv4_fwd", "kv4_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _KV_NAMES:
+        from . import kv
+
+        globals().update({n: getattr(kv, n) for n in _KV_NAMES})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,759 @@
+// kv4_attn.cuh -- attention of a few query rows over the paged 4-bit cache (decode).
+//
+//     O_i = sum_j p_ij v_j,   p_ij = softmax_j(scale q_i . k_j),   LSE_i = log sum_j e^(scale q_i . k_j)
+//
+// over the keys j < len of the row's request (causal: j <= len - q_len + i, the new tokens being the
+// last of the cache).  A row that sees no key gets O = 0 and LSE = -inf.
+//
+// What bounds it.  Each cached value is 4.5 bits and meets 8 query rows or fewer: the floor is the
+// cache's bytes over HBM.  At 6.7 TB/s an SM has to widen about 41 values a clock, and its ALU and
+// FMA pipes each start 64 lanes a clock, so conversions are counted in instructions per value:
+//  * one cvt widens two e2m1 codes to f16 and one f16x2 multiply applies their scales (code * scale
+//    is exact in f16), one instruction a value in all;
+//  * the products run as mma.m16n8k16 with the CACHE as the 16-row operand, straight from the
+//    registers that widened it: S^T = K Q^T and O^T = V^T P^T, queries in the 8-wide operand.  The
+//    tensor core then does 8 products a value (queries as the 16-row operand: 16, half of them
+//    padding).  tcgen05 takes its wide operand from shared or tensor memory only: each widened value
+//    would be written and read there again, 4 bytes of on-chip traffic for each half byte of HBM;
+//  * the contraction index of a product may be permuted freely, so each lane owns 16 or 32
+//    neighbouring dims (K) or 16 dims of four tokens (V) and reads its codes with wide loads;
+//  * V needs two TOKENS side by side in a register: nibbles of two tokens' words are interleaved
+//    before they are widened, 4 logic instructions for 16 values;
+//  * P^T leaves the S^T accumulators in the layout that movmatrix transposes into the operand's.
+// Queries are scaled by a power of two per row into [1, 2) before they become f16, so the conversion
+// keeps bf16's 8 bits down to 2^-17 of the row's largest value.
+//
+// Split.  The work of all requests is one line of tiles (128 keys of one key head, for one block of
+// query rows); CTA i of n takes the i-th n-th of it, so ragged lengths balance by themselves and a
+// single long request fills the GPU.  In a tile each warp takes 32 keys, in its own ring of
+// cp.async stages, with its own softmax state: warps meet only at the end of a unit (one key head of
+// one block of rows).  A unit that crosses CTAs leaves partial sums (O, max, sum) in the workspace,
+// which a second kernel merges in a fixed order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "kv4_cache.cuh"
+#include "rope.cuh"
+#include "sm103_ptx.cuh"
+
+namespace exattn {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStrip = 32;                     // keys of one warp in a tile
+constexpr int kDecTile = kDecStrip * kDecWarps;   // keys of a tile
+constexpr int kDecStages = 3;
+constexpr float kLn2F = 0.6931471805599453f;
+// The reference m of a row's probabilities 2^(x - m) is set kDecBelow under the running maximum and
+// O and l are rescaled only when the maximum has grown by more than 8 (log2) since: P then lies
+// below 2^15, inside f16, keeps f16's full precision down to 2^-21 of the largest, and most strips
+// skip the reduction over the warp.
+constexpr float kDecBelow = 7.f;
+constexpr float kDecLazy = kDecBelow + 8.f;
+
+struct Kv4Args {
+  const __nv_bfloat16* q;  // [T, Hq, d], strides in elements
+  long long q_row, q_head;
+  const uint8_t* cache;
+  const int* table;        // [B, width]
+  const int* lens;         // [B]
+  const int* q_offsets;    // [B + 1], or null: q_len rows each
+  __nv_bfloat16* o;        // [T, Hq, d]
+  float* lse;              // [T, Hq]
+  float* part_o;           // [2 n][R][d]
+  float2* part_ml;         // [2 n][R] (max, sum)
+  int4* desc;              // [n] unit to merge: {first slot or -1, request, unit, last CTA}
+  long long q_len;
+  int t, b, hq, hk, group, width, page_shift, pages;
+  int causal;
+  float c;                 // scale * log2(e) * key descale
+  float v_descale;
+};
+
+struct ReqShape {
+  int q0, q_len, keys;
+};
+
+__device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
+  ReqShape s;
+  long long q0, q1;
+  if (a.q_offsets) {
+    q0 = __ldg(a.q_offsets + r);
+    q1 = __ldg(a.q_offsets + r + 1);
+  } else {
+    q0 = a.q_len * r;
+    q1 = q0 + a.q_len;
+  }
+  // offsets and lengths are device data: keep what they address inside the buffers
+  s.q0 = static_cast<int>(min(max(q0, 0ll), static_cast<long long>(a.t)));
+  s.q_len = static_cast<int>(min(max(q1, static_cast<long long>(s.q0)), static_cast<long long>(a.t))) - s.q0;
+  const long long room = static_cast<long long>(a.width) << a.page_shift;
+  s.keys = static_cast<int>(min(static_cast<long long>(max(__ldg(a.lens + r), 0)), room));
+  return s;
+}
+
+// Units (key head x block of R rows) and tiles per unit of a request; a request without keys keeps
+// one (empty) tile, so that its rows are written.
+template <int R>
+__device__ __forceinline__ int kv4_units(const Kv4Args& a, const ReqShape& s) {
+  return static_cast<int>((static_cast<long long>(s.q_len) * a.group + R - 1) / R) * a.hk;
+}
+__device__ __forceinline__ int kv4_tiles(const ReqShape& s) {
+  return max(1, (s.keys - 1) / kDecTile + 1);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Row k of a 16-key group's product operands is key (k & 8) | kv4_perm(k & 7): neighbouring lanes
+// then read rows of both parities, which halves the bank conflicts of V's loads.
+__device__ __forceinline__ int kv4_perm(int r) { return r ^ ((r >> 1) & 1); }
+
+// Where the CTA's line of tiles runs: request, unit, tile.
+struct TileCursor {
+  int r, u, tile, units, tiles;
+};
+
+template <int R>
+__device__ __forceinline__ void cursor_next(const Kv4Args& a, TileCursor& c) {
+  if (++c.tile < c.tiles) return;
+  c.tile = 0;
+  if (++c.u < c.units) return;
+  c.u = 0;
+  while (++c.r < a.b) {
+    const ReqShape s = kv4_request(a, c.r);
+    c.units = kv4_units<R>(a, s);
+    c.tiles = kv4_tiles(s);
+    if (c.units > 0) return;
+  }
+}
+
+// The CTA's range [first, last) of the line of `total` tiles, and the cursor at its first tile.
+// Returns the number of CTAs that have work.
+template <int R>
+__device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, TileCursor* s_cur,
+                                            long long& total, long long& first, long long& last) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  auto cost = [&](int r, int& units, int& tiles) -> long long {
+    units = 0;
+    tiles = 1;
+    if (r >= a.b) return 0;
+    const ReqShape s = kv4_request(a, r);
+    units = kv4_units<R>(a, s);
+    tiles = kv4_tiles(s);
+    return static_cast<long long>(units) * tiles;
+  };
+  int units, tiles;
+  long long mine = 0;
+  for (int r = tid; r < a.b; r += kDecThreads) mine += cost(r, units, tiles);
+#pragma unroll
+  for (int o = 16; o; o /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= n) return n;
+  first = total * blockIdx.x / n;
+  last = total * (blockIdx.x + 1) / n;
+  long long base = 0;
+  for (int r0 = 0; r0 < a.b; r0 += kDecThreads) {
+    __syncthreads();
+    const long long c = cost(r0 + tid, units, tiles);
+    long long inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    long long before = base, all = base;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      before += w < warp ? s_sum[w] : 0;
+      all += s_sum[w];
+    }
+    const long long lo = before + inc - c;
+    if (first >= lo && first < lo + c) {
+      const long long off = first - lo;
+      s_cur->r = r0 + tid;
+      s_cur->u = static_cast<int>(off / tiles);
+      s_cur->tile = static_cast<int>(off % tiles);
+      s_cur->units = units;
+      s_cur->tiles = tiles;
+    }
+    base = all;
+    if (first < base) break;
+  }
+  __syncthreads();
+  return n;
+}
+
+template <int D>
+__host__ __device__ constexpr int dec_strip_bytes() { return kDecStrip * (D + D / 8); }
+
+template <int D, int NT>
+__host__ __device__ constexpr int dec_smem_bytes() {
+  return kDecWarps * kDecStages * dec_strip_bytes<D>() + 2 * (D / 16) * NT * 32 * 16;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kernel(const Kv4Args a) {
+  constexpr int R = 8 * NT;            // query rows of a unit
+  constexpr int MT = D / 16;           // 16-dim tiles of O^T
+  constexpr int QW = D / 8;            // f16x2 words of one lane's share of a query row
+  constexpr int KW = D / 32;           // code words of a lane's share of a key
+  constexpr int VW = D / 64;           // code words of a lane's share of a value
+  constexpr int kCode = D / 2, kScale = D / 16;  // bytes of a row's codes and scales
+  constexpr int kKs = kDecStrip * kCode, kV = kKs + kDecStrip * kScale, kVs = kV + kKs;
+  extern __shared__ __align__(128) uint8_t dec_smem[];
+  __shared__ long long s_sum[kDecWarps];
+  __shared__ TileCursor s_cur;
+  __shared__ float s_m[kDecWarps][R], s_l[kDecWarps][R];
+
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int g8 = lane / 4, t4 = lane % 4;
+  uint8_t* const ring = dec_smem + warp * (kDecStages * dec_strip_bytes<D>());
+  float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D>());
+
+  long long total, first, last;
+  const int n_cta = kv4_my_range<R>(a, s_sum, &s_cur, total, first, last);
+  if (static_cast<int>(blockIdx.x) >= n_cta) {
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  const int steps = static_cast<int>(last - first);
+  TileCursor cur = s_cur, ld = s_cur;
+  const int page_rows = 1 << a.page_shift;
+  const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
+
+  // ---- loads: the strip's two 16-key groups, one page id each, fetched a step ahead
+  int id[2];
+  int ld_left = steps;
+  unsigned seen = 0;  // two bits a strip in flight: the group's page exists
+  auto fetch_ids = [&]() {
+    const int key0 = ld.tile * kDecTile + warp * kDecStrip;
+    const int keys = kv4_request(a, ld.r).keys;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int key = key0 + 16 * j;
+      id[j] = key < keys ? __ldg(a.table + static_cast<size_t>(ld.r) * a.width + (key >> a.page_shift)) : -1;
+    }
+  };
+  auto issue = [&](int stage) {
+    seen <<= 2;
+    if (ld_left > 0) {
+      const int key0 = ld.tile * kDecTile + warp * kDecStrip;
+      const int head = ld.u % a.hk;
+      const uint8_t* src[2];
+      uint32_t bytes[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool ok = id[j] >= 0 && id[j] < a.pages;
+        const int row = (key0 + 16 * j) & (page_rows - 1);
+        src[j] = a.cache;
+        if (ok) src[j] += (static_cast<size_t>(id[j]) * a.hk + head) * 2 * block_bytes + row * kCode;
+        bytes[j] = ok ? 16u : 0u;  // 0: the copy writes zeros and reads nothing
+        seen |= (ok ? 1u : 0u) << j;
+      }
+      // scales start behind the codes of the whole page; row * kCode is already in src
+      const uint32_t dst = smem_u32(ring + stage * dec_strip_bytes<D>());
+      constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* v = src[j] + (bytes[j] ? block_bytes : 0);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const int at = (p * 32 + lane) * 16;
+          cp_async16(dst + j * 16 * kCode + at, src[j] + (bytes[j] ? at : 0), bytes[j]);
+          cp_async16(dst + kV + j * 16 * kCode + at, v + (bytes[j] ? at : 0), bytes[j]);
+        }
+      }
+      // 16 * kScale bytes of scales a group: kScale copies, K and V, both groups
+      if (lane < 4 * kScale) {
+        const int which = lane / kScale, j = which & 1, kv = which >> 1;
+        const int at = (lane % kScale) * 16;
+        const int row = (key0 + 16 * j) & (page_rows - 1);
+        const uint32_t ok = j ? bytes[1] : bytes[0];
+        const uint8_t* p = j ? src[1] : src[0];
+        if (ok)
+          p += (kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * kCode - row * kCode + row * kScale + at;
+        cp_async16(dst + (kv ? kVs : kKs) + j * 16 * kScale + at, p, ok);
+      }
+      if (--ld_left > 0) {
+        cursor_next<R>(a, ld);
+        fetch_ids();
+      }
+    }
+    cp_async_commit();
+  };
+
+  fetch_ids();
+#pragma unroll
+  for (int s = 0; s < kDecStages; ++s) issue(s);
+
+  // ---- state of the unit at hand
+  ReqShape req;
+  uint32_t qf[NT][QW];
+  float cs[NT][2];       // factor of each S^T column (query row)
+  int lim[NT][2];        // keys it sees
+  int min_lim = 0, max_lim = 0;
+  float m[NT][2], l[NT][2], o[MT][NT][4];
+  bool fresh = true, whole_start = cur.tile == 0;
+  int unit_no = 0;
+  int4 merge = make_int4(-1, 0, 0, 0);
+
+  int stage = 0;
+  for (int step = 0; step < steps; ++step) {
+    if (fresh) {
+      fresh = false;
+      req = kv4_request(a, cur.r);
+      const int head = cur.u % a.hk, row0 = cur.u / a.hk * R, rows = req.q_len * a.group;
+      min_lim = 0x7fffffff;
+      max_lim = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + nt * 8 + g8;
+        uint4 raw[QW / 4];
+        const bool live = row < rows;
+        const int qi = row / a.group, qg = row - qi * a.group;
+        const __nv_bfloat16* src = a.q + static_cast<long long>(req.q0 + qi) * a.q_row +
+                                   static_cast<long long>(head * a.group + qg) * a.q_head + t4 * (D / 4);
+        float amax = 0.f;
+#pragma unroll
+        for (int w = 0; w < QW / 4; ++w) {
+          raw[w] = live ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0u, 0u, 0u, 0u);
+          float f[8];
+          unpack_bf16x8(raw[w], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // power of two that brings the row's largest value into [1, 2) (below 4 at the top end);
+        // an infinite or NaN row is left as it is
+        uint32_t ex = __float_as_uint(amax) >> 23;
+        ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
+        const float down = __uint_as_float((254u - ex) << 23);
+        const float up = a.c * __uint_as_float(ex << 23);
+#pragma unroll
+        for (int w = 0; w < QW / 4; ++w) {
+          float f[8];
+          unpack_bf16x8(raw[w], f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[nt][4 * w + e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+        }
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          cs[nt][cc] = __shfl_sync(0xffffffffu, up, 8 * t4 + 4 * cc);
+          const int crow = row0 + nt * 8 + 2 * t4 + cc;
+          int k = req.keys;
+          if (a.causal && crow < rows) k = min(k, max(0, req.keys - req.q_len + crow / a.group + 1));
+          lim[nt][cc] = k;
+          min_lim = min(min_lim, k);
+          if (crow < rows) max_lim = max(max_lim, k);
+          m[nt][cc] = -INFINITY;
+          l[nt][cc] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 1; x <= 2; x *= 2) {
+        min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, x));
+        max_lim = max(max_lim, __shfl_xor_sync(0xffffffffu, max_lim, x));
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+    }
+
+    cp_async_wait<kDecStages - 1>();
+    __syncwarp();
+    const int key0 = cur.tile * kDecTile + warp * kDecStrip;
+    const unsigned have = (seen >> (2 * (kDecStages - 1))) & 3u;
+    if (key0 < max_lim && have) {
+      const uint8_t* const st = ring + stage * dec_strip_bytes<D>();
+      const bool full = key0 + kDecStrip <= min_lim && have == 3u;
+      float x[2][NT][4];
+      // ---- S^T = K Q^T
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[tg][nt][e] = 0.f;
+        const int k0 = tg * 16 + kv4_perm(g8), k1 = k0 + 8;
+        uint32_t w0[KW], w1[KW];
+        uint32_t sc0[2], sc1[2];  // scales of the lane's first and second 16 dims, as pairs
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint4*>(w0) = *reinterpret_cast<const uint4*>(st + k0 * kCode + t4 * 16);
+          *reinterpret_cast<uint4*>(w1) = *reinterpret_cast<const uint4*>(st + k1 * kCode + t4 * 16);
+          const uint32_t h0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k0 * kScale + t4 * 2));
+          const uint32_t h1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k1 * kScale + t4 * 2));
+          sc0[0] = __byte_perm(h0, 0u, 0x1010);
+          sc0[1] = __byte_perm(h0, 0u, 0x3232);
+          sc1[0] = __byte_perm(h1, 0u, 0x1010);
+          sc1[1] = __byte_perm(h1, 0u, 0x3232);
+        } else {
+          *reinterpret_cast<uint2*>(w0) = *reinterpret_cast<const uint2*>(st + k0 * kCode + t4 * 8);
+          *reinterpret_cast<uint2*>(w1) = *reinterpret_cast<const uint2*>(st + k1 * kCode + t4 * 8);
+          const uint32_t b0 = st[kKs + k0 * kScale + t4], b1 = st[kKs + k1 * kScale + t4];
+          sc0[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b0 | (b0 << 8)));
+          sc1[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b1 | (b1 << 8)));
+          sc0[1] = sc0[0];
+          sc1[1] = sc1[0];
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t h0[4], h1[4];
+          unpack_e2m1x8(w0[w], h0);
+          unpack_e2m1x8(w1[w], h1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h0[e] = mul_f16x2(h0[e], sc0[w / 2]);
+            h1[e] = mul_f16x2(h1[e], sc1[w / 2]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(x[tg][nt], h0[0], h1[0], h0[1], h1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+            mma_16816(x[tg][nt], h0[2], h1[2], h0[3], h1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[tg][nt][e] *= cs[nt][e & 1];
+      }
+
+      // ---- V codes and scales of the lane's tokens (two pairs a group)
+      uint32_t vw[2][4][VW], vs[2][2];
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint2*>(vw[tg][e]) = *reinterpret_cast<const uint2*>(st + kV + tok * kCode + g8 * 8);
+            b[e] = st[kVs + tok * kScale + g8];
+          } else {
+            vw[tg][e][0] = *reinterpret_cast<const uint32_t*>(st + kV + tok * kCode + g8 * 4);
+            b[e] = st[kVs + tok * kScale + g8 / 2];
+          }
+          // keys past the end and on missing pages must not meet P's zeros with a NaN scale
+          if (!full && (key0 + tok >= req.keys || !((have >> tg) & 1u))) b[e] = 0u;
+        }
+        vs[tg][0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[0] | (b[1] << 8)));
+        vs[tg][1] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[2] | (b[3] << 8)));
+      }
+      // A value vector that is not a number makes the rows that see its key NaN through their
+      // scores; its scales become zero, because rows that do not see it multiply it by zero.
+      const uint32_t any = hadd_f16x2(hadd_f16x2(vs[0][0], vs[0][1]), hadd_f16x2(vs[1][0], vs[1][1]));
+      const float2 any2 = f16x2_to_f32x2(any);
+      const bool poisoned = __any_sync(0xffffffffu, !(any2.x + any2.y == any2.x + any2.y));
+
+      if (!full || poisoned) {
+#pragma unroll
+        for (int tg = 0; tg < 2; ++tg) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = tg * 16 + kv4_perm(g8) + 8 * (e >> 1);
+            const bool gone = !((have >> tg) & 1u);
+            const bool nan = (st[kVs + tok * kScale] & 0x7fu) == 0x7fu;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (nan) x[tg][nt][e] = __uint_as_float(0x7fffffffu);
+              if (gone || key0 + tok >= lim[nt][e & 1]) x[tg][nt][e] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            const float2 f = f16x2_to_f32x2(vs[tg][pr]);
+            vs[tg][pr] = pack_f16x2(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f);
+          }
+        }
+      }
+
+      // ---- softmax over the strip
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          top[nt][cc] = fmaxf(fmaxf(x[0][nt][cc], x[0][nt][2 + cc]), fmaxf(x[1][nt][cc], x[1][nt][2 + cc]));
+          grow |= top[nt][cc] > m[nt][cc] + kDecLazy;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float v = top[nt][cc];
+#pragma unroll
+            for (int s = 4; s <= 16; s *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+            v = fmaxf(v - kDecBelow, m[nt][cc]);
+            const float alpha = v == -INFINITY ? 1.f : ex2_mufu(m[nt][cc] - v);
+            m[nt][cc] = v;
+            l[nt][cc] *= alpha;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[i][nt][cc] *= alpha;
+              o[i][nt][2 + cc] *= alpha;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int tg = 0; tg < 2; ++tg) {
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr) {
+            const float p0 = ex2_mufu(x[tg][nt][2 * hr] - m0), p1 = ex2_mufu(x[tg][nt][2 * hr + 1] - m1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pb[tg][nt][hr] = movmatrix_trans(pack_f16x2(p0, p1));
+          }
+        }
+      }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t even[2][4], odd[2][4];  // [token pair][dim pair]: dims 2i and 2i + 1
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            const uint32_t xa = vw[tg][2 * pr][w], xb = vw[tg][2 * pr + 1][w];
+            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even[pr]);
+            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd[pr]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              even[pr][e] = mul_f16x2(even[pr][e], vs[tg][pr]);
+              odd[pr][e] = mul_f16x2(odd[pr][e], vs[tg][pr]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(o[4 * w + e][nt], even[0][e], odd[0][e], even[1][e], odd[1][e], pb[tg][nt][0],
+                        pb[tg][nt][1]);
+        }
+    }
+    __syncwarp();
+    issue(stage);
+    stage = stage + 1 == kDecStages ? 0 : stage + 1;
+
+    // ---- end of the unit, or of the CTA's share of it
+    const bool unit_ends = cur.tile + 1 == cur.tiles;
+    if (unit_ends || step + 1 == steps) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll
+          for (int s = 4; s <= 16; s *= 2) l[nt][cc] += __shfl_xor_sync(0xffffffffu, l[nt][cc], s);
+          if (g8 == 0) {
+            s_m[warp][nt * 8 + 2 * t4 + cc] = m[nt][cc];
+            s_l[warp][nt * 8 + 2 * t4 + cc] = l[nt][cc];
+          }
+        }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int col = nt * 8 + 2 * t4 + cc;
+          float big = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) big = fmaxf(big, s_m[w][col]);
+          const float base = big == -INFINITY ? 0.f : big;
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) sum += s_l[w][col] * ex2_mufu(s_m[w][col] - base);
+          const float f = ex2_mufu(m[nt][cc] - base);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[i][nt][cc] *= f;
+            o[i][nt][2 + cc] *= f;
+          }
+          m[nt][cc] = big;
+          l[nt][cc] = sum;
+        }
+      // (2, 3) into (0, 1), then 1 into 0, through the lanes' own places
+      auto place = [&](int which, int i, int nt) -> float4& {
+        return area[(which * MT * NT + i * NT + nt) * 32 + lane];
+      };
+      auto put = [&](int which) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            place(which, i, nt) = make_float4(o[i][nt][0], o[i][nt][1], o[i][nt][2], o[i][nt][3]);
+      };
+      auto add = [&](int which) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float4 y = place(which, i, nt);
+            o[i][nt][0] += y.x;
+            o[i][nt][1] += y.y;
+            o[i][nt][2] += y.z;
+            o[i][nt][3] += y.w;
+          }
+      };
+      if (warp >= 2) put(warp - 2);
+      __syncthreads();
+      if (warp < 2) add(warp);
+      if (warp == 1) put(1);
+      __syncthreads();
+      const bool complete = unit_ends && whole_start;
+      if (warp == 0) {
+        add(1);
+        const int head = cur.u % a.hk, row0 = cur.u / a.hk * R, rows = req.q_len * a.group;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int row = nt * 8 + 2 * t4 + cc;
+            if (row0 + row >= rows) continue;
+            if (complete) {
+              const int qi = (row0 + row) / a.group, qg = row0 + row - qi * a.group;
+              const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
+              // nothing seen: O = 0 (a NaN sum stays NaN)
+              const float inv = l[nt][cc] == 0.f ? 0.f : a.v_descale / l[nt][cc];
+              uint32_t w[MT];
+#pragma unroll
+              for (int i = 0; i < MT; ++i) w[i] = pack_bf16x2(o[i][nt][cc] * inv, o[i][nt][2 + cc] * inv);
+              uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + g8 * (D / 8));
+#pragma unroll
+              for (int i = 0; i < MT / 4; ++i)
+                dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              if (g8 == 0) a.lse[at] = l[nt][cc] == 0.f ? -INFINITY : m[nt][cc] * kLn2F + logf(l[nt][cc]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(slot) * R + row) * D + g8 * (D / 8));
+#pragma unroll
+              for (int i = 0; i < MT / 2; ++i)
+                dst[i] = make_float4(o[2 * i][nt][cc], o[2 * i][nt][2 + cc], o[2 * i + 1][nt][cc],
+                                     o[2 * i + 1][nt][2 + cc]);
+              if (g8 == 0) a.part_ml[static_cast<size_t>(slot) * R + row] = make_float2(m[nt][cc], l[nt][cc]);
+            }
+          }
+      }
+      if (whole_start && !unit_ends) {
+        // the unit begins here and ends in a later CTA: x is its last tile on the line
+        const long long x = first + step + (cur.tiles - 1 - cur.tile);
+        merge = make_int4(unit_no > 0 ? 1 : 0, cur.r, cur.u, static_cast<int>(((x + 1) * n_cta - 1) / total));
+      }
+      ++unit_no;
+      fresh = true;
+      whole_start = true;
+    }
+    if (step + 1 < steps) cursor_next<R>(a, cur);
+  }
+  cp_async_wait<0>();
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = merge;
+}
+
+// Merge of units that cross CTAs: block (i, row) adds up row `row` of the unit that begins in CTA i
+// and ends later, if there is one.  Warps take every eighth part, in a fixed order.
+constexpr int kMergeThreads = 256;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Args a) {
+  constexpr int kWarps = kMergeThreads / 32, kPer = D / 32;
+  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+  const int4 u = a.desc[blockIdx.x];
+  if (u.x < 0) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = blockIdx.y;
+  const ReqShape req = kv4_request(a, u.y);
+  const int head = u.z % a.hk, at_row = u.z / a.hk * R + row;
+  if (at_row >= req.q_len * a.group) return;
+  const int parts = u.w - static_cast<int>(blockIdx.x) + 1;
+  auto slot = [&](int k) {  // part k: this CTA's, then the first of each later one
+    return static_cast<size_t>(2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? u.x : 0)) * R + row;
+  };
+  float big = -INFINITY;
+  for (int k = threadIdx.x; k < parts; k += kMergeThreads) big = fmaxf(big, a.part_ml[slot(k)].x);
+#pragma unroll
+  for (int s = 16; s; s /= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+  if (lane == 0) s_m[warp] = big;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w]);
+  const float base = big == -INFINITY ? 0.f : big;
+  float acc[kPer], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < parts; k += kWarps) {
+    const float2 ml = a.part_ml[slot(k)];
+    const float f = ex2_mufu(ml.x - base);
+    sum += ml.y * f;
+    const float* src = a.part_o + slot(k) * D + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(src + i);
+      acc[i] = fmaf(y.x, f, acc[i]);
+      acc[i + 1] = fmaf(y.y, f, acc[i + 1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i];
+  if (lane == 0) s_l[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      l += s_l[w];
+      y0 += s_o[w][2 * threadIdx.x];
+      y1 += s_o[w][2 * threadIdx.x + 1];
+    }
+    const int qi = at_row / a.group, qg = at_row - qi * a.group;
+    const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
+    const float inv = l == 0.f ? 0.f : a.v_descale / l;
+    *reinterpret_cast<uint32_t*>(a.o + at * D + 2 * threadIdx.x) = pack_bf16x2(y0 * inv, y1 * inv);
+    if (threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : big * kLn2F + logf(l);
+  }
+}
+
+}  // namespace exattn

@@ -1,0 +1,338 @@
+// kv_api.cu -- host side of the operators around attention: rotary positions, page planning, the
+// 4-bit key/value cache and attention over it.  Argument checks and launches of the C ABI declared
+// in include/exact_attention.h; no call allocates, synchronises or throws.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/exact_attention.h"
+#include "kv4_attn.cuh"
+#include "kv4_cache.cuh"
+#include "page_plan.cuh"
+#include "rope.cuh"
+
+namespace exattn {
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kMaxKvDevices = 64;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool power_of_two(float x) {
+  if (!(x > 0.f) || !std::isfinite(x)) return false;
+  int e = 0;
+  return std::frexp(x, &e) == 0.5f && e >= -60 && e <= 60;
+}
+
+bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// Opt a kernel into `bytes` of dynamic shared memory, once per device.
+template <typename K>
+int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxKvDevices) return FA_ERR_CUDA;
+  if (done.load(std::memory_order_acquire) & (1ull << dev)) return FA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return FA_ERR_CUDA;
+  done.fetch_or(1ull << dev, std::memory_order_acq_rel);
+  return FA_OK;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// ---------------------------------------------------------------------------------- rope
+int rope_tensor(RopeTensor& t, const void* x, const long long* xs, void* y, const long long* ys,
+                int heads) {
+  t = RopeTensor{};
+  if (heads == 0) return FA_OK;
+  if (heads < 0 || !x || !y || !xs || !ys) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (xs[i] < 0 || ys[i] < 0) return FA_ERR_INVALID_ARG;
+    if (xs[i] % 8 || ys[i] % 8) return FA_ERR_MISALIGNED;
+  }
+  if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_MISALIGNED;
+  t.x = static_cast<const __nv_bfloat16*>(x);
+  t.y = static_cast<__nv_bfloat16*>(y);
+  t.xb = xs[0];
+  t.xh = xs[1];
+  t.xn = xs[2];
+  t.yb = ys[0];
+  t.yh = ys[1];
+  t.yn = ys[2];
+  t.heads = heads;
+  return FA_OK;
+}
+
+// ---------------------------------------------------------------------------------- cache
+int cache_checks(const void* cache, int pages, int heads, int page, int d) {
+  if (!cache || pages < 1 || heads < 1) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || !page_size_ok(page) || heads > 65535) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(pages) * page > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  return aligned(cache, 16) ? FA_OK : FA_ERR_MISALIGNED;
+}
+
+int row_grid(long long groups, unsigned& grid) {
+  const long long blocks = (groups + kKv4Threads - 1) / kKv4Threads;
+  if (blocks > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  grid = static_cast<unsigned>(blocks);
+  return FA_OK;
+}
+
+// ---------------------------------------------------------------------------------- attention
+// CTAs of one SM, by rows of a unit: 64 to 87 KB of shared memory and up to 168 (255) registers.
+constexpr int dec_ctas_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+
+// Query rows that share a unit, in eights: the smallest of 8, 16 and 32 that hold the rows of one
+// key head (fewer padded rows), 32 when none does (the cache is then read once per 32 rows).
+int dec_row_eights(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+size_t dec_workspace(int nt, int d) {
+  const size_t n = static_cast<size_t>(kSms) * dec_ctas_per_sm(nt);
+  const size_t rows = 2 * n * 8 * nt;
+  return (rows * d * 4 + rows * 8 + n * 16 + 255) / 256 * 256;
+}
+
+template <int D, int NT>
+int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
+  constexpr int n = kSms * dec_ctas_per_sm(NT);
+  constexpr size_t rows = static_cast<size_t>(2) * n * 8 * NT;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * D);
+  a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
+  constexpr int smem = dec_smem_bytes<D, NT>();
+  static_assert(dec_ctas_per_sm(NT) * (smem + 4096) <= 227 * 1024, "shared memory per SM");
+  static std::atomic<uint64_t> done{0};
+  auto kern = kv4_decode_kernel<D, NT>;
+  if (int rc = opt_in_smem(kern, smem, done)) return rc;
+  kern<<<n, kDecThreads, smem, s>>>(a);
+  if (int rc = launched()) return rc;
+  kv4_merge_kernel<D, 8 * NT><<<dim3(n, 8 * NT), kMergeThreads, 0, s>>>(a);
+  return launched();
+}
+
+template <int D>
+int launch_kv4(Kv4Args& a, int nt, void* workspace, cudaStream_t s) {
+  return nt == 1   ? launch_decode<D, 1>(a, workspace, s)
+         : nt == 2 ? launch_decode<D, 2>(a, workspace, s)
+                   : launch_decode<D, 4>(a, workspace, s);
+}
+
+}  // namespace
+}  // namespace exattn
+
+using namespace exattn;
+
+extern "C" {
+
+int fa_rope(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+            int Hq, const void* k, const long long* k_strides, void* k_out,
+            const long long* k_out_strides, int Hk, int B, int N, int d, const int* positions,
+            long long positions_batch_stride, const long long* turns, int rotary_dim, int flags,
+            float mscale, void* stream) {
+  if (!positions || !turns || B < 1 || N < 1 || Hq < 1 || Hk < 0 || positions_batch_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  if (flags & ~(FA_ROPE_INTERLEAVED | FA_ROPE_INVERSE)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > d || rotary_dim % 16) return FA_ERR_UNSUPPORTED;
+  if (!aligned(positions, 4) || !aligned(turns, 8)) return FA_ERR_MISALIGNED;
+  RopeArgs a;
+  if (int rc = rope_tensor(a.t[0], q, q_strides, q_out, q_out_strides, Hq)) return rc;
+  if (int rc = rope_tensor(a.t[1], k, k_strides, k_out, k_out_strides, Hk)) return rc;
+  a.positions = positions;
+  a.turns = turns;
+  a.pos_batch = positions_batch_stride;
+  a.rows = static_cast<long long>(B) * N;
+  a.n = N;
+  a.d = d;
+  a.r = rotary_dim;
+  a.mscale = mscale;
+  const long long blocks = (a.rows * (d / 16) + kRopeThreads - 1) / kRopeThreads;
+  if (blocks > 0x7fffffffll || static_cast<long long>(Hq) + Hk > 65535) return FA_ERR_UNSUPPORTED;
+  // Heads per thread: all of them once the rows alone fill the GPU (angles are computed once),
+  // fewer when there are not enough rows for about 8 blocks a SM.
+  const int heads = Hq + Hk;
+  long long slices = (8ll * kSms + blocks - 1) / blocks;
+  if (slices > heads) slices = heads;
+  a.heads_per_thread = static_cast<int>((heads + slices - 1) / slices);
+  const dim3 grid(static_cast<unsigned>(blocks),
+                  static_cast<unsigned>((heads + a.heads_per_thread - 1) / a.heads_per_thread));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool il = flags & FA_ROPE_INTERLEAVED, inv = flags & FA_ROPE_INVERSE;
+  if (il && inv) rope_kernel<true, true><<<grid, kRopeThreads, 0, s>>>(a);
+  if (il && !inv) rope_kernel<true, false><<<grid, kRopeThreads, 0, s>>>(a);
+  if (!il && inv) rope_kernel<false, true><<<grid, kRopeThreads, 0, s>>>(a);
+  if (!il && !inv) rope_kernel<false, false><<<grid, kRopeThreads, 0, s>>>(a);
+  return launched();
+}
+
+int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_width, int* queue,
+                 int queue_size, const int* queue_state, int B, int page_size, int num_tokens,
+                 int* lens_out, int* q_offsets, int* positions, int* slots, int* queue_state_out,
+                 void* stream) {
+  if (!lens || !new_lens || !table || !queue || !queue_state || !lens_out || !q_offsets ||
+      !queue_state_out)
+    return FA_ERR_INVALID_ARG;
+  if (B < 1 || table_width < 1 || queue_size < 1 || num_tokens < 0) return FA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!positions || !slots)) return FA_ERR_INVALID_ARG;
+  // other thread blocks read the old lengths and state while the new ones are written
+  if (lens_out == lens || lens_out == new_lens || queue_state_out == queue_state)
+    return FA_ERR_INVALID_ARG;
+  if (B > kPlanMaxBatch || !page_size_ok(page_size)) return FA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(table), static_cast<const void*>(queue),
+                        static_cast<const void*>(queue_state), static_cast<const void*>(lens_out),
+                        static_cast<const void*>(q_offsets), static_cast<const void*>(positions),
+                        static_cast<const void*>(slots), static_cast<const void*>(queue_state_out)})
+    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  PlanArgs a{lens,     new_lens,  table, queue,           queue_state, lens_out,   q_offsets,
+             positions, slots,    queue_state_out, B,     table_width, queue_size, page_size,
+             num_tokens};
+  const int smem = (3 * B + 1) * 4;
+  static std::atomic<uint64_t> done{0};
+  if (int rc = opt_in_smem(page_plan_kernel, (3 * kPlanMaxBatch + 1) * 4, done)) return rc;
+  // a warp per request and a thread per token, four passes each, one CTA a SM at most: each CTA
+  // repeats the scan over the lengths
+  const long long items = num_tokens > 32ll * B ? num_tokens : 32ll * B;
+  long long grid = (items + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  if (grid > kSms) grid = kSms;
+  page_plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, smem,
+                     static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d) {
+  if (num_pages < 1 || Hkv < 1 || !page_size_ok(page_size) || (d != 64 && d != 128)) return 0;
+  return static_cast<size_t>(num_pages) * Hkv * 2 * kv4_block_bytes(page_size, d);
+}
+
+int fa_kv4_append(const void* k, long long k_row_stride, long long k_head_stride, const void* v,
+                  long long v_row_stride, long long v_head_stride, void* cache, int num_pages,
+                  int page_size, const int* slots, int T, int Hkv, int d, float k_descale,
+                  float v_descale, void* stream) {
+  if (!k || !v || !slots || T < 1) return FA_ERR_INVALID_ARG;
+  if (k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
+  if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
+  if (k_row_stride % 8 || k_head_stride % 8 || v_row_stride % 8 || v_head_stride % 8 ||
+      !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4))
+    return FA_ERR_MISALIGNED;
+  Kv4Rows a{};
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.cache = static_cast<uint8_t*>(cache);
+  a.slots = slots;
+  a.k_row = k_row_stride;
+  a.k_head = k_head_stride;
+  a.v_row = v_row_stride;
+  a.v_head = v_head_stride;
+  a.total = static_cast<long long>(T) * Hkv * 2 * (d / kKv4Group);
+  a.t = T;
+  a.heads = Hkv;
+  a.page = page_size;
+  a.pages = num_pages;
+  a.k_descale = k_descale;
+  a.v_descale = v_descale;
+  unsigned grid;
+  if (int rc = row_grid(a.total, grid)) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    kv4_append_kernel<64><<<grid, kKv4Threads, 0, s>>>(a);
+  else
+    kv4_append_kernel<128><<<grid, kKv4Threads, 0, s>>>(a);
+  return launched();
+}
+
+int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slots, void* k, void* v,
+                int T, int Hkv, int d, float k_descale, float v_descale, void* stream) {
+  if (!k || !v || !slots || T < 1) return FA_ERR_INVALID_ARG;
+  if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
+  if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return FA_ERR_MISALIGNED;
+  Kv4Rows a{};
+  a.k_out = static_cast<__nv_bfloat16*>(k);
+  a.v_out = static_cast<__nv_bfloat16*>(v);
+  a.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  a.slots = slots;
+  a.total = static_cast<long long>(T) * Hkv * 2 * (d / kKv4Group);
+  a.t = T;
+  a.heads = Hkv;
+  a.page = page_size;
+  a.pages = num_pages;
+  a.k_descale = k_descale;
+  a.v_descale = v_descale;
+  unsigned grid;
+  if (int rc = row_grid(a.total, grid)) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    kv4_read_kernel<64><<<grid, kKv4Threads, 0, s>>>(a);
+  else
+    kv4_read_kernel<128><<<grid, kKv4Threads, 0, s>>>(a);
+  return launched();
+}
+
+size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
+  return dec_workspace(dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv)), d);
+}
+
+int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache,
+               int num_pages, int page_size, const int* table, int table_width, const int* lens,
+               const int* q_offsets, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
+               int max_q, float scale, int causal, float k_descale, float v_descale,
+               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !table || !lens || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+  if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!q_offsets && T % B) return FA_ERR_INVALID_ARG;
+  if (q_row_stride < 0 || q_head_stride < 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID_ARG;
+  if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
+  if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
+  if (static_cast<long long>(T) * Hq > 0x3fffffffll) return FA_ERR_UNSUPPORTED;
+  const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
+  if (workspace_bytes < dec_workspace(nt, d)) return FA_ERR_INVALID_ARG;
+  if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) ||
+      !aligned(workspace, 16))
+    return FA_ERR_MISALIGNED;
+  const double c = static_cast<double>(scale) * 1.4426950408889634 * k_descale;
+  if (!(c <= 3.0e38)) return FA_ERR_INVALID_ARG;
+  Kv4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = table;
+  a.lens = lens;
+  a.q_offsets = q_offsets;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_len = T / B;
+  a.t = T;
+  a.b = B;
+  a.hq = Hq;
+  a.hk = Hkv;
+  a.group = Hq / Hkv;
+  a.width = table_width;
+  a.page_shift = log2_of(page_size);
+  a.pages = num_pages;
+  a.causal = causal != 0;
+  a.c = static_cast<float>(c);
+  a.v_descale = v_descale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_kv4<64>(a, nt, workspace, s) : launch_kv4<128>(a, nt, workspace, s);
+}
+
+}  // extern "C"

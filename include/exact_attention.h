@@ -227,6 +227,132 @@ FA_API int fa_bwd(const void* q, const void* k, const void* v, const void* o, co
 /* Workspace bytes fa_bwd needs: B * H * N * 4, rounded up to 256; 0 for invalid arguments. */
 FA_API size_t fa_bwd_workspace_bytes(int B, int H, int N);
 
+/* fa_rope flags */
+#define FA_ROPE_INTERLEAVED 1  /* pairs (2i, 2i + 1); without it (i, i + rotary_dim / 2) */
+#define FA_ROPE_INVERSE 2      /* turn by the negative angle: the gradient of the forward map */
+
+/*
+ * Rotary positions of one or two tensors (queries and keys) in one launch.  Pair i of the first
+ * `rotary_dim` values of each head vector at position p is turned by p * f_i:
+ *     y_a = mscale (a cos - b sin),  y_b = mscale (b cos + a sin)
+ * the other d - rotary_dim values are copied.  The map is mscale times a rotation, so the gradient
+ * dL/dx of a loss is the same call on dL/dy with FA_ROPE_INVERSE and the same mscale.
+ *   q, k            : device pointers, bf16 (16-byte aligned), last dimension contiguous;
+ *                     *_strides = {batch, head, row} strides in elements, multiples of 8, >= 0.
+ *                     [B, H, N, d] and packed tokens [T, H, d] (B = 1, N = T) are both such
+ *   q_out, k_out    : outputs, likewise; an output may be its own input (same pointer and
+ *                     strides), any other overlap gives undefined results
+ *   Hq, Hk          : heads of each; Hk = 0: no second tensor (k, k_out and strides unused)
+ *   positions       : device int32, [N] with positions_batch_stride = 0 (shared by the batch) or
+ *                     [B, N]; any int32 value
+ *   turns           : device int64, [rotary_dim / 2]: f_i / (2 pi) in units of 2^-64 turn.  The
+ *                     product with a position wraps to the exact fraction of a turn, so angles of
+ *                     far positions keep fp32 accuracy.  Scalings for long contexts are made in
+ *                     this table (and in mscale)
+ *   d               : 64 or 128;  rotary_dim : a multiple of 16, <= d
+ * Arithmetic is fp32 with one rounding to bf16.  Returns an fa_status; asynchronous like fa_fwd.
+ */
+FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
+                   const long long* q_out_strides, int Hq, const void* k,
+                   const long long* k_strides, void* k_out, const long long* k_out_strides, int Hk,
+                   int B, int N, int d, const int* positions, long long positions_batch_stride,
+                   const long long* turns, int rotary_dim, int flags, float mscale, void* stream);
+
+/*
+ * One step of a paged cache's bookkeeping, on the device: which request gets which pages, and
+ * where each new token goes.  Request b holds lens[b] tokens in the pages table[b, 0 ..
+ * ceil(lens[b] / page_size)); it brings new_lens[b] tokens, or, with new_lens[b] < 0, it has ended
+ * and its pages return to the free ones.
+ *   queue, queue_state : ring of `queue_size` free page ids; queue_state = {head, count}: the free
+ *                        pages are queue[(head + i) % queue_size], i < count.  The ring must have
+ *                        room for every page there is
+ * Requests take pages from the front in their order.  A request is refused (keeps its length and
+ * pages, gets no slots) when its table row is too narrow, or when it needs pages and the sum of
+ * all needs up to and with its own exceeds count.  Pages of ended requests become free behind the
+ * others, for the next step.
+ *   table           : [B, table_width], new entries written, others left as they are
+ *   lens_out        : [B] lengths after the step (0 for ended requests)
+ *   q_offsets       : [B + 1] first token of each request in the packed batch, and their number
+ *   positions, slots: [num_tokens] position and cache slot (page * page_size + row) of each token;
+ *                     slot -1 for tokens of refused requests; position 0 and slot -1 past the last
+ *                     token.  num_tokens = 0: neither is written (they may be NULL)
+ *   queue_state_out : {head, count} after the step
+ *   page_size       : 16, 32, 64 or 128;  B <= 16384;  the tokens of a step number < 2^31
+ * All arrays are device int32.  lens_out and queue_state_out may not be the inputs.  One launch,
+ * integers only: results do not depend on scheduling.
+ */
+FA_API int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_width,
+                        int* queue, int queue_size, const int* queue_state, int B, int page_size,
+                        int num_tokens, int* lens_out, int* q_offsets, int* positions, int* slots,
+                        int* queue_state_out, void* stream);
+
+/*
+ * The 4-bit key/value cache: [num_pages, Hkv, 2 (keys, values), page_size * 9 d / 16] bytes.  Each
+ * block holds page_size rows of d / 2 bytes of e2m1 codes (value 2i in the low half of byte i),
+ * then page_size rows of d / 16 e4m3 scales, one for 16 neighbouring values:
+ *     scale = e4m3(max |x / descale| / 6),  code = e2m1(x / descale / scale),
+ *     value = code * scale * descale              (both roundings to nearest even, saturating)
+ * descale is one power of two per tensor, the same in every call on the cache.  A head vector that
+ * holds a NaN or an infinity reads back as NaN.  Slot s is row s % page_size of page s / page_size.
+ * Bytes of such a cache; 0 for invalid arguments.
+ */
+FA_API size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d);
+
+/*
+ * Write keys and values into the cache.
+ *   k, v      : device pointers, [T, Hkv, d] bf16 (16-byte aligned), last dimension contiguous, row
+ *               and head strides in elements (multiples of 8, >= 0)
+ *   cache     : device pointer (16-byte aligned)
+ *   slots     : device int32 [T]; tokens whose slot lies outside the cache (-1) are skipped.  Of
+ *               tokens with the same slot, which one's values each group keeps is undefined
+ *   d 64 or 128;  page_size 16, 32, 64 or 128;  num_pages * page_size < 2^31;  descales powers of
+ *   two in [2^-61, 2^59]
+ */
+FA_API int fa_kv4_append(const void* k, long long k_row_stride, long long k_head_stride,
+                         const void* v, long long v_row_stride, long long v_head_stride,
+                         void* cache, int num_pages, int page_size, const int* slots, int T,
+                         int Hkv, int d, float k_descale, float v_descale, void* stream);
+
+/* Read cached rows back as bf16 (exact): k, v are outputs [T, Hkv, d], contiguous, 16-byte
+ * aligned; rows whose slot lies outside the cache are zeros.  Other arguments as fa_kv4_append. */
+FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slots, void* k,
+                       void* v, int T, int Hkv, int d, float k_descale, float v_descale,
+                       void* stream);
+
+/*
+ * Attention of packed query tokens over the paged 4-bit cache.  Request b's queries are rows
+ * q_offsets[b] .. q_offsets[b + 1) of q; its keys are the first lens[b] tokens of the pages
+ * table[b, :].  Query head h reads key head h / (Hq / Hkv).  Causal: the queries are the last
+ * tokens of the cache, so query i of n sees keys j <= lens[b] - n + i; otherwise all lens[b].
+ * A row that sees no key gets O = 0 and LSE = -inf.
+ *   q           : device pointer, [T, Hq, d] bf16 (16-byte aligned), last dimension contiguous, row
+ *                 and head strides in elements (multiples of 8, >= 0)
+ *   table, lens : device int32, [B, table_width] and [B].  Lengths outside [0, table_width *
+ *                 page_size] are clamped; keys on a page id outside [0, num_pages) are not seen
+ *   q_offsets   : device int32 [B + 1], not decreasing, or NULL: T / B queries each (T % B == 0).
+ *                 Rows of q past q_offsets[B] are not read, their outputs left as they were
+ *   o, lse      : outputs [T, Hq, d] bf16 (16-byte aligned) and [T, Hq] fp32
+ *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks how
+ *                 many query rows share a pass over the cache
+ *   scale       : softmax scale, finite and >= 0
+ *   workspace   : device scratch of fa_kv4_fwd_workspace_bytes(Hq, Hkv, d, max_q) bytes, 16-byte
+ *                 aligned, contents on entry do not matter; calls that may run at the same time
+ *                 need one each
+ *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30; d, page_size and descales as fa_kv4_append
+ * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
+ * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums
+ * are merged in a fixed order: the same call gives the same bits.
+ */
+FA_API int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride,
+                      const void* cache, int num_pages, int page_size, const int* table,
+                      int table_width, const int* lens, const int* q_offsets, void* o, float* lse,
+                      int T, int B, int Hq, int Hkv, int d, int max_q, float scale, int causal,
+                      float k_descale, float v_descale, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Workspace bytes fa_kv4_fwd needs; 0 for invalid arguments. */
+FA_API size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q);
+
 /*
  * Read, and if `clear` is nonzero reset to FA_OK, the library's status word on the current
  * device.  Synchronises the device first.  Writes FA_OK or FA_ERR_DEVICE_TIMEOUT to *out.

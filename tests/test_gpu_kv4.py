@@ -1,0 +1,337 @@
+"""The 4-bit cache and attention over it against the fp64 reference."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_13_gb300 as ea
+from oracle import kv
+
+pytestmark = pytest.mark.gpu
+
+
+def numpy64(t):
+    return t.double().cpu().numpy()
+
+
+def normal(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+# --------------------------------------------------------------------------------- write and read
+@pytest.mark.parametrize("d,page,H,T", [(128, 16, 1, 1), (64, 16, 3, 50), (128, 64, 2, 77),
+                                        (64, 128, 4, 200), (128, 32, 8, 33)])
+@pytest.mark.parametrize("kd,vd", [(1.0, 1.0), (0.25, 2.0 ** -6)])
+def test_append_and_read_are_exact(d, page, H, T, kd, vd):
+    pages = -(-2 * T // page)
+    cache = ea.kv4_cache(pages, H, page, d)
+    cache.random_(0, 256, generator=torch.Generator("cuda").manual_seed(1))
+    before = cache.clone()
+    row = (normal(T, 2 * H, d) * torch.logspace(-3, 3, d)).bfloat16()
+    row[0, 0] = 0
+    row[T // 2, 1, :16] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6] * 2)  # ties
+    row = row.cuda()
+    k, v = row[:, :H], row[:, H:]
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(2))[:T].int()
+    slots[T // 3] = -1
+    if T > 5:
+        slots[5] = pages * page  # the first slot past the cache
+    ea.kv4_append(k, v, cache, slots.cuda(), kd, vd)
+    ko, vo = ea.kv4_read(cache, slots.cuda(), d, kd, vd)
+    touched = np.zeros(cache.shape, dtype=bool)
+    for x, y, n, ds in ((k, ko, 0, kd), (v, vo, 1, vd)):
+        code, s8 = kv.quantise(numpy64(x), ds)
+        want = kv.dequantise(code, s8, ds)
+        for t, s in enumerate(slots.tolist()):
+            if not 0 <= s < pages * page:
+                assert (y[t] == 0).all()
+                continue
+            assert np.array_equal(numpy64(y[t]), want[t])
+            p, i = divmod(s, page)
+            for h in range(H):
+                raw = cache[p, h, n].cpu().numpy()
+                c, sc = kv.unblock(raw, page, d)
+                assert np.array_equal(c[i], code[t, h]) and np.array_equal(sc[i], s8[t, h])
+            touched[p, :, n, i * d // 2:(i + 1) * d // 2] = True
+            at = page * d // 2 + i * d // 16
+            touched[p, :, n, at:at + d // 16] = True
+    same = (cache == before).cpu().numpy()
+    assert same[~touched].all()  # nothing beside the rows was written
+
+
+def test_extreme_values():
+    d, page = 128, 16
+    cache = ea.kv4_cache(1, 1, page, d)
+    x = normal(8, 1, d).bfloat16()
+    x[0] *= 1e-4           # below e4m3's smallest scale: zeros
+    x[1] *= 1e37           # saturates at 448 * 6
+    x[2, 0, 100] = math.nan
+    x[3, 0, 0] = -math.inf
+    x[4] = 6 * 448
+    x[5] = -0.0
+    slots = torch.arange(8, dtype=torch.int32).cuda()
+    ea.kv4_append(x.cuda(), x.cuda(), cache, slots)
+    k, v = ea.kv4_read(cache, slots, d)
+    want = kv.dequantise(*kv.quantise(numpy64(x)))
+    for y in (k, v):
+        assert np.array_equal(numpy64(y), want, equal_nan=True)
+    assert (want[0] == 0).all() and np.abs(want[1]).max() == 2688 and np.isnan(want[2:4]).all()
+
+
+# --------------------------------------------------------------------------------- attention
+def make(lens, width, page, Hkv, d, seed=0, extra=3):
+    """A cache of normal keys and values with scattered pages, and its table.  Bytes that no request
+    owns are 0xff: NaN scales."""
+    rng = np.random.default_rng(seed)
+    B = len(lens)
+    pages = B * width + extra
+    table = rng.permutation(pages)[:B * width].reshape(B, width)
+    cache = torch.full((pages, Hkv, 2, page * 9 * d // 16), 255, dtype=torch.uint8).cuda()
+    slots, n = [], 0
+    for b, m in enumerate(lens):
+        j = np.arange(max(0, min(m, width * page)))
+        slots += (table[b, j // page] * page + j % page).tolist()
+    if slots:
+        k, v = normal(len(slots), Hkv, d, seed=seed + 1), normal(len(slots), Hkv, d, seed=seed + 2)
+        k[:, :, 3] *= 6
+        ea.kv4_append(k.bfloat16().cuda(), v.bfloat16().cuda(), cache, ints(slots))
+    return cache, table
+
+
+def check(q, cache, table, lens, offsets, d, causal=True, scale=None, kd=1.0, vd=1.0, got=None, **kw):
+    """Tolerances.  A score is a sum of exact products in fp32 (d roundings at most, some by
+    truncation) of queries rounded 2^-25 of the row's largest value: off by delta = 2^-18 scale
+    sum|q k| at most.  p then is off by delta relative, f16 P by 2^-11 relative or, where it is
+    subnormal, half of 2^-24 absolute with the row's largest P at 2^7 or more (2^-32 of it: sum p
+    is at least the largest, so O is off by 2^-32 sum |v|), ex2 by 2^-21, and O = sum p v / sum p by
+    the relative part twice over; bf16 O by 2^-8.  LSE is off by delta and fp32 roundings of a few 2^-22 (1 + |LSE|)."""
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    q64 = numpy64(q)
+    o64, lse64, mass, total, dot = kv.kv4_attention(q64, cache.cpu().numpy(), np.asarray(table), lens, offsets,
+                                             d, scale, causal, kd, vd)
+    if got is None:
+        got = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), causal=causal,
+                         scale=scale, k_descale=kd, v_descale=vd, **kw)
+    o, lse = (numpy64(t) for t in got)
+    n = offsets[-1]
+    delta = 2.0 ** -18 * scale * dot[:n]
+    tol = 2.0 ** -8 * np.abs(o64[:n]) + (2 * delta[..., None] + 2.0 ** -10) * mass[:n] + 2.0 ** -32 * total[:n]
+    finite = np.isfinite(lse64[:n])
+    assert (np.abs(o[:n] - o64[:n]) <= tol).all(), np.nanmax(np.abs(o[:n] - o64[:n]) / tol)
+    assert np.array_equal(np.isneginf(lse[:n]), ~finite)
+    err = np.abs(lse[:n] - np.where(finite, lse64[:n], 0))[finite]
+    lim = (delta + 2.0 ** -20 * (1 + np.abs(np.where(finite, lse64[:n], 0))))[finite]
+    assert (err <= lim).all(), (err / lim).max()
+    return got
+
+
+def queries(T, Hq, d, seed=9):
+    return (normal(T, Hq, d, seed=seed) * 2).bfloat16().cuda()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (8, 2), (7, 1), (24, 2)])
+def test_decode_lengths(d, page, Hq, Hkv):
+    lens = [1, 0, 15, 16, 17, 31, 33, 127, 128, 129, 300, 500]
+    width = -(-500 // page)
+    cache, table = make(lens, width, page, Hkv, d)
+    check(queries(len(lens), Hq, d), cache, table, lens, list(range(len(lens) + 1)), d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,qlens", [
+    (4, 1, [2, 0, 1, 3, 4]), (4, 4, [9, 1, 7, 8, 16]), (6, 2, [1, 5, 2, 0, 6]),
+    (3, 1, [40, 3, 20, 1, 64]), (16, 2, [130, 2, 33, 5, 1]),
+])
+def test_several_queries_per_request(d, causal, Hq, Hkv, qlens):
+    """Row blocks of 8, 16 and 32, several of them, rows before the cache's first key."""
+    lens = [130, 64, 5, 0, 333]
+    cache, table = make(lens, 6, 64, Hkv, d)
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    check(queries(offsets[-1], Hq, d), cache, table, lens, offsets, d, causal=causal,
+          max_q=max(qlens))
+    check(queries(offsets[-1], Hq, d), cache, table, lens, offsets, d, causal=causal, max_q=1)
+
+
+@pytest.mark.parametrize("d,page,lens,qlens,Hq,Hkv", [
+    (128, 64, [20000], [1], 8, 1), (64, 16, [9000, 3], [2, 1], 4, 1),
+    (128, 128, [5000, 0, 7001, 1], [1, 1, 3, 1], 10, 2), (128, 32, [30000], [8], 4, 1),
+])
+def test_long_caches_split_over_the_gpu(d, page, lens, qlens, Hq, Hkv):
+    cache, table = make(lens, -(-max(lens) // page), page, Hkv, d)
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    q = queries(offsets[-1], Hq, d)
+    ws = torch.full((ea.kv4_workspace_bytes(Hq, Hkv, d, max(qlens)),), 255, dtype=torch.uint8).cuda()
+    a = check(q, cache, table, lens, offsets, d, max_q=max(qlens), workspace=ws)
+    b = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), max_q=max(qlens),
+                   workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # the same bits again
+
+
+def test_many_short_requests():
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 70, 700).tolist()
+    cache, table = make(lens, 5, 16, 1, 64)
+    check(queries(700, 2, 64), cache, table, lens, list(range(701)), 64)
+
+
+def test_scale_descales_and_large_scores():
+    lens, d = [200, 77], 128
+    cache, table = make(lens, 4, 64, 2, d)
+    q = queries(2, 4, d)
+    for scale, kd, vd in ((0.0, 1.0, 1.0), (3.0, 1.0, 0.5), (0.02, 8.0, 2.0 ** -9)):
+        check(q, cache, table, lens, [0, 1, 2], d, scale=scale * 1.0, kd=kd, vd=vd)
+    big = q.clone()
+    big[0, 0] *= 1e30
+    big[0, 1] *= 1e-30
+    big[1, 0] = 0
+    check(big, cache, table, lens, [0, 1, 2], d, scale=1e-30)
+    # rising scores: the running maximum moves in every strip
+    k = torch.ones(200, 2, d) * torch.linspace(0.1, 6, 200)[:, None, None]
+    slots = ints((np.asarray(table)[0][np.arange(200) // 64] * 64 + np.arange(200) % 64))
+    ea.kv4_append(k.bfloat16().cuda(), k.bfloat16().cuda(), cache, slots)
+    check(torch.ones(2, 4, d).bfloat16().cuda(), cache, table, lens, [0, 1, 2], d, scale=1.0)
+    check(-torch.ones(2, 4, d).bfloat16().cuda(), cache, table, lens, [0, 1, 2], d, scale=1.0)
+
+
+def test_masked_places_hold_anything():
+    """NaN keys and values past a request's length and after a query's own position."""
+    d, lens, qlens = 128, [100, 40], [4, 2]
+    cache, table = make(lens, 2, 64, 1, d)
+    q = queries(6, 2, d)
+    want = check(q, cache, table, lens, [0, 4, 6], d)
+    slot = ints([np.asarray(table)[0][1] * 64 + 99 - 64])  # request 0's last key: row 3 alone sees it
+    bad = torch.full((1, 1, d), math.nan).bfloat16().cuda()
+    good_k, good_v = ea.kv4_read(cache, slot, d)
+    for k, v in ((bad, good_v), (good_k, bad)):
+        ea.kv4_append(k, v, cache, slot)
+        o, lse = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints([0, 4, 6]))
+        rows = [0, 1, 2, 4, 5]
+        assert torch.equal(o[rows], want[0][rows]) and torch.equal(lse[rows], want[1][rows])
+        assert o[3].isnan().all() and lse[3].isnan().all()
+
+
+def test_bad_device_data_is_not_followed():
+    """Page ids outside the cache are keys that are not there; lengths and offsets are clamped."""
+    d, lens = 64, [192, 130, 20]
+    cache, table = make(lens, 3, 64, 2, d)
+    table[0, 0], table[1, 1], table[2, 0] = -1, 10 ** 6, 2 ** 31 - 1
+    q = queries(3, 4, d)
+    check(q, cache, table, lens, [0, 1, 2, 3], d)
+    huge = [2 ** 31 - 1, -5, 1]
+    check(q, cache, table, huge, [0, 1, 2, 3], d)
+    out = torch.full((3, 4, d), 7.0, dtype=torch.bfloat16).cuda()
+    ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints([-3, 2, 1, 2 ** 31 - 1]), out=out)
+    torch.cuda.synchronize()
+
+
+def test_rows_past_the_last_request_stay():
+    d, lens = 128, [50, 70]
+    cache, table = make(lens, 2, 64, 1, d)
+    q = queries(5, 2, d)
+    q[3:] = math.nan
+    out = torch.full((5, 2, d), 7.0, dtype=torch.bfloat16).cuda()
+    lse = torch.full((5, 2), 8.0).cuda()
+    got = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints([0, 1, 3]), out=out, lse=lse)
+    check(q[:3], cache, table, lens, [0, 1, 3], d, got=(got[0][:3], got[1][:3]))
+    assert (out[3:] == 7).all() and (lse[3:] == 8).all()
+
+
+def test_strided_queries_and_uniform_rows():
+    d, lens = 64, [50, 170, 9]
+    cache, table = make(lens, 3, 64, 2, d)
+    wide = queries(6, 9, d)
+    q = wide[:, 2:6]
+    a = ea.kv4_fwd(q, cache, ints(table), ints(lens))
+    b = check(q.contiguous(), cache, table, lens, [0, 2, 4, 6], d)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_streams_and_two_captured_graphs():
+    d, lens = 128, [3000, 10, 500]
+    cache, table = make(lens, 47, 64, 2, d)
+    q = queries(3, 8, d)
+    tab, ln = ints(table), ints(lens)
+    want = check(q, cache, table, lens, [0, 1, 2, 3], d)
+    side, outs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for s in side:  # two calls at once, each with its own workspace
+        with torch.cuda.stream(s):
+            outs.append([ea.kv4_fwd(q, cache, tab, ln) for _ in range(3)])
+    torch.cuda.synchronize()
+    graphs, res = [], []
+    ws = torch.empty(ea.kv4_workspace_bytes(8, 2, d, 1), dtype=torch.uint8).cuda()
+    for _ in range(2):  # two graphs that share a workspace, replayed one after the other
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res.append(ea.kv4_fwd(q, cache, tab, ln, workspace=ws))
+        graphs.append(g)
+    for g in graphs + graphs[::-1]:
+        ws.fill_(255)
+        g.replay()
+    torch.cuda.synchronize()
+    for o, lse in [x for run in outs for x in run] + res:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_refusals():
+    d, lens = 128, [5]
+    cache, table = make(lens, 1, 16, 2, d)
+    q, tab, ln = queries(1, 4, d), ints(table), ints(lens)
+    ok = dict(q=q, cache=cache, table=tab, lens=ln)
+    for bad in (dict(q=q.float()), dict(q=queries(1, 3, d)), dict(q=queries(1, 4, 64)[..., ::2]),
+                dict(cache=cache.cpu()), dict(cache=cache[:, :, :, :-16]), dict(table=tab.long()),
+                dict(table=tab[0]), dict(lens=ints([1, 2])), dict(q_offsets=ints([0])),
+                dict(q=queries(3, 4, d), table=ints([[0], [1]]), lens=ints([1, 2])),
+                dict(out=torch.empty(1, 4, d).cuda()), dict(lse=torch.empty(1, 3).cuda()),
+                dict(q_offsets=torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            ea.kv4_fwd(**{**ok, **bad})
+    for bad in (dict(scale=-1.0), dict(k_descale=3.0), dict(max_q=0),
+                dict(workspace=torch.empty(16, dtype=torch.uint8).cuda())):
+        with pytest.raises((ea.AttentionError, ValueError)):
+            ea.kv4_fwd(**{**ok, **bad})
+    k = normal(2, 2, d).bfloat16().cuda()
+    for args in ((k, k, cache, ints([0])), (k[:, :1], k[:, :1], cache, ints([0, 1])),
+                 (k, k[:1], cache, ints([0, 1])), (k.float(), k.float(), cache, ints([0, 1]))):
+        with pytest.raises(ValueError):
+            ea.kv4_append(*args)
+    with pytest.raises(ValueError):
+        ea.kv4_read(cache, ints([[0]]), d)
+
+
+# --------------------------------------------------------------------------------- a serving loop
+@pytest.mark.parametrize("d,page,Hq,Hkv", [(128, 16, 8, 2), (64, 64, 4, 4)])
+def test_a_serving_loop(d, page, Hq, Hkv):
+    """plan -> rope -> append -> attention over several steps (prompt chunks, single tokens, a request
+    that ends and one that starts), against the fp64 attention on the cache's own bytes, and the
+    cache against the quantised fp64 keys."""
+    rng = np.random.default_rng(7)
+    B, width = 4, 12
+    pages = B * width
+    turns, m = ea.rope_turns(d, scaling="linear", factor=2.0)
+    cache = ea.kv4_cache(pages, Hkv, page, d)
+    table = torch.zeros(B, width, dtype=torch.int32).cuda()
+    queue = ints(rng.permutation(pages))
+    state, lens = ints([0, pages]), ints([0] * B)
+    for step, new in enumerate([[30, 5, 0, 17], [1, 1, 20, 1], [1, 1, 1, -1], [3, 2, 1, 40], [1, 1, 1, 1]]):
+        T = sum(max(n, 0) for n in new)
+        plan = ea.page_plan(lens, ints(new), table, queue, state, page, T)
+        q, k = queries(T, Hq, d, seed=10 + step), queries(T, Hkv, d, seed=20 + step)
+        v = queries(T, Hkv, d, seed=30 + step)
+        qr, kr = ea.rope(q, k, plan.positions, turns, mscale=m)
+        ea.kv4_append(kr, v, cache, plan.slots)
+        kc, vc = ea.kv4_read(cache, plan.slots, d)
+        assert np.array_equal(numpy64(kc), kv.dequantise(*kv.quantise(numpy64(kr))))
+        assert np.array_equal(numpy64(vc), kv.dequantise(*kv.quantise(numpy64(v))))
+        got = ea.kv4_fwd(qr, cache, table, plan.lens, q_offsets=plan.q_offsets, max_q=max(new))
+        check(qr, cache, table.cpu().numpy(), plan.lens.tolist(), plan.q_offsets.tolist(), d, got=got)
+        lens, state = plan.lens, plan.queue_state
+    assert lens.tolist() == [36, 10, 23, 41]

@@ -1,0 +1,92 @@
+"""Page planning on the GPU against the sequential reference: integers, equal."""
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_13_gb300 as ea
+from oracle import kv
+
+pytestmark = pytest.mark.gpu
+
+
+def setup(rng, B, page, width, free, head, maxlen=None):
+    lens = rng.integers(0, (maxlen or width * page) + 1, B)
+    table = rng.permutation(B * width).reshape(B, width)
+    cap = B * width
+    queue = np.full(cap, -7)
+    have = -(-lens // page)
+    spare = np.concatenate([table[b, have[b]:] for b in range(B)])[:free]
+    queue[(head + np.arange(len(spare))) % cap] = spare
+    return lens, table, queue, [head, len(spare)]
+
+
+def compare(lens, new, table, queue, state, page, T):
+    cuda = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32).cuda()  # noqa: E731
+    tab, que = cuda(table), cuda(queue)
+    plan = ea.page_plan(cuda(lens), cuda(new), tab, que, cuda(state), page, T)
+    want = kv.page_plan(lens, new, np.asarray(table).tolist(), np.asarray(queue).tolist(), state, page, T)
+    got = [*plan, tab, que]
+    for name, g, w in zip(("lens", "q_offsets", "positions", "slots", "state", "table", "queue"), got, want):
+        assert g.tolist() == w, name
+    return got
+
+
+@pytest.mark.parametrize("B,page,width,free,chunk", [
+    (1, 16, 4, 3, 1), (8, 64, 8, 40, 1), (33, 16, 9, 150, 40), (600, 32, 5, 1000, 30),
+    (1025, 128, 2, 700, 100), (3, 16, 300, 20, 500),
+])
+def test_against_the_reference(B, page, width, free, chunk):
+    rng = np.random.default_rng(B)
+    lens, table, queue, state = setup(rng, B, page, width, free, head=(3 * B) % (B * width))
+    new = rng.integers(-1, chunk + 1, B)
+    total = int(np.maximum(new, 0).sum())
+    compare(lens, new, table, queue, state, page, total + 5)
+    if total > 3:  # a packed batch smaller than the tokens: what fits is written
+        compare(lens, new, table, queue, state, page, total - 3)
+
+
+def test_refused_requests_and_no_tokens():
+    # 0: too wide; 1: takes 2 of 2 pages; 2: refused; 3: fits in its last page; 4: ended
+    lens, new = [60, 0, 16, 17, 33], [10, 32, 1, 3, -1]
+    table = np.arange(20).reshape(5, 4)
+    queue, state = [18, 19] + [-1] * 18, [0, 2]
+    got = compare(lens, new, table, queue, state, 16, 50)
+    assert got[0].tolist() == [60, 32, 16, 20, 0]
+    assert got[3].tolist()[:10] == [-1] * 10 and got[3].tolist()[42] == -1
+    assert got[4].tolist() == [2, 3]
+    compare([0, 5], [0, 0], np.zeros((2, 1), int), [0], [0, 0], 16, 0)
+    compare([0, 5], [-1, -1], np.array([[3], [4]]), [9, 9], [1, 0], 16, 0)
+
+
+def test_many_steps_keep_every_page_once():
+    rng = np.random.default_rng(5)
+    B, page, width = 40, 16, 6
+    lens, table, queue, state = setup(rng, B, page, width, 10 ** 6, 0)
+    for _ in range(6):
+        new = rng.integers(-1, 25, B)
+        got = compare(lens, new, table, queue, state, page, 1200)
+        lens, state, table, queue = got[0].tolist(), got[4].tolist(), got[5].cpu().numpy(), got[6].cpu().numpy()
+
+
+def test_captured_into_a_graph_and_given_buffers():
+    rng = np.random.default_rng(6)
+    B, page, width = 5, 32, 6
+    lens, table, queue, state = setup(rng, B, page, width, 20, 4, maxlen=40)
+    cuda = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32).cuda()  # noqa: E731
+    ins = [cuda(x) for x in (lens, [1] * B, table, queue, state)]
+    out = ea.page_plan(*ins, page, B)
+    with pytest.raises(ea.AttentionError):  # not in place
+        ea.page_plan(*ins, page, B, out=out._replace(lens=ins[0]))
+    with pytest.raises(ValueError):
+        ea.page_plan(*ins, page, B + 1, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ea.page_plan(*ins, page, B, out=out)
+        ins[0].copy_(out.lens)
+        ins[4].copy_(out.queue_state)
+    for step in range(40):
+        want = kv.page_plan(ins[0].tolist(), [1] * B, ins[2].tolist(), ins[3].tolist(), ins[4].tolist(), page, B)
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip([*out, ins[2], ins[3]], want):
+            assert g.tolist() == w
