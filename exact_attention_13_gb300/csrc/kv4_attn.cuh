@@ -32,6 +32,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cstdint>
 
 #include "kv4_cache.cuh"
@@ -44,7 +45,7 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStrip = 32;                     // keys of one warp in a tile
 constexpr int kDecTile = kDecStrip * kDecWarps;   // keys of a tile
-constexpr int kDecStages = 3;
+constexpr int kDecStages = 2;
 constexpr float kLn2F = 0.6931471805599453f;
 // The reference m of a row's probabilities 2^(x - m) is set kDecBelow under the running maximum and
 // O and l are rescaled only when the maximum has grown by more than 8 (log2) since: P then lies
@@ -52,6 +53,8 @@ constexpr float kLn2F = 0.6931471805599453f;
 // skip the reduction over the warp.
 constexpr float kDecBelow = 7.f;
 constexpr float kDecLazy = kDecBelow + 8.f;
+// m before a row has seen a key: finite, so that 2^(x - m) is 0 for a masked x = -inf and 2^(m - m') 0
+constexpr float kDecNone = -3.0e38f;
 
 struct Kv4Args {
   const __nv_bfloat16* q;  // [T, Hq, d], strides in elements
@@ -94,11 +97,11 @@ __device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
   return s;
 }
 
-// Units (key head x block of R rows) and tiles per unit of a request; a request without keys keeps
-// one (empty) tile, so that its rows are written.
+// Blocks of R query rows, and tiles of a unit (one block, one key head) of a request; a request
+// without keys keeps one (empty) tile, so that its rows are written.
 template <int R>
-__device__ __forceinline__ int kv4_units(const Kv4Args& a, const ReqShape& s) {
-  return static_cast<int>((static_cast<long long>(s.q_len) * a.group + R - 1) / R) * a.hk;
+__device__ __forceinline__ int kv4_blocks(const Kv4Args& a, const ReqShape& s) {
+  return static_cast<int>((static_cast<long long>(s.q_len) * a.group + R - 1) / R);
 }
 __device__ __forceinline__ int kv4_tiles(const ReqShape& s) {
   return max(1, (s.keys - 1) / kDecTile + 1);
@@ -119,6 +122,22 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
+// Both halves of a times the low (high) half of s.
+__device__ __forceinline__ uint32_t mul_f16x2_lo(uint32_t a, uint32_t s) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            __low2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t mul_f16x2_hi(uint32_t a, uint32_t s) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// Whether either half is NaN.
+__device__ __forceinline__ bool any_nan_f16x2(uint32_t x) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&x);
+  return !__hbeq2(h, h);
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -136,23 +155,29 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // then read rows of both parities, which halves the bank conflicts of V's loads.
 __device__ __forceinline__ int kv4_perm(int r) { return r ^ ((r >> 1) & 1); }
 
-// Where the CTA's line of tiles runs: request, unit, tile.
+// Where the CTA's line of tiles runs: request, block of query rows, key head, tile (the unit's
+// number within its request is block * hk + head).
 struct TileCursor {
-  int r, u, tile, units, tiles;
+  int r, block, head, tile, blocks, tiles, keys;
 };
 
+// To the next tile; true when the next unit begins with it.
 template <int R>
-__device__ __forceinline__ void cursor_next(const Kv4Args& a, TileCursor& c) {
-  if (++c.tile < c.tiles) return;
+__device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
+  if (++c.tile < c.tiles) return false;
   c.tile = 0;
-  if (++c.u < c.units) return;
-  c.u = 0;
+  if (++c.head < a.hk) return true;
+  c.head = 0;
+  if (++c.block < c.blocks) return true;
+  c.block = 0;
   while (++c.r < a.b) {
     const ReqShape s = kv4_request(a, c.r);
-    c.units = kv4_units<R>(a, s);
+    c.blocks = kv4_blocks<R>(a, s);
     c.tiles = kv4_tiles(s);
-    if (c.units > 0) return;
+    c.keys = s.keys;
+    if (c.blocks > 0) break;
   }
+  return true;
 }
 
 // The CTA's range [first, last) of the line of `total` tiles, and the cursor at its first tile.
@@ -161,22 +186,33 @@ template <int R>
 __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, TileCursor* s_cur,
                                             long long& total, long long& first, long long& last) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  auto cost = [&](int r, int& units, int& tiles) -> long long {
-    units = 0;
-    tiles = 1;
+  TileCursor c;
+  auto cost = [&](int r) -> long long {
+    c = TileCursor{r, 0, 0, 0, 0, 1, 0};
     if (r >= a.b) return 0;
     const ReqShape s = kv4_request(a, r);
-    units = kv4_units<R>(a, s);
-    tiles = kv4_tiles(s);
-    return static_cast<long long>(units) * tiles;
+    c.blocks = kv4_blocks<R>(a, s);
+    c.tiles = kv4_tiles(s);
+    c.keys = s.keys;
+    return static_cast<long long>(c.blocks) * a.hk * c.tiles;
   };
-  int units, tiles;
-  long long mine = 0;
-  for (int r = tid; r < a.b; r += kDecThreads) mine += cost(r, units, tiles);
+  // inclusive scan over the block; s_sum keeps the warps' sums until the next barrier
+  auto scan = [&](long long x) {
 #pragma unroll
-  for (int o = 16; o; o /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
+    for (int o = 1; o < 32; o *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w)
+      if (w < warp) x += s_sum[w];
+    return x;
+  };
+  long long mine = 0, tiles = 0;
+  for (int r = tid; r < a.b; r += kDecThreads) mine += tiles = cost(r);
+  long long inc = scan(mine);
   total = 0;
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
@@ -184,32 +220,26 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
   if (static_cast<int>(blockIdx.x) >= n) return n;
   first = total * blockIdx.x / n;
   last = total * (blockIdx.x + 1) / n;
+  // up to one request a thread, the scan above is the line itself; else it is redone in pieces
   long long base = 0;
   for (int r0 = 0; r0 < a.b; r0 += kDecThreads) {
-    __syncthreads();
-    const long long c = cost(r0 + tid, units, tiles);
-    long long inc = c;
+    long long all = total;
+    if (a.b > kDecThreads) {
+      __syncthreads();
+      tiles = cost(r0 + tid);
+      inc = scan(tiles) + base;
+      all = base;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+      for (int w = 0; w < kDecWarps; ++w) all += s_sum[w];
     }
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    long long before = base, all = base;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      before += w < warp ? s_sum[w] : 0;
-      all += s_sum[w];
-    }
-    const long long lo = before + inc - c;
-    if (first >= lo && first < lo + c) {
+    const long long lo = inc - tiles;
+    if (first >= lo && first < inc) {
       const long long off = first - lo;
-      s_cur->r = r0 + tid;
-      s_cur->u = static_cast<int>(off / tiles);
-      s_cur->tile = static_cast<int>(off % tiles);
-      s_cur->units = units;
-      s_cur->tiles = tiles;
+      const int u = static_cast<int>(off / c.tiles);
+      c.tile = static_cast<int>(off - static_cast<long long>(u) * c.tiles);
+      c.block = u / a.hk;
+      c.head = u - c.block * a.hk;
+      *s_cur = c;
     }
     base = all;
     if (first < base) break;
@@ -227,7 +257,7 @@ __host__ __device__ constexpr int dec_smem_bytes() {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kernel(const Kv4Args a) {
   constexpr int R = 8 * NT;            // query rows of a unit
   constexpr int MT = D / 16;           // 16-dim tiles of O^T
   constexpr int QW = D / 8;            // f16x2 words of one lane's share of a query row
@@ -245,6 +275,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
   uint8_t* const ring = dec_smem + warp * (kDecStages * dec_strip_bytes<D>());
   float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D>());
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long total, first, last;
   const int n_cta = kv4_my_range<R>(a, s_sum, &s_cur, total, first, last);
   if (static_cast<int>(blockIdx.x) >= n_cta) {
@@ -257,66 +288,66 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
   const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
 
   // ---- loads: the strip's two 16-key groups, one page id each, fetched a step ahead
-  int id[2];
+  const size_t page_bytes = block_bytes * 2 * a.hk;
+  constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
+  // the lane's copy of the strip's scales: kScale copies for each of (K, V) x (group 0, 1)
+  const bool sc_lane = lane < 4 * kScale;
+  const int sc_group = (lane / kScale) & 1, sc_kv = (lane / kScale) >> 1;
+  const int sc_dst = (sc_kv ? kVs : kKs) + sc_group * 16 * kScale + (lane % kScale) * 16;
+  const uint32_t ring_u32 = smem_u32(ring);
+  const uint8_t *code_base, *scale_base;  // of the head, with the lane's offset
+  const int* row_ids;                     // the request's row of the table
+  auto set_head = [&]() {
+    const uint8_t* h = a.cache + static_cast<size_t>(ld.head) * 2 * block_bytes;
+    code_base = h + lane * 16;
+    scale_base = h + (sc_kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * kCode + (lane % kScale) * 16;
+    row_ids = a.table + static_cast<size_t>(ld.r) * a.width;
+  };
+  int id0, id1;
   int ld_left = steps;
   unsigned seen = 0;  // two bits a strip in flight: the group's page exists
   auto fetch_ids = [&]() {
     const int key0 = ld.tile * kDecTile + warp * kDecStrip;
-    const int keys = kv4_request(a, ld.r).keys;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int key = key0 + 16 * j;
-      id[j] = key < keys ? __ldg(a.table + static_cast<size_t>(ld.r) * a.width + (key >> a.page_shift)) : -1;
-    }
+    id0 = key0 < ld.keys ? __ldg(row_ids + (key0 >> a.page_shift)) : -1;
+    id1 = id0;
+    if (a.page_shift == 4) id1 = key0 + 16 < ld.keys ? __ldg(row_ids + (key0 >> 4) + 1) : -1;
   };
   auto issue = [&](int stage) {
     seen <<= 2;
     if (ld_left > 0) {
+      const uint32_t dst = ring_u32 + stage * dec_strip_bytes<D>();
       const int key0 = ld.tile * kDecTile + warp * kDecStrip;
-      const int head = ld.u % a.hk;
-      const uint8_t* src[2];
-      uint32_t bytes[2];
+      const int row0 = key0 & (page_rows - 1);
+      const int row1 = a.page_shift == 4 ? 0 : row0 + 16;
+      const bool ok0 = static_cast<unsigned>(id0) < static_cast<unsigned>(a.pages);
+      const bool ok1 = static_cast<unsigned>(id1) < static_cast<unsigned>(a.pages);
+      // a page that is not there: copies of zero bytes, which write zeros and read nothing
+      const uint32_t n0 = ok0 ? 16u : 0u, n1 = ok1 ? 16u : 0u;
+      const size_t at0 = ok0 ? id0 * page_bytes : 0, at1 = ok1 ? id1 * page_bytes : 0;
+      const uint8_t* k0 = code_base + at0 + row0 * kCode;
+      const uint8_t* k1 = code_base + at1 + row1 * kCode;
+      const uint8_t *v0 = k0 + block_bytes, *v1 = k1 + block_bytes;
+      const uint32_t to = dst + lane * 16;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool ok = id[j] >= 0 && id[j] < a.pages;
-        const int row = (key0 + 16 * j) & (page_rows - 1);
-        src[j] = a.cache;
-        if (ok) src[j] += (static_cast<size_t>(id[j]) * a.hk + head) * 2 * block_bytes + row * kCode;
-        bytes[j] = ok ? 16u : 0u;  // 0: the copy writes zeros and reads nothing
-        seen |= (ok ? 1u : 0u) << j;
+      for (int p = 0; p < kPer; ++p) {
+        cp_async16(to + p * 512, k0 + p * 512, n0);
+        cp_async16(to + 16 * kCode + p * 512, k1 + p * 512, n1);
+        cp_async16(to + kV + p * 512, v0 + p * 512, n0);
+        cp_async16(to + kV + 16 * kCode + p * 512, v1 + p * 512, n1);
       }
-      // scales start behind the codes of the whole page; row * kCode is already in src
-      const uint32_t dst = smem_u32(ring + stage * dec_strip_bytes<D>());
-      constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint8_t* v = src[j] + (bytes[j] ? block_bytes : 0);
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-          const int at = (p * 32 + lane) * 16;
-          cp_async16(dst + j * 16 * kCode + at, src[j] + (bytes[j] ? at : 0), bytes[j]);
-          cp_async16(dst + kV + j * 16 * kCode + at, v + (bytes[j] ? at : 0), bytes[j]);
-        }
-      }
-      // 16 * kScale bytes of scales a group: kScale copies, K and V, both groups
-      if (lane < 4 * kScale) {
-        const int which = lane / kScale, j = which & 1, kv = which >> 1;
-        const int at = (lane % kScale) * 16;
-        const int row = (key0 + 16 * j) & (page_rows - 1);
-        const uint32_t ok = j ? bytes[1] : bytes[0];
-        const uint8_t* p = j ? src[1] : src[0];
-        if (ok)
-          p += (kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * kCode - row * kCode + row * kScale + at;
-        cp_async16(dst + (kv ? kVs : kKs) + j * 16 * kScale + at, p, ok);
-      }
+      if (sc_lane)
+        cp_async16(dst + sc_dst, scale_base + (sc_group ? at1 + row1 * kScale : at0 + row0 * kScale),
+                   sc_group ? n1 : n0);
+      seen |= (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
       if (--ld_left > 0) {
-        cursor_next<R>(a, ld);
+        if (cursor_next<R>(a, ld)) set_head();
         fetch_ids();
       }
     }
     cp_async_commit();
   };
 
+  set_head();
   fetch_ids();
 #pragma unroll
   for (int s = 0; s < kDecStages; ++s) issue(s);
@@ -337,7 +368,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
     if (fresh) {
       fresh = false;
       req = kv4_request(a, cur.r);
-      const int head = cur.u % a.hk, row0 = cur.u / a.hk * R, rows = req.q_len * a.group;
+      const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
       min_lim = 0x7fffffff;
       max_lim = 0;
 #pragma unroll
@@ -381,7 +412,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
           lim[nt][cc] = k;
           min_lim = min(min_lim, k);
           if (crow < rows) max_lim = max(max_lim, k);
-          m[nt][cc] = -INFINITY;
+          m[nt][cc] = kDecNone;
           l[nt][cc] = 0.f;
         }
       }
@@ -415,24 +446,17 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
           for (int e = 0; e < 4; ++e) x[tg][nt][e] = 0.f;
         const int k0 = tg * 16 + kv4_perm(g8), k1 = k0 + 8;
         uint32_t w0[KW], w1[KW];
-        uint32_t sc0[2], sc1[2];  // scales of the lane's first and second 16 dims, as pairs
+        uint32_t sc0, sc1;  // scales of the lane's first and second 16 dims
         if constexpr (D == 128) {
           *reinterpret_cast<uint4*>(w0) = *reinterpret_cast<const uint4*>(st + k0 * kCode + t4 * 16);
           *reinterpret_cast<uint4*>(w1) = *reinterpret_cast<const uint4*>(st + k1 * kCode + t4 * 16);
-          const uint32_t h0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k0 * kScale + t4 * 2));
-          const uint32_t h1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k1 * kScale + t4 * 2));
-          sc0[0] = __byte_perm(h0, 0u, 0x1010);
-          sc0[1] = __byte_perm(h0, 0u, 0x3232);
-          sc1[0] = __byte_perm(h1, 0u, 0x1010);
-          sc1[1] = __byte_perm(h1, 0u, 0x3232);
+          sc0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k0 * kScale + t4 * 2));
+          sc1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kKs + k1 * kScale + t4 * 2));
         } else {
           *reinterpret_cast<uint2*>(w0) = *reinterpret_cast<const uint2*>(st + k0 * kCode + t4 * 8);
           *reinterpret_cast<uint2*>(w1) = *reinterpret_cast<const uint2*>(st + k1 * kCode + t4 * 8);
-          const uint32_t b0 = st[kKs + k0 * kScale + t4], b1 = st[kKs + k1 * kScale + t4];
-          sc0[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b0 | (b0 << 8)));
-          sc1[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b1 | (b1 << 8)));
-          sc0[1] = sc0[0];
-          sc1[1] = sc1[0];
+          sc0 = e4m3x2_to_f16x2(st[kKs + k0 * kScale + t4]);
+          sc1 = e4m3x2_to_f16x2(st[kKs + k1 * kScale + t4]);
         }
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
@@ -441,8 +465,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
           unpack_e2m1x8(w1[w], h1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            h0[e] = mul_f16x2(h0[e], sc0[w / 2]);
-            h1[e] = mul_f16x2(h1[e], sc1[w / 2]);
+            h0[e] = w / 2 ? mul_f16x2_hi(h0[e], sc0) : mul_f16x2_lo(h0[e], sc0);
+            h1[e] = w / 2 ? mul_f16x2_hi(h1[e], sc1) : mul_f16x2_lo(h1[e], sc1);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -453,35 +477,48 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[tg][nt][e] *= cs[nt][e & 1];
+          for (int e = 0; e < 4; e += 2) {
+            const float2 y = mul_f32x2(f32x2(x[tg][nt][e], x[tg][nt][e + 1]), f32x2(cs[nt][0], cs[nt][1]));
+            x[tg][nt][e] = y.x;
+            x[tg][nt][e + 1] = y.y;
+          }
       }
 
       // ---- V codes and scales of the lane's tokens (two pairs a group)
-      uint32_t vw[2][4][VW], vs[2][2];
+      uint32_t vw[2][4][VW], vs[2][2], b[2][4];
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg) {
-        uint32_t b[4];
+      for (int tg = 0; tg < 2; ++tg)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
           if constexpr (D == 128) {
             *reinterpret_cast<uint2*>(vw[tg][e]) = *reinterpret_cast<const uint2*>(st + kV + tok * kCode + g8 * 8);
-            b[e] = st[kVs + tok * kScale + g8];
+            b[tg][e] = st[kVs + tok * kScale + g8];
           } else {
             vw[tg][e][0] = *reinterpret_cast<const uint32_t*>(st + kV + tok * kCode + g8 * 4);
-            b[e] = st[kVs + tok * kScale + g8 / 2];
+            b[tg][e] = st[kVs + tok * kScale + g8 / 2];
           }
-          // keys past the end and on missing pages must not meet P's zeros with a NaN scale
-          if (!full && (key0 + tok >= req.keys || !((have >> tg) & 1u))) b[e] = 0u;
         }
-        vs[tg][0] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[0] | (b[1] << 8)));
-        vs[tg][1] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[2] | (b[3] << 8)));
+      if (!full) {
+        // keys past the end and on missing pages must not meet P's zeros with a NaN scale
+#pragma unroll
+        for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
+            if (key0 + tok >= req.keys || !((have >> tg) & 1u)) b[tg][e] = 0u;
+          }
       }
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr)
+          vs[tg][pr] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[tg][2 * pr] | (b[tg][2 * pr + 1] << 8)));
       // A value vector that is not a number makes the rows that see its key NaN through their
       // scores; its scales become zero, because rows that do not see it multiply it by zero.
-      const uint32_t any = hadd_f16x2(hadd_f16x2(vs[0][0], vs[0][1]), hadd_f16x2(vs[1][0], vs[1][1]));
-      const float2 any2 = f16x2_to_f32x2(any);
-      const bool poisoned = __any_sync(0xffffffffu, !(any2.x + any2.y == any2.x + any2.y));
+      const bool poisoned = __any_sync(
+          0xffffffffu,
+          any_nan_f16x2(hadd_f16x2(hadd_f16x2(vs[0][0], vs[0][1]), hadd_f16x2(vs[1][0], vs[1][1]))));
 
       if (!full || poisoned) {
 #pragma unroll
@@ -512,7 +549,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          top[nt][cc] = fmaxf(fmaxf(x[0][nt][cc], x[0][nt][2 + cc]), fmaxf(x[1][nt][cc], x[1][nt][2 + cc]));
+          top[nt][cc] = max3f(fmaxf(x[0][nt][cc], x[0][nt][2 + cc]), x[1][nt][cc], x[1][nt][2 + cc]);
           grow |= top[nt][cc] > m[nt][cc] + kDecLazy;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -524,7 +561,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
 #pragma unroll
             for (int s = 4; s <= 16; s *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
             v = fmaxf(v - kDecBelow, m[nt][cc]);
-            const float alpha = v == -INFINITY ? 1.f : ex2_mufu(m[nt][cc] - v);
+            const float alpha = ex2_mufu(m[nt][cc] - v);
             m[nt][cc] = v;
             l[nt][cc] *= alpha;
 #pragma unroll
@@ -537,18 +574,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float2 below = f32x2(-m[nt][0], -m[nt][1]);
+        float2 sum = f32x2(l[nt][0], l[nt][1]);
 #pragma unroll
         for (int tg = 0; tg < 2; ++tg) {
 #pragma unroll
           for (int hr = 0; hr < 2; ++hr) {
-            const float p0 = ex2_mufu(x[tg][nt][2 * hr] - m0), p1 = ex2_mufu(x[tg][nt][2 * hr + 1] - m1);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            pb[tg][nt][hr] = movmatrix_trans(pack_f16x2(p0, p1));
+            const float2 y = add_f32x2(f32x2(x[tg][nt][2 * hr], x[tg][nt][2 * hr + 1]), below);
+            const float2 p = f32x2(ex2_mufu(y.x), ex2_mufu(y.y));
+            sum = add_f32x2(sum, p);
+            pb[tg][nt][hr] = movmatrix_trans(pack_f16x2(p.x, p.y));
           }
         }
+        l[nt][0] = sum.x;
+        l[nt][1] = sum.y;
       }
 
       // ---- O^T += V^T P^T
@@ -600,14 +639,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int col = nt * 8 + 2 * t4 + cc;
-          float big = -INFINITY;
+          float big = kDecNone;
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) big = fmaxf(big, s_m[w][col]);
-          const float base = big == -INFINITY ? 0.f : big;
           float sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) sum += s_l[w][col] * ex2_mufu(s_m[w][col] - base);
-          const float f = ex2_mufu(m[nt][cc] - base);
+          for (int w = 0; w < kDecWarps; ++w) sum += s_l[w][col] * ex2_mufu(s_m[w][col] - big);
+          const float f = ex2_mufu(m[nt][cc] - big);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             o[i][nt][cc] *= f;
@@ -647,7 +685,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
       const bool complete = unit_ends && whole_start;
       if (warp == 0) {
         add(1);
-        const int head = cur.u % a.hk, row0 = cur.u / a.hk * R, rows = req.q_len * a.group;
+        const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
         const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -681,78 +719,98 @@ __global__ void __launch_bounds__(kDecThreads, NT == 4 ? 2 : 3) kv4_decode_kerne
       if (whole_start && !unit_ends) {
         // the unit begins here and ends in a later CTA: x is its last tile on the line
         const long long x = first + step + (cur.tiles - 1 - cur.tile);
-        merge = make_int4(unit_no > 0 ? 1 : 0, cur.r, cur.u, static_cast<int>(((x + 1) * n_cta - 1) / total));
+        merge = make_int4(unit_no > 0 ? 1 : 0, cur.r, cur.block * a.hk + cur.head,
+                          static_cast<int>(((x + 1) * n_cta - 1) / total));
       }
       ++unit_no;
       fresh = true;
       whole_start = true;
     }
-    if (step + 1 < steps) cursor_next<R>(a, cur);
+    if (step + 1 < steps) (void)cursor_next<R>(a, cur);
   }
   cp_async_wait<0>();
   if (threadIdx.x == 0) a.desc[blockIdx.x] = merge;
 }
 
-// Merge of units that cross CTAs: block (i, row) adds up row `row` of the unit that begins in CTA i
-// and ends later, if there is one.  Warps take every eighth part, in a fixed order.
+// Merge of units that cross CTAs.  Block (i, y) takes rows y, y + gridDim.y, ... of the unit that
+// begins in CTA i and ends later, if there is one; its warps share the rows and, of a row, the
+// parts, and always add in the same order.  It is launched while the decode kernel still runs and
+// waits for its end.
 constexpr int kMergeThreads = 256;
 
 template <int D, int R>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Args a) {
   constexpr int kWarps = kMergeThreads / 32, kPer = D / 32;
   __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = a.desc[blockIdx.x];
   if (u.x < 0) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, row = blockIdx.y;
-  const ReqShape req = kv4_request(a, u.y);
-  const int head = u.z % a.hk, at_row = u.z / a.hk * R + row;
-  if (at_row >= req.q_len * a.group) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int parts = u.w - static_cast<int>(blockIdx.x) + 1;
-  auto slot = [&](int k) {  // part k: this CTA's, then the first of each later one
-    return static_cast<size_t>(2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? u.x : 0)) * R + row;
-  };
-  float big = -INFINITY;
-  for (int k = threadIdx.x; k < parts; k += kMergeThreads) big = fmaxf(big, a.part_ml[slot(k)].x);
+  // warps on one row: all of them for many parts or few rows, else one
+  const bool alone = parts <= kWarps && static_cast<int>(gridDim.y) == 1;
+  const int sharing = alone ? 1 : kWarps;
+  const ReqShape req = kv4_request(a, u.y);
+  const int block = u.z / a.hk, head = u.z - block * a.hk;
+  const int rows = min(R, req.q_len * a.group - block * R);
+  const int step = alone ? kWarps : gridDim.y;
+  for (int row = alone ? warp : blockIdx.y; row < rows; row += step) {
+    auto slot = [&](int k) {  // part k: this CTA's, then the first of each later one
+      return static_cast<size_t>(2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? u.x : 0)) * R + row;
+    };
+    const int k0 = alone ? 0 : warp;
+    float big = kDecNone, sum = 0.f, acc[kPer];
 #pragma unroll
-  for (int s = 16; s; s /= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
-  if (lane == 0) s_m[warp] = big;
-  __syncthreads();
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    // running maximum: sums so far are rescaled when it grows
+#pragma unroll 8
+    for (int k = k0; k < parts; k += sharing) {
+      const float2 ml = a.part_ml[slot(k)];
+      const float* src = a.part_o + slot(k) * D + lane * kPer;
+      const float top = fmaxf(big, ml.x);
+      const float f = ex2_mufu(ml.x - top), g = ex2_mufu(big - top);
+      big = top;
+      sum = fmaf(sum, g, ml.y * f);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w]);
-  const float base = big == -INFINITY ? 0.f : big;
-  float acc[kPer], sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int k = warp; k < parts; k += kWarps) {
-    const float2 ml = a.part_ml[slot(k)];
-    const float f = ex2_mufu(ml.x - base);
-    sum += ml.y * f;
-    const float* src = a.part_o + slot(k) * D + lane * kPer;
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + i);
-      acc[i] = fmaf(y.x, f, acc[i]);
-      acc[i + 1] = fmaf(y.y, f, acc[i + 1]);
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + i);
+        acc[i] = fmaf(acc[i], g, y.x * f);
+        acc[i + 1] = fmaf(acc[i + 1], g, y.y * f);
+      }
     }
-  }
+    if (!alone) {
+      if (lane == 0) s_m[warp] = big;
+      __syncthreads();
+      const float own = big;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i];
-  if (lane == 0) s_l[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float l = 0.f, y0 = 0.f, y1 = 0.f;
+      for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w]);
+      const float f = ex2_mufu(own - big);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      l += s_l[w];
-      y0 += s_o[w][2 * threadIdx.x];
-      y1 += s_o[w][2 * threadIdx.x + 1];
+      for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i] * f;
+      if (lane == 0) s_l[warp] = sum * f;
+      __syncthreads();
+      if (warp == 0) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          sum += s_l[w];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) acc[i] += s_o[w][lane * kPer + i];
+        }
+      }
     }
-    const int qi = at_row / a.group, qg = at_row - qi * a.group;
-    const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
-    const float inv = l == 0.f ? 0.f : a.v_descale / l;
-    *reinterpret_cast<uint32_t*>(a.o + at * D + 2 * threadIdx.x) = pack_bf16x2(y0 * inv, y1 * inv);
-    if (threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : big * kLn2F + logf(l);
+    if (alone || warp == 0) {
+      const int at_row = block * R + row, qi = at_row / a.group, qg = at_row - qi * a.group;
+      const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
+      const float inv = sum == 0.f ? 0.f : a.v_descale / sum;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2)
+        *reinterpret_cast<uint32_t*>(a.o + at * D + lane * kPer + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      if (lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : big * kLn2F + logf(sum);
+    }
+    if (!alone) __syncthreads();
   }
 }
 

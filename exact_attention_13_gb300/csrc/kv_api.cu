@@ -90,7 +90,7 @@ int row_grid(long long groups, unsigned& grid) {
 
 // ---------------------------------------------------------------------------------- attention
 // CTAs of one SM, by rows of a unit: 64 to 87 KB of shared memory and up to 168 (255) registers.
-constexpr int dec_ctas_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 // Query rows that share a unit, in eights: the smallest of 8, 16 and 32 that hold the rows of one
 // key head (fewer padded rows), 32 when none does (the cache is then read once per 32 rows).
@@ -116,8 +116,19 @@ int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   if (int rc = opt_in_smem(kern, smem, done)) return rc;
   kern<<<n, kDecThreads, smem, s>>>(a);
   if (int rc = launched()) return rc;
-  kv4_merge_kernel<D, 8 * NT><<<dim3(n, 8 * NT), kMergeThreads, 0, s>>>(a);
-  return launched();
+  // Few units: each may span many CTAs, and rows get blocks of their own (one block for all rows of
+  // a unit that spans the whole GPU would take about 10 us); else a block takes all rows of its unit.
+  const unsigned row_blocks = static_cast<long long>(a.b) * a.hk <= n / 8 ? 8 * NT : 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(n, row_blocks);
+  config.blockDim = dim3(kMergeThreads);
+  config.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kv4_merge_kernel<D, 8 * NT>, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D>

@@ -24,28 +24,34 @@ from typing import NamedTuple
 
 import torch
 
+from . import _check, lib
 from ._kv_abi import FA_ROPE_INTERLEAVED, FA_ROPE_INVERSE
 
-_strides = ctypes.c_longlong * 3
+_bf16, _i32, _f32 = torch.bfloat16, torch.int32, torch.float32
+_Strides = ctypes.c_longlong * 3
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_bound = {}
 
 
-def _lib():
-    from . import lib
+def _fn(name):
+    """The library's entry point (looked up once: these calls are made once per layer and token)."""
+    f = _bound.get(name)
+    if f is None:
+        f = _bound[name] = getattr(lib(), name)
+    return f
 
-    return lib()
 
-
-def _run(fn, device, *args):
-    """Call a library entry point on `device`'s current stream; raise on a status code."""
-    from . import _check
-
-    f = getattr(_lib(), fn)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _check(f(*args, stream), fn)
+def _run(name, index, *args):
+    """Call an entry point on device `index`'s current stream; raise on a status code."""
+    f = _bound.get(name) or _fn(name)
+    if index == _current_device():
+        rc = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _check(f(*args, stream), fn)
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
+    if rc:
+        _check(rc, name)
 
 
 def _need(ok, what):
@@ -53,10 +59,10 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _int32(t, shape, device, name):
-    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous()
-          and tuple(t.shape) == shape,
-          f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+def _ints(t, shape, index, name):
+    if (t.dtype is not _i32 or t.get_device() != index or t.shape != shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
 
 
 # ---------------------------------------------------------------------------------------------
@@ -105,17 +111,23 @@ def rope_turns(rotary_dim: int, base: float = 10000.0, scaling: str | None = Non
     return torch.tensor([round(x * unit) for x in f], dtype=torch.int64, device=device), mscale
 
 
-def _head_strides(x, name):
-    """(B, H, N, d) and {batch, head, row} strides of [B, H, N, d] or packed [T, H, d]."""
-    s = x.stride()
-    if x.dim() == 4:
-        shape, strides = tuple(x.shape), (s[0], s[1], s[2])
+def _heads(x, index, name):
+    """(B, H, N, d) and the {batch, head, row} strides of [B, H, N, d] or packed [T, H, d]."""
+    if x.dtype is not _bf16 or x.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor, all on one device")
+    dim = x.dim()
+    if dim == 4:
+        s0, s1, s2, last = x.stride()
+        shape, strides = x.shape, (s0, s1, s2)
+    elif dim == 3:
+        s0, s1, last = x.stride()
+        T, H, d = x.shape
+        shape, strides = (1, H, T, d), (0, s1, s0)
     else:
-        _need(x.dim() == 3, f"{name} must be [B, H, N, d] or [T, H, d]")
-        shape, strides = (1, x.shape[1], x.shape[0], x.shape[2]), (0, s[1], s[0])
-    _need(x.is_cuda and x.dtype == torch.bfloat16, f"{name} must be a bf16 CUDA tensor")
-    _need(s[-1] == 1, f"{name}'s last dimension must be contiguous")
-    return shape, strides
+        raise ValueError(f"{name} must be [B, H, N, d] or [T, H, d]")
+    if last != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return shape, _Strides(*strides)
 
 
 def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = False,
@@ -129,30 +141,33 @@ def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = Fals
     rotary_dim / 2) or, ``interleaved``, (2i, 2i + 1); the rest is copied.  ``inverse`` turns back:
     the gradients of q and k from those of the outputs, with the same ``mscale``.  ``q_out`` and
     ``k_out`` may be q and k themselves (in place)."""
-    shape, qs = _head_strides(q, "q")
-    B, Hq, N, d = shape
-    dev = q.device
+    index = q.get_device()
+    (B, Hq, N, d), qs = _heads(q, index, "q")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _need(q_out.shape == q.shape and q_out.device == dev, "q_out must match q")
-    qos = _head_strides(q_out, "q_out")[1]
+        q_out = torch.empty(q.shape, dtype=_bf16, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    qos = _heads(q_out, index, "q_out")[1]
     Hk, kp, ko, ks, kos = 0, None, None, None, None
     if k is not None:
-        kshape, ks = _head_strides(k, "k")
-        Hk = kshape[1]
-        _need(k.dim() == q.dim() and kshape[0] == B and kshape[2:] == (N, d) and k.device == dev,
-              "k must be like q but for its heads")
+        (Bk, Hk, Nk, dk), ks = _heads(k, index, "k")
+        if Bk != B or Nk != N or dk != d or k.dim() != q.dim():
+            raise ValueError("k must be like q but for its heads")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        _need(k_out.shape == k.shape and k_out.device == dev, "k_out must match k")
-        kos = _strides(*_head_strides(k_out, "k_out")[1])
-        ks, kp, ko = _strides(*ks), k.data_ptr(), k_out.data_ptr()
-    _int32(positions, (B, N) if positions.dim() == 2 else (N,), dev, "positions")
-    _need(turns.dtype == torch.int64 and turns.dim() == 1 and turns.device == dev
-          and turns.is_contiguous(), f"turns must be a contiguous int64 vector on {dev}")
-    _run("fa_rope", dev, q.data_ptr(), _strides(*qs), q_out.data_ptr(), _strides(*qos), Hq, kp, ks,
-         ko, kos, Hk, B, N, d, positions.data_ptr(), N if positions.dim() == 2 else 0,
-         turns.data_ptr(), 2 * turns.shape[0],
+            k_out = torch.empty(k.shape, dtype=_bf16, device=k.device)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        kos = _heads(k_out, index, "k_out")[1]
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    else:
+        k_out = None
+    per_batch = positions.dim() == 2
+    _ints(positions, (B, N) if per_batch else (N,), index, "positions")
+    if (turns.dtype is not torch.int64 or turns.dim() != 1 or turns.get_device() != index
+            or not turns.is_contiguous()):
+        raise ValueError(f"turns must be a contiguous int64 vector on cuda:{index}")
+    _run("fa_rope", index, q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, kp, ks, ko, kos, Hk, B, N,
+         d, positions.data_ptr(), N if per_batch else 0, turns.data_ptr(), 2 * turns.shape[0],
          (FA_ROPE_INTERLEAVED if interleaved else 0) | (FA_ROPE_INVERSE if inverse else 0),
          mscale)
     return q_out, k_out
@@ -182,31 +197,27 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
     get their pages keep their length and get slots of -1 (see fa_page_plan in
     include/exact_attention.h).  ``out``: a plan of the right sizes to write into; its ``lens`` and
     ``queue_state`` must not be this call's inputs."""
-    dev = lens.device
-    _need(lens.is_cuda and lens.dim() == 1, "lens must be an int32 CUDA vector")
-    _need(table.dim() == 2 and queue.dim() == 1, "table must be [B, width], queue a vector")
-    _need(num_tokens >= 0, "num_tokens must be >= 0")
-    B, width = lens.shape[0], table.shape[1]
-    for t, shape, name in ((lens, (B,), "lens"), (new_lens, (B,), "new_lens"),
-                           (table, (B, width), "table"), (queue, tuple(queue.shape), "queue"),
-                           (queue_state, (2,), "queue_state")):
-        _int32(t, shape, dev, name)
+    index = lens.get_device()
+    if index < 0 or lens.dim() != 1 or table.dim() != 2 or queue.dim() != 1 or num_tokens < 0:
+        raise ValueError("lens and queue must be int32 CUDA vectors, table [B, width], num_tokens >= 0")
+    B, width, cap = lens.shape[0], table.shape[1], queue.shape[0]
+    _ints(lens, (B,), index, "lens")
+    _ints(new_lens, (B,), index, "new_lens")
+    _ints(table, (B, width), index, "table")
+    _ints(queue, (cap,), index, "queue")
+    _ints(queue_state, (2,), index, "queue_state")
+    sizes = (B, B + 1, num_tokens, num_tokens, 2)
     if out is None:
-        # one allocation, each part on a 16-byte boundary
-        sizes = (B, B + 1, num_tokens, num_tokens, 2)
-        flat = torch.empty(sum(-(-n // 4) * 4 for n in sizes), dtype=torch.int32, device=dev)
-        parts, at = [], 0
-        for n in sizes:
-            parts.append(flat[at:at + n])
-            at += -(-n // 4) * 4
-        out = PagePlan(*parts)
+        # one allocation for the five parts
+        flat = torch.empty(2 * (B + num_tokens) + 3, dtype=_i32, device=lens.device)
+        out = PagePlan._make(flat.split(sizes))
     else:
-        for t, n, name in zip(out, (B, B + 1, num_tokens, num_tokens, 2), PagePlan._fields):
-            _int32(t, (n,), dev, f"out.{name}")
-    _run("fa_page_plan", dev, lens.data_ptr(), new_lens.data_ptr(), table.data_ptr(), width,
-         queue.data_ptr(), queue.shape[0], queue_state.data_ptr(), B, page_size, num_tokens,
-         out.lens.data_ptr(), out.q_offsets.data_ptr(), out.positions.data_ptr(),
-         out.slots.data_ptr(), out.queue_state.data_ptr())
+        for t, n, name in zip(out, sizes, PagePlan._fields):
+            _ints(t, (n,), index, f"out.{name}")
+    _run("fa_page_plan", index, lens.data_ptr(), new_lens.data_ptr(), table.data_ptr(), width,
+         queue.data_ptr(), cap, queue_state.data_ptr(), B, page_size, num_tokens,
+         out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+         out[4].data_ptr())
     return out
 
 
@@ -215,7 +226,7 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
 # ---------------------------------------------------------------------------------------------
 def kv4_cache(num_pages: int, heads: int, page_size: int, d: int, device="cuda"):
     """An empty 4-bit cache: uint8 zeros [num_pages, heads, 2, page_size * 9 d / 16]."""
-    total = int(_lib().fa_kv4_cache_bytes(num_pages, heads, page_size, d))
+    total = int(_fn("fa_kv4_cache_bytes")(num_pages, heads, page_size, d))
     _need(total > 0, f"unsupported cache (pages {num_pages}, heads {heads}, page size {page_size},"
                      f" d {d})")
     return torch.zeros((num_pages, heads, 2, total // (2 * num_pages * heads)), dtype=torch.uint8,
@@ -224,53 +235,61 @@ def kv4_cache(num_pages: int, heads: int, page_size: int, d: int, device="cuda")
 
 def _cache_shape(cache, d):
     """(pages, heads, page size) of a cache of head dim d."""
-    _need(cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 4 and cache.shape[2] == 2
-          and cache.is_contiguous() and cache.shape[3] * 16 % (9 * d) == 0,
-          f"cache must be a contiguous uint8 CUDA tensor as kv4_cache makes it for d = {d}")
-    return cache.shape[0], cache.shape[1], cache.shape[3] * 16 // (9 * d)
+    if cache.dim() != 4 or d < 16:
+        raise ValueError("cache must be as kv4_cache makes it")
+    pages, heads, two, block = cache.shape
+    page, rest = divmod(block * 16, 9 * d)
+    if rest or two != 2 or cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        raise ValueError(f"cache must be a contiguous uint8 tensor as kv4_cache makes it for d = {d}")
+    return pages, heads, page
 
 
 def kv4_append(k, v, cache, slots, k_descale: float = 1.0, v_descale: float = 1.0):
     """Quantise k and v (bf16 [T, H, d], last dimension contiguous) and write them into the cache
     at ``slots`` (int32 [T]; rows with a slot outside the cache, such as -1, are skipped).  Descales
     are powers of two: values are stored divided by them."""
-    _need(k.is_cuda and k.dtype == torch.bfloat16 and k.dim() == 3 and k.shape == v.shape
-          and v.dtype == k.dtype and v.device == k.device,
-          "k and v must be bf16 CUDA tensors of one shape [T, H, d]")
-    ks, vs = k.stride(), v.stride()
-    _need(ks[2] == 1 and vs[2] == 1, "the last dimension of k and v must be contiguous")
+    index = k.get_device()
+    if (k.dtype is not _bf16 or v.dtype is not _bf16 or k.dim() != 3 or k.shape != v.shape
+            or index < 0 or v.get_device() != index):
+        raise ValueError("k and v must be bf16 CUDA tensors of one shape [T, H, d]")
+    (k0, k1, k2), (v0, v1, v2) = k.stride(), v.stride()
+    if k2 != 1 or v2 != 1:
+        raise ValueError("the last dimension of k and v must be contiguous")
     T, H, d = k.shape
     pages, heads, page = _cache_shape(cache, d)
-    _need(heads == H and cache.device == k.device, "the cache must have k's heads and device")
-    _int32(slots, (T,), k.device, "slots")
-    _run("fa_kv4_append", k.device, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-         cache.data_ptr(), pages, page, slots.data_ptr(), T, H, d, k_descale, v_descale)
+    if heads != H or cache.get_device() != index:
+        raise ValueError("the cache must have k's heads and device")
+    _ints(slots, (T,), index, "slots")
+    _run("fa_kv4_append", index, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, cache.data_ptr(),
+         pages, page, slots.data_ptr(), T, H, d, k_descale, v_descale)
 
 
 def kv4_read(cache, slots, d: int, k_descale: float = 1.0, v_descale: float = 1.0, k=None, v=None):
     """The cached keys and values at ``slots`` (int32 [T]) as bf16 [T, H, d] (exact); rows whose slot
     lies outside the cache are zeros.  Returns (k, v)."""
-    _need(d in (64, 128), "d must be 64 or 128")
+    index = cache.get_device()
     pages, heads, page = _cache_shape(cache, d)
-    dev = cache.device
-    _need(slots.dim() == 1, "slots must be a vector")
+    if index < 0 or slots.dim() != 1:
+        raise ValueError("the cache must be on a CUDA device, slots a vector")
     T = slots.shape[0]
-    _int32(slots, (T,), dev, "slots")
-    outs = []
-    for name, t in (("k", k), ("v", v)):
-        if t is None:
-            t = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev)
-        _need(tuple(t.shape) == (T, heads, d) and t.dtype == torch.bfloat16 and t.device == dev
-              and t.is_contiguous(), f"{name} must be a contiguous bf16 [T, H, d] tensor")
-        outs.append(t)
-    _run("fa_kv4_read", dev, cache.data_ptr(), pages, page, slots.data_ptr(), outs[0].data_ptr(),
-         outs[1].data_ptr(), T, heads, d, k_descale, v_descale)
-    return outs[0], outs[1]
+    _ints(slots, (T,), index, "slots")
+    shape = (T, heads, d)
+    if k is None:
+        k = torch.empty(shape, dtype=_bf16, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=_bf16, device=cache.device)
+    for t in (k, v):
+        if (t.shape != shape or t.dtype is not _bf16 or t.get_device() != index
+                or not t.is_contiguous()):
+            raise ValueError("k and v must be contiguous bf16 [T, H, d] tensors")
+    _run("fa_kv4_read", index, cache.data_ptr(), pages, page, slots.data_ptr(), k.data_ptr(),
+         v.data_ptr(), T, heads, d, k_descale, v_descale)
+    return k, v
 
 
 def kv4_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int = 1) -> int:
     """Bytes of scratch ``kv4_fwd`` needs (whatever the lengths are)."""
-    return int(_lib().fa_kv4_fwd_workspace_bytes(Hq, Hkv, d, max_q))
+    return int(_fn("fa_kv4_fwd_workspace_bytes")(Hq, Hkv, d, max_q))
 
 
 def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, causal: bool = True,
@@ -286,43 +305,48 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     rows share a pass over the cache.  Rows of q past the last request's are left as they are.
     ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes, not shared by calls that may run
     at the same time; without it torch allocates one."""
-    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3,
-          "q must be a bf16 CUDA tensor [T, Hq, d]")
-    qs = q.stride()
-    _need(qs[2] == 1, "q's last dimension must be contiguous")
+    index = q.get_device()
+    if q.dtype is not _bf16 or q.dim() != 3 or index < 0:
+        raise ValueError("q must be a bf16 CUDA tensor [T, Hq, d]")
+    q0, q1, q2 = q.stride()
     T, Hq, d = q.shape
-    dev = q.device
-    _need(d in (64, 128), "d must be 64 or 128")
     pages, Hkv, page = _cache_shape(cache, d)
-    _need(cache.device == dev and Hq % Hkv == 0, "q's heads must be a multiple of the cache's")
-    _need(table.dim() == 2, "table must be [B, width]")
+    if q2 != 1 or cache.get_device() != index or Hkv < 1 or Hq % Hkv:
+        raise ValueError("q's last dimension must be contiguous, its heads a multiple of the cache's, "
+                         "both on one device")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, width]")
     B, width = table.shape
-    _int32(table, (B, width), dev, "table")
-    _int32(lens, (B,), dev, "lens")
+    _ints(table, (B, width), index, "table")
+    _ints(lens, (B,), index, "lens")
+    offsets = None
     if q_offsets is not None:
-        _int32(q_offsets, (B + 1,), dev, "q_offsets")
-    else:
-        _need(B > 0 and T % B == 0, "without q_offsets T must be a multiple of B")
+        _ints(q_offsets, (B + 1,), index, "q_offsets")
+        offsets = q_offsets.data_ptr()
+    elif B < 1 or T % B:
+        raise ValueError("without q_offsets T must be a multiple of B")
     if max_q is None:
         max_q = max(1, -(-T // max(B, 1)))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, Hq, d), dtype=_bf16, device=q.device)
+    elif (out.shape != q.shape or out.dtype is not _bf16 or out.get_device() != index
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    _need(out.shape == q.shape and out.dtype == torch.bfloat16 and out.is_contiguous()
-          and out.device == dev, "out must be a contiguous bf16 tensor shaped like q")
-    _need(tuple(lse.shape) == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous()
-          and lse.device == dev, "lse must be a contiguous fp32 [T, Hq] tensor")
+        lse = torch.empty((T, Hq), dtype=_f32, device=q.device)
+    elif (lse.shape != (T, Hq) or lse.dtype is not _f32 or lse.get_device() != index
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [T, Hq] tensor")
     if workspace is None:
-        workspace = torch.empty(kv4_workspace_bytes(Hq, Hkv, d, max_q), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace.device == dev and workspace.is_contiguous(),
-          "workspace must be a contiguous tensor on q's device")
-    _run("fa_kv4_fwd", dev, q.data_ptr(), qs[0], qs[1], cache.data_ptr(), pages, page,
-         table.data_ptr(), width, lens.data_ptr(),
-         q_offsets.data_ptr() if q_offsets is not None else None, out.data_ptr(), lse.data_ptr(),
-         T, B, Hq, Hkv, d, max_q, scale, bool(causal), k_descale, v_descale, workspace.data_ptr(),
-         workspace.numel() * workspace.element_size())
+        size = kv4_workspace_bytes(Hq, Hkv, d, max_q)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        size = workspace.numel() * workspace.element_size()
+    _run("fa_kv4_fwd", index, q.data_ptr(), q0, q1, cache.data_ptr(), pages, page,
+         table.data_ptr(), width, lens.data_ptr(), offsets, out.data_ptr(), lse.data_ptr(), T, B,
+         Hq, Hkv, d, max_q, scale, bool(causal), k_descale, v_descale, workspace.data_ptr(), size)
     return out, lse
