@@ -23,9 +23,9 @@
 // Queries are scaled by a power of two per row into [1, 2) before they become f16, so the conversion
 // keeps bf16's 8 bits down to 2^-17 of the row's largest value.
 //
-// Split.  The work of all requests is one line of tiles (128 keys of one key head, for one block of
-// query rows); CTA i of n takes the i-th n-th of it, so ragged lengths balance by themselves and a
-// single long request fills the GPU.  In a tile each warp takes 32 keys, in its own ring of
+// Split.  The work of all requests is one line of tiles (128 or 256 keys of one key head, for one
+// block of query rows); CTA i of n takes the i-th n-th of it, so ragged lengths balance by themselves and a
+// single long request fills the GPU.  In a tile each warp takes 32 keys (64 at head dim 64), in its own ring of
 // cp.async stages, with its own softmax state: warps meet only at the end of a unit (one key head of
 // one block of rows).  A unit that crosses CTAs leaves partial sums (O, max, sum) in the workspace,
 // which a second kernel merges in a fixed order.
@@ -43,8 +43,13 @@ namespace exattn {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecStrip = 32;                     // keys of one warp in a tile
-constexpr int kDecTile = kDecStrip * kDecWarps;   // keys of a tile
+// 16-key groups of a strip, one warp's share of a tile
+template <int D>
+__host__ __device__ constexpr int dec_groups() { return D == 128 ? 2 : 4; }
+template <int D>
+__host__ __device__ constexpr int dec_strip() { return 16 * dec_groups<D>(); }
+template <int D>
+__host__ __device__ constexpr int dec_tile() { return kDecWarps * dec_strip<D>(); }
 constexpr int kDecStages = 2;
 constexpr float kLn2F = 0.6931471805599453f;
 // The reference m of a row's probabilities 2^(x - m) is set kDecBelow under the running maximum and
@@ -71,6 +76,7 @@ struct Kv4Args {
   long long q_len;
   int t, b, hq, hk, group, width, page_shift, pages;
   int causal;
+  int whole_tiles;         // > 0: units are not split, each counts as this many tiles
   float c;                 // scale * log2(e) * key descale
   float v_descale;
 };
@@ -103,8 +109,9 @@ template <int R>
 __device__ __forceinline__ int kv4_blocks(const Kv4Args& a, const ReqShape& s) {
   return static_cast<int>((static_cast<long long>(s.q_len) * a.group + R - 1) / R);
 }
+template <int D>
 __device__ __forceinline__ int kv4_tiles(const ReqShape& s) {
-  return max(1, (s.keys - 1) / kDecTile + 1);
+  return max(1, (s.keys - 1) / dec_tile<D>() + 1);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -162,7 +169,7 @@ struct TileCursor {
 };
 
 // To the next tile; true when the next unit begins with it.
-template <int R>
+template <int D, int R>
 __device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
   if (++c.tile < c.tiles) return false;
   c.tile = 0;
@@ -173,7 +180,7 @@ __device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
   while (++c.r < a.b) {
     const ReqShape s = kv4_request(a, c.r);
     c.blocks = kv4_blocks<R>(a, s);
-    c.tiles = kv4_tiles(s);
+    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
     c.keys = s.keys;
     if (c.blocks > 0) break;
   }
@@ -182,7 +189,7 @@ __device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
 
 // The CTA's range [first, last) of the line of `total` tiles, and the cursor at its first tile.
 // Returns the number of CTAs that have work.
-template <int R>
+template <int D, int R>
 __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, TileCursor* s_cur,
                                             long long& total, long long& first, long long& last) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -192,7 +199,7 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
     if (r >= a.b) return 0;
     const ReqShape s = kv4_request(a, r);
     c.blocks = kv4_blocks<R>(a, s);
-    c.tiles = kv4_tiles(s);
+    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
     c.keys = s.keys;
     return static_cast<long long>(c.blocks) * a.hk * c.tiles;
   };
@@ -216,10 +223,11 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
   total = 0;
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
-  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  const long long piece = a.whole_tiles ? a.whole_tiles : 1;  // shares are whole pieces
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total / piece));
   if (static_cast<int>(blockIdx.x) >= n) return n;
-  first = total * blockIdx.x / n;
-  last = total * (blockIdx.x + 1) / n;
+  first = total / piece * blockIdx.x / n * piece;
+  last = total / piece * (blockIdx.x + 1) / n * piece;
   // up to one request a thread, the scan above is the line itself; else it is redone in pieces
   long long base = 0;
   for (int r0 = 0; r0 < a.b; r0 += kDecThreads) {
@@ -249,7 +257,7 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
 }
 
 template <int D>
-__host__ __device__ constexpr int dec_strip_bytes() { return kDecStrip * (D + D / 8); }
+__host__ __device__ constexpr int dec_strip_bytes() { return dec_strip<D>() * (D + D / 8); }
 
 template <int D, int NT>
 __host__ __device__ constexpr int dec_smem_bytes() {
@@ -264,7 +272,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   constexpr int KW = D / 32;           // code words of a lane's share of a key
   constexpr int VW = D / 64;           // code words of a lane's share of a value
   constexpr int kCode = D / 2, kScale = D / 16;  // bytes of a row's codes and scales
-  constexpr int kKs = kDecStrip * kCode, kV = kKs + kDecStrip * kScale, kVs = kV + kKs;
+  constexpr int TG = dec_groups<D>(), kStrip = dec_strip<D>();
+  constexpr int kKs = kStrip * kCode, kV = kKs + kStrip * kScale, kVs = kV + kKs;
+  constexpr unsigned kAll = (1u << TG) - 1;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ long long s_sum[kDecWarps];
   __shared__ TileCursor s_cur;
@@ -277,9 +287,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long total, first, last;
-  const int n_cta = kv4_my_range<R>(a, s_sum, &s_cur, total, first, last);
+  const int n_cta = kv4_my_range<D, R>(a, s_sum, &s_cur, total, first, last);
   if (static_cast<int>(blockIdx.x) >= n_cta) {
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
   const int steps = static_cast<int>(last - first);
@@ -287,12 +297,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   const int page_rows = 1 << a.page_shift;
   const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
 
-  // ---- loads: the strip's two 16-key groups, one page id each, fetched a step ahead
+  // ---- loads: the strip's 16-key groups, one page id each, fetched a step ahead
   const size_t page_bytes = block_bytes * 2 * a.hk;
   constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
-  // the lane's copy of the strip's scales: kScale copies for each of (K, V) x (group 0, 1)
-  const bool sc_lane = lane < 4 * kScale;
-  const int sc_group = (lane / kScale) & 1, sc_kv = (lane / kScale) >> 1;
+  // the lane's copy of the strip's scales: kScale copies for each of (K, V) x groups, 32 in all
+  static_assert(2 * TG * kScale == 32, "one copy of scales a lane");
+  const int sc_group = lane / kScale % TG, sc_kv = lane / (kScale * TG);
   const int sc_dst = (sc_kv ? kVs : kKs) + sc_group * 16 * kScale + (lane % kScale) * 16;
   const uint32_t ring_u32 = smem_u32(ring);
   const uint8_t *code_base, *scale_base;  // of the head, with the lane's offset
@@ -303,44 +313,50 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
     scale_base = h + (sc_kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * kCode + (lane % kScale) * 16;
     row_ids = a.table + static_cast<size_t>(ld.r) * a.width;
   };
-  int id0, id1;
+  int id[TG];
   int ld_left = steps;
-  unsigned seen = 0;  // two bits a strip in flight: the group's page exists
+  unsigned seen = 0;  // TG bits a strip in flight: the group's page exists
   auto fetch_ids = [&]() {
-    const int key0 = ld.tile * kDecTile + warp * kDecStrip;
-    id0 = key0 < ld.keys ? __ldg(row_ids + (key0 >> a.page_shift)) : -1;
-    id1 = id0;
-    if (a.page_shift == 4) id1 = key0 + 16 < ld.keys ? __ldg(row_ids + (key0 >> 4) + 1) : -1;
+    const int key0 = ld.tile * dec_tile<D>() + warp * kStrip;
+#pragma unroll
+    for (int g = 0; g < TG; ++g) {
+      const int key = key0 + 16 * g;
+      // groups that share a page share its id
+      if (g > 0 && (key & (page_rows - 1)) != 0) id[g] = id[g - 1];
+      else id[g] = key < ld.keys ? __ldg(row_ids + (key >> a.page_shift)) : -1;
+    }
   };
   auto issue = [&](int stage) {
-    seen <<= 2;
+    seen <<= TG;
     if (ld_left > 0) {
       const uint32_t dst = ring_u32 + stage * dec_strip_bytes<D>();
-      const int key0 = ld.tile * kDecTile + warp * kDecStrip;
-      const int row0 = key0 & (page_rows - 1);
-      const int row1 = a.page_shift == 4 ? 0 : row0 + 16;
-      const bool ok0 = static_cast<unsigned>(id0) < static_cast<unsigned>(a.pages);
-      const bool ok1 = static_cast<unsigned>(id1) < static_cast<unsigned>(a.pages);
-      // a page that is not there: copies of zero bytes, which write zeros and read nothing
-      const uint32_t n0 = ok0 ? 16u : 0u, n1 = ok1 ? 16u : 0u;
-      const size_t at0 = ok0 ? id0 * page_bytes : 0, at1 = ok1 ? id1 * page_bytes : 0;
-      const uint8_t* k0 = code_base + at0 + row0 * kCode;
-      const uint8_t* k1 = code_base + at1 + row1 * kCode;
-      const uint8_t *v0 = k0 + block_bytes, *v1 = k1 + block_bytes;
-      const uint32_t to = dst + lane * 16;
+      const int key0 = ld.tile * dec_tile<D>() + warp * kStrip;
+      uint32_t sc_n = 0;
+      size_t sc_at = 0;
 #pragma unroll
-      for (int p = 0; p < kPer; ++p) {
-        cp_async16(to + p * 512, k0 + p * 512, n0);
-        cp_async16(to + 16 * kCode + p * 512, k1 + p * 512, n1);
-        cp_async16(to + kV + p * 512, v0 + p * 512, n0);
-        cp_async16(to + kV + 16 * kCode + p * 512, v1 + p * 512, n1);
+      for (int g = 0; g < TG; ++g) {
+        const bool ok = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
+        // a page that is not there: copies of zero bytes, which write zeros and read nothing
+        const uint32_t n = ok ? 16u : 0u;
+        const size_t at = ok ? id[g] * page_bytes : 0;
+        const int row = (key0 + 16 * g) & (page_rows - 1);
+        const uint8_t* k = code_base + at + row * kCode;
+        const uint8_t* v = k + block_bytes;
+        const uint32_t to = dst + g * 16 * kCode + lane * 16;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          cp_async16(to + p * 512, k + p * 512, n);
+          cp_async16(to + kV + p * 512, v + p * 512, n);
+        }
+        if (sc_group == g) {
+          sc_n = n;
+          sc_at = at + row * kScale;
+        }
+        seen |= (ok ? 1u : 0u) << g;
       }
-      if (sc_lane)
-        cp_async16(dst + sc_dst, scale_base + (sc_group ? at1 + row1 * kScale : at0 + row0 * kScale),
-                   sc_group ? n1 : n0);
-      seen |= (ok0 ? 1u : 0u) | (ok1 ? 2u : 0u);
+      cp_async16(dst + sc_dst, scale_base + sc_at, sc_n);
       if (--ld_left > 0) {
-        if (cursor_next<R>(a, ld)) set_head();
+        if (cursor_next<D, R>(a, ld)) set_head();
         fetch_ids();
       }
     }
@@ -431,15 +447,15 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 
     cp_async_wait<kDecStages - 1>();
     __syncwarp();
-    const int key0 = cur.tile * kDecTile + warp * kDecStrip;
-    const unsigned have = (seen >> (2 * (kDecStages - 1))) & 3u;
+    const int key0 = cur.tile * dec_tile<D>() + warp * kStrip;
+    const unsigned have = (seen >> (TG * (kDecStages - 1))) & kAll;
     if (key0 < max_lim && have) {
       const uint8_t* const st = ring + stage * dec_strip_bytes<D>();
-      const bool full = key0 + kDecStrip <= min_lim && have == 3u;
-      float x[2][NT][4];
+      const bool full = key0 + kStrip <= min_lim && have == kAll;
+      float x[TG][NT][4];
       // ---- S^T = K Q^T
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg) {
+      for (int tg = 0; tg < TG; ++tg) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -484,25 +500,19 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
           }
       }
 
-      // ---- V codes and scales of the lane's tokens (two pairs a group)
-      uint32_t vw[2][4][VW], vs[2][2], b[2][4];
+      // ---- V scales of the lane's tokens (two pairs a group)
+      uint32_t vs[TG][2], b[TG][4];
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
+      for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
-          if constexpr (D == 128) {
-            *reinterpret_cast<uint2*>(vw[tg][e]) = *reinterpret_cast<const uint2*>(st + kV + tok * kCode + g8 * 8);
-            b[tg][e] = st[kVs + tok * kScale + g8];
-          } else {
-            vw[tg][e][0] = *reinterpret_cast<const uint32_t*>(st + kV + tok * kCode + g8 * 4);
-            b[tg][e] = st[kVs + tok * kScale + g8 / 2];
-          }
+          b[tg][e] = st[kVs + tok * kScale + (D == 128 ? g8 : g8 / 2)];
         }
       if (!full) {
         // keys past the end and on missing pages must not meet P's zeros with a NaN scale
 #pragma unroll
-        for (int tg = 0; tg < 2; ++tg)
+        for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
@@ -510,19 +520,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
           }
       }
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
+      for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
         for (int pr = 0; pr < 2; ++pr)
           vs[tg][pr] = e4m3x2_to_f16x2(static_cast<uint16_t>(b[tg][2 * pr] | (b[tg][2 * pr + 1] << 8)));
       // A value vector that is not a number makes the rows that see its key NaN through their
       // scores; its scales become zero, because rows that do not see it multiply it by zero.
-      const bool poisoned = __any_sync(
-          0xffffffffu,
-          any_nan_f16x2(hadd_f16x2(hadd_f16x2(vs[0][0], vs[0][1]), hadd_f16x2(vs[1][0], vs[1][1]))));
+      uint32_t sum_vs = hadd_f16x2(vs[0][0], vs[0][1]);
+#pragma unroll
+      for (int tg = 1; tg < TG; ++tg) sum_vs = hadd_f16x2(sum_vs, hadd_f16x2(vs[tg][0], vs[tg][1]));
+      const bool poisoned = __any_sync(0xffffffffu, any_nan_f16x2(sum_vs));
 
       if (!full || poisoned) {
 #pragma unroll
-        for (int tg = 0; tg < 2; ++tg) {
+        for (int tg = 0; tg < TG; ++tg) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = tg * 16 + kv4_perm(g8) + 8 * (e >> 1);
@@ -549,7 +560,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          top[nt][cc] = max3f(fmaxf(x[0][nt][cc], x[0][nt][2 + cc]), x[1][nt][cc], x[1][nt][2 + cc]);
+          top[nt][cc] = fmaxf(x[0][nt][cc], x[0][nt][2 + cc]);
+#pragma unroll
+          for (int tg = 1; tg < TG; ++tg) top[nt][cc] = max3f(top[nt][cc], x[tg][nt][cc], x[tg][nt][2 + cc]);
           grow |= top[nt][cc] > m[nt][cc] + kDecLazy;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -571,13 +584,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
             }
           }
       }
-      uint32_t pb[2][NT][2];
+      uint32_t pb[TG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 below = f32x2(-m[nt][0], -m[nt][1]);
         float2 sum = f32x2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int tg = 0; tg < 2; ++tg) {
+        for (int tg = 0; tg < TG; ++tg) {
 #pragma unroll
           for (int hr = 0; hr < 2; ++hr) {
             const float2 y = add_f32x2(f32x2(x[tg][nt][2 * hr], x[tg][nt][2 * hr + 1]), below);
@@ -592,13 +605,22 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
+      for (int tg = 0; tg < TG; ++tg) {
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint8_t* p = st + kV + (tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1)) * kCode;
+          if constexpr (D == 128)
+            *reinterpret_cast<uint2*>(vw[e]) = *reinterpret_cast<const uint2*>(p + g8 * 8);
+          else
+            vw[e][0] = *reinterpret_cast<const uint32_t*>(p + g8 * 4);
+        }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           uint32_t even[2][4], odd[2][4];  // [token pair][dim pair]: dims 2i and 2i + 1
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
-            const uint32_t xa = vw[tg][2 * pr][w], xb = vw[tg][2 * pr + 1][w];
+            const uint32_t xa = vw[2 * pr][w], xb = vw[2 * pr + 1][w];
             unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even[pr]);
             unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd[pr]);
 #pragma unroll
@@ -614,6 +636,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
               mma_16816(o[4 * w + e][nt], even[0][e], odd[0][e], even[1][e], odd[1][e], pb[tg][nt][0],
                         pb[tg][nt][1]);
         }
+      }
     }
     __syncwarp();
     issue(stage);
@@ -726,10 +749,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       fresh = true;
       whole_start = true;
     }
-    if (step + 1 < steps) (void)cursor_next<R>(a, cur);
+    if (step + 1 < steps) (void)cursor_next<D, R>(a, cur);
   }
   cp_async_wait<0>();
-  if (threadIdx.x == 0) a.desc[blockIdx.x] = merge;
+  if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = merge;
 }
 
 // Merge of units that cross CTAs.  Block (i, y) takes rows y, y + gridDim.y, ... of the unit that

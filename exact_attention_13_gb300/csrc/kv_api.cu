@@ -102,13 +102,24 @@ size_t dec_workspace(int nt, int d) {
   return (rows * d * 4 + rows * 8 + n * 16 + 255) / 256 * 256;
 }
 
+// Tables of at most this many tiles: units are not split, which saves the merge kernel and the
+// workspace; a unit's tiles then run one after the other.
+constexpr int kWholeTiles = 4;
+int dec_whole_tiles(int d, int page, int width) {
+  const int tile = d == 64 ? dec_tile<64>() : dec_tile<128>();
+  const long long tiles = (static_cast<long long>(page) * width + tile - 1) / tile;
+  return tiles <= kWholeTiles ? static_cast<int>(tiles) : 0;
+}
+
 template <int D, int NT>
 int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   constexpr int n = kSms * dec_ctas_per_sm(NT);
   constexpr size_t rows = static_cast<size_t>(2) * n * 8 * NT;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * D);
-  a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
+  if (!a.whole_tiles) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * D);
+    a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
+  }
   constexpr int smem = dec_smem_bytes<D, NT>();
   static_assert(dec_ctas_per_sm(NT) * (smem + 4096) <= 227 * 1024, "shared memory per SM");
   static std::atomic<uint64_t> done{0};
@@ -116,6 +127,7 @@ int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   if (int rc = opt_in_smem(kern, smem, done)) return rc;
   kern<<<n, kDecThreads, smem, s>>>(a);
   if (int rc = launched()) return rc;
+  if (a.whole_tiles) return FA_OK;
   // Few units: each may span many CTAs, and rows get blocks of their own (one block for all rows of
   // a unit that spans the whole GPU would take about 10 us); else a block takes all rows of its unit.
   const unsigned row_blocks = static_cast<long long>(a.b) * a.hk <= n / 8 ? 8 * NT : 1;
@@ -293,8 +305,11 @@ int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slot
   return launched();
 }
 
-size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
+size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size,
+                                  int table_width) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
+  if (!page_size_ok(page_size) || table_width < 1) return 0;
+  if (dec_whole_tiles(d, page_size, table_width)) return 0;
   return dec_workspace(dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv)), d);
 }
 
@@ -303,7 +318,7 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
                const int* q_offsets, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
                int max_q, float scale, int causal, float k_descale, float v_descale,
                void* workspace, size_t workspace_bytes, void* stream) {
-  if (!q || !table || !lens || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+  if (!q || !table || !lens || !o || !lse) return FA_ERR_INVALID_ARG;
   if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1)
     return FA_ERR_INVALID_ARG;
   if (!q_offsets && T % B) return FA_ERR_INVALID_ARG;
@@ -313,7 +328,8 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
   if (static_cast<long long>(T) * Hq > 0x3fffffffll) return FA_ERR_UNSUPPORTED;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  if (workspace_bytes < dec_workspace(nt, d)) return FA_ERR_INVALID_ARG;
+  const int whole = dec_whole_tiles(d, page_size, table_width);
+  if (!whole && (!workspace || workspace_bytes < dec_workspace(nt, d))) return FA_ERR_INVALID_ARG;
   if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) ||
       !aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) ||
       !aligned(workspace, 16))
@@ -340,6 +356,7 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   a.page_shift = log2_of(page_size);
   a.pages = num_pages;
   a.causal = causal != 0;
+  a.whole_tiles = whole;
   a.c = static_cast<float>(c);
   a.v_descale = v_descale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -19,6 +19,7 @@ and in training, with the gradients of the rotated tensors turned back:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple
 
@@ -28,8 +29,7 @@ from . import _check, lib
 from ._kv_abi import FA_ROPE_INTERLEAVED, FA_ROPE_INVERSE
 
 _bf16, _i32, _f32 = torch.bfloat16, torch.int32, torch.float32
-_Strides = ctypes.c_longlong * 3
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _bound = {}
 
@@ -52,6 +52,12 @@ def _run(name, index, *args):
             rc = f(*args, _raw_stream(index))
     if rc:
         _check(rc, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(batch, head, row):
+    """A C array of three strides (only ever read)."""
+    return (ctypes.c_longlong * 3)(batch, head, row)
 
 
 def _need(ok, what):
@@ -115,19 +121,25 @@ def _heads(x, index, name):
     """(B, H, N, d) and the {batch, head, row} strides of [B, H, N, d] or packed [T, H, d]."""
     if x.dtype is not _bf16 or x.get_device() != index or index < 0:
         raise ValueError(f"{name} must be a bf16 CUDA tensor, all on one device")
-    dim = x.dim()
-    if dim == 4:
-        s0, s1, s2, last = x.stride()
-        shape, strides = x.shape, (s0, s1, s2)
-    elif dim == 3:
-        s0, s1, last = x.stride()
-        T, H, d = x.shape
-        shape, strides = (1, H, T, d), (0, s1, s0)
+    shape, s = x.shape, x.stride()
+    if len(shape) == 4:
+        strides = _strides(s[0], s[1], s[2])
+    elif len(shape) == 3:
+        shape, strides = (1, shape[1], shape[0], shape[2]), _strides(0, s[1], s[0])
     else:
         raise ValueError(f"{name} must be [B, H, N, d] or [T, H, d]")
-    if last != 1:
+    if s[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return shape, _Strides(*strides)
+    return shape, strides
+
+
+def _out_like(x, out, index, name):
+    """`out`, or a new contiguous tensor like x, and its strides."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=_bf16, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    return out, _heads(out, index, name)[1]
 
 
 def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = False,
@@ -143,24 +155,15 @@ def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = Fals
     ``k_out`` may be q and k themselves (in place)."""
     index = q.get_device()
     (B, Hq, N, d), qs = _heads(q, index, "q")
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=_bf16, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    qos = _heads(q_out, index, "q_out")[1]
-    Hk, kp, ko, ks, kos = 0, None, None, None, None
-    if k is not None:
+    q_out, qos = _out_like(q, q_out, index, "q_out")
+    if k is None:
+        k_out, Hk, kp, ko, ks, kos = None, 0, None, None, None, None
+    else:
         (Bk, Hk, Nk, dk), ks = _heads(k, index, "k")
         if Bk != B or Nk != N or dk != d or k.dim() != q.dim():
             raise ValueError("k must be like q but for its heads")
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=_bf16, device=k.device)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        kos = _heads(k_out, index, "k_out")[1]
+        k_out, kos = _out_like(k, k_out, index, "k_out")
         kp, ko = k.data_ptr(), k_out.data_ptr()
-    else:
-        k_out = None
     per_batch = positions.dim() == 2
     _ints(positions, (B, N) if per_batch else (N,), index, "positions")
     if (turns.dtype is not torch.int64 or turns.dim() != 1 or turns.get_device() != index
@@ -210,7 +213,7 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
     if out is None:
         # one allocation for the five parts
         flat = torch.empty(2 * (B + num_tokens) + 3, dtype=_i32, device=lens.device)
-        out = PagePlan._make(flat.split(sizes))
+        out = PagePlan._make(torch.split_with_sizes(flat, sizes))
     else:
         for t, n, name in zip(out, sizes, PagePlan._fields):
             _ints(t, (n,), index, f"out.{name}")
@@ -287,9 +290,11 @@ def kv4_read(cache, slots, d: int, k_descale: float = 1.0, v_descale: float = 1.
     return k, v
 
 
-def kv4_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int = 1) -> int:
-    """Bytes of scratch ``kv4_fwd`` needs (whatever the lengths are)."""
-    return int(_fn("fa_kv4_fwd_workspace_bytes")(Hq, Hkv, d, max_q))
+@functools.lru_cache(maxsize=1024)
+def kv4_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int, page_size: int, width: int) -> int:
+    """Bytes of scratch ``kv4_fwd`` needs for tables of ``width`` pages, whatever the lengths are
+    (0: none, when no key head's work is ever split)."""
+    return int(_fn("fa_kv4_fwd_workspace_bytes")(Hq, Hkv, d, max_q, page_size, width))
 
 
 def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, causal: bool = True,
@@ -303,7 +308,7 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     each without ``q_offsets``.  ``causal``: the queries are the last tokens of the cache.
     ``max_q``: about the most queries of a request (default T / B, rounded up); it only picks how many
     rows share a pass over the cache.  Rows of q past the last request's are left as they are.
-    ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes, not shared by calls that may run
+    ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes or more, not shared by calls that may run
     at the same time; without it torch allocates one."""
     index = q.get_device()
     if q.dtype is not _bf16 or q.dim() != 3 or index < 0:
@@ -339,14 +344,17 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     elif (lse.shape != (T, Hq) or lse.dtype is not _f32 or lse.get_device() != index
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [T, Hq] tensor")
+    scratch = None
     if workspace is None:
-        size = kv4_workspace_bytes(Hq, Hkv, d, max_q)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        size = kv4_workspace_bytes(Hq, Hkv, d, max_q, page, width)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            scratch = workspace.data_ptr()
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
-        size = workspace.numel() * workspace.element_size()
+        size, scratch = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     _run("fa_kv4_fwd", index, q.data_ptr(), q0, q1, cache.data_ptr(), pages, page,
          table.data_ptr(), width, lens.data_ptr(), offsets, out.data_ptr(), lse.data_ptr(), T, B,
-         Hq, Hkv, d, max_q, scale, bool(causal), k_descale, v_descale, workspace.data_ptr(), size)
+         Hq, Hkv, d, max_q, scale, 1 if causal else 0, k_descale, v_descale, scratch, size)
     return out, lse

@@ -335,9 +335,9 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks how
  *                 many query rows share a pass over the cache
  *   scale       : softmax scale, finite and >= 0
- *   workspace   : device scratch of fa_kv4_fwd_workspace_bytes(Hq, Hkv, d, max_q) bytes, 16-byte
- *                 aligned, contents on entry do not matter; calls that may run at the same time
- *                 need one each
+ *   workspace   : device scratch of fa_kv4_fwd_workspace_bytes(...) bytes, 16-byte aligned (NULL
+ *                 when that is 0), contents on entry do not matter; calls that may run at the same
+ *                 time need one each
  *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30; d, page_size and descales as fa_kv4_append
  * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
  * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums
@@ -350,8 +350,10 @@ FA_API int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_st
                       float k_descale, float v_descale, void* workspace, size_t workspace_bytes,
                       void* stream);
 
-/* Workspace bytes fa_kv4_fwd needs; 0 for invalid arguments. */
-FA_API size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q);
+/* Workspace bytes fa_kv4_fwd needs for tables of `table_width` pages; 0 when it needs none (short
+ * tables: no key head's work is split), and for invalid arguments. */
+FA_API size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size,
+                                         int table_width);
 
 /*
  * Read, and if `clear` is nonzero reset to FA_OK, the library's status word on the current

@@ -168,7 +168,8 @@ def test_long_caches_split_over_the_gpu(d, page, lens, qlens, Hq, Hkv):
     cache, table = make(lens, -(-max(lens) // page), page, Hkv, d)
     offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
     q = queries(offsets[-1], Hq, d)
-    ws = torch.full((ea.kv4_workspace_bytes(Hq, Hkv, d, max(qlens)),), 255, dtype=torch.uint8).cuda()
+    size = ea.kv4_workspace_bytes(Hq, Hkv, d, max(qlens), page, table.shape[1])
+    ws = torch.full((size,), 255, dtype=torch.uint8).cuda()
     a = check(q, cache, table, lens, offsets, d, max_q=max(qlens), workspace=ws)
     b = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), max_q=max(qlens),
                    workspace=ws)
@@ -267,7 +268,7 @@ def test_streams_and_two_captured_graphs():
             outs.append([ea.kv4_fwd(q, cache, tab, ln) for _ in range(3)])
     torch.cuda.synchronize()
     graphs, res = [], []
-    ws = torch.empty(ea.kv4_workspace_bytes(8, 2, d, 1), dtype=torch.uint8).cuda()
+    ws = torch.empty(ea.kv4_workspace_bytes(8, 2, d, 1, 64, 47), dtype=torch.uint8).cuda()
     for _ in range(2):  # two graphs that share a workspace, replayed one after the other
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
@@ -283,13 +284,13 @@ def test_streams_and_two_captured_graphs():
 
 def test_refusals():
     d, lens = 128, [5]
-    cache, table = make(lens, 1, 16, 2, d)
+    cache, table = make(lens, 50, 16, 2, d)
     q, tab, ln = queries(1, 4, d), ints(table), ints(lens)
     ok = dict(q=q, cache=cache, table=tab, lens=ln)
     for bad in (dict(q=q.float()), dict(q=queries(1, 3, d)), dict(q=queries(1, 4, 64)[..., ::2]),
                 dict(cache=cache.cpu()), dict(cache=cache[:, :, :, :-16]), dict(table=tab.long()),
                 dict(table=tab[0]), dict(lens=ints([1, 2])), dict(q_offsets=ints([0])),
-                dict(q=queries(3, 4, d), table=ints([[0], [1]]), lens=ints([1, 2])),
+                dict(q=queries(3, 4, d), table=ints([[0] * 50, [1] * 50]), lens=ints([1, 2])),
                 dict(out=torch.empty(1, 4, d).cuda()), dict(lse=torch.empty(1, 3).cuda()),
                 dict(q_offsets=torch.zeros(2, dtype=torch.int32))):
         with pytest.raises(ValueError):

@@ -27,7 +27,7 @@ GOOD = {
     "fa_page_plan": [P, P, P, 4, P, 16, P, 2, 16, 8, P + 64, P, P, P, P + 64, None],
     "fa_kv4_append": [P, 128, 128, P, 128, 128, P, 4, 16, P, 8, 1, 128, 1.0, 1.0, None],
     "fa_kv4_read": [P, 4, 16, P, P, P, 8, 1, 128, 1.0, 1.0, None],
-    "fa_kv4_fwd": [P, 512, 128, P, 4, 16, P, 4, P, P, P, P, 8, 2, 4, 1, 128, 4, 0.1, 1, 1.0, 1.0, P,
+    "fa_kv4_fwd": [P, 512, 128, P, 4, 16, P, 100, P, P, P, P, 8, 2, 4, 1, 128, 4, 0.1, 1, 1.0, 1.0, P,
                    1 << 30, None],
 }
 CASES = [
@@ -88,9 +88,12 @@ def test_sizes():
     assert lib.fa_kv4_cache_bytes(1 << 20, 64, 128, 128) == (1 << 20) * 64 * 2 * 128 * 72
     for bad in ((0, 1, 16, 128), (1, 0, 16, 128), (1, 1, 20, 128), (1, 1, 16, 96)):
         assert lib.fa_kv4_cache_bytes(*bad) == 0
-    assert ea.kv4_workspace_bytes(32, 8, 128, 1) > 0
+    assert ea.kv4_workspace_bytes(32, 8, 128, 1, 64, 9) > 0
+    assert ea.kv4_workspace_bytes(32, 8, 128, 1, 64, 8) == 0  # 512 keys: nothing is split
     for bad in ((0, 1, 128, 1), (3, 2, 128, 1), (4, 2, 96, 1), (4, 2, 128, 0)):
-        assert ea.kv4_workspace_bytes(*bad) == 0
+        assert ea.kv4_workspace_bytes(*bad, 64, 100) == 0
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 24, 100) == 0
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 64, 0) == 0
 
 
 def test_python_checks():
