@@ -12,7 +12,7 @@ LIB_PATH = os.path.join(PKG, "libexattn.so")
 SOURCES = [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "kv_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "fa_fwd_kernel.cuh", "fa_quant.cuh", "fa_bwd_kernel.cuh", "sm103_ptx.cuh", "rope.cuh",
-    "page_plan.cuh", "kv4_cache.cuh", "kv4_attn.cuh")] + [
+    "page_plan.cuh", "kv4_cache.cuh", "kv4_attn.cuh", "kv4_chunk.cuh")] + [
     os.path.join(ROOT, "include", "exact_attention.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",

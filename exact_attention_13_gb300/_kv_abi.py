@@ -15,6 +15,6 @@ SIGNATURES = {
     "fa_kv4_append": (_i, [_p, _l, _l, _p, _l, _l, _p, _i, _i, _p, _i, _i, _i, _f, _f, _p]),
     "fa_kv4_read": (_i, [_p, _i, _i, _p, _p, _p, _i, _i, _i, _f, _f, _p]),
     "fa_kv4_fwd": (_i, [_p, _l, _l, _p, _i, _i, _p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f,
-                        _i, _f, _f, _p, _z, _p]),
+                        _i, _f, _f, _p, _z, _p, _p]),
     "fa_kv4_fwd_workspace_bytes": (_z, [_i, _i, _i, _i, _i, _i]),
 }

@@ -49,7 +49,10 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Device-side address of g_device_status for the current device, looked up once per device.
+}  // namespace
+
+// Device-side address of g_device_status for the current device, looked up once per device (also
+// used by kv_api.cu).
 int* library_status_ptr(int dev) {
   static std::atomic<int*> cache[kMaxDevices];
   int* p = cache[dev].load(std::memory_order_acquire);
@@ -59,6 +62,8 @@ int* library_status_ptr(int dev) {
   cache[dev].store(static_cast<int*>(addr), std::memory_order_release);
   return static_cast<int*>(addr);
 }
+
+namespace {
 
 // [B*H, N, d] view of one operand, tiles of box_rows (128) rows x (one swizzle span) with the
 // swizzle the MMA descriptors expect.  Rows past N (per head) read as zero (loads) or are clipped

@@ -72,6 +72,7 @@ struct Kv4Args {
   float* lse;              // [T, Hq]
   float* part_o;           // [2 n][R][d]
   float2* part_ml;         // [2 n][R] (max, sum)
+  int* status;             // device status word (kv4_chunk.cuh)
   int4* desc;              // [n] unit to merge: {first slot or -1, request, unit, last CTA}
   long long q_len;
   int t, b, hq, hk, group, width, page_shift, pages;
@@ -755,9 +756,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = merge;
 }
 
-// Merge of units that cross CTAs.  Block (i, y) takes rows y, y + gridDim.y, ... of the unit that
-// begins in CTA i and ends later, if there is one; its warps share the rows and, of a row, the
-// parts, and always add in the same order.  It is launched while the decode kernel still runs and
+// Merge of units that cross CTAs.  The blocks (i, *) share the rows of the unit that begins in CTA i
+// and ends later, if there is one.  Of a unit in few parts each warp takes rows of its own; of one
+// in many parts a block takes a row and its warps share the parts.  Always in the same order.  It is launched while the decode kernel still runs and
 // waits for its end.
 constexpr int kMergeThreads = 256;
 
@@ -770,14 +771,13 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Args 
   if (u.x < 0) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int parts = u.w - static_cast<int>(blockIdx.x) + 1;
-  // warps on one row: all of them for many parts or few rows, else one
-  const bool alone = parts <= kWarps && static_cast<int>(gridDim.y) == 1;
+  const bool alone = parts <= kWarps;
   const int sharing = alone ? 1 : kWarps;
   const ReqShape req = kv4_request(a, u.y);
   const int block = u.z / a.hk, head = u.z - block * a.hk;
   const int rows = min(R, req.q_len * a.group - block * R);
-  const int step = alone ? kWarps : gridDim.y;
-  for (int row = alone ? warp : blockIdx.y; row < rows; row += step) {
+  const int step = alone ? kWarps * gridDim.y : gridDim.y;
+  for (int row = alone ? blockIdx.y * kWarps + warp : blockIdx.y; row < rows; row += step) {
     auto slot = [&](int k) {  // part k: this CTA's, then the first of each later one
       return static_cast<size_t>(2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? u.x : 0)) * R + row;
     };

@@ -1,0 +1,617 @@
+// kv4_chunk.cuh -- attention of many query rows over the paged 4-bit cache (prompt chunks).
+//
+// The same operation as kv4_attn.cuh for units of 256 query rows (one key head of one request, rows
+// ordered by token, then by head of the group).  With that many rows the two products, not the
+// cache's bytes, are the floor, so they run on tcgen05: S_h = Q_h K^T and O_h += P_h V for two tiles
+// h of 128 rows, accumulators and probabilities in tensor memory, one thread per row in the softmax.
+// The cache is widened once per tile of 128 keys and serves both row tiles: f16 K and V tiles in a
+// ring of shared-memory slots, in the 128-byte-swizzled layout that the MMA descriptors expect.
+//
+// Roles (512 threads, one CTA a SM):
+//   warps 0-7    softmax of tile 0 / tile 1; also load the query rows (scaled by a power of two into
+//                [1, 2), f16) and write O and the log-sum-exp
+//   warps 8-11   widen the cache: codes and scales from global memory to registers a tile ahead,
+//                code * scale (exact) to the ring
+//   warp  12     issues the MMAs:  S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
+// TMEM: S_0 at columns 0-127, S_1 at 128-255 (P_h, f16, over S_h), O_0 at 256, O_1 at 384.
+//
+// A CTA takes an equal share of the line of all tiles, as in kv4_attn.cuh; a unit that crosses CTAs
+// is merged from partial sums afterwards.  Units of one key head follow each other on the line, so
+// CTAs that run together read the same keys from L2.  Every mbarrier wait is bounded in time; one
+// that runs out sets the CTA's abort flag and the status word, and all roles leave.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "fa_fwd_kernel.cuh"
+#include "kv4_attn.cuh"
+
+namespace exattn {
+
+constexpr int kChThreads = 512;
+constexpr int kChRows = 256;
+constexpr int kChKeys = 128;
+// register shares of the warpgroups: 128 (2 x 200 + 80 + 32) = 512 x 128
+constexpr int kChSoftmaxRegs = 200, kChWidenRegs = 80, kChMmaRegs = 32;
+static_assert(2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs <= 512, "registers of the block at launch");
+
+template <int D>
+struct ChunkGeo {
+  static constexpr int kTileBytes = 128 * D * 2;          // 128 rows of f16, boxes of 64 columns
+  static constexpr int kSlots = D == 128 ? 4 : 8;         // K and V tiles in flight
+  static constexpr int kKSteps = D / 16;                  // MMAs of one S
+  static constexpr uint32_t kIdescS = instr_desc(128, 128, 0, false, false);
+  static constexpr uint32_t kIdescPV = instr_desc(128, D, 0, false, true);
+  __host__ __device__ static constexpr int s_off(int kb) {
+    return kb >= kKSteps ? 0 : ((kb * 32 / 128) * 128 * 128 + kb * 32 % 128) >> 4;
+  }
+  static constexpr int kPvStep = 16 * 128 >> 4;
+};
+
+// One share of a unit: tiles [tile, tile + n) of its `tiles`.
+struct ChunkSegment {
+  int r, head, block, tile, n, tiles;
+  ReqShape req;
+};
+
+struct ChunkCtrl {
+  uint64_t q_full[2], s_full[2], o_full[2], p_full[2][2];
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  long long sum[kChThreads / 32];
+  ChunkSegment start;
+};
+
+template <int D>
+constexpr int chunk_smem_bytes() {
+  return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
+}
+
+// Tiles that the 256 rows of a block need: up to the last key that its last row sees.
+__device__ __forceinline__ int chunk_tiles(const Kv4Args& a, const ReqShape& s, int block) {
+  int seen = s.keys;
+  if (a.causal) {
+    const int last_row = min(s.q_len * a.group, (block + 1) * kChRows) - 1;
+    seen = max(0, s.keys - s.q_len + last_row / a.group + 1);
+  }
+  return max(1, (min(seen, s.keys) - 1) / kChKeys + 1);
+}
+
+__device__ __forceinline__ int chunk_blocks(const Kv4Args& a, const ReqShape& s) {
+  return (s.q_len * a.group + kChRows - 1) / kChRows;
+}
+
+// Walks the CTA's share of the line segment by segment; every role walks it by itself.
+struct ChunkWalk {
+  ChunkSegment s;
+  long long left;  // tiles of the share from s.tile on
+  int blocks;
+
+  __device__ __forceinline__ ChunkWalk(const Kv4Args& a, const ChunkSegment& start, long long tiles)
+      : s(start), left(tiles) {
+    blocks = chunk_blocks(a, s.req);
+    s.n = static_cast<int>(min(static_cast<long long>(s.tiles - s.tile), left));
+  }
+  // To the next segment; false at the end of the share.
+  __device__ __forceinline__ bool next(const Kv4Args& a) {
+    left -= s.n;
+    if (left <= 0) return false;
+    s.tile = 0;
+    if (++s.block == blocks) {
+      s.block = 0;
+      if (++s.head == a.hk) {
+        s.head = 0;
+        do {
+          ++s.r;
+          s.req = kv4_request(a, s.r);
+          blocks = chunk_blocks(a, s.req);
+        } while (blocks == 0 && s.r + 1 < a.b);
+      }
+    }
+    s.tiles = chunk_tiles(a, s.req, s.block);
+    s.n = static_cast<int>(min(static_cast<long long>(s.tiles), left));
+    return true;
+  }
+};
+
+// The CTA's share [first, last) of the line of `total` tiles; fills ctl->start.  Returns the number
+// of CTAs that have work.
+__device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, long long& total,
+                                              long long& first, long long& last) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  ReqShape s;
+  long long per_head = 0;
+  auto cost = [&](int r) -> long long {
+    per_head = 0;
+    if (r >= a.b) return 0;
+    s = kv4_request(a, r);
+    const int blocks = chunk_blocks(a, s);
+    for (int b = 0; b < blocks; ++b) per_head += chunk_tiles(a, s, b);
+    return per_head * a.hk;
+  };
+  auto scan = [&](long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) ctl->sum[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += ctl->sum[w];
+    return x;
+  };
+  long long mine = 0, tiles = 0;
+  for (int r = threadIdx.x; r < a.b; r += kChThreads) mine += tiles = cost(r);
+  long long inc = scan(mine);
+  total = 0;
+  for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= n) return n;
+  first = total * blockIdx.x / n;
+  last = total * (blockIdx.x + 1) / n;
+  long long base = 0;
+  for (int r0 = 0; r0 < a.b; r0 += kChThreads) {
+    long long all = total;
+    if (a.b > kChThreads) {
+      __syncthreads();
+      tiles = cost(r0 + threadIdx.x);
+      inc = scan(tiles) + base;
+      all = base;
+      for (int w = 0; w < kChThreads / 32; ++w) all += ctl->sum[w];
+    }
+    if (first >= inc - tiles && first < inc) {
+      long long off = first - (inc - tiles);
+      ChunkSegment& c = ctl->start;
+      c.r = r0 + threadIdx.x;
+      c.req = s;
+      c.head = static_cast<int>(off / per_head);
+      off -= c.head * per_head;
+      c.block = 0;
+      while (off >= chunk_tiles(a, s, c.block)) off -= chunk_tiles(a, s, c.block++);
+      c.tile = static_cast<int>(off);
+      c.tiles = chunk_tiles(a, s, c.block);
+    }
+    base = all;
+    if (first < base) break;
+  }
+  __syncthreads();
+  return n;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args a) {
+  using G = ChunkGeo<D>;
+  extern __shared__ __align__(1024) uint8_t ch_smem[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ch_smem) + 1023) &
+                                                   ~static_cast<uintptr_t>(1023));
+  uint8_t* const s_q = smem;
+  uint8_t* const s_ring = smem + 2 * G::kTileBytes;
+  ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_ring + G::kSlots * G::kTileBytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  long long total, first, last;
+  const int n_cta = chunk_my_range(a, ctl, total, first, last);
+  if (static_cast<int>(blockIdx.x) >= n_cta) {
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(smem_u32(&ctl->q_full[h]), 4);   // one arrival per softmax warp of the tile
+      mbar_init(smem_u32(&ctl->s_full[h]), 1);
+      mbar_init(smem_u32(&ctl->o_full[h]), 1);
+      for (int p = 0; p < 2; ++p) mbar_init(smem_u32(&ctl->p_full[h][p]), 4);
+    }
+    for (int i = 0; i < G::kSlots; ++i) {
+      mbar_init(smem_u32(&ctl->kv_full[i]), 4);  // one arrival per widening warp
+      mbar_init(smem_u32(&ctl->kv_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  int* const abort_flag = &ctl->abort;
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait_phase(smem_u32(&bar), parity & 1u, abort_flag, a.status));
+  };
+
+  if (warp >= 12) {
+    regs_dec<kChMmaRegs>();
+    if (warp == 12) {
+      // ========================================================== MMA issuer
+      ChunkWalk w(a, ctl->start, last - first);
+      int tile_no = 0;                 // key tiles before this segment
+      int steps[2] = {0, 0}, segs[2] = {0, 0};
+      const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = smem_desc(smem_u32(s_ring), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(s_ring), 128 * 128, 1024, kSwizzle128B);
+      constexpr uint64_t kTile16 = G::kTileBytes >> 4;
+      bool ok = true;
+      auto issue_s = [&](int h, int t) {
+        const uint64_t qd = q_desc + h * kTile16, kd = k_desc + (t % G::kSlots) * kTile16;
+        if (elect_one()) {
+          mma_chain_ss_off<G::kKSteps, 0, G::s_off(1), G::s_off(2), G::s_off(3), G::s_off(4),
+                           G::s_off(5), G::s_off(6), G::s_off(7)>(tmem + h * 128, G::kIdescS, 0u, qd, kd);
+          tc_commit(smem_u32(&ctl->s_full[h]));
+        }
+        __syncwarp();
+      };
+      do {
+        const int tiles_h = w.s.req.q_len * a.group - w.s.block * kChRows > 128 ? 2 : 1;
+        for (int h = 0; h < tiles_h && ok; ++h) ok = wait(ctl->q_full[h], segs[h]++);
+        int t = 2 * tile_no;
+        ok = ok && wait(ctl->kv_full[t % G::kSlots], t / G::kSlots);
+        if (!ok) break;
+        tc_fence_after();
+        for (int h = 0; h < tiles_h; ++h) issue_s(h, t);
+        for (int j = 0; j < w.s.n && ok; ++j, t += 2) {
+          const int tv = t + 1, tk = t + 2;
+          const bool more = j + 1 < w.s.n;
+          ok = wait(ctl->kv_full[tv % G::kSlots], tv / G::kSlots);
+          if (ok && more) ok = wait(ctl->kv_full[tk % G::kSlots], tk / G::kSlots);
+          for (int h = 0; h < tiles_h && ok; ++h) {
+#pragma unroll
+            for (int part = 0; part < 2 && ok; ++part) {
+              ok = wait(ctl->p_full[h][part], steps[h]);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t vd = v_desc + (tv % G::kSlots) * kTile16 + part * 4 * G::kPvStep;
+              if (elect_one())
+                mma_chain_ts_off<4, 0, G::kPvStep, 8, 16, 24, 32, 40, 48, 56>(
+                    tmem + 256 + h * 128, G::kIdescPV, j > 0 || part > 0 ? 1u : 0u,
+                    tmem + h * 128 + part * 32, vd);
+              __syncwarp();
+            }
+            if (!ok) break;
+            ++steps[h];
+            if (more) {
+              issue_s(h, tk);
+            } else {
+              if (elect_one()) tc_commit(smem_u32(&ctl->o_full[h]));
+              __syncwarp();
+            }
+          }
+        }
+        tile_no += w.s.n;
+      } while (ok && w.next(a));
+      // nothing this warp issued may still run when the TMEM is released
+      __syncwarp();
+      if (elect_one()) tc_commit(smem_u32(&ctl->drain));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  } else if (warp >= 8) {
+    regs_dec<kChWidenRegs>();
+    // ============================================================ widening the cache
+    // A lane holds 32 codes (16 bytes, two scales) of one row: 4 (d = 128) or 2 lanes a row.
+    constexpr int kLanes = D / 32, kRowsWarp = 32 / kLanes, kPass = 4 * kRowsWarp, kIt = 128 / kPass;
+    constexpr int kCode = D / 2, kScale = D / 16;
+    const int part = lane % kLanes, row0 = (warp - 8) * kRowsWarp + lane / kLanes;
+    const int page_rows = 1 << a.page_shift;
+    const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
+    // swizzled offset of 16-byte chunk i of the lane's four, for row r of a tile; lanes of the
+    // second half of a row store their chunks in another order (fewer bank conflicts)
+    auto chunk_at = [&](int r, int i) {
+      const int g = part * 4 + (i ^ (part & 2));
+      return (g / 8) * (128 * 128) + r * 128 + (((g & 7) ^ (r & 7)) << 4);
+    };
+    ChunkWalk w(a, ctl->start, last - first);
+    int j = 0;  // tile within the segment that is loaded next
+    uint4 kc[kIt], vc[kIt];
+    uint16_t ks[kIt], vs[kIt], vs_next[kIt];
+    const uint8_t* base[kIt];  // the row's codes in the K block, null when there is no such key
+    auto load_k = [&]() {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int key = (w.s.tile + j) * kChKeys + it * kPass + row0;
+        base[it] = nullptr;
+        kc[it] = make_uint4(0u, 0u, 0u, 0u);
+        ks[it] = vs_next[it] = 0;
+        if (key < w.s.req.keys) {
+          const int id = __ldg(a.table + static_cast<size_t>(w.s.r) * a.width + (key >> a.page_shift));
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(a.pages)) {
+            const int row = key & (page_rows - 1);
+            const uint8_t* b = a.cache + (static_cast<size_t>(id) * a.hk + w.s.head) * 2 * block_bytes;
+            const uint8_t* sc = b + page_rows * kCode + row * kScale + part * 2;
+            base[it] = b + row * kCode + part * 16;
+            kc[it] = __ldg(reinterpret_cast<const uint4*>(base[it]));
+            ks[it] = __ldg(reinterpret_cast<const uint16_t*>(sc));
+            vs_next[it] = __ldg(reinterpret_cast<const uint16_t*>(sc + block_bytes));
+          }
+        }
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        vc[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (base[it]) vc[it] = __ldg(reinterpret_cast<const uint4*>(base[it] + block_bytes));
+      }
+    };
+    // 32 codes times their two scales, as four 16-byte chunks of a row
+    auto store = [&](uint32_t slot, int r, uint4 c, uint32_t scales) {
+      if (part & 2) {
+        c = make_uint4(c.z, c.w, c.x, c.y);
+        scales = __byte_perm(scales, 0u, 0x1032);
+      }
+      const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h[4];
+        unpack_e2m1x8(word[i], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = i & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
+        st_shared_v4(slot + chunk_at(r, i), h[0], h[1], h[2], h[3]);
+      }
+    };
+    const uint32_t ring = smem_u32(s_ring);
+    auto publish = [&](int t) {
+      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[t % G::kSlots]));
+    };
+    auto slot_free = [&](int t) {
+      return t < G::kSlots || wait(ctl->kv_empty[t % G::kSlots], t / G::kSlots - 1);
+    };
+    auto nan2 = [](uint32_t s) { return (s & 0x7fu) == 0x7fu || (s & 0x7f00u) == 0x7f00u; };
+    load_k();
+    load_v();
+    bool ok = true, more = true;
+    for (int t = 0; more; t += 2) {
+      ok = slot_free(t);
+      if (!ok) break;
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        vs[it] = vs_next[it];
+        // a value vector that is not a number makes its key's scores NaN (and is zero itself: rows
+        // that do not see the key multiply it by zero)
+        uint32_t sc = e4m3x2_to_f16x2(nan2(vs[it]) ? static_cast<uint16_t>(0x7f7f) : ks[it]);
+        store(ring + (t % G::kSlots) * G::kTileBytes, it * kPass + row0, kc[it], sc);
+        if (nan2(vs[it])) vs[it] = 0;
+      }
+      publish(t);
+      if (++j == w.s.n) {
+        j = 0;
+        more = w.next(a);
+      }
+      if (more) load_k();
+      ok = slot_free(t + 1);
+      if (!ok) break;
+#pragma unroll
+      for (int it = 0; it < kIt; ++it)
+        store(ring + ((t + 1) % G::kSlots) * G::kTileBytes, it * kPass + row0, vc[it], e4m3x2_to_f16x2(vs[it]));
+      publish(t + 1);
+      if (more) load_v();
+    }
+  } else {
+    regs_inc<kChSoftmaxRegs>();
+    // ============================================================ softmax, queries, outputs
+    const int h = warp / 4, r_tile = threadIdx.x % 128;
+    const uint32_t lane_addr = static_cast<uint32_t>(warp % 4 * 32) << 16;
+    const uint32_t t_s = tmem + lane_addr + h * 128, t_o = tmem + lane_addr + 256 + h * 128;
+    const uint32_t q_row = smem_u32(s_q) + h * G::kTileBytes + r_tile * 128;
+    ChunkWalk w(a, ctl->start, last - first);
+    int tile_no = 0, step = 0, seg = 0, unit_no = 0;
+    int4 merge = make_int4(-1, 0, 0, 0);
+    bool ok = true;
+    do {
+      const int rows = w.s.req.q_len * a.group - w.s.block * kChRows;  // of this unit, from its first
+      const int n = w.s.n;
+      const bool two = rows > 128;
+      if (threadIdx.x == 0 && w.s.tile == 0 && n < w.s.tiles) {
+        // the unit begins here and ends in a later CTA: x is its last tile on the line
+        const long long x = last - w.left + w.s.tiles - 1;
+        merge = make_int4(unit_no > 0 ? 1 : 0, w.s.r, w.s.block * a.hk + w.s.head,
+                          static_cast<int>(((x + 1) * n_cta - 1) / total));
+      }
+      if (h == 0 || two) {
+        const int row = h * 128 + r_tile;
+        const bool live = row < rows;
+        const int urow = w.s.block * kChRows + row;
+        const int qi = urow / a.group, qg = urow - qi * a.group;
+        // ---- the query row, scaled into [1, 2)
+        float c;
+        {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + static_cast<long long>(w.s.req.q0 + qi) * a.q_row +
+              static_cast<long long>(w.s.head * a.group + qg) * a.q_head);
+          uint4 raw[D / 8];
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            float f[8];
+            unpack_bf16x8(raw[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+          }
+          uint32_t ex = __float_as_uint(amax) >> 23;
+          ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
+          const float down = __uint_as_float((254u - ex) << 23);
+          c = a.c * __uint_as_float(ex << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            unpack_bf16x8(raw[i], f);
+            st_shared_v4(q_row + (i / 8) * (128 * 128) + (((i & 7) ^ (r_tile & 7)) << 4),
+                         pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
+                         pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[h]));
+        }
+        int sees = w.s.req.keys;  // keys this row sees
+        if (a.causal && live) sees = min(sees, max(0, w.s.req.keys - w.s.req.q_len + qi + 1));
+        // pages of the segment that are not there: then every tile looks at its own page ids
+        bool holes = false;
+        const int key_end = min(w.s.req.keys, (w.s.tile + n) * kChKeys);
+        const int* ids = a.table + static_cast<size_t>(w.s.r) * a.width;
+        for (int p = ((w.s.tile * kChKeys) >> a.page_shift) + lane; (p << a.page_shift) < key_end; p += 32)
+          holes |= static_cast<unsigned>(__ldg(ids + p)) >= static_cast<unsigned>(a.pages);
+        holes = __any_sync(0xffffffffu, holes);
+
+        float m = kDecNone, l = 0.f;
+        for (int j = 0; j < n; ++j, ++step) {
+          ok = wait(ctl->s_full[h], step);
+          if (!ok) break;
+          tc_fence_after();
+          // The last tile's S is issued after both tiles' P V of the previous keys: slots go back
+          if (threadIdx.x % 128 == 0 && (h == 1 || !two)) {
+            const int t = 2 * (tile_no + j);
+            mbar_arrive(smem_u32(&ctl->kv_empty[t % G::kSlots]));
+            if (j > 0) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
+          }
+          float s[128];
+          {
+            uint32_t r[4][32];
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) tmem_ld32(t_s + cb * 32, r[cb]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[cb * 32 + i] = __uint_as_float(r[cb][i]);
+          }
+          const int key0 = (w.s.tile + j) * kChKeys;
+          const int lim = sees - key0;
+          const bool masked = holes || __any_sync(0xffffffffu, lim < kChKeys);
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= lim) s[i] = -INFINITY;
+            if (holes) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                const int key = key0 + 16 * g;
+                if (key < key_end &&
+                    static_cast<unsigned>(__ldg(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages)) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) s[16 * g + i] = -INFINITY;
+                }
+              }
+            }
+          }
+          float mp[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mp[k] = fmaxf(s[2 * k], s[2 * k + 1]);
+#pragma unroll
+          for (int i = 16; i < 128; i += 2) mp[(i / 2) % 8] = max3f(mp[(i / 2) % 8], s[i], s[i + 1]);
+#pragma unroll
+          for (int k = 4; k >= 1; k /= 2)
+#pragma unroll
+            for (int i = 0; i < k; ++i) mp[i] = fmaxf(mp[i], mp[i + k]);
+          // the reference m: kDecBelow under the maximum, moved when that grew by 8 since
+          const float top = mp[0] * c;
+          if (j == 0) {
+            m = fmaxf(top - kDecBelow, m);
+          } else if (__any_sync(0xffffffffu, top > m + kDecLazy)) {
+            const float m_new = fmaxf(top - kDecBelow, m);
+            const float alpha = ex2_mufu(m - m_new);
+            uint32_t r[32];
+#pragma unroll
+            for (int cb = 0; cb < D / 32; ++cb) {
+              tmem_ld32(t_o + cb * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 v = mul_f32x2(f32x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f32x2(alpha, alpha));
+                r[i] = __float_as_uint(v.x);
+                r[i + 1] = __float_as_uint(v.y);
+              }
+              tmem_st32(t_o + cb * 32, r);
+            }
+            l *= alpha;
+            m = m_new;
+          }
+          // P = 2^(s c - m) in f16 over S, published in two parts of 64 keys
+          float2 sum[4] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+          const float2 c2 = f32x2(c, c), nm = f32x2(-m, -m);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int k = 64 * part + 2 * i;
+              const float2 x = fma_f32x2(f32x2(s[k], s[k + 1]), c2, nm);
+              float p0 = ex2_mufu(x.x), p1 = ex2_mufu(x.y);
+              if (masked) {
+                p0 = s[k] == -INFINITY ? 0.f : p0;
+                p1 = s[k + 1] == -INFINITY ? 0.f : p1;
+              }
+              sum[i % 4] = add_f32x2(sum[i % 4], f32x2(p0, p1));
+              r[i] = pack_f16x2(p0, p1);
+            }
+            tmem_st32(t_s + 32 * part, r);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[h][part]));
+          }
+          sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
+        }
+        if (!ok) break;
+        // ---- O and the log-sum-exp, or the unit's partial sums
+        ok = wait(ctl->o_full[h], seg++);
+        if (!ok) break;
+        tc_fence_after();
+        if (threadIdx.x % 128 == 0 && (h == 1 || !two))
+          mbar_arrive(smem_u32(&ctl->kv_empty[(2 * (tile_no + n) - 1) % G::kSlots]));
+        const bool whole = n == w.s.tiles;
+        const float inv = l == 0.f ? 0.f : a.v_descale / l;
+        const size_t at = static_cast<size_t>(w.s.req.q0 + qi) * a.hq + w.s.head * a.group + qg;
+        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (unit_no > 0 ? 1 : 0)) * kChRows + row;
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t r[32];
+          tmem_ld32(t_o + cb * 32, r);
+          tmem_ld_wait();
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + cb * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                p[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv, __uint_as_float(r[8 * i + 2 * e + 1]) * inv);
+              dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          } else if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * D + cb * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          }
+        }
+        if (live && whole) a.lse[at] = l == 0.f ? -INFINITY : m * kLn2F + logf(l);
+        if (live && !whole) a.part_ml[slot] = make_float2(m, l);
+        tc_fence_before();
+      }
+      tile_no += n;
+      ++unit_no;
+    } while (w.next(a));
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = ok ? merge : make_int4(-1, 0, 0, 0);
+  }
+
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace exattn

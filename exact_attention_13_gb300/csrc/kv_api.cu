@@ -11,10 +11,14 @@
 #include "../../include/exact_attention.h"
 #include "kv4_attn.cuh"
 #include "kv4_cache.cuh"
+#include "kv4_chunk.cuh"
 #include "page_plan.cuh"
 #include "rope.cuh"
 
 namespace exattn {
+
+int* library_status_ptr(int dev);  // fa_api.cu
+
 namespace {
 
 constexpr int kSms = 152;
@@ -93,13 +97,16 @@ int row_grid(long long groups, unsigned& grid) {
 constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 // Query rows that share a unit, in eights: the smallest of 8, 16 and 32 that hold the rows of one
-// key head (fewer padded rows), 32 when none does (the cache is then read once per 32 rows).
-int dec_row_eights(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// key head (fewer padded rows); 0 for more rows than that: the kernel for prompt chunks.
+int dec_row_eights(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 0; }
 
-size_t dec_workspace(int nt, int d) {
-  const size_t n = static_cast<size_t>(kSms) * dec_ctas_per_sm(nt);
-  const size_t rows = 2 * n * 8 * nt;
-  return (rows * d * 4 + rows * 8 + n * 16 + 255) / 256 * 256;
+// CTAs and rows of a unit of the kernel for `nt` eights of rows, and its workspace.
+constexpr int kv4_ctas(int nt) { return nt ? kSms * dec_ctas_per_sm(nt) : kSms; }
+constexpr size_t kv4_part_rows(int nt) {
+  return static_cast<size_t>(2) * kv4_ctas(nt) * (nt ? 8 * nt : kChRows);
+}
+size_t kv4_workspace(int nt, int d) {
+  return (kv4_part_rows(nt) * (d * 4 + 8) + kv4_ctas(nt) * 16 + 255) / 256 * 256;
 }
 
 // Tables of at most this many tiles: units are not split, which saves the merge kernel and the
@@ -112,14 +119,31 @@ int dec_whole_tiles(int d, int page, int width) {
 }
 
 template <int D, int NT>
+void split_workspace(Kv4Args& a, void* workspace) {
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + kv4_part_rows(NT) * D);
+  a.desc = reinterpret_cast<int4*>(a.part_ml + kv4_part_rows(NT));
+}
+
+// The merge of units that cross CTAs, launched while the first kernel runs.
+template <int D, int R>
+int launch_merge(const Kv4Args& a, int ctas, unsigned row_blocks, cudaStream_t s) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(ctas, row_blocks);
+  config.blockDim = dim3(kMergeThreads);
+  config.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kv4_merge_kernel<D, R>, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int NT>
 int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
-  constexpr int n = kSms * dec_ctas_per_sm(NT);
-  constexpr size_t rows = static_cast<size_t>(2) * n * 8 * NT;
-  if (!a.whole_tiles) {
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * D);
-    a.desc = reinterpret_cast<int4*>(a.part_ml + rows);
-  }
+  constexpr int n = kv4_ctas(NT);
+  if (!a.whole_tiles) split_workspace<D, NT>(a, workspace);
   constexpr int smem = dec_smem_bytes<D, NT>();
   static_assert(dec_ctas_per_sm(NT) * (smem + 4096) <= 227 * 1024, "shared memory per SM");
   static std::atomic<uint64_t> done{0};
@@ -131,21 +155,35 @@ int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   // Few units: each may span many CTAs, and rows get blocks of their own (one block for all rows of
   // a unit that spans the whole GPU would take about 10 us); else a block takes all rows of its unit.
   const unsigned row_blocks = static_cast<long long>(a.b) * a.hk <= n / 8 ? 8 * NT : 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(n, row_blocks);
-  config.blockDim = dim3(kMergeThreads);
-  config.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &early;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kv4_merge_kernel<D, 8 * NT>, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_merge<D, 8 * NT>(a, n, row_blocks, s);
+}
+
+template <int D>
+int launch_chunk(Kv4Args& a, void* workspace, cudaStream_t s) {
+  constexpr int n = kv4_ctas(0);
+  split_workspace<D, 0>(a, workspace);
+  constexpr int smem = chunk_smem_bytes<D>();
+  // more than half of an SM's, so that one CTA (with all of the tensor memory) runs there
+  static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "shared memory per CTA");
+  static std::atomic<uint64_t> done{0};
+  auto kern = kv4_chunk_kernel<D>;
+  if (!(done.load(std::memory_order_acquire))) {
+    // the warpgroups redistribute 512 x 128 registers: a build with fewer at launch would wait
+    // forever for the rest
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
+    if (attr.numRegs * 4 < 2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs) return FA_ERR_UNSUPPORTED;
+  }
+  if (int rc = opt_in_smem(kern, smem, done)) return rc;
+  kern<<<n, kChThreads, smem, s>>>(a);
+  if (int rc = launched()) return rc;
+  return launch_merge<D, kChRows>(a, n, kChRows / 8, s);
 }
 
 template <int D>
 int launch_kv4(Kv4Args& a, int nt, void* workspace, cudaStream_t s) {
-  return nt == 1   ? launch_decode<D, 1>(a, workspace, s)
+  return nt == 0   ? launch_chunk<D>(a, workspace, s)
+         : nt == 1 ? launch_decode<D, 1>(a, workspace, s)
          : nt == 2 ? launch_decode<D, 2>(a, workspace, s)
                    : launch_decode<D, 4>(a, workspace, s);
 }
@@ -309,15 +347,15 @@ size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_si
                                   int table_width) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
   if (!page_size_ok(page_size) || table_width < 1) return 0;
-  if (dec_whole_tiles(d, page_size, table_width)) return 0;
-  return dec_workspace(dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv)), d);
+  const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
+  return nt && dec_whole_tiles(d, page_size, table_width) ? 0 : kv4_workspace(nt, d);
 }
 
 int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache,
                int num_pages, int page_size, const int* table, int table_width, const int* lens,
                const int* q_offsets, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
                int max_q, float scale, int causal, float k_descale, float v_descale,
-               void* workspace, size_t workspace_bytes, void* stream) {
+               void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
   if (!q || !table || !lens || !o || !lse) return FA_ERR_INVALID_ARG;
   if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1)
     return FA_ERR_INVALID_ARG;
@@ -328,11 +366,11 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
   if (static_cast<long long>(T) * Hq > 0x3fffffffll) return FA_ERR_UNSUPPORTED;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  const int whole = dec_whole_tiles(d, page_size, table_width);
-  if (!whole && (!workspace || workspace_bytes < dec_workspace(nt, d))) return FA_ERR_INVALID_ARG;
+  const int whole = nt ? dec_whole_tiles(d, page_size, table_width) : 0;
+  if (!whole && (!workspace || workspace_bytes < kv4_workspace(nt, d))) return FA_ERR_INVALID_ARG;
   if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) ||
       !aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) ||
-      !aligned(workspace, 16))
+      !aligned(workspace, 16) || !aligned(dev_status, 4))
     return FA_ERR_MISALIGNED;
   const double c = static_cast<double>(scale) * 1.4426950408889634 * k_descale;
   if (!(c <= 3.0e38)) return FA_ERR_INVALID_ARG;
@@ -359,6 +397,13 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   a.whole_tiles = whole;
   a.c = static_cast<float>(c);
   a.v_descale = v_descale;
+  a.status = dev_status;
+  if (!a.status && nt == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxKvDevices) return FA_ERR_CUDA;
+    a.status = library_status_ptr(dev);
+    if (!a.status) return FA_ERR_CUDA;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_kv4<64>(a, nt, workspace, s) : launch_kv4<128>(a, nt, workspace, s);
 }

@@ -299,17 +299,17 @@ def kv4_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int, page_size: int, w
 
 def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, causal: bool = True,
             scale: float | None = None, k_descale: float = 1.0, v_descale: float = 1.0, out=None,
-            lse=None, workspace=None):
+            lse=None, workspace=None, status=None):
     """Attention of packed query tokens q (bf16 [T, Hq, d]) over the 4-bit cache; returns (o bf16
     [T, Hq, d], lse fp32 [T, Hq]).
 
     ``table`` int32 [B, width] and ``lens`` int32 [B] (the new tokens included) say where the keys
     are; request b's queries are rows q_offsets[b] .. q_offsets[b + 1) (int32 [B + 1]), or T / B rows
     each without ``q_offsets``.  ``causal``: the queries are the last tokens of the cache.
-    ``max_q``: about the most queries of a request (default T / B, rounded up); it only picks how many
-    rows share a pass over the cache.  Rows of q past the last request's are left as they are.
+    ``max_q``: about the most queries of a request (default T / B, rounded up); it only picks the
+    kernel (how many rows share a pass over the cache).  Rows of q past the last request's are left as they are.
     ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes or more, not shared by calls that may run
-    at the same time; without it torch allocates one."""
+    at the same time; without it torch allocates one.  ``status``: as in ``fwd``."""
     index = q.get_device()
     if q.dtype is not _bf16 or q.dim() != 3 or index < 0:
         raise ValueError("q must be a bf16 CUDA tensor [T, Hq, d]")
@@ -356,5 +356,6 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
         size, scratch = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     _run("fa_kv4_fwd", index, q.data_ptr(), q0, q1, cache.data_ptr(), pages, page,
          table.data_ptr(), width, lens.data_ptr(), offsets, out.data_ptr(), lse.data_ptr(), T, B,
-         Hq, Hkv, d, max_q, scale, 1 if causal else 0, k_descale, v_descale, scratch, size)
+         Hq, Hkv, d, max_q, scale, 1 if causal else 0, k_descale, v_descale, scratch, size,
+         status.data_ptr() if status is not None else None)
     return out, lse

@@ -332,12 +332,13 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *   q_offsets   : device int32 [B + 1], not decreasing, or NULL: T / B queries each (T % B == 0).
  *                 Rows of q past q_offsets[B] are not read, their outputs left as they were
  *   o, lse      : outputs [T, Hq, d] bf16 (16-byte aligned) and [T, Hq] fp32
- *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks how
- *                 many query rows share a pass over the cache
+ *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks the
+ *                 kernel: how many query rows share a pass over the cache
  *   scale       : softmax scale, finite and >= 0
  *   workspace   : device scratch of fa_kv4_fwd_workspace_bytes(...) bytes, 16-byte aligned (NULL
  *                 when that is 0), contents on entry do not matter; calls that may run at the same
  *                 time need one each
+ *   dev_status  : as fa_fwd_opts.dev_status (NULL = the library's status word)
  *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30; d, page_size and descales as fa_kv4_append
  * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
  * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums
@@ -348,7 +349,7 @@ FA_API int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_st
                       int table_width, const int* lens, const int* q_offsets, void* o, float* lse,
                       int T, int B, int Hq, int Hkv, int d, int max_q, float scale, int causal,
                       float k_descale, float v_descale, void* workspace, size_t workspace_bytes,
-                      void* stream);
+                      int* dev_status, void* stream);
 
 /* Workspace bytes fa_kv4_fwd needs for tables of `table_width` pages; 0 when it needs none (short
  * tables: no key head's work is split), and for invalid arguments. */

@@ -19,7 +19,7 @@ NAMES = {
     "fa_kv4_append": "k kr kh v vr vh cache pages page slots T H d kd vd stream",
     "fa_kv4_read": "cache pages page slots k v T H d kd vd stream",
     "fa_kv4_fwd": "q qr qh cache pages page table width lens off o lse T B Hq Hkv d max_q scale "
-                  "causal kd vd ws ws_bytes stream",
+                  "causal kd vd ws ws_bytes status stream",
 }
 GOOD = {
     "fa_rope": [P, S3(0, 128, 512), P, S3(0, 128, 512), 4, P, S3(0, 128, 128), P, S3(0, 128, 128), 1,
@@ -28,7 +28,7 @@ GOOD = {
     "fa_kv4_append": [P, 128, 128, P, 128, 128, P, 4, 16, P, 8, 1, 128, 1.0, 1.0, None],
     "fa_kv4_read": [P, 4, 16, P, P, P, 8, 1, 128, 1.0, 1.0, None],
     "fa_kv4_fwd": [P, 512, 128, P, 4, 16, P, 100, P, P, P, P, 8, 2, 4, 1, 128, 4, 0.1, 1, 1.0, 1.0, P,
-                   1 << 30, None],
+                   1 << 30, None, None],
 }
 CASES = [
     ("fa_rope", dict(q=0), BAD), ("fa_rope", dict(ko=0), BAD), ("fa_rope", dict(pos=0), BAD),
@@ -65,6 +65,7 @@ CASES = [
     ("fa_kv4_fwd", dict(page=1024), UNS), ("fa_kv4_fwd", dict(T=1 << 29), UNS),
     ("fa_kv4_fwd", dict(q=P + 2), MIS), ("fa_kv4_fwd", dict(qr=100), MIS),
     ("fa_kv4_fwd", dict(lse=P + 2), MIS), ("fa_kv4_fwd", dict(ws=P + 8), MIS),
+    ("fa_kv4_fwd", dict(status=P + 2), MIS), ("fa_kv4_fwd", dict(max_q=64, ws_bytes=1 << 20), BAD),
 ]
 
 
