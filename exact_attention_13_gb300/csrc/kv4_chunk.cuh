@@ -10,8 +10,8 @@
 // Roles (512 threads, one CTA a SM):
 //   warps 0-7    softmax of tile 0 / tile 1; also load the query rows (scaled by a power of two into
 //                [1, 2), f16) and write O and the log-sum-exp
-//   warps 8-11   widen the cache: codes and scales from global memory to registers a tile ahead,
-//                code * scale (exact) to the ring
+//   warps 8-11   widen the cache, 32 keys each: codes and scales come by cp.async into a small ring of
+//                the warp's own, code * scale (exact) goes to the tile ring
 //   warp  12     issues the MMAs:  S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
 // TMEM: S_0 at columns 0-127, S_1 at 128-255 (P_h, f16, over S_h), O_0 at 256, O_1 at 384.
 //
@@ -33,8 +33,8 @@ namespace exattn {
 constexpr int kChThreads = 512;
 constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
-// register shares of the warpgroups: 128 (2 x 200 + 80 + 32) = 512 x 128
-constexpr int kChSoftmaxRegs = 200, kChWidenRegs = 80, kChMmaRegs = 32;
+// register shares of the warpgroups: 128 (2 x 208 + 64 + 32) = 512 x 128
+constexpr int kChSoftmaxRegs = 208, kChWidenRegs = 64, kChMmaRegs = 32;
 static_assert(2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs <= 512, "registers of the block at launch");
 
 template <int D>
@@ -48,12 +48,22 @@ struct ChunkGeo {
     return kb >= kKSteps ? 0 : ((kb * 32 / 128) * 128 * 128 + kb * 32 % 128) >> 4;
   }
   static constexpr int kPvStep = 16 * 128 >> 4;
+  // a widening warp's ring: codes, scales and (for K) the values' scales of 32 keys a stage
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStageBytes = 32 * (D / 2 + 2 * (D / 16));
 };
 
 // One share of a unit: tiles [tile, tile + n) of its `tiles`.
 struct ChunkSegment {
   int r, head, block, tile, n, tiles;
   ReqShape req;
+};
+
+// A warp's place on the line, in shared memory: registers are scarce in the loops.
+struct ChunkWalk {
+  ChunkSegment s;
+  int blocks;
+  long long left;  // tiles of the share from s.tile on
 };
 
 struct ChunkCtrl {
@@ -63,12 +73,15 @@ struct ChunkCtrl {
   uint32_t tmem_base;
   int abort;
   long long sum[kChThreads / 32];
+  long long total, first, last;
   ChunkSegment start;
+  ChunkWalk walk[13];
 };
 
 template <int D>
 constexpr int chunk_smem_bytes() {
-  return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
+  return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes +
+         4 * ChunkGeo<D>::kStages * ChunkGeo<D>::kStageBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
 }
 
 // Tiles that the 256 rows of a block need: up to the last key that its last row sees.
@@ -85,38 +98,47 @@ __device__ __forceinline__ int chunk_blocks(const Kv4Args& a, const ReqShape& s)
   return (s.q_len * a.group + kChRows - 1) / kChRows;
 }
 
-// Walks the CTA's share of the line segment by segment; every role walks it by itself.
-struct ChunkWalk {
-  ChunkSegment s;
-  long long left;  // tiles of the share from s.tile on
-  int blocks;
+// Every role walks the CTA's share of the line by itself, segment by segment (warp-collective).
+__device__ __forceinline__ void walk_begin(const Kv4Args& a, ChunkWalk* w, const ChunkCtrl* ctl) {
+  if (threadIdx.x % 32 == 0) {
+    w->s = ctl->start;
+    w->blocks = chunk_blocks(a, w->s.req);
+    w->left = ctl->last - ctl->first;
+    w->s.n = static_cast<int>(min(static_cast<long long>(w->s.tiles - w->s.tile), w->left));
+  }
+  __syncwarp();
+}
 
-  __device__ __forceinline__ ChunkWalk(const Kv4Args& a, const ChunkSegment& start, long long tiles)
-      : s(start), left(tiles) {
-    blocks = chunk_blocks(a, s.req);
-    s.n = static_cast<int>(min(static_cast<long long>(s.tiles - s.tile), left));
-  }
-  // To the next segment; false at the end of the share.
-  __device__ __forceinline__ bool next(const Kv4Args& a) {
-    left -= s.n;
-    if (left <= 0) return false;
-    s.tile = 0;
-    if (++s.block == blocks) {
-      s.block = 0;
-      if (++s.head == a.hk) {
-        s.head = 0;
-        do {
-          ++s.r;
-          s.req = kv4_request(a, s.r);
-          blocks = chunk_blocks(a, s.req);
-        } while (blocks == 0 && s.r + 1 < a.b);
+// To the next segment; false at the end of the share.
+__device__ __forceinline__ bool walk_next(const Kv4Args& a, ChunkWalk* w) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) {
+    w->left -= w->s.n;
+    if (w->left > 0) {
+      w->s.tile = 0;
+      if (++w->s.block == w->blocks) {
+        w->s.block = 0;
+        if (++w->s.head == a.hk) {
+          w->s.head = 0;
+          do {
+            ++w->s.r;
+            w->s.req = kv4_request(a, w->s.r);
+            w->blocks = chunk_blocks(a, w->s.req);
+          } while (w->blocks == 0 && w->s.r + 1 < a.b);
+        }
       }
+      w->s.tiles = chunk_tiles(a, w->s.req, w->s.block);
+      w->s.n = static_cast<int>(min(static_cast<long long>(w->s.tiles), w->left));
     }
-    s.tiles = chunk_tiles(a, s.req, s.block);
-    s.n = static_cast<int>(min(static_cast<long long>(s.tiles), left));
-    return true;
   }
-};
+  __syncwarp();
+  return w->left > 0;
+}
+
+// Rows of the segment's unit, from its first one.
+__device__ __forceinline__ int walk_rows(const Kv4Args& a, const ChunkWalk* w) {
+  return w->s.req.q_len * a.group - w->s.block * kChRows;
+}
 
 // The CTA's share [first, last) of the line of `total` tiles; fills ctl->start.  Returns the number
 // of CTAs that have work.
@@ -182,6 +204,38 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   return n;
 }
 
+// P = 2^(s c - m) of one row in f16 over its S columns, published in two parts of 64 keys; returns
+// the row's sum.  MASKED: scores of -inf give 0 whatever c is.
+template <bool MASKED>
+__device__ __forceinline__ float chunk_publish_p(float (&s)[128], float c, float m, uint32_t t_s, uint32_t bar,
+                                                 int lane) {
+  float2 sum[4] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+  const float2 c2 = f32x2(c, c), nm = f32x2(-m, -m);
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int k = 64 * part + 2 * i;
+      const float2 x = fma_f32x2(f32x2(s[k], s[k + 1]), c2, nm);
+      float p0 = ex2_mufu(x.x), p1 = ex2_mufu(x.y);
+      if constexpr (MASKED) {
+        p0 = s[k] == -INFINITY ? 0.f : p0;
+        p1 = s[k + 1] == -INFINITY ? 0.f : p1;
+      }
+      sum[i % 4] = add_f32x2(sum[i % 4], f32x2(p0, p1));
+      r[i] = pack_f16x2(p0, p1);
+    }
+    tmem_st32(t_s + 32 * part, r);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + 8 * part);
+  }
+  sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+  return sum[0].x + sum[0].y;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args a) {
   using G = ChunkGeo<D>;
@@ -190,15 +244,23 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
                                                    ~static_cast<uintptr_t>(1023));
   uint8_t* const s_q = smem;
   uint8_t* const s_ring = smem + 2 * G::kTileBytes;
-  ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_ring + G::kSlots * G::kTileBytes);
+  uint8_t* const s_raw = s_ring + G::kSlots * G::kTileBytes;
+  ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_raw + 4 * G::kStages * G::kStageBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  long long total, first, last;
-  const int n_cta = chunk_my_range(a, ctl, total, first, last);
-  if (static_cast<int>(blockIdx.x) >= n_cta) {
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
+  {
+    long long total, first, last;
+    const int n_cta = chunk_my_range(a, ctl, total, first, last);
+    if (static_cast<int>(blockIdx.x) >= n_cta) {
+      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    if (threadIdx.x == 0) {
+      ctl->total = total;
+      ctl->first = first;
+      ctl->last = last;
+    }
   }
   if (warp == 12) {
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
@@ -232,16 +294,17 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
     regs_dec<kChMmaRegs>();
     if (warp == 12) {
       // ========================================================== MMA issuer
-      ChunkWalk w(a, ctl->start, last - first);
-      int tile_no = 0;                 // key tiles before this segment
+      ChunkWalk* const w = &ctl->walk[12];
+      walk_begin(a, w, ctl);
+      int t = 0;  // K's number in the ring (V: t + 1)
       int steps[2] = {0, 0}, segs[2] = {0, 0};
       const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
       const uint64_t k_desc = smem_desc(smem_u32(s_ring), 16, 1024, kSwizzle128B);
       const uint64_t v_desc = smem_desc(smem_u32(s_ring), 128 * 128, 1024, kSwizzle128B);
       constexpr uint64_t kTile16 = G::kTileBytes >> 4;
       bool ok = true;
-      auto issue_s = [&](int h, int t) {
-        const uint64_t qd = q_desc + h * kTile16, kd = k_desc + (t % G::kSlots) * kTile16;
+      auto issue_s = [&](int h, int tk) {
+        const uint64_t qd = q_desc + h * kTile16, kd = k_desc + (tk % G::kSlots) * kTile16;
         if (elect_one()) {
           mma_chain_ss_off<G::kKSteps, 0, G::s_off(1), G::s_off(2), G::s_off(3), G::s_off(4),
                            G::s_off(5), G::s_off(6), G::s_off(7)>(tmem + h * 128, G::kIdescS, 0u, qd, kd);
@@ -249,44 +312,50 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         }
         __syncwarp();
       };
+      // P V of one key tile, then S of the next (which overwrites P): V, the next K and the first
+      // part of P have mostly come, so one probe looks for all three
+      auto step = [&](int h, bool begins, bool more) -> bool {
+        const int tv = t + 1, tk = more ? t + 2 : t + 1;
+        uint64_t &bv = ctl->kv_full[tv % G::kSlots], &bk = ctl->kv_full[tk % G::kSlots];
+        if (!__all_sync(0xffffffffu,
+                        mbar_try_wait3(smem_u32(&bv), (tv / G::kSlots) & 1, smem_u32(&bk), (tk / G::kSlots) & 1,
+                                       smem_u32(&ctl->p_full[h][0]), steps[h] & 1)))
+          if (!wait(bv, tv / G::kSlots) || !wait(bk, tk / G::kSlots) || !wait(ctl->p_full[h][0], steps[h])) return false;
+        const uint64_t vd = v_desc + (tv % G::kSlots) * kTile16;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1 && !wait(ctl->p_full[h][1], steps[h])) return false;
+          tc_fence_after();
+          if (elect_one())
+            mma_chain_ts_off<4, 0, G::kPvStep, 8, 16, 24, 32, 40, 48, 56>(
+                tmem + 256 + h * 128, G::kIdescPV, begins && part == 0 ? 0u : 1u, tmem + h * 128 + part * 32,
+                vd + part * 4 * G::kPvStep);
+          __syncwarp();
+        }
+        ++steps[h];
+        if (more) {
+          issue_s(h, tk);
+        } else {
+          if (elect_one()) tc_commit(smem_u32(&ctl->o_full[h]));
+          __syncwarp();
+        }
+        return true;
+      };
       do {
-        const int tiles_h = w.s.req.q_len * a.group - w.s.block * kChRows > 128 ? 2 : 1;
-        for (int h = 0; h < tiles_h && ok; ++h) ok = wait(ctl->q_full[h], segs[h]++);
-        int t = 2 * tile_no;
+        const bool two = walk_rows(a, w) > 128;
+        const int n = w->s.n;
+        ok = wait(ctl->q_full[0], segs[0]++);
+        if (two) ok = ok && wait(ctl->q_full[1], segs[1]++);
         ok = ok && wait(ctl->kv_full[t % G::kSlots], t / G::kSlots);
         if (!ok) break;
         tc_fence_after();
-        for (int h = 0; h < tiles_h; ++h) issue_s(h, t);
-        for (int j = 0; j < w.s.n && ok; ++j, t += 2) {
-          const int tv = t + 1, tk = t + 2;
-          const bool more = j + 1 < w.s.n;
-          ok = wait(ctl->kv_full[tv % G::kSlots], tv / G::kSlots);
-          if (ok && more) ok = wait(ctl->kv_full[tk % G::kSlots], tk / G::kSlots);
-          for (int h = 0; h < tiles_h && ok; ++h) {
-#pragma unroll
-            for (int part = 0; part < 2 && ok; ++part) {
-              ok = wait(ctl->p_full[h][part], steps[h]);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t vd = v_desc + (tv % G::kSlots) * kTile16 + part * 4 * G::kPvStep;
-              if (elect_one())
-                mma_chain_ts_off<4, 0, G::kPvStep, 8, 16, 24, 32, 40, 48, 56>(
-                    tmem + 256 + h * 128, G::kIdescPV, j > 0 || part > 0 ? 1u : 0u,
-                    tmem + h * 128 + part * 32, vd);
-              __syncwarp();
-            }
-            if (!ok) break;
-            ++steps[h];
-            if (more) {
-              issue_s(h, tk);
-            } else {
-              if (elect_one()) tc_commit(smem_u32(&ctl->o_full[h]));
-              __syncwarp();
-            }
-          }
+        issue_s(0, t);
+        if (two) issue_s(1, t);
+        for (int j = 0; j < n && ok; ++j, t += 2) {
+          ok = step(0, j == 0, j + 1 < n);
+          if (two) ok = ok && step(1, j == 0, j + 1 < n);
         }
-        tile_no += w.s.n;
-      } while (ok && w.next(a));
+      } while (ok && walk_next(a, w));
       // nothing this warp issued may still run when the TMEM is released
       __syncwarp();
       if (elect_one()) tc_commit(smem_u32(&ctl->drain));
@@ -297,138 +366,153 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
   } else if (warp >= 8) {
     regs_dec<kChWidenRegs>();
     // ============================================================ widening the cache
-    // A lane holds 32 codes (16 bytes, two scales) of one row: 4 (d = 128) or 2 lanes a row.
-    constexpr int kLanes = D / 32, kRowsWarp = 32 / kLanes, kPass = 4 * kRowsWarp, kIt = 128 / kPass;
+    // The warp's 32 keys of a tile: a lane takes 32 codes (16 bytes, two scales) of one row at a
+    // time, 4 (d = 128) or 2 lanes a row.
+    constexpr int kLanes = D / 32, kRowsIt = 32 / kLanes, kIt = 32 / kRowsIt;
     constexpr int kCode = D / 2, kScale = D / 16;
-    const int part = lane % kLanes, row0 = (warp - 8) * kRowsWarp + lane / kLanes;
+    constexpr int kSc = 32 * kCode, kVsc = kSc + 32 * kScale;  // in a stage: scales, values' scales
+    const int part = lane % kLanes, row_in = lane / kLanes, row_w = (warp - 8) * 32;
     const int page_rows = 1 << a.page_shift;
-    const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
-    // swizzled offset of 16-byte chunk i of the lane's four, for row r of a tile; lanes of the
-    // second half of a row store their chunks in another order (fewer bank conflicts)
-    auto chunk_at = [&](int r, int i) {
-      const int g = part * 4 + (i ^ (part & 2));
-      return (g / 8) * (128 * 128) + r * 128 + (((g & 7) ^ (r & 7)) << 4);
+    const int block_bytes = kv4_block_bytes(page_rows, D);
+    ChunkWalk* const w = &ctl->walk[warp];
+    walk_begin(a, w, ctl);
+    uint8_t* const raw = s_raw + (warp - 8) * G::kStages * G::kStageBytes;
+    const uint32_t raw_u32 = smem_u32(raw), ring = smem_u32(s_ring);
+
+    // ---- loads: half a tile (K, then V) a stage, the page ids of the two 16-key groups a tile ahead
+    int key = w->s.tile * kChKeys + row_w, tiles_left = w->s.n, keys = w->s.req.keys;
+    const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+    const uint8_t* head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
+    bool loads_left = true;
+    int id[2];
+    auto fetch_ids = [&]() {
+      id[0] = key < keys ? __ldg(ids + (key >> a.page_shift)) : -1;
+      id[1] = id[0];
+      if (a.page_shift == 4) id[1] = key + 16 < keys ? __ldg(ids + (key >> 4) + 1) : -1;
     };
-    ChunkWalk w(a, ctl->start, last - first);
-    int j = 0;  // tile within the segment that is loaded next
-    uint4 kc[kIt], vc[kIt];
-    uint16_t ks[kIt], vs[kIt], vs_next[kIt];
-    const uint8_t* base[kIt];  // the row's codes in the K block, null when there is no such key
-    auto load_k = [&]() {
+    int load_no = 0;  // half tiles asked for so far
+    auto load = [&]() {
+      if (loads_left) {
+        const bool v = load_no & 1;
+        const uint32_t dst = raw_u32 + load_no % G::kStages * G::kStageBytes;
+        constexpr int kPer = 16 * kCode / 512;
 #pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int key = (w.s.tile + j) * kChKeys + it * kPass + row0;
-        base[it] = nullptr;
-        kc[it] = make_uint4(0u, 0u, 0u, 0u);
-        ks[it] = vs_next[it] = 0;
-        if (key < w.s.req.keys) {
-          const int id = __ldg(a.table + static_cast<size_t>(w.s.r) * a.width + (key >> a.page_shift));
-          if (static_cast<unsigned>(id) < static_cast<unsigned>(a.pages)) {
-            const int row = key & (page_rows - 1);
-            const uint8_t* b = a.cache + (static_cast<size_t>(id) * a.hk + w.s.head) * 2 * block_bytes;
-            const uint8_t* sc = b + page_rows * kCode + row * kScale + part * 2;
-            base[it] = b + row * kCode + part * 16;
-            kc[it] = __ldg(reinterpret_cast<const uint4*>(base[it]));
-            ks[it] = __ldg(reinterpret_cast<const uint16_t*>(sc));
-            vs_next[it] = __ldg(reinterpret_cast<const uint16_t*>(sc + block_bytes));
+        for (int g = 0; g < 2; ++g) {
+          const bool there = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
+          const uint32_t n = there ? 16u : 0u;  // 0: the copy writes zeros and reads nothing
+          const int row = (key + 16 * g) & (page_rows - 1);
+          const uint8_t* b = head + (there ? static_cast<size_t>(id[g]) * a.hk * 2 * block_bytes : 0) + (v ? block_bytes : 0);
+#pragma unroll
+          for (int p = 0; p < kPer; ++p)
+            cp_async16(dst + g * 16 * kCode + p * 512 + lane * 16, b + row * kCode + p * 512 + lane * 16, n);
+          // kScale copies of scales; for K the values' scales too
+          const uint8_t* sc = b + page_rows * kCode + row * kScale + lane % kScale * 16;
+          if (lane < kScale) cp_async16(dst + kSc + g * 16 * kScale + lane * 16, sc, n);
+          else if (!v && lane < 2 * kScale)
+            cp_async16(dst + kVsc + g * 16 * kScale + lane % kScale * 16, sc + block_bytes, n);
+        }
+        ++load_no;
+        if (v) {
+          if (--tiles_left > 0) {
+            key += kChKeys;
+          } else {
+            loads_left = walk_next(a, w);
+            key = w->s.tile * kChKeys + row_w;
+            tiles_left = w->s.n;
+            keys = w->s.req.keys;
+            ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+            head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
           }
+          if (loads_left) fetch_ids();
         }
       }
+      cp_async_commit();
     };
-    auto load_v = [&]() {
+    // number of half tiles of the share
+    const long long halves = 2 * (ctl->last - ctl->first);
+    fetch_ids();
+#pragma unroll
+    for (int i = 0; i < G::kStages; ++i) load();
+    auto nan2 = [](uint32_t s) { return (s & 0x7fu) == 0x7fu || (s & 0x7f00u) == 0x7f00u; };
+    for (int t = 0; t < halves; ++t) {
+      if (t >= G::kSlots && !wait(ctl->kv_empty[t % G::kSlots], t / G::kSlots - 1)) break;
+      cp_async_wait<G::kStages - 1>();
+      __syncwarp();
+      const uint8_t* st = raw + t % G::kStages * G::kStageBytes;
+      const uint32_t slot = ring + t % G::kSlots * G::kTileBytes;
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
-        vc[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (base[it]) vc[it] = __ldg(reinterpret_cast<const uint4*>(base[it] + block_bytes));
-      }
-    };
-    // 32 codes times their two scales, as four 16-byte chunks of a row
-    auto store = [&](uint32_t slot, int r, uint4 c, uint32_t scales) {
-      if (part & 2) {
-        c = make_uint4(c.z, c.w, c.x, c.y);
-        scales = __byte_perm(scales, 0u, 0x1032);
-      }
-      const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+        const int r = it * kRowsIt + row_in;
+        uint4 c = *reinterpret_cast<const uint4*>(st + r * kCode + part * 16);
+        uint32_t sc = *reinterpret_cast<const uint16_t*>(st + kSc + r * kScale + part * 2);
+        // A value vector that is not a number makes its key's scores NaN and is zero itself: rows
+        // that do not see the key multiply it by zero.
+        if (t & 1) {
+          if (nan2(sc)) sc = 0u;
+        } else if (nan2(*reinterpret_cast<const uint16_t*>(st + kVsc + r * kScale + part * 2))) {
+          sc = 0x7f7fu;
+        }
+        uint32_t scales = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
+        // Chunk g of a row (8 values) lies at chunk g ^ (row % 8); lanes of the second half of a
+        // row store their four in another order (fewer bank conflicts).
+        if (part & 2) {
+          c = make_uint4(c.z, c.w, c.x, c.y);
+          scales = __byte_perm(scales, 0u, 0x1032);
+        }
+        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t row = slot + (part / 2) * (128 * 128) + (row_w + r) * 128;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[4];
-        unpack_e2m1x8(word[i], h);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[4];
+          unpack_e2m1x8(word[i], h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = i & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
-        st_shared_v4(slot + chunk_at(r, i), h[0], h[1], h[2], h[3]);
+          for (int e = 0; e < 4; ++e) h[e] = i & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
+          const int g = (part * 4 + (i ^ (part & 2))) & 7;
+          st_shared_v4(row + ((g ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
       }
-    };
-    const uint32_t ring = smem_u32(s_ring);
-    auto publish = [&](int t) {
       fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[t % G::kSlots]));
-    };
-    auto slot_free = [&](int t) {
-      return t < G::kSlots || wait(ctl->kv_empty[t % G::kSlots], t / G::kSlots - 1);
-    };
-    auto nan2 = [](uint32_t s) { return (s & 0x7fu) == 0x7fu || (s & 0x7f00u) == 0x7f00u; };
-    load_k();
-    load_v();
-    bool ok = true, more = true;
-    for (int t = 0; more; t += 2) {
-      ok = slot_free(t);
-      if (!ok) break;
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        vs[it] = vs_next[it];
-        // a value vector that is not a number makes its key's scores NaN (and is zero itself: rows
-        // that do not see the key multiply it by zero)
-        uint32_t sc = e4m3x2_to_f16x2(nan2(vs[it]) ? static_cast<uint16_t>(0x7f7f) : ks[it]);
-        store(ring + (t % G::kSlots) * G::kTileBytes, it * kPass + row0, kc[it], sc);
-        if (nan2(vs[it])) vs[it] = 0;
-      }
-      publish(t);
-      if (++j == w.s.n) {
-        j = 0;
-        more = w.next(a);
-      }
-      if (more) load_k();
-      ok = slot_free(t + 1);
-      if (!ok) break;
-#pragma unroll
-      for (int it = 0; it < kIt; ++it)
-        store(ring + ((t + 1) % G::kSlots) * G::kTileBytes, it * kPass + row0, vc[it], e4m3x2_to_f16x2(vs[it]));
-      publish(t + 1);
-      if (more) load_v();
+      load();
     }
+    cp_async_wait<0>();
   } else {
     regs_inc<kChSoftmaxRegs>();
     // ============================================================ softmax, queries, outputs
     const int h = warp / 4, r_tile = threadIdx.x % 128;
     const uint32_t lane_addr = static_cast<uint32_t>(warp % 4 * 32) << 16;
     const uint32_t t_s = tmem + lane_addr + h * 128, t_o = tmem + lane_addr + 256 + h * 128;
-    const uint32_t q_row = smem_u32(s_q) + h * G::kTileBytes + r_tile * 128;
-    ChunkWalk w(a, ctl->start, last - first);
-    int tile_no = 0, step = 0, seg = 0, unit_no = 0;
-    int4 merge = make_int4(-1, 0, 0, 0);
+    ChunkWalk* const w = &ctl->walk[warp];
+    walk_begin(a, w, ctl);
+    int t = 0;  // K's number in the ring
+    int step = 0, seg = 0, unit_no = 0;
     bool ok = true;
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     do {
-      const int rows = w.s.req.q_len * a.group - w.s.block * kChRows;  // of this unit, from its first
-      const int n = w.s.n;
-      const bool two = rows > 128;
-      if (threadIdx.x == 0 && w.s.tile == 0 && n < w.s.tiles) {
+      const int n = w->s.n;
+      const bool two = walk_rows(a, w) > 128;
+      if (threadIdx.x == 0 && w->s.tile == 0 && n < w->s.tiles) {
         // the unit begins here and ends in a later CTA: x is its last tile on the line
-        const long long x = last - w.left + w.s.tiles - 1;
-        merge = make_int4(unit_no > 0 ? 1 : 0, w.s.r, w.s.block * a.hk + w.s.head,
-                          static_cast<int>(((x + 1) * n_cta - 1) / total));
+        const long long x = ctl->last - w->left + w->s.tiles - 1, total = ctl->total;
+        const long long n_cta = min(static_cast<long long>(gridDim.x), total);
+        a.desc[blockIdx.x] = make_int4(unit_no > 0 ? 1 : 0, w->s.r, w->s.block * a.hk + w->s.head,
+                                       static_cast<int>(((x + 1) * n_cta - 1) / total));
       }
       if (h == 0 || two) {
-        const int row = h * 128 + r_tile;
-        const bool live = row < rows;
-        const int urow = w.s.block * kChRows + row;
-        const int qi = urow / a.group, qg = urow - qi * a.group;
-        // ---- the query row, scaled into [1, 2)
-        float c;
+        const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
+        float c;   // factor of the row's scores
+        int sees;  // keys that the row sees
         {
+          const int row = h * 128 + r_tile, urow = w->s.block * kChRows + row;
+          const bool live = row < walk_rows(a, w);
+          const int qi = urow / a.group, qg = urow - qi * a.group;
+          sees = w->s.req.keys;
+          if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.q_len + qi + 1));
+          // ---- the query row, scaled into [1, 2)
           const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + static_cast<long long>(w.s.req.q0 + qi) * a.q_row +
-              static_cast<long long>(w.s.head * a.group + qg) * a.q_head);
+              a.q + static_cast<long long>(w->s.req.q0 + qi) * a.q_row +
+              static_cast<long long>(w->s.head * a.group + qg) * a.q_head);
           uint4 raw[D / 8];
           float amax = 0.f;
 #pragma unroll
@@ -443,6 +527,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
           const float down = __uint_as_float((254u - ex) << 23);
           c = a.c * __uint_as_float(ex << 23);
+          const uint32_t q_row = smem_u32(s_q) + h * G::kTileBytes + r_tile * 128;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
             float f[8];
@@ -455,24 +540,24 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[h]));
         }
-        int sees = w.s.req.keys;  // keys this row sees
-        if (a.causal && live) sees = min(sees, max(0, w.s.req.keys - w.s.req.q_len + qi + 1));
         // pages of the segment that are not there: then every tile looks at its own page ids
         bool holes = false;
-        const int key_end = min(w.s.req.keys, (w.s.tile + n) * kChKeys);
-        const int* ids = a.table + static_cast<size_t>(w.s.r) * a.width;
-        for (int p = ((w.s.tile * kChKeys) >> a.page_shift) + lane; (p << a.page_shift) < key_end; p += 32)
-          holes |= static_cast<unsigned>(__ldg(ids + p)) >= static_cast<unsigned>(a.pages);
+        {
+          const int key_end = min(w->s.req.keys, (w->s.tile + n) * kChKeys);
+          const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+          for (int p = ((w->s.tile * kChKeys) >> a.page_shift) + lane; (p << a.page_shift) < key_end; p += 32)
+            holes |= static_cast<unsigned>(__ldg(ids + p)) >= static_cast<unsigned>(a.pages);
+        }
         holes = __any_sync(0xffffffffu, holes);
-
+        int lim = sees - w->s.tile * kChKeys;  // keys of the next tile that the row sees
         float m = kDecNone, l = 0.f;
-        for (int j = 0; j < n; ++j, ++step) {
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++step, t += 2, lim -= kChKeys) {
           ok = wait(ctl->s_full[h], step);
           if (!ok) break;
           tc_fence_after();
           // The last tile's S is issued after both tiles' P V of the previous keys: slots go back
-          if (threadIdx.x % 128 == 0 && (h == 1 || !two)) {
-            const int t = 2 * (tile_no + j);
+          if (frees) {
             mbar_arrive(smem_u32(&ctl->kv_empty[t % G::kSlots]));
             if (j > 0) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
           }
@@ -487,18 +572,18 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[cb * 32 + i] = __uint_as_float(r[cb][i]);
           }
-          const int key0 = (w.s.tile + j) * kChKeys;
-          const int lim = sees - key0;
           const bool masked = holes || __any_sync(0xffffffffu, lim < kChKeys);
           if (masked) {
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i >= lim) s[i] = -INFINITY;
             if (holes) {
+              const int key0 = (w->s.tile + j) * kChKeys;
+              const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
 #pragma unroll
               for (int g = 0; g < 8; ++g) {
                 const int key = key0 + 16 * g;
-                if (key < key_end &&
+                if (key < w->s.req.keys &&
                     static_cast<unsigned>(__ldg(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages)) {
 #pragma unroll
                   for (int i = 0; i < 16; ++i) s[16 * g + i] = -INFINITY;
@@ -538,43 +623,20 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
             l *= alpha;
             m = m_new;
           }
-          // P = 2^(s c - m) in f16 over S, published in two parts of 64 keys
-          float2 sum[4] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-          const float2 c2 = f32x2(c, c), nm = f32x2(-m, -m);
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint32_t r[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int k = 64 * part + 2 * i;
-              const float2 x = fma_f32x2(f32x2(s[k], s[k + 1]), c2, nm);
-              float p0 = ex2_mufu(x.x), p1 = ex2_mufu(x.y);
-              if (masked) {
-                p0 = s[k] == -INFINITY ? 0.f : p0;
-                p1 = s[k + 1] == -INFINITY ? 0.f : p1;
-              }
-              sum[i % 4] = add_f32x2(sum[i % 4], f32x2(p0, p1));
-              r[i] = pack_f16x2(p0, p1);
-            }
-            tmem_st32(t_s + 32 * part, r);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[h][part]));
-          }
-          sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
-          l += sum[0].x + sum[0].y;
+          l += masked ? chunk_publish_p<true>(s, c, m, t_s, smem_u32(&ctl->p_full[h][0]), lane)
+                      : chunk_publish_p<false>(s, c, m, t_s, smem_u32(&ctl->p_full[h][0]), lane);
         }
         if (!ok) break;
         // ---- O and the log-sum-exp, or the unit's partial sums
         ok = wait(ctl->o_full[h], seg++);
         if (!ok) break;
         tc_fence_after();
-        if (threadIdx.x % 128 == 0 && (h == 1 || !two))
-          mbar_arrive(smem_u32(&ctl->kv_empty[(2 * (tile_no + n) - 1) % G::kSlots]));
-        const bool whole = n == w.s.tiles;
+        if (frees) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
+        const int row = h * 128 + r_tile, urow = w->s.block * kChRows + row;
+        const bool live = row < walk_rows(a, w), whole = n == w->s.tiles;
+        const int qi = urow / a.group, qg = urow - qi * a.group;
         const float inv = l == 0.f ? 0.f : a.v_descale / l;
-        const size_t at = static_cast<size_t>(w.s.req.q0 + qi) * a.hq + w.s.head * a.group + qg;
+        const size_t at = static_cast<size_t>(w->s.req.q0 + qi) * a.hq + w->s.head * a.group + qg;
         const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (unit_no > 0 ? 1 : 0)) * kChRows + row;
 #pragma unroll
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -600,11 +662,11 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         if (live && whole) a.lse[at] = l == 0.f ? -INFINITY : m * kLn2F + logf(l);
         if (live && !whole) a.part_ml[slot] = make_float2(m, l);
         tc_fence_before();
+      } else {
+        t += 2 * n;
       }
-      tile_no += n;
       ++unit_no;
-    } while (w.next(a));
-    if (threadIdx.x == 0) a.desc[blockIdx.x] = ok ? merge : make_int4(-1, 0, 0, 0);
+    } while (walk_next(a, w));
   }
 
   __syncthreads();
