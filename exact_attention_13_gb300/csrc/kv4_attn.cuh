@@ -166,8 +166,28 @@ __device__ __forceinline__ int kv4_perm(int r) { return r ^ ((r >> 1) & 1); }
 // Where the CTA's line of tiles runs: request, block of query rows, key head, tile (the unit's
 // number within its request is block * hk + head).
 struct TileCursor {
-  int r, block, head, tile, blocks, tiles, keys;
+  int r, block, head, tile, blocks, tiles;
+  ReqShape req;
 };
+
+// The line of `total` tiles in n equal shares (n <= total), the first total % n one longer: where
+// share i begins, and the share that holds tile x.
+__device__ __forceinline__ long long share_begin(long long total, int n, int i) {
+  if (total <= 0x7fffffffll) {  // 64-bit divisions take about 100 instructions
+    const unsigned t = static_cast<unsigned>(total), q = t / n, more = t - q * n;
+    return q * i + min(more, static_cast<unsigned>(i));
+  }
+  return total / n * i + min(total % n, static_cast<long long>(i));
+}
+__device__ __forceinline__ int share_of(long long total, int n, long long x) {
+  if (total <= 0x7fffffffll) {
+    const unsigned t = static_cast<unsigned>(total), q = t / n, more = t - q * n;
+    const unsigned y = static_cast<unsigned>(x), longer = more * (q + 1);
+    return static_cast<int>(y < longer ? y / (q + 1) : more + (y - longer) / q);
+  }
+  const long long q = total / n, more = total % n, longer = more * (q + 1);
+  return static_cast<int>(x < longer ? x / (q + 1) : more + (x - longer) / q);
+}
 
 // To the next tile; true when the next unit begins with it.
 template <int D, int R>
@@ -182,7 +202,7 @@ __device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
     const ReqShape s = kv4_request(a, c.r);
     c.blocks = kv4_blocks<R>(a, s);
     c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
-    c.keys = s.keys;
+    c.req = s;
     if (c.blocks > 0) break;
   }
   return true;
@@ -196,12 +216,12 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   TileCursor c;
   auto cost = [&](int r) -> long long {
-    c = TileCursor{r, 0, 0, 0, 0, 1, 0};
+    c = TileCursor{r, 0, 0, 0, 0, 1, {0, 0, 0}};
     if (r >= a.b) return 0;
     const ReqShape s = kv4_request(a, r);
     c.blocks = kv4_blocks<R>(a, s);
     c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
-    c.keys = s.keys;
+    c.req = s;
     return static_cast<long long>(c.blocks) * a.hk * c.tiles;
   };
   // inclusive scan over the block; s_sum keeps the warps' sums until the next barrier
@@ -225,10 +245,11 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
 #pragma unroll
   for (int w = 0; w < kDecWarps; ++w) total += s_sum[w];
   const long long piece = a.whole_tiles ? a.whole_tiles : 1;  // shares are whole pieces
-  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total / piece));
+  const long long pieces = a.whole_tiles ? total / piece : total;
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), pieces));
   if (static_cast<int>(blockIdx.x) >= n) return n;
-  first = total / piece * blockIdx.x / n * piece;
-  last = total / piece * (blockIdx.x + 1) / n * piece;
+  first = share_begin(pieces, n, blockIdx.x) * piece;
+  last = share_begin(pieces, n, blockIdx.x + 1) * piece;
   // up to one request a thread, the scan above is the line itself; else it is redone in pieces
   long long base = 0;
   for (int r0 = 0; r0 < a.b; r0 += kDecThreads) {
@@ -244,7 +265,7 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
     const long long lo = inc - tiles;
     if (first >= lo && first < inc) {
       const long long off = first - lo;
-      const int u = static_cast<int>(off / c.tiles);
+      const int u = off <= 0x7fffffffll ? static_cast<int>(off) / c.tiles : static_cast<int>(off / c.tiles);
       c.tile = static_cast<int>(off - static_cast<long long>(u) * c.tiles);
       c.block = u / a.hk;
       c.head = u - c.block * a.hk;
@@ -262,7 +283,8 @@ __host__ __device__ constexpr int dec_strip_bytes() { return dec_strip<D>() * (D
 
 template <int D, int NT>
 __host__ __device__ constexpr int dec_smem_bytes() {
-  return kDecWarps * kDecStages * dec_strip_bytes<D>() + 2 * (D / 16) * NT * 32 * 16;
+  return kDecWarps * kDecStages * dec_strip_bytes<D>() + kDecWarps * (D / 16) * NT * 32 * 16 +
+         NT * (D / 32) * 32 * 16;
 }
 
 template <int D, int NT>
@@ -279,12 +301,14 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ long long s_sum[kDecWarps];
   __shared__ TileCursor s_cur;
-  __shared__ float s_m[kDecWarps][R], s_l[kDecWarps][R];
+  __shared__ float s_m[kDecWarps][R], s_l[kDecWarps][R], s_c[R];
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g8 = lane / 4, t4 = lane % 4;
   uint8_t* const ring = dec_smem + warp * (kDecStages * dec_strip_bytes<D>());
+  // the warps' sums at the end of a unit, and its queries as the products' operand
   float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D>());
+  uint4* const s_q = reinterpret_cast<uint4*>(area + kDecWarps * MT * NT * 32);  // [nt][w][lane]
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long total, first, last;
@@ -296,10 +320,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   const int steps = static_cast<int>(last - first);
   TileCursor cur = s_cur, ld = s_cur;
   const int page_rows = 1 << a.page_shift;
-  const size_t block_bytes = static_cast<size_t>(kv4_block_bytes(page_rows, D));
+  const int block_bytes = kv4_block_bytes(page_rows, D);
 
   // ---- loads: the strip's 16-key groups, one page id each, fetched a step ahead
-  const size_t page_bytes = block_bytes * 2 * a.hk;
+  const unsigned page_bytes = static_cast<unsigned>(block_bytes) * 2u * static_cast<unsigned>(a.hk);
   constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
   // the lane's copy of the strip's scales: kScale copies for each of (K, V) x groups, 32 in all
   static_assert(2 * TG * kScale == 32, "one copy of scales a lane");
@@ -314,6 +338,21 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
     scale_base = h + (sc_kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * kCode + (lane % kScale) * 16;
     row_ids = a.table + static_cast<size_t>(ld.r) * a.width;
   };
+  // Brings a unit's query rows into L1 ahead of their use: the loads' results are not wanted.
+  auto touch_queries = [&]() {
+    constexpr int kLines = D * 2 / 128;
+#pragma unroll
+    for (int x = 0; x < (R * kLines + 31) / 32; ++x) {
+      const int line = x * 32 + lane, row = ld.block * R + line / kLines;
+      if (line < R * kLines && row < ld.req.q_len * a.group) {
+        const int qi = row / a.group, qg = row - qi * a.group;
+        const __nv_bfloat16* p = a.q + static_cast<long long>(ld.req.q0 + qi) * a.q_row +
+                                 static_cast<long long>(ld.head * a.group + qg) * a.q_head + line % kLines * 64;
+        uint32_t unused;
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(unused) : "l"(p));
+      }
+    }
+  };
   int id[TG];
   int ld_left = steps;
   unsigned seen = 0;  // TG bits a strip in flight: the group's page exists
@@ -324,7 +363,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       const int key = key0 + 16 * g;
       // groups that share a page share its id
       if (g > 0 && (key & (page_rows - 1)) != 0) id[g] = id[g - 1];
-      else id[g] = key < ld.keys ? __ldg(row_ids + (key >> a.page_shift)) : -1;
+      else id[g] = key < ld.req.keys ? __ldg(row_ids + (key >> a.page_shift)) : -1;
     }
   };
   auto issue = [&](int stage) {
@@ -339,7 +378,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         const bool ok = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
         // a page that is not there: copies of zero bytes, which write zeros and read nothing
         const uint32_t n = ok ? 16u : 0u;
-        const size_t at = ok ? id[g] * page_bytes : 0;
+        const size_t at = static_cast<size_t>(ok ? static_cast<unsigned>(id[g]) : 0u) * page_bytes;
         const int row = (key0 + 16 * g) & (page_rows - 1);
         const uint8_t* k = code_base + at + row * kCode;
         const uint8_t* v = k + block_bytes;
@@ -357,7 +396,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       }
       cp_async16(dst + sc_dst, scale_base + sc_at, sc_n);
       if (--ld_left > 0) {
-        if (cursor_next<D, R>(a, ld)) set_head();
+        if (cursor_next<D, R>(a, ld)) {
+          set_head();
+          touch_queries();
+        }
         fetch_ids();
       }
     }
@@ -366,12 +408,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 
   set_head();
   fetch_ids();
+  touch_queries();
 #pragma unroll
   for (int s = 0; s < kDecStages; ++s) issue(s);
 
   // ---- state of the unit at hand
   ReqShape req;
-  uint32_t qf[NT][QW];
   float cs[NT][2];       // factor of each S^T column (query row)
   int lim[NT][2];        // keys it sees
   int min_lim = 0, max_lim = 0;
@@ -384,13 +426,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      req = kv4_request(a, cur.r);
+      req = cur.req;
       const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
-      min_lim = 0x7fffffff;
-      max_lim = 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int row = row0 + nt * 8 + g8;
+      // Warp nt turns eight rows into the operand for all warps: held in registers by each warp they
+      // would cost 16 registers (of 128) per eight rows, and four conversions.
+      if (warp < NT) {
+        const int row = row0 + warp * 8 + g8;
         uint4 raw[QW / 4];
         const bool live = row < rows;
         const int qi = row / a.group, qg = row - qi * a.group;
@@ -412,17 +453,24 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         uint32_t ex = __float_as_uint(amax) >> 23;
         ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
         const float down = __uint_as_float((254u - ex) << 23);
-        const float up = a.c * __uint_as_float(ex << 23);
 #pragma unroll
         for (int w = 0; w < QW / 4; ++w) {
           float f[8];
           unpack_bf16x8(raw[w], f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qf[nt][4 * w + e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+          s_q[(warp * (QW / 4) + w) * 32 + lane] =
+              make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
+                         pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
         }
+        if (t4 == 0) s_c[warp * 8 + g8] = a.c * __uint_as_float(ex << 23);
+      }
+      __syncthreads();
+      min_lim = 0x7fffffff;
+      max_lim = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          cs[nt][cc] = __shfl_sync(0xffffffffu, up, 8 * t4 + 4 * cc);
+          cs[nt][cc] = s_c[nt * 8 + 2 * t4 + cc];
           const int crow = row0 + nt * 8 + 2 * t4 + cc;
           int k = req.keys;
           if (a.causal && crow < rows) k = min(k, max(0, req.keys - req.q_len + crow / a.group + 1));
@@ -487,8 +535,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(x[tg][nt], h0[0], h1[0], h0[1], h1[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-            mma_16816(x[tg][nt], h0[2], h1[2], h0[3], h1[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            const uint4 q = s_q[(nt * KW + w) * 32 + lane];
+            mma_16816(x[tg][nt], h0[0], h1[0], h0[1], h1[1], q.x, q.y);
+            mma_16816(x[tg][nt], h0[2], h1[2], h0[3], h1[3], q.z, q.w);
           }
         }
 #pragma unroll
@@ -657,94 +706,81 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
             s_l[warp][nt * 8 + 2 * t4 + cc] = l[nt][cc];
           }
         }
-      __syncthreads();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          area[((warp * MT + i) * NT + nt) * 32 + lane] =
+              make_float4(o[i][nt][0], o[i][nt][1], o[i][nt][2], o[i][nt][3]);
+      __syncthreads();  // (the one at the next unit's start keeps its sums out until all have read these)
+      // Each warp adds up a quarter of the 16-dim tiles: the lanes' own places of all four warps.
+      const bool complete = unit_ends && whole_start;
+      const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0);
+      constexpr int kMine = MT / kDecWarps;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[kDecWarps][2], big[2], sum[2];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int col = nt * 8 + 2 * t4 + cc;
-          float big = kDecNone;
+          big[cc] = kDecNone;
+          sum[cc] = 0.f;
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) big = fmaxf(big, s_m[w][col]);
-          float sum = 0.f;
+          for (int w = 0; w < kDecWarps; ++w) big[cc] = fmaxf(big[cc], s_m[w][col]);
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) sum += s_l[w][col] * ex2_mufu(s_m[w][col] - big);
-          const float f = ex2_mufu(m[nt][cc] - big);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[i][nt][cc] *= f;
-            o[i][nt][2 + cc] *= f;
+          for (int w = 0; w < kDecWarps; ++w) {
+            f[w][cc] = ex2_mufu(s_m[w][col] - big[cc]);
+            sum[cc] = fmaf(s_l[w][col], f[w][cc], sum[cc]);
           }
-          m[nt][cc] = big;
-          l[nt][cc] = sum;
         }
-      // (2, 3) into (0, 1), then 1 into 0, through the lanes' own places
-      auto place = [&](int which, int i, int nt) -> float4& {
-        return area[(which * MT * NT + i * NT + nt) * 32 + lane];
-      };
-      auto put = [&](int which) {
+        float y[kMine][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < kMine; ++i) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            place(which, i, nt) = make_float4(o[i][nt][0], o[i][nt][1], o[i][nt][2], o[i][nt][3]);
-      };
-      auto add = [&](int which) {
+          for (int e = 0; e < 4; ++e) y[i][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float4 y = place(which, i, nt);
-            o[i][nt][0] += y.x;
-            o[i][nt][1] += y.y;
-            o[i][nt][2] += y.z;
-            o[i][nt][3] += y.w;
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float4 x = area[((w * MT + warp * kMine + i) * NT + nt) * 32 + lane];
+            y[i][0] = fmaf(x.x, f[w][0], y[i][0]);
+            y[i][1] = fmaf(x.y, f[w][1], y[i][1]);
+            y[i][2] = fmaf(x.z, f[w][0], y[i][2]);
+            y[i][3] = fmaf(x.w, f[w][1], y[i][3]);
           }
-      };
-      if (warp >= 2) put(warp - 2);
-      __syncthreads();
-      if (warp < 2) add(warp);
-      if (warp == 1) put(1);
-      __syncthreads();
-      const bool complete = unit_ends && whole_start;
-      if (warp == 0) {
-        add(1);
-        const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0);
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int cc = 0; cc < 2; ++cc) {
+          const int row = nt * 8 + 2 * t4 + cc;
+          if (row0 + row >= rows) continue;
+          const int dim = g8 * (D / 8) + warp * kMine * 2;  // the lane's 2 kMine dims
+          if (complete) {
+            const int qi = (row0 + row) / a.group, qg = row0 + row - qi * a.group;
+            const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
+            // nothing seen: O = 0 (a NaN sum stays NaN)
+            const float inv = sum[cc] == 0.f ? 0.f : a.v_descale / sum[cc];
+            uint32_t p[kMine];
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const int row = nt * 8 + 2 * t4 + cc;
-            if (row0 + row >= rows) continue;
-            if (complete) {
-              const int qi = (row0 + row) / a.group, qg = row0 + row - qi * a.group;
-              const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
-              // nothing seen: O = 0 (a NaN sum stays NaN)
-              const float inv = l[nt][cc] == 0.f ? 0.f : a.v_descale / l[nt][cc];
-              uint32_t w[MT];
+            for (int i = 0; i < kMine; ++i) p[i] = pack_bf16x2(y[i][cc] * inv, y[i][2 + cc] * inv);
+            if constexpr (kMine == 2)
+              *reinterpret_cast<uint2*>(a.o + at * D + dim) = make_uint2(p[0], p[1]);
+            else
+              *reinterpret_cast<uint32_t*>(a.o + at * D + dim) = p[0];
+            if (g8 == 0 && warp == 0)
+              a.lse[at] = sum[cc] == 0.f ? -INFINITY : big[cc] * kLn2F + logf(sum[cc]);
+          } else {
+            float* dst = a.part_o + (static_cast<size_t>(slot) * R + row) * D + dim;
 #pragma unroll
-              for (int i = 0; i < MT; ++i) w[i] = pack_bf16x2(o[i][nt][cc] * inv, o[i][nt][2 + cc] * inv);
-              uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + g8 * (D / 8));
-#pragma unroll
-              for (int i = 0; i < MT / 4; ++i)
-                dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-              if (g8 == 0) a.lse[at] = l[nt][cc] == 0.f ? -INFINITY : m[nt][cc] * kLn2F + logf(l[nt][cc]);
-            } else {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(slot) * R + row) * D + g8 * (D / 8));
-#pragma unroll
-              for (int i = 0; i < MT / 2; ++i)
-                dst[i] = make_float4(o[2 * i][nt][cc], o[2 * i][nt][2 + cc], o[2 * i + 1][nt][cc],
-                                     o[2 * i + 1][nt][2 + cc]);
-              if (g8 == 0) a.part_ml[static_cast<size_t>(slot) * R + row] = make_float2(m[nt][cc], l[nt][cc]);
-            }
+            for (int i = 0; i < kMine; ++i)
+              *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(y[i][cc], y[i][2 + cc]);
+            if (g8 == 0 && warp == 0) a.part_ml[static_cast<size_t>(slot) * R + row] = make_float2(big[cc], sum[cc]);
           }
+        }
       }
       if (whole_start && !unit_ends) {
         // the unit begins here and ends in a later CTA: x is its last tile on the line
         const long long x = first + step + (cur.tiles - 1 - cur.tile);
         merge = make_int4(unit_no > 0 ? 1 : 0, cur.r, cur.block * a.hk + cur.head,
-                          static_cast<int>(((x + 1) * n_cta - 1) / total));
+                          share_of(total, n_cta, x));
       }
       ++unit_no;
       fresh = true;

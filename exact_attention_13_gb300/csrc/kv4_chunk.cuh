@@ -173,8 +173,8 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   if (static_cast<int>(blockIdx.x) >= n) return n;
-  first = total * blockIdx.x / n;
-  last = total * (blockIdx.x + 1) / n;
+  first = share_begin(total, n, blockIdx.x);
+  last = share_begin(total, n, blockIdx.x + 1);
   long long base = 0;
   for (int r0 = 0; r0 < a.b; r0 += kChThreads) {
     long long all = total;
@@ -495,9 +495,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       if (threadIdx.x == 0 && w->s.tile == 0 && n < w->s.tiles) {
         // the unit begins here and ends in a later CTA: x is its last tile on the line
         const long long x = ctl->last - w->left + w->s.tiles - 1, total = ctl->total;
-        const long long n_cta = min(static_cast<long long>(gridDim.x), total);
+        const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
         a.desc[blockIdx.x] = make_int4(unit_no > 0 ? 1 : 0, w->s.r, w->s.block * a.hk + w->s.head,
-                                       static_cast<int>(((x + 1) * n_cta - 1) / total));
+                                       share_of(total, n_cta, x));
       }
       if (h == 0 || two) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);

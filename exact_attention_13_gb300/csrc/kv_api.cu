@@ -145,7 +145,7 @@ int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   constexpr int n = kv4_ctas(NT);
   if (!a.whole_tiles) split_workspace<D, NT>(a, workspace);
   constexpr int smem = dec_smem_bytes<D, NT>();
-  static_assert(dec_ctas_per_sm(NT) * (smem + 4096) <= 227 * 1024, "shared memory per SM");
+  static_assert(dec_ctas_per_sm(NT) * (smem + 2048) <= 228 * 1024, "shared memory per SM");
   static std::atomic<uint64_t> done{0};
   auto kern = kv4_decode_kernel<D, NT>;
   if (int rc = opt_in_smem(kern, smem, done)) return rc;

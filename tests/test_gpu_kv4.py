@@ -183,6 +183,106 @@ def test_many_short_requests():
     check(queries(700, 2, 64), cache, table, lens, list(range(701)), 64)
 
 
+def check_on_gpu(q, cache, table, lens, offsets, d, causal=True, kd=1.0, vd=1.0, **kw):
+    """As ``check``, with the fp64 reference computed by torch on the GPU (large shapes); pages that
+    are not in the cache hold keys that nobody sees."""
+    scale = 1 / math.sqrt(d)
+    pages, Hkv = cache.shape[:2]
+    page, group = cache.shape[3] * 16 // (9 * d), q.shape[1] // Hkv
+    raw = cache.cpu().numpy()
+    o, lse = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), causal=causal,
+                        k_descale=kd, v_descale=vd, **kw)
+    for b, n in enumerate(lens):
+        rows = offsets[b + 1] - offsets[b]
+        if rows == 0:
+            continue
+        if n == 0:
+            assert (o[offsets[b]:offsets[b + 1]] == 0).all()
+            assert (lse[offsets[b]:offsets[b + 1]] == -math.inf).all()
+            continue
+        ids = [int(p) for p in np.asarray(table)[b, :-(-n // page)]]
+        there = torch.tensor([0 <= p < pages for p in ids]).repeat_interleave(page)[:n].cuda()
+        kv64 = []
+        for kind, ds in ((0, kd), (1, vd)):
+            blocks = [[kv.dequantise(*kv.unblock(raw[p if 0 <= p < pages else 0, h, kind], page, d), ds)
+                       for p in ids] for h in range(Hkv)]
+            kv64.append(torch.tensor(np.stack([np.concatenate(x) for x in blocks]))[:, :n].cuda())
+        k, v = (x.repeat_interleave(group, 0) for x in kv64)  # [Hq, n, d]
+        x = q[offsets[b]:offsets[b + 1]].double().transpose(0, 1)
+        s = scale * x @ k.transpose(1, 2)
+        seen = there[None].expand(rows, n)
+        if causal:
+            seen = seen & (torch.arange(n, device="cuda")[None]
+                           <= n - rows + torch.arange(rows, device="cuda")[:, None])
+        s = s.masked_fill(~seen, -math.inf)
+        want_l = torch.logsumexp(s, -1)
+        p = torch.where(want_l[..., None] > -math.inf, torch.exp(s - want_l[..., None]), 0.0)
+        want_o, mass = p @ v, p @ v.abs()
+        dot = scale * (x.abs() @ k.abs().transpose(1, 2)).amax(-1)
+        total = v.abs().sum(1)[:, None]
+        got_o = o[offsets[b]:offsets[b + 1]].double().transpose(0, 1)
+        got_l = lse[offsets[b]:offsets[b + 1]].double().T
+        delta = 2.0 ** -18 * dot
+        tol = 2.0 ** -8 * want_o.abs() + (2 * delta[..., None] + 2.0 ** -10) * mass + 2.0 ** -32 * total
+        assert ((got_o - want_o).abs() <= tol).all()
+        dead = want_l == -math.inf
+        assert torch.equal(got_l == -math.inf, dead)
+        err = (got_l - want_l).abs()[~dead]
+        assert (err <= (delta + 2.0 ** -20 * (1 + want_l.abs()))[~dead]).all()
+    return o, lse
+
+
+@pytest.mark.parametrize("d,page,Hq,Hkv,lens,qlens,causal", [
+    (128, 64, 8, 2, [1500, 700, 300], [700, 33, 300], True),   # rows that see nothing but themselves
+    (64, 16, 4, 1, [2000, 65], [1000, 65], True),
+    (128, 16, 4, 4, [1000, 129, 0, 640], [128, 129, 5, 257], False),
+    (64, 128, 6, 2, [900, 1, 50], [90, 1, 60], True),          # more queries than keys
+    (128, 32, 32, 1, [513], [9], True),                        # few tokens, many heads of one group
+    (128, 128, 16, 16, [400] * 12, [130] * 12, True),          # more units than CTAs: several in a row
+])
+def test_prompt_chunks(d, page, Hq, Hkv, lens, qlens, causal):
+    cache, table = make(lens, -(-max(lens) // page) + 1, page, Hkv, d)
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    q = queries(offsets[-1], Hq, d)
+    a = check_on_gpu(q, cache, table, lens, offsets, d, causal=causal, max_q=max(qlens), vd=0.5)
+    b = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), causal=causal,
+                   max_q=max(qlens), v_descale=0.5)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # the same bits again
+    assert ea.device_status() == 0
+
+
+def test_prompt_chunk_split_over_many_ctas():
+    """One key head and two blocks of rows: every CTA takes a few tiles, all of them are merged."""
+    d, page, lens, qlens = 128, 64, [20000], [100]
+    cache, table = make(lens, 313, page, 1, d)
+    size = ea.kv4_workspace_bytes(4, 1, d, 100, page, 313)
+    ws = torch.full((size,), 255, dtype=torch.uint8).cuda()
+    check_on_gpu(queries(100, 4, d), cache, table, lens, [0, 100], d, max_q=100, workspace=ws)
+
+
+def test_prompt_chunks_with_masked_places_and_missing_pages():
+    d, page, lens, qlens = 64, 32, [700, 300], [200, 90]
+    cache, table = make(lens, 22, page, 2, d)
+    offsets = [0, 200, 290]
+    q = queries(290, 4, d)
+    want = check_on_gpu(q, cache, table, lens, offsets, d, max_q=200)
+    # the key of request 0's query 150 becomes NaN: queries before it do not see it
+    at = 700 - 200 + 150
+    slot = ints([table[0][at // page] * page + at % page])
+    bad = torch.full((1, 2, d), math.nan).bfloat16().cuda()
+    good_k, good_v = ea.kv4_read(cache, slot, d)
+    for k, v in ((bad, good_v), (good_k, bad)):
+        ea.kv4_append(k, v, cache, slot)
+        o, lse = ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=ints(offsets), max_q=200)
+        sees = torch.zeros(290, dtype=torch.bool)
+        sees[150:200] = True
+        assert torch.equal(o[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
+        assert o[sees].isnan().all() and lse[sees].isnan().all()
+    ea.kv4_append(good_k, good_v, cache, slot)
+    table[0, 3], table[0, 20], table[1, 0], table[1, 9] = -1, 2 ** 31 - 1, -7, 10 ** 6
+    check_on_gpu(q, cache, table, lens, offsets, d, max_q=200)
+
+
 def test_scale_descales_and_large_scores():
     lens, d = [200, 77], 128
     cache, table = make(lens, 4, 64, 2, d)
