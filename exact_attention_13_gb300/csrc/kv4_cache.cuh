@@ -8,18 +8,22 @@
 // A head vector that holds a NaN or an infinity gets NaN scales throughout: it reads back as NaN
 // instead of as a large finite number.  code * s has at most six significant bits, so it is exact
 // in bf16 and in f16.
-// The quotients decide exactly as in real arithmetic: max |x| / 6 and x / s are correctly rounded
-// fp32 quotients of numbers of at most 8 significant bits; on a rounding boundary of e4m3 or e2m1
-// they are exact, and off it by a relative 2^-9 or more, far above fp32's rounding.
+// The roundings decide exactly as in real arithmetic.  max |x| / 6 is one correctly rounded fp32
+// quotient of numbers of at most 8 significant bits: on a midpoint of e4m3 it is exact, off it by a
+// relative 2^-8 or more.  x / s is x times the reciprocal of s, off by 2^-23 relative; a midpoint of
+// e2m1 times s has at most 7 significant bits and x has 8, so x / s lies on a midpoint or a relative
+// 2^-8 off it.  Rounding the product to the grid of 2^-14 brings the former onto the midpoint (a
+// multiple of 2^-2) and moves the latter by 2^-15, less than a tenth of its distance (2^-10 at the
+// smallest midpoint, 1/4).  (Sixteen divisions a group took most of the kernel's instructions.)
 //
 // Layout.  cache[page][head][K, V][block]; a block is page_size rows of d / 2 code bytes (value 2i
 // in the low, 2i + 1 in the high half of byte i), then page_size rows of d / 16 scale bytes: the
 // keys and the values of a page's head are one contiguous run of page_size * 9 d / 8 bytes.  Slot s
 // is row s % page_size of page s / page_size.
 //
-// Both kernels give one thread a group: 32 bytes of bf16 on one side, 8 code bytes and a scale byte
-// on the other, neighbouring lanes holding neighbouring groups.  They are bound by memory (or, for
-// a decode step's few rows, by the launch).
+// Both kernels give one thread the same group of the keys and of the values: 32 bytes of bf16 on one
+// side, 8 code bytes and a scale byte on the other for each, neighbouring lanes holding neighbouring
+// groups.  They are bound by memory (or, for a decode step's few rows, by the launch).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -63,101 +67,125 @@ __device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
 }
 
 struct Kv4Rows {
-  const __nv_bfloat16* k;  // append: [T, H, d] in (strides in elements)
-  const __nv_bfloat16* v;
-  __nv_bfloat16* k_out;    // read: [T, H, d] out, contiguous
-  __nv_bfloat16* v_out;
+  const __nv_bfloat16* in[2];   // append: keys and values [T, H, d] (strides in elements)
+  __nv_bfloat16* out[2];        // read: [T, H, d], contiguous
   uint8_t* cache;
-  const int* slots;        // [T]
-  long long k_row, k_head, v_row, v_head;
-  long long total;         // T * H * 2 * (d / 16) groups
-  int t, heads, page, pages;
-  float k_descale, v_descale;
+  const int* slots;             // [T]
+  long long row[2], head[2];
+  float descale[2];
+  int groups;                   // T * H * (d / 16) of this launch, below 2^31
+  int heads, page_shift, pages;
 };
 
-// Group g of (tensor n, token, head): where its codes and its scale live; false when the slot lies
-// outside the cache (such rows are skipped).
+// A thread's group: (token, head, group of the head).
 template <int D>
-__device__ __forceinline__ bool kv4_place(const Kv4Rows& a, int n, int token, int head, int g,
-                                          size_t& codes, size_t& scale) {
-  const int slot = a.slots[token];
-  if (slot < 0 || slot / a.page >= a.pages) return false;
-  const int page = slot / a.page, row = slot - page * a.page;
-  const size_t block = (static_cast<size_t>(page) * a.heads + head) * 2 + n;
-  const size_t base = block * kv4_block_bytes(a.page, D);
-  codes = base + row * (D / 2) + g * 8;
-  scale = base + a.page * (D / 2) + row * (D / kKv4Group) + g;
-  return true;
-}
+struct Kv4Index {
+  static constexpr int kGroups = D / kKv4Group;
+  int token, head, g;
+  __device__ __forceinline__ Kv4Index(const Kv4Rows& a, int i) {
+    const int vec = i / kGroups;
+    g = i % kGroups;
+    token = vec / a.heads;
+    head = vec - token * a.heads;
+  }
+};
+
+// Where its codes in the K block lie: the scale is `scale` bytes on, the V block `block` bytes on.
+// at < 0: the slot lies outside the cache.
+template <int D>
+struct Kv4Place {
+  long long at;
+  int scale, block;
+  __device__ __forceinline__ Kv4Place(const Kv4Rows& a, const Kv4Index<D>& x, int slot) {
+    const int page = slot >> a.page_shift, rows = 1 << a.page_shift, row = slot & (rows - 1);
+    block = kv4_block_bytes(rows, D);
+    scale = rows * (D / 2) + row * (D / kKv4Group - D / 2) - x.g * 7;
+    at = slot < 0 || page >= a.pages
+             ? -1
+             : (static_cast<long long>(page) * a.heads + x.head) * 2 * block + row * (D / 2) + x.g * 8;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a) {
-  constexpr int kGroups = D / kKv4Group;  // 8 or 4 neighbouring lanes hold one head vector
-  const long long id = static_cast<long long>(blockIdx.x) * kKv4Threads + threadIdx.x;
-  const bool live = id < a.total;
-  const long long i = live ? id : a.total - 1;  // idle lanes repeat the last group, for the shuffles
-  const int g = static_cast<int>(i % kGroups);
-  const long long vec = i / kGroups;
-  const int head = static_cast<int>(vec % a.heads);
-  const long long row = vec / a.heads;
-  const int n = row >= a.t ? 1 : 0;
-  const int token = static_cast<int>(n ? row - a.t : row);
-
-  const __nv_bfloat16* src = n ? a.v + token * a.v_row + head * a.v_head
-                               : a.k + token * a.k_row + head * a.k_head;
-  const uint4* p = reinterpret_cast<const uint4*>(src + g * kKv4Group);
-  float x[2][8];
-  unpack_bf16x8(__ldg(p), x[0]);
-  unpack_bf16x8(__ldg(p + 1), x[1]);
-  const float inv = 1.f / (n ? a.v_descale : a.k_descale);  // a power of two: exact
-  float amax = 0.f;
-  bool odd = false;
+  using P = Kv4Index<D>;
+  const int id = blockIdx.x * kKv4Threads + threadIdx.x;
+  const bool live = id < a.groups;
+  const P x0(a, live ? id : a.groups - 1);  // idle lanes repeat the last group, for the votes
+  const int slot = __ldg(a.slots + x0.token);
+  uint4 raw[2][2];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float& f = x[j / 8][j % 8];
-    odd |= !(fabsf(f) < INFINITY);
-    f *= inv;
-    amax = fmaxf(amax, fabsf(f));
+  for (int n = 0; n < 2; ++n) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.in[n] + x0.token * a.row[n] + x0.head * a.head[n]) + x0.g * 2;
+    raw[n][0] = __ldg(src);
+    raw[n][1] = __ldg(src + 1);
   }
-  const unsigned mask = __ballot_sync(0xffffffffu, odd);
-  const unsigned mine = ((1u << kGroups) - 1u) << (threadIdx.x % 32 / kGroups * kGroups);
-  uint32_t s8 = pack_e4m3x4(__fdiv_rn(amax, 6.f), 0.f, 0.f, 0.f) & 0xffu;
-  uint32_t code[2] = {0u, 0u};
-  if (mask & mine) {
-    s8 = 0x7fu;  // NaN
-  } else if (s8 != 0u) {
-    const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(s8))).x;
+  const Kv4Place<D> p(a, x0, slot);
+  const unsigned mine = ((1u << P::kGroups) - 1u) << (threadIdx.x % 32 / P::kGroups * P::kGroups);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j / 8][j % 8] = __fdiv_rn(x[j / 8][j % 8], s);
-    code[0] = pack_e2m1x8(x[0]);
-    code[1] = pack_e2m1x8(x[1]);
-  }
-  size_t codes, scale;
-  if (live && kv4_place<D>(a, n, token, head, g, codes, scale)) {
-    *reinterpret_cast<uint2*>(a.cache + codes) = make_uint2(code[0], code[1]);
-    a.cache[scale] = static_cast<uint8_t>(s8);
+  for (int n = 0; n < 2; ++n) {
+    float x[16];
+    unpack_bf16x8(raw[n][0], reinterpret_cast<float(&)[8]>(x[0]));
+    unpack_bf16x8(raw[n][1], reinterpret_cast<float(&)[8]>(x[8]));
+    // 0 x is 0 but for infinities and NaN
+    float amax = 0.f;
+    float2 odd = f32x2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      amax = max3f(amax, fabsf(x[j]), fabsf(x[j + 1]));
+      odd = fma_f32x2(f32x2(x[j], x[j + 1]), f32x2(0.f, 0.f), odd);
+    }
+    const unsigned bad = __ballot_sync(0xffffffffu, !(odd.x + odd.y == 0.f));
+    const float descale = a.descale[n];
+    // descale is a power of two: dividing by it is exact
+    uint32_t s8 = pack_e4m3x4(__fdiv_rn(amax * (1.f / descale), 6.f), 0.f, 0.f, 0.f) & 0xffu;
+    uint32_t code[2] = {0u, 0u};
+    if (bad & mine) {
+      s8 = 0x7fu;  // NaN
+    } else if (s8 != 0u) {
+      const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(s8))).x;
+      const float inv = 1.f / (s * descale);
+      // 768 = 1.5 * 2^9: adding it rounds to multiples of 2^-14; the sign of zeros is put back
+      const float2 inv2 = f32x2(inv, inv), up = f32x2(768.f, 768.f), down = f32x2(-768.f, -768.f);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float2 t = add_f32x2(fma_f32x2(f32x2(x[j], x[j + 1]), inv2, up), down);
+        x[j] = copysignf(t.x, x[j]);
+        x[j + 1] = copysignf(t.y, x[j + 1]);
+      }
+      code[0] = pack_e2m1x8(x);
+      code[1] = pack_e2m1x8(x + 8);
+    }
+    if (live && p.at >= 0) {
+      uint8_t* dst = a.cache + p.at + n * p.block;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+      dst[p.scale] = static_cast<uint8_t>(s8);
+    }
   }
 }
 
 // Rows of invalid slots read as zeros.
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) {
-  constexpr int kGroups = D / kKv4Group;
-  const long long i = static_cast<long long>(blockIdx.x) * kKv4Threads + threadIdx.x;
-  if (i >= a.total) return;
-  const int g = static_cast<int>(i % kGroups);
-  const long long vec = i / kGroups;
-  const int head = static_cast<int>(vec % a.heads);
-  const long long row = vec / a.heads;
-  const int n = row >= a.t ? 1 : 0;
-  const int token = static_cast<int>(n ? row - a.t : row);
-  uint4 out[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  size_t codes, scale;
-  if (kv4_place<D>(a, n, token, head, g, codes, scale)) {
-    const uint2 c = *reinterpret_cast<const uint2*>(a.cache + codes);
-    const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(a.cache[scale])).x *
-                    (n ? a.v_descale : a.k_descale);
-    const uint32_t w[2] = {c.x, c.y};
+  const int id = blockIdx.x * kKv4Threads + threadIdx.x;
+  if (id >= a.groups) return;
+  const Kv4Index<D> x0(a, id);
+  const Kv4Place<D> p(a, x0, __ldg(a.slots + x0.token));
+  uint2 codes[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+  uint8_t s8[2] = {0, 0};
+  if (p.at >= 0) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint8_t* src = a.cache + p.at + n * p.block;
+      codes[n] = *reinterpret_cast<const uint2*>(src);
+      s8[n] = src[p.scale];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(s8[n])).x * a.descale[n];
+    const uint32_t w[2] = {codes[n].x, codes[n].y};
+    uint4* dst = reinterpret_cast<uint4*>(a.out[n] + static_cast<size_t>(id) * kKv4Group);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       uint32_t h[4];
@@ -169,13 +197,9 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) 
         f[2 * j] = two.x * s;
         f[2 * j + 1] = two.y * s;
       }
-      out[q] = pack_bf16x8(f);
+      dst[q] = pack_bf16x8(f);
     }
   }
-  __nv_bfloat16* dst = (n ? a.v_out : a.k_out) +
-                       (static_cast<size_t>(token) * a.heads + head) * D + g * kKv4Group;
-  reinterpret_cast<uint4*>(dst)[0] = out[0];
-  reinterpret_cast<uint4*>(dst)[1] = out[1];
 }
 
 }  // namespace exattn

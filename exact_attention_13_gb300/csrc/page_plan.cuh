@@ -34,7 +34,7 @@ struct PlanArgs {
   int* positions;        // [T]
   int* slots;            // [T]
   int* state_out;        // {head, count}
-  int b, width, cap, page, t;
+  int b, width, cap, page_shift, t;
 };
 
 // Exclusive prefix sums over the block's threads of three values, and their totals.
@@ -78,10 +78,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   int head = a.state[0], count = a.state[1];
   count = min(max(count, 0), a.cap);
   head = static_cast<int>(static_cast<unsigned>(head) % static_cast<unsigned>(a.cap));
-  const int limit = static_cast<int>(min(static_cast<long long>(a.width) * a.page, 0x7fffffffll));
+  const int limit = static_cast<int>(min(static_cast<long long>(a.width) << a.page_shift, 0x7fffffffll));
   // a request's length as far as its table row can hold it
   auto length = [&](int r) { return min(max(a.lens[r], 0), limit); };
-  auto pages = [&](int tokens) { return (tokens + a.page - 1) / a.page; };
+  auto pages = [&](int tokens) { return tokens ? ((tokens - 1) >> a.page_shift) + 1 : 0; };
   auto wants = [&](int r, int len, int add) {
     return static_cast<long long>(len) + add <= limit ? pages(len + add) - pages(len) : -1;
   };
@@ -115,7 +115,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
 
   const int gthread = blockIdx.x * kPlanThreads + threadIdx.x;
   const int gthreads = gridDim.x * kPlanThreads;
-  auto ring = [&](long long i) { return static_cast<int>((head + i) % a.cap); };
+  // place i <= cap of the ring, counted from its head
+  auto ring = [&](int i) {
+    const unsigned x = static_cast<unsigned>(head) + static_cast<unsigned>(i), cap = static_cast<unsigned>(a.cap);
+    return static_cast<int>(x >= cap ? x - cap : x);
+  };
   if (gthread == 0) {
     a.state_out[0] = ring(s_taken);
     a.state_out[1] = static_cast<int>(min(static_cast<long long>(a.cap),
@@ -136,12 +140,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     if (add < 0) {
       for (int i = lane; i < have; i += 32) {
         const long long at = static_cast<long long>(count) + s_back[r] + i;
-        if (at < a.cap) a.queue[ring(at)] = row[i];
+        if (at < a.cap) a.queue[ring(static_cast<int>(at))] = row[i];
       }
     } else if (s_need[r] >= 0) {
       const int need = pages(len + add) - have;
       for (int i = lane; i < need; i += 32)
-        row[have + i] = a.queue[ring(static_cast<long long>(s_need[r]) + i)];
+        row[have + i] = a.queue[ring(s_need[r] + i)];
     }
   }
   for (int t = gthread; t < a.t; t += gthreads) {
@@ -155,10 +159,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       const int len = length(lo);
       pos = len + (t - s_tok[lo]);
       if (s_need[lo] >= 0) {
-        const int p = pos / a.page, have = pages(len);
+        const int p = pos >> a.page_shift, have = pages(len);
         const int id = p < have ? a.table[static_cast<long long>(lo) * a.width + p]
-                                : a.queue[ring(static_cast<long long>(s_need[lo]) + p - have)];
-        slot = id * a.page + (pos - p * a.page);
+                                : a.queue[ring(s_need[lo] + p - have)];
+        slot = (id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
       }
     }
     a.positions[t] = pos;
