@@ -8,22 +8,25 @@
 // A head vector that holds a NaN or an infinity gets NaN scales throughout: it reads back as NaN
 // instead of as a large finite number.  code * s has at most six significant bits, so it is exact
 // in bf16 and in f16.
-// The roundings decide exactly as in real arithmetic.  max |x| / 6 is one correctly rounded fp32
-// quotient of numbers of at most 8 significant bits: on a midpoint of e4m3 it is exact, off it by a
-// relative 2^-8 or more.  x / s is x times the reciprocal of s, off by 2^-23 relative; a midpoint of
-// e2m1 times s has at most 7 significant bits and x has 8, so x / s lies on a midpoint or a relative
-// 2^-8 off it.  Rounding the product to the grid of 2^-14 brings the former onto the midpoint (a
-// multiple of 2^-2) and moves the latter by 2^-15, less than a tenth of its distance (2^-10 at the
-// smallest midpoint, 1/4).  (Sixteen divisions a group took most of the kernel's instructions.)
+// The roundings decide exactly as in real arithmetic, without divisions.  A midpoint of e4m3 times 6
+// has at most 7 significant bits and max |x| has 8, so max |x| / 6 lies on a midpoint or a relative
+// 2^-8 off it.  The product with 1/6 is off by 2^-23; rounding it to f16 first (2^-12) brings the
+// former onto the midpoint, which f16 holds, and leaves the latter on its side.  Likewise x / s lies
+// on a midpoint of e2m1 (a multiple of 2^-2) or a relative 2^-8 off it; the product with the
+// reciprocal of s (off by 2^-22) is rounded to the grid of 2^-14, which moves it by 2^-15, less than a
+// tenth of that distance at the smallest midpoint, 1/4.  (17 divisions a group took most of the
+// instructions.)
 //
 // Layout.  cache[page][head][K, V][block]; a block is page_size rows of d / 2 code bytes (value 2i
 // in the low, 2i + 1 in the high half of byte i), then page_size rows of d / 16 scale bytes: the
 // keys and the values of a page's head are one contiguous run of page_size * 9 d / 8 bytes.  Slot s
 // is row s % page_size of page s / page_size.
 //
-// Both kernels give one thread the same group of the keys and of the values: 32 bytes of bf16 on one
-// side, 8 code bytes and a scale byte on the other for each, neighbouring lanes holding neighbouring
-// groups.  They are bound by memory (or, for a decode step's few rows, by the launch).
+// A thread of the append kernel takes the same group of the keys and of the values, one of the read
+// kernel half of it: 8 values are 16 bytes of bf16, so the read kernel's stores are whole lines.
+// (Groups in both: 11.2 us to read 8191 tokens of 8 heads of 128 from consecutive slots instead of
+// 10.0; halves in both: 11.3 us to append them instead of the 9 of groups, whose code stores are
+// twice as wide.)  Both are bound by memory or, for a decode step's few rows, by the launch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,6 +69,19 @@ __device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
+// The f16 in the low half as e4m3 (nearest even, saturating).
+__device__ __forceinline__ uint32_t e4m3_from_f16(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r & 0xffu;
+}
+// 1 / x, within 2^-23 of it.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct Kv4Rows {
   const __nv_bfloat16* in[2];   // append: keys and values [T, H, d] (strides in elements)
   __nv_bfloat16* out[2];        // read: [T, H, d], contiguous
@@ -73,18 +89,18 @@ struct Kv4Rows {
   const int* slots;             // [T]
   long long row[2], head[2];
   float descale[2];
-  int groups;                   // T * H * (d / 16) of this launch, below 2^31
+  int pieces;                   // threads of this launch, T * H * (d / 16 or d / 8), below 2^31
   int heads, page_shift, pages;
 };
 
-// A thread's group: (token, head, group of the head).
-template <int D>
+// A thread's piece of kSize values: (token, head, piece of the head).
+template <int D, int kSize>
 struct Kv4Index {
-  static constexpr int kGroups = D / kKv4Group;
-  int token, head, g;
+  static constexpr int kPieces = D / kSize;
+  int token, head, p;
   __device__ __forceinline__ Kv4Index(const Kv4Rows& a, int i) {
-    const int vec = i / kGroups;
-    g = i % kGroups;
+    const int vec = i / kPieces;
+    p = i % kPieces;
     token = vec / a.heads;
     head = vec - token * a.heads;
   }
@@ -92,36 +108,38 @@ struct Kv4Index {
 
 // Where its codes in the K block lie: the scale is `scale` bytes on, the V block `block` bytes on.
 // at < 0: the slot lies outside the cache.
-template <int D>
+template <int D, int kSize>
 struct Kv4Place {
   long long at;
   int scale, block;
-  __device__ __forceinline__ Kv4Place(const Kv4Rows& a, const Kv4Index<D>& x, int slot) {
+  __device__ __forceinline__ Kv4Place(const Kv4Rows& a, const Kv4Index<D, kSize>& x, int slot) {
     const int page = slot >> a.page_shift, rows = 1 << a.page_shift, row = slot & (rows - 1);
+    const int code = x.p * (kSize / 2);
     block = kv4_block_bytes(rows, D);
-    scale = rows * (D / 2) + row * (D / kKv4Group - D / 2) - x.g * 7;
+    scale = rows * (D / 2) + row * (D / kKv4Group - D / 2) + x.p * kSize / kKv4Group - code;
     at = slot < 0 || page >= a.pages
              ? -1
-             : (static_cast<long long>(page) * a.heads + x.head) * 2 * block + row * (D / 2) + x.g * 8;
+             : (static_cast<long long>(page) * a.heads + x.head) * 2 * block + row * (D / 2) + code;
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a) {
-  using P = Kv4Index<D>;
+  using Index = Kv4Index<D, kKv4Group>;
+  constexpr int kPieces = Index::kPieces;  // 8 or 4 neighbouring lanes hold one head vector
   const int id = blockIdx.x * kKv4Threads + threadIdx.x;
-  const bool live = id < a.groups;
-  const P x0(a, live ? id : a.groups - 1);  // idle lanes repeat the last group, for the votes
-  const int slot = __ldg(a.slots + x0.token);
+  const bool live = id < a.pieces;
+  const Index ix(a, live ? id : a.pieces - 1);  // idle lanes repeat the last piece, for the votes
+  const int slot = __ldg(a.slots + ix.token);
   uint4 raw[2][2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.in[n] + x0.token * a.row[n] + x0.head * a.head[n]) + x0.g * 2;
+    const uint4* src = reinterpret_cast<const uint4*>(a.in[n] + ix.token * a.row[n] + ix.head * a.head[n]) + 2 * ix.p;
     raw[n][0] = __ldg(src);
     raw[n][1] = __ldg(src + 1);
   }
-  const Kv4Place<D> p(a, x0, slot);
-  const unsigned mine = ((1u << P::kGroups) - 1u) << (threadIdx.x % 32 / P::kGroups * P::kGroups);
+  const Kv4Place<D, kKv4Group> place(a, ix, slot);
+  const unsigned mine = ((1u << kPieces) - 1u) << (threadIdx.x % 32 / kPieces * kPieces);
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     float x[16];
@@ -136,15 +154,15 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a
       odd = fma_f32x2(f32x2(x[j], x[j + 1]), f32x2(0.f, 0.f), odd);
     }
     const unsigned bad = __ballot_sync(0xffffffffu, !(odd.x + odd.y == 0.f));
-    const float descale = a.descale[n];
-    // descale is a power of two: dividing by it is exact
-    uint32_t s8 = pack_e4m3x4(__fdiv_rn(amax * (1.f / descale), 6.f), 0.f, 0.f, 0.f) & 0xffu;
+    const float inv_descale = 1.f / a.descale[n];
+    // inv_descale is a power of two: the product with it is exact
+    uint32_t s8 = e4m3_from_f16(pack_f16x2(amax * inv_descale * (1.f / 6.f), 0.f));
     uint32_t code[2] = {0u, 0u};
     if (bad & mine) {
       s8 = 0x7fu;  // NaN
     } else if (s8 != 0u) {
       const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(s8))).x;
-      const float inv = 1.f / (s * descale);
+      const float inv = rcp_approx(s) * inv_descale;
       // 768 = 1.5 * 2^9: adding it rounds to multiples of 2^-14; the sign of zeros is put back
       const float2 inv2 = f32x2(inv, inv), up = f32x2(768.f, 768.f), down = f32x2(-768.f, -768.f);
 #pragma unroll
@@ -156,10 +174,10 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a
       code[0] = pack_e2m1x8(x);
       code[1] = pack_e2m1x8(x + 8);
     }
-    if (live && p.at >= 0) {
-      uint8_t* dst = a.cache + p.at + n * p.block;
+    if (live && place.at >= 0) {
+      uint8_t* dst = a.cache + place.at + n * place.block;
       *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-      dst[p.scale] = static_cast<uint8_t>(s8);
+      dst[place.scale] = static_cast<uint8_t>(s8);
     }
   }
 }
@@ -168,37 +186,32 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) {
   const int id = blockIdx.x * kKv4Threads + threadIdx.x;
-  if (id >= a.groups) return;
-  const Kv4Index<D> x0(a, id);
-  const Kv4Place<D> p(a, x0, __ldg(a.slots + x0.token));
-  uint2 codes[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+  if (id >= a.pieces) return;
+  const Kv4Index<D, 8> ix(a, id);
+  const Kv4Place<D, 8> place(a, ix, __ldg(a.slots + ix.token));
+  uint32_t codes[2] = {0u, 0u};
   uint8_t s8[2] = {0, 0};
-  if (p.at >= 0) {
+  if (place.at >= 0) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const uint8_t* src = a.cache + p.at + n * p.block;
-      codes[n] = *reinterpret_cast<const uint2*>(src);
-      s8[n] = src[p.scale];
+      const uint8_t* src = a.cache + place.at + n * place.block;
+      codes[n] = *reinterpret_cast<const uint32_t*>(src);
+      s8[n] = src[place.scale];
     }
   }
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const float s = f16x2_to_f32x2(e4m3x2_to_f16x2(s8[n])).x * a.descale[n];
-    const uint32_t w[2] = {codes[n].x, codes[n].y};
-    uint4* dst = reinterpret_cast<uint4*>(a.out[n] + static_cast<size_t>(id) * kKv4Group);
+    uint32_t h[4];
+    unpack_e2m1x8(codes[n], h);
+    float f[8];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t h[4];
-      unpack_e2m1x8(w[q], h);
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 two = f16x2_to_f32x2(h[j]);
-        f[2 * j] = two.x * s;
-        f[2 * j + 1] = two.y * s;
-      }
-      dst[q] = pack_bf16x8(f);
+    for (int j = 0; j < 4; ++j) {
+      const float2 two = f16x2_to_f32x2(h[j]);
+      f[2 * j] = two.x * s;
+      f[2 * j + 1] = two.y * s;
     }
+    reinterpret_cast<uint4*>(a.out[n])[id] = pack_bf16x8(f);
   }
 }
 

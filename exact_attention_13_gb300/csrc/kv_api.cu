@@ -85,15 +85,15 @@ int cache_checks(const void* cache, int pages, int heads, int page, int d) {
   return aligned(cache, 16) ? FA_OK : FA_ERR_MISALIGNED;
 }
 
-// Append or read T tokens, in launches of fewer than 2^31 groups (32-bit indices).
+// Append or read T tokens, in launches of fewer than 2^31 pieces (32-bit indices).
 template <typename K64, typename K128>
-int launch_rows(Kv4Rows a, int T, int heads, int d, K64 k64, K128 k128, cudaStream_t s) {
-  const int per_token = heads * (d / kKv4Group);
+int launch_rows(Kv4Rows a, int T, int heads, int d, int piece, K64 k64, K128 k128, cudaStream_t s) {
+  const int per_token = heads * (d / piece);
   const int most = ((1 << 30) / per_token);
   for (int t = 0; t < T; t += most) {
     const int n = T - t < most ? T - t : most;
-    a.groups = n * per_token;
-    const unsigned grid = static_cast<unsigned>((a.groups + kKv4Threads - 1) / kKv4Threads);
+    a.pieces = n * per_token;
+    const unsigned grid = static_cast<unsigned>((a.pieces + kKv4Threads - 1) / kKv4Threads);
     if (d == 64)
       k64<<<grid, kKv4Threads, 0, s>>>(a);
     else
@@ -324,7 +324,7 @@ int fa_kv4_append(const void* k, long long k_row_stride, long long k_head_stride
   a.pages = num_pages;
   a.descale[0] = k_descale;
   a.descale[1] = v_descale;
-  return launch_rows(a, T, Hkv, d, kv4_append_kernel<64>, kv4_append_kernel<128>,
+  return launch_rows(a, T, Hkv, d, kKv4Group, kv4_append_kernel<64>, kv4_append_kernel<128>,
                      static_cast<cudaStream_t>(stream));
 }
 
@@ -344,7 +344,7 @@ int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slot
   a.pages = num_pages;
   a.descale[0] = k_descale;
   a.descale[1] = v_descale;
-  return launch_rows(a, T, Hkv, d, kv4_read_kernel<64>, kv4_read_kernel<128>,
+  return launch_rows(a, T, Hkv, d, 8, kv4_read_kernel<64>, kv4_read_kernel<128>,
                      static_cast<cudaStream_t>(stream));
 }
 
