@@ -37,6 +37,17 @@ constexpr int kChKeys = 128;
 constexpr int kChSoftmaxRegs = 208, kChWidenRegs = 64, kChMmaRegs = 32;
 static_assert(2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs <= 512, "registers of the block at launch");
 
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {  // NaN: the other one
+  uint32_t y;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+
 template <int D>
 struct ChunkGeo {
   static constexpr int kTileBytes = 128 * D * 2;          // 128 rows of f16, boxes of 64 columns
@@ -48,9 +59,9 @@ struct ChunkGeo {
     return kb >= kKSteps ? 0 : ((kb * 32 / 128) * 128 * 128 + kb * 32 % 128) >> 4;
   }
   static constexpr int kPvStep = 16 * 128 >> 4;
-  // a widening warp's ring: codes, scales and (for K) the values' scales of 32 keys a stage
+  // a widening warp's ring: codes and scales of 32 keys, or of their values, a stage
   static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kStageBytes = 32 * (D / 2 + 2 * (D / 16));
+  static constexpr int kStageBytes = 32 * (D / 2 + D / 16);
 };
 
 // One share of a unit: tiles [tile, tile + n) of its `tiles`.
@@ -370,49 +381,45 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
     // time, 4 (d = 128) or 2 lanes a row.
     constexpr int kLanes = D / 32, kRowsIt = 32 / kLanes, kIt = 32 / kRowsIt;
     constexpr int kCode = D / 2, kScale = D / 16;
-    constexpr int kSc = 32 * kCode, kVsc = kSc + 32 * kScale;  // in a stage: scales, values' scales
+    constexpr int kSc = 32 * kCode;  // in a stage: the scales
     const int part = lane % kLanes, row_in = lane / kLanes, row_w = (warp - 8) * 32;
     const int page_rows = 1 << a.page_shift;
     const int block_bytes = kv4_block_bytes(page_rows, D);
+    const unsigned page_bytes = static_cast<unsigned>(block_bytes) * 2u * static_cast<unsigned>(a.hk);
     ChunkWalk* const w = &ctl->walk[warp];
     walk_begin(a, w, ctl);
     uint8_t* const raw = s_raw + (warp - 8) * G::kStages * G::kStageBytes;
-    const uint32_t raw_u32 = smem_u32(raw), ring = smem_u32(s_ring);
 
-    // ---- loads: half a tile (K, then V) a stage, the page ids of the two 16-key groups a tile ahead
+    // ---- loads: the keys of a tile, then the values; the page ids of the two 16-key groups come a
+    // tile ahead
     int key = w->s.tile * kChKeys + row_w, tiles_left = w->s.n, keys = w->s.req.keys;
     const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
     const uint8_t* head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
-    bool loads_left = true;
     int id[2];
     auto fetch_ids = [&]() {
       id[0] = key < keys ? __ldg(ids + (key >> a.page_shift)) : -1;
       id[1] = id[0];
       if (a.page_shift == 4) id[1] = key + 16 < keys ? __ldg(ids + (key >> 4) + 1) : -1;
     };
-    int load_no = 0;  // half tiles asked for so far
+    int stage_in = 0;
+    bool loads_left = true, values_next = false;
+    // where the lane copies from: codes of the groups' first rows, and its 16 bytes of scales
+    const uint8_t *codes[2], *scales_from = nullptr;
+    uint32_t there = 0;  // bit g: the group's page exists
+    const int sc_group = lane / kScale % 2;
     auto load = [&]() {
-      if (loads_left) {
-        const bool v = load_no & 1;
-        const uint32_t dst = raw_u32 + load_no % G::kStages * G::kStageBytes;
-        constexpr int kPer = 16 * kCode / 512;
+      if (loads_left || values_next) {
+        if (!values_next) {
+          there = 0;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const bool there = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
-          const uint32_t n = there ? 16u : 0u;  // 0: the copy writes zeros and reads nothing
-          const int row = (key + 16 * g) & (page_rows - 1);
-          const uint8_t* b = head + (there ? static_cast<size_t>(id[g]) * a.hk * 2 * block_bytes : 0) + (v ? block_bytes : 0);
-#pragma unroll
-          for (int p = 0; p < kPer; ++p)
-            cp_async16(dst + g * 16 * kCode + p * 512 + lane * 16, b + row * kCode + p * 512 + lane * 16, n);
-          // kScale copies of scales; for K the values' scales too
-          const uint8_t* sc = b + page_rows * kCode + row * kScale + lane % kScale * 16;
-          if (lane < kScale) cp_async16(dst + kSc + g * 16 * kScale + lane * 16, sc, n);
-          else if (!v && lane < 2 * kScale)
-            cp_async16(dst + kVsc + g * 16 * kScale + lane % kScale * 16, sc + block_bytes, n);
-        }
-        ++load_no;
-        if (v) {
+          for (int g = 0; g < 2; ++g) {
+            const bool ok = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
+            const int row = (key + 16 * g) & (page_rows - 1);
+            const uint8_t* b = head + static_cast<size_t>(ok ? static_cast<unsigned>(id[g]) : 0u) * page_bytes;
+            codes[g] = b + row * kCode + lane * 16;
+            if (sc_group == g) scales_from = b + page_rows * kCode + row * kScale + lane % kScale * 16;
+            there |= (ok ? 1u : 0u) << g;
+          }
           if (--tiles_left > 0) {
             key += kChKeys;
           } else {
@@ -425,55 +432,82 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           }
           if (loads_left) fetch_ids();
         }
+        const uint32_t dst = smem_u32(raw) + stage_in * G::kStageBytes;
+        const int from = values_next ? block_bytes : 0;
+        constexpr int kPer = 16 * kCode / 512;
+        // a page that is not there: copies of zero bytes, which write zeros and read nothing
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int p = 0; p < kPer; ++p)
+            cp_async16(dst + g * 16 * kCode + p * 512 + lane * 16, codes[g] + from + p * 512, there >> g & 1u ? 16u : 0u);
+        if (lane < 2 * kScale) cp_async16(dst + kSc + lane * 16, scales_from + from, there >> sc_group & 1u ? 16u : 0u);
+        stage_in = stage_in + 1 == G::kStages ? 0 : stage_in + 1;
+        values_next = !values_next;
       }
       cp_async_commit();
     };
-    // number of half tiles of the share
     const long long halves = 2 * (ctl->last - ctl->first);
     fetch_ids();
+
+    // Chunk g of a row (8 values, 16 bytes) lies at chunk g ^ (row % 8) of its 128-byte line.  Lanes of
+    // the second half of a row take their codes' halves in the other order: else they would store
+    // to the banks that the first half stores to.
+    const int swap = part & 2 ? 8 : 0;
+    const uint32_t scale_sel = part & 2 ? 0x1032u : 0x3210u;
+    uint32_t store_at[4];
 #pragma unroll
-    for (int i = 0; i < G::kStages; ++i) load();
-    auto nan2 = [](uint32_t s) { return (s & 0x7fu) == 0x7fu || (s & 0x7f00u) == 0x7f00u; };
-    for (int t = 0; t < halves; ++t) {
-      if (t >= G::kSlots && !wait(ctl->kv_empty[t % G::kSlots], t / G::kSlots - 1)) break;
-      cp_async_wait<G::kStages - 1>();
-      __syncwarp();
-      const uint8_t* st = raw + t % G::kStages * G::kStageBytes;
-      const uint32_t slot = ring + t % G::kSlots * G::kTileBytes;
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int r = it * kRowsIt + row_in;
-        uint4 c = *reinterpret_cast<const uint4*>(st + r * kCode + part * 16);
-        uint32_t sc = *reinterpret_cast<const uint16_t*>(st + kSc + r * kScale + part * 2);
-        // A value vector that is not a number makes its key's scores NaN and is zero itself: rows
-        // that do not see the key multiply it by zero.
-        if (t & 1) {
-          if (nan2(sc)) sc = 0u;
-        } else if (nan2(*reinterpret_cast<const uint16_t*>(st + kVsc + r * kScale + part * 2))) {
-          sc = 0x7f7fu;
+    for (int i = 0; i < 4; ++i) {
+      const int g = (part * 4 + (i ^ (part & 2))) & 7;
+      store_at[i] = smem_u32(s_ring) + (part / 2) * (128 * 128) + (row_w + row_in) * 128 + ((g ^ (row_in & 7)) << 4);
+    }
+    static_assert(kRowsIt % 8 == 0, "rows of later iterations keep their swizzle");
+    // One copy of this code for keys and values, and of the loads for the first stages and the later
+    // ones: the roles' loops together have to stay in the instruction cache.
+    int stage = 0;
+#pragma unroll 1
+    for (long long i = -G::kStages; i < halves; ++i) {
+      if (i >= 0) {
+        const bool values = i & 1;
+        const int slot = static_cast<int>(i % G::kSlots);
+        if (i >= G::kSlots && !wait(ctl->kv_empty[slot], static_cast<uint32_t>(i / G::kSlots - 1))) break;
+        if (!values) {
+          cp_async_wait<G::kStages - 2>();  // the keys and the values
+          __syncwarp();
         }
-        uint32_t scales = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
-        // Chunk g of a row (8 values) lies at chunk g ^ (row % 8); lanes of the second half of a
-        // row store their four in another order (fewer bank conflicts).
-        if (part & 2) {
-          c = make_uint4(c.z, c.w, c.x, c.y);
-          scales = __byte_perm(scales, 0u, 0x1032);
-        }
-        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-        const uint32_t row = slot + (part / 2) * (128 * 128) + (row_w + r) * 128;
+        const uint8_t* st = raw + stage * G::kStageBytes;
+        stage = stage + 1 == G::kStages ? 0 : stage + 1;
+        const uint8_t* st_values = values ? st : raw + stage * G::kStageBytes;
+        // A value vector that is not a number (NaN scales) makes its key's scores NaN and is zero
+        // itself: rows that do not see the key multiply it by zero.  max takes NaN to the other
+        // operand, 0; the values' scale times 0 is 0 or NaN.
+        const uint32_t to = slot * G::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t h[4];
-          unpack_e2m1x8(word[i], h);
+        for (int it = 0; it < kIt; ++it) {
+          const uint8_t* p = st + (it * kRowsIt + row_in) * kCode + part * 16;
+          const int sc = kSc + (it * kRowsIt + row_in) * kScale + part * 2;
+          const uint2 c0 = *reinterpret_cast<const uint2*>(p + swap), c1 = *reinterpret_cast<const uint2*>(p + (swap ^ 8));
+          uint32_t scales = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + sc));
+          uint32_t v_scales = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st_values + sc));
+          if (values)
+            scales = max_f16x2(scales, 0u);
+          else
+            scales = fma_f16x2(v_scales, 0u, scales);
+          scales = __byte_perm(scales, 0u, scale_sel);
+          const uint32_t word[4] = {c0.x, c0.y, c1.x, c1.y};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = i & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
-          const int g = (part * 4 + (i ^ (part & 2))) & 7;
-          st_shared_v4(row + ((g ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            unpack_e2m1x8(word[x], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = x & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
+            st_shared_v4(store_at[x] + to + it * kRowsIt * 128, h[0], h[1], h[2], h[3]);
+          }
         }
+        fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[slot]));
       }
-      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[t % G::kSlots]));
       load();
     }
     cp_async_wait<0>();
