@@ -7,12 +7,13 @@
 // The cache is widened once per tile of 128 keys and serves both row tiles: f16 K and V tiles in a
 // ring of shared-memory slots, in the 128-byte-swizzled layout that the MMA descriptors expect.
 //
-// Roles (512 threads, one CTA a SM):
+// Roles (544 threads, one CTA a SM):
 //   warps 0-7    softmax of tile 0 / tile 1; also load the query rows (scaled by a power of two into
 //                [1, 2), f16) and write O and the log-sum-exp
-//   warps 8-11   widen the cache, 32 keys each: codes and scales come by cp.async into a small ring of
-//                the warp's own, code * scale (exact) goes to the tile ring
-//   warp  12     issues the MMAs:  S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
+//   warps 8-11   widen the keys, 32 of a tile each: codes and scales from global memory to registers a
+//                tile ahead, code * scale (exact) to the ring
+//   warps 12-15  widen the values, likewise
+//   warp  16     issues the MMAs:  S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
 // TMEM: S_0 at columns 0-127, S_1 at 128-255 (P_h, f16, over S_h), O_0 at 256, O_1 at 384.
 //
 // A CTA takes an equal share of the line of all tiles, as in kv4_attn.cuh; a unit that crosses CTAs
@@ -30,12 +31,14 @@
 
 namespace exattn {
 
-constexpr int kChThreads = 512;
+constexpr int kChThreads = 544;
+constexpr int kChMmaWarp = 16;
 constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
-// register shares of the warpgroups: 128 (2 x 208 + 64 + 32) = 512 x 128
-constexpr int kChSoftmaxRegs = 208, kChWidenRegs = 64, kChMmaRegs = 32;
-static_assert(2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs <= 512, "registers of the block at launch");
+// 544 threads get 96 registers each at launch; the widening warpgroups give up what the softmax takes
+// (the MMA warp, alone in its warpgroup, keeps its 96).
+constexpr int kChLaunchRegs = 96, kChSoftmaxRegs = 136, kChWidenRegs = 56;
+static_assert(kChSoftmaxRegs + kChWidenRegs == 2 * kChLaunchRegs, "registers of the block at launch");
 
 __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {  // NaN: the other one
   uint32_t y;
@@ -59,9 +62,11 @@ struct ChunkGeo {
     return kb >= kKSteps ? 0 : ((kb * 32 / 128) * 128 * 128 + kb * 32 % 128) >> 4;
   }
   static constexpr int kPvStep = 16 * 128 >> 4;
-  // a widening warp's ring: codes and scales of 32 keys, or of their values, a stage
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kStageBytes = 32 * (D / 2 + D / 16);
+};
+
+template <bool B>
+struct ChunkMasked {
+  static constexpr bool value = B;
 };
 
 // One share of a unit: tiles [tile, tile + n) of its `tiles`.
@@ -86,13 +91,12 @@ struct ChunkCtrl {
   long long sum[kChThreads / 32];
   long long total, first, last;
   ChunkSegment start;
-  ChunkWalk walk[13];
+  ChunkWalk walk[kChThreads / 32];
 };
 
 template <int D>
 constexpr int chunk_smem_bytes() {
-  return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes +
-         4 * ChunkGeo<D>::kStages * ChunkGeo<D>::kStageBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
+  return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
 }
 
 // Tiles that the 256 rows of a block need: up to the last key that its last row sees.
@@ -215,38 +219,6 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   return n;
 }
 
-// P = 2^(s c - m) of one row in f16 over its S columns, published in two parts of 64 keys; returns
-// the row's sum.  MASKED: scores of -inf give 0 whatever c is.
-template <bool MASKED>
-__device__ __forceinline__ float chunk_publish_p(float (&s)[128], float c, float m, uint32_t t_s, uint32_t bar,
-                                                 int lane) {
-  float2 sum[4] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-  const float2 c2 = f32x2(c, c), nm = f32x2(-m, -m);
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    uint32_t r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int k = 64 * part + 2 * i;
-      const float2 x = fma_f32x2(f32x2(s[k], s[k + 1]), c2, nm);
-      float p0 = ex2_mufu(x.x), p1 = ex2_mufu(x.y);
-      if constexpr (MASKED) {
-        p0 = s[k] == -INFINITY ? 0.f : p0;
-        p1 = s[k + 1] == -INFINITY ? 0.f : p1;
-      }
-      sum[i % 4] = add_f32x2(sum[i % 4], f32x2(p0, p1));
-      r[i] = pack_f16x2(p0, p1);
-    }
-    tmem_st32(t_s + 32 * part, r);
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar + 8 * part);
-  }
-  sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
-  return sum[0].x + sum[0].y;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args a) {
   using G = ChunkGeo<D>;
@@ -255,8 +227,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
                                                    ~static_cast<uintptr_t>(1023));
   uint8_t* const s_q = smem;
   uint8_t* const s_ring = smem + 2 * G::kTileBytes;
-  uint8_t* const s_raw = s_ring + G::kSlots * G::kTileBytes;
-  ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_raw + 4 * G::kStages * G::kStageBytes);
+  ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_ring + G::kSlots * G::kTileBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -273,7 +244,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       ctl->last = last;
     }
   }
-  if (warp == 12) {
+  if (warp == kChMmaWarp) {
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish();
   }
@@ -301,154 +272,92 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
     return __all_sync(0xffffffffu, wait_phase(smem_u32(&bar), parity & 1u, abort_flag, a.status));
   };
 
-  if (warp >= 12) {
-    regs_dec<kChMmaRegs>();
-    if (warp == 12) {
-      // ========================================================== MMA issuer
-      ChunkWalk* const w = &ctl->walk[12];
-      walk_begin(a, w, ctl);
-      int t = 0;  // K's number in the ring (V: t + 1)
-      int steps[2] = {0, 0}, segs[2] = {0, 0};
-      const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
-      const uint64_t k_desc = smem_desc(smem_u32(s_ring), 16, 1024, kSwizzle128B);
-      const uint64_t v_desc = smem_desc(smem_u32(s_ring), 128 * 128, 1024, kSwizzle128B);
-      constexpr uint64_t kTile16 = G::kTileBytes >> 4;
-      bool ok = true;
-      auto issue_s = [&](int h, int tk) {
-        const uint64_t qd = q_desc + h * kTile16, kd = k_desc + (tk % G::kSlots) * kTile16;
-        if (elect_one()) {
-          mma_chain_ss_off<G::kKSteps, 0, G::s_off(1), G::s_off(2), G::s_off(3), G::s_off(4),
-                           G::s_off(5), G::s_off(6), G::s_off(7)>(tmem + h * 128, G::kIdescS, 0u, qd, kd);
-          tc_commit(smem_u32(&ctl->s_full[h]));
-        }
-        __syncwarp();
-      };
-      // P V of one key tile, then S of the next (which overwrites P): V, the next K and the first
-      // part of P have mostly come, so one probe looks for all three
-      auto step = [&](int h, bool begins, bool more) -> bool {
-        const int tv = t + 1, tk = more ? t + 2 : t + 1;
-        uint64_t &bv = ctl->kv_full[tv % G::kSlots], &bk = ctl->kv_full[tk % G::kSlots];
-        if (!__all_sync(0xffffffffu,
-                        mbar_try_wait3(smem_u32(&bv), (tv / G::kSlots) & 1, smem_u32(&bk), (tk / G::kSlots) & 1,
-                                       smem_u32(&ctl->p_full[h][0]), steps[h] & 1)))
-          if (!wait(bv, tv / G::kSlots) || !wait(bk, tk / G::kSlots) || !wait(ctl->p_full[h][0], steps[h])) return false;
-        const uint64_t vd = v_desc + (tv % G::kSlots) * kTile16;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (part == 1 && !wait(ctl->p_full[h][1], steps[h])) return false;
-          tc_fence_after();
-          if (elect_one())
-            mma_chain_ts_off<4, 0, G::kPvStep, 8, 16, 24, 32, 40, 48, 56>(
-                tmem + 256 + h * 128, G::kIdescPV, begins && part == 0 ? 0u : 1u, tmem + h * 128 + part * 32,
-                vd + part * 4 * G::kPvStep);
-          __syncwarp();
-        }
-        ++steps[h];
-        if (more) {
-          issue_s(h, tk);
-        } else {
-          if (elect_one()) tc_commit(smem_u32(&ctl->o_full[h]));
-          __syncwarp();
-        }
-        return true;
-      };
-      do {
-        const bool two = walk_rows(a, w) > 128;
-        const int n = w->s.n;
-        ok = wait(ctl->q_full[0], segs[0]++);
-        if (two) ok = ok && wait(ctl->q_full[1], segs[1]++);
-        ok = ok && wait(ctl->kv_full[t % G::kSlots], t / G::kSlots);
-        if (!ok) break;
-        tc_fence_after();
-        issue_s(0, t);
-        if (two) issue_s(1, t);
-        for (int j = 0; j < n && ok; ++j, t += 2) {
-          ok = step(0, j == 0, j + 1 < n);
-          if (two) ok = ok && step(1, j == 0, j + 1 < n);
-        }
-      } while (ok && walk_next(a, w));
-      // nothing this warp issued may still run when the TMEM is released
-      __syncwarp();
-      if (elect_one()) tc_commit(smem_u32(&ctl->drain));
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+  if (warp == kChMmaWarp) {
+    // ============================================================ MMA issuer
+    ChunkWalk* const w = &ctl->walk[kChMmaWarp];
+    walk_begin(a, w, ctl);
+    int t = 0;  // K's number in the ring (V: t + 1)
+    int steps[2] = {0, 0}, segs[2] = {0, 0};
+    const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
+    const uint64_t k_desc = smem_desc(smem_u32(s_ring), 16, 1024, kSwizzle128B);
+    const uint64_t v_desc = smem_desc(smem_u32(s_ring), 128 * 128, 1024, kSwizzle128B);
+    constexpr uint64_t kTile16 = G::kTileBytes >> 4;
+    bool ok = true;
+    auto issue_s = [&](int h, int tk) {
+      const uint64_t qd = q_desc + h * kTile16, kd = k_desc + (tk % G::kSlots) * kTile16;
+      if (elect_one()) {
+        mma_chain_ss_off<G::kKSteps, 0, G::s_off(1), G::s_off(2), G::s_off(3), G::s_off(4),
+                         G::s_off(5), G::s_off(6), G::s_off(7)>(tmem + h * 128, G::kIdescS, 0u, qd, kd);
+        tc_commit(smem_u32(&ctl->s_full[h]));
       }
+      __syncwarp();
+    };
+    // P V of one key tile, then S of the next (which overwrites P): V, the next K and the first
+    // part of P have mostly come, so one probe looks for all three
+    auto step = [&](int h, bool begins, bool more) -> bool {
+      const int tv = t + 1, tk = more ? t + 2 : t + 1;
+      uint64_t &bv = ctl->kv_full[tv % G::kSlots], &bk = ctl->kv_full[tk % G::kSlots];
+      if (!__all_sync(0xffffffffu,
+                      mbar_try_wait3(smem_u32(&bv), (tv / G::kSlots) & 1, smem_u32(&bk), (tk / G::kSlots) & 1,
+                                     smem_u32(&ctl->p_full[h][0]), steps[h] & 1)))
+        if (!wait(bv, tv / G::kSlots) || !wait(bk, tk / G::kSlots) || !wait(ctl->p_full[h][0], steps[h])) return false;
+      const uint64_t vd = v_desc + (tv % G::kSlots) * kTile16;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1 && !wait(ctl->p_full[h][1], steps[h])) return false;
+        tc_fence_after();
+        if (elect_one())
+          mma_chain_ts_off<4, 0, G::kPvStep, 8, 16, 24, 32, 40, 48, 56>(
+              tmem + 256 + h * 128, G::kIdescPV, begins && part == 0 ? 0u : 1u, tmem + h * 128 + part * 32,
+              vd + part * 4 * G::kPvStep);
+        __syncwarp();
+      }
+      ++steps[h];
+      if (more) {
+        issue_s(h, tk);
+      } else {
+        if (elect_one()) tc_commit(smem_u32(&ctl->o_full[h]));
+        __syncwarp();
+      }
+      return true;
+    };
+    do {
+      const bool two = walk_rows(a, w) > 128;
+      const int n = w->s.n;
+      ok = wait(ctl->q_full[0], segs[0]++);
+      if (two) ok = ok && wait(ctl->q_full[1], segs[1]++);
+      ok = ok && wait(ctl->kv_full[t % G::kSlots], t / G::kSlots);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(0, t);
+      if (two) issue_s(1, t);
+#pragma unroll 1
+      for (int i = 0; i < (two ? 2 * n : n) && ok; ++i) {  // one copy of the step's code
+        const int h = two ? i & 1 : 0, j = two ? i >> 1 : i;
+        ok = step(h, j == 0, j + 1 < n);
+        if (h == (two ? 1 : 0)) t += 2;
+      }
+    } while (ok && walk_next(a, w));
+    // nothing this warp issued may still run when the TMEM is released
+    __syncwarp();
+    if (elect_one()) tc_commit(smem_u32(&ctl->drain));
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
     }
   } else if (warp >= 8) {
     regs_dec<kChWidenRegs>();
     // ============================================================ widening the cache
-    // The warp's 32 keys of a tile: a lane takes 32 codes (16 bytes, two scales) of one row at a
-    // time, 4 (d = 128) or 2 lanes a row.
+    // The warp's 32 keys of a tile, or their values: a lane takes 32 codes (16 bytes, two scales) of
+    // one row at a time, 4 (d = 128) or 2 lanes a row.
     constexpr int kLanes = D / 32, kRowsIt = 32 / kLanes, kIt = 32 / kRowsIt;
     constexpr int kCode = D / 2, kScale = D / 16;
-    constexpr int kSc = 32 * kCode;  // in a stage: the scales
-    const int part = lane % kLanes, row_in = lane / kLanes, row_w = (warp - 8) * 32;
+    const bool values = warp >= 12;
+    const int part = lane % kLanes, row_in = lane / kLanes, row_w = warp % 4 * 32;
     const int page_rows = 1 << a.page_shift;
     const int block_bytes = kv4_block_bytes(page_rows, D);
     const unsigned page_bytes = static_cast<unsigned>(block_bytes) * 2u * static_cast<unsigned>(a.hk);
     ChunkWalk* const w = &ctl->walk[warp];
     walk_begin(a, w, ctl);
-    uint8_t* const raw = s_raw + (warp - 8) * G::kStages * G::kStageBytes;
-
-    // ---- loads: the keys of a tile, then the values; the page ids of the two 16-key groups come a
-    // tile ahead
-    int key = w->s.tile * kChKeys + row_w, tiles_left = w->s.n, keys = w->s.req.keys;
-    const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
-    const uint8_t* head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
-    int id[2];
-    auto fetch_ids = [&]() {
-      id[0] = key < keys ? __ldg(ids + (key >> a.page_shift)) : -1;
-      id[1] = id[0];
-      if (a.page_shift == 4) id[1] = key + 16 < keys ? __ldg(ids + (key >> 4) + 1) : -1;
-    };
-    int stage_in = 0;
-    bool loads_left = true, values_next = false;
-    // where the lane copies from: codes of the groups' first rows, and its 16 bytes of scales
-    const uint8_t *codes[2], *scales_from = nullptr;
-    uint32_t there = 0;  // bit g: the group's page exists
-    const int sc_group = lane / kScale % 2;
-    auto load = [&]() {
-      if (loads_left || values_next) {
-        if (!values_next) {
-          there = 0;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const bool ok = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
-            const int row = (key + 16 * g) & (page_rows - 1);
-            const uint8_t* b = head + static_cast<size_t>(ok ? static_cast<unsigned>(id[g]) : 0u) * page_bytes;
-            codes[g] = b + row * kCode + lane * 16;
-            if (sc_group == g) scales_from = b + page_rows * kCode + row * kScale + lane % kScale * 16;
-            there |= (ok ? 1u : 0u) << g;
-          }
-          if (--tiles_left > 0) {
-            key += kChKeys;
-          } else {
-            loads_left = walk_next(a, w);
-            key = w->s.tile * kChKeys + row_w;
-            tiles_left = w->s.n;
-            keys = w->s.req.keys;
-            ids = a.table + static_cast<size_t>(w->s.r) * a.width;
-            head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
-          }
-          if (loads_left) fetch_ids();
-        }
-        const uint32_t dst = smem_u32(raw) + stage_in * G::kStageBytes;
-        const int from = values_next ? block_bytes : 0;
-        constexpr int kPer = 16 * kCode / 512;
-        // a page that is not there: copies of zero bytes, which write zeros and read nothing
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int p = 0; p < kPer; ++p)
-            cp_async16(dst + g * 16 * kCode + p * 512 + lane * 16, codes[g] + from + p * 512, there >> g & 1u ? 16u : 0u);
-        if (lane < 2 * kScale) cp_async16(dst + kSc + lane * 16, scales_from + from, there >> sc_group & 1u ? 16u : 0u);
-        stage_in = stage_in + 1 == G::kStages ? 0 : stage_in + 1;
-        values_next = !values_next;
-      }
-      cp_async_commit();
-    };
-    const long long halves = 2 * (ctl->last - ctl->first);
-    fetch_ids();
 
     // Chunk g of a row (8 values, 16 bytes) lies at chunk g ^ (row % 8) of its 128-byte line.  Lanes of
     // the second half of a row take their codes' halves in the other order: else they would store
@@ -461,56 +370,91 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       const int g = (part * 4 + (i ^ (part & 2))) & 7;
       store_at[i] = smem_u32(s_ring) + (part / 2) * (128 * 128) + (row_w + row_in) * 128 + ((g ^ (row_in & 7)) << 4);
     }
-    static_assert(kRowsIt % 8 == 0, "rows of later iterations keep their swizzle");
-    // One copy of this code for keys and values, and of the loads for the first stages and the later
-    // ones: the roles' loops together have to stay in the instruction cache.
-    int stage = 0;
-#pragma unroll 1
-    for (long long i = -G::kStages; i < halves; ++i) {
-      if (i >= 0) {
-        const bool values = i & 1;
-        const int slot = static_cast<int>(i % G::kSlots);
-        if (i >= G::kSlots && !wait(ctl->kv_empty[slot], static_cast<uint32_t>(i / G::kSlots - 1))) break;
-        if (!values) {
-          cp_async_wait<G::kStages - 2>();  // the keys and the values
-          __syncwarp();
+    static_assert(kRowsIt % 8 == 0 && kIt % 2 == 0, "iterations keep the swizzle and a 16-key group");
+
+    // ---- loads, a tile ahead; the page ids of the two 16-key groups come a tile before them
+    int key = w->s.tile * kChKeys + row_w, tiles_left = w->s.n, keys = w->s.req.keys;
+    const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+    const uint8_t* head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
+    int id[2];
+    auto fetch_ids = [&]() {
+      id[0] = key < keys ? __ldg(ids + (key >> a.page_shift)) : -1;
+      id[1] = id[0];
+      if (a.page_shift == 4) id[1] = key + 16 < keys ? __ldg(ids + (key >> 4) + 1) : -1;
+    };
+    uint2 c0[kIt], c1[kIt];
+    uint16_t sc[kIt], sc_values[kIt];
+    auto load = [&]() {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const bool ok = static_cast<unsigned>(id[g]) < static_cast<unsigned>(a.pages);
+        const int row = ((key + 16 * g) & (page_rows - 1)) + row_in;
+        const uint8_t* k = head + static_cast<size_t>(ok ? static_cast<unsigned>(id[g]) : 0u) * page_bytes;
+        const uint8_t* codes = k + (values ? block_bytes : 0) + row * kCode + part * 16;
+        const uint8_t* scales = k + page_rows * kCode + row * kScale + part * 2;
+#pragma unroll
+        for (int x = 0; x < kIt / 2; ++x) {
+          const int it = g * (kIt / 2) + x;
+          c0[it] = c1[it] = make_uint2(0u, 0u);
+          sc[it] = sc_values[it] = 0;
+          if (ok) {  // (a page that is not there: zeros, and the scores are masked)
+            c0[it] = __ldg(reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + swap));
+            c1[it] = __ldg(reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + (swap ^ 8)));
+            sc[it] = __ldg(reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + (values ? block_bytes : 0)));
+            if (!values) sc_values[it] = __ldg(reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + block_bytes));
+          }
         }
-        const uint8_t* st = raw + stage * G::kStageBytes;
-        stage = stage + 1 == G::kStages ? 0 : stage + 1;
-        const uint8_t* st_values = values ? st : raw + stage * G::kStageBytes;
-        // A value vector that is not a number (NaN scales) makes its key's scores NaN and is zero
-        // itself: rows that do not see the key multiply it by zero.  max takes NaN to the other
-        // operand, 0; the values' scale times 0 is 0 or NaN.
-        const uint32_t to = slot * G::kTileBytes;
+      }
+    };
+    const long long tiles = ctl->last - ctl->first;
+    fetch_ids();
+    // One copy of the code for the first loads and the later ones: the roles' loops together have to
+    // stay in the instruction cache (a second copy of loads and conversions cost 8 %).
+#pragma unroll 1
+    for (long long i = -1; i < tiles; ++i) {
+      if (i >= 0) {
+        const long long t = 2 * i + (values ? 1 : 0);
+        const int slot = static_cast<int>(t % G::kSlots);
+        if (t >= G::kSlots && !wait(ctl->kv_empty[slot], static_cast<uint32_t>(t / G::kSlots - 1))) break;
 #pragma unroll
         for (int it = 0; it < kIt; ++it) {
-          const uint8_t* p = st + (it * kRowsIt + row_in) * kCode + part * 16;
-          const int sc = kSc + (it * kRowsIt + row_in) * kScale + part * 2;
-          const uint2 c0 = *reinterpret_cast<const uint2*>(p + swap), c1 = *reinterpret_cast<const uint2*>(p + (swap ^ 8));
-          uint32_t scales = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + sc));
-          uint32_t v_scales = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st_values + sc));
+          // A value vector that is not a number (NaN scales) makes its key's scores NaN and is zero
+          // itself: rows that do not see the key multiply it by zero.  max takes NaN to its other
+          // operand, 0; the values' scale times 0 is 0 or NaN.
+          uint32_t scales = e4m3x2_to_f16x2(sc[it]);
           if (values)
             scales = max_f16x2(scales, 0u);
           else
-            scales = fma_f16x2(v_scales, 0u, scales);
+            scales = fma_f16x2(e4m3x2_to_f16x2(sc_values[it]), 0u, scales);
           scales = __byte_perm(scales, 0u, scale_sel);
-          const uint32_t word[4] = {c0.x, c0.y, c1.x, c1.y};
+          const uint32_t word[4] = {c0[it].x, c0[it].y, c1[it].x, c1[it].y};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t h[4];
             unpack_e2m1x8(word[x], h);
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = x & 2 ? mul_f16x2_hi(h[e], scales) : mul_f16x2_lo(h[e], scales);
-            st_shared_v4(store_at[x] + to + it * kRowsIt * 128, h[0], h[1], h[2], h[3]);
+            st_shared_v4(store_at[x] + slot * G::kTileBytes + it * kRowsIt * 128, h[0], h[1], h[2], h[3]);
           }
         }
         fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[slot]));
       }
-      load();
+      if (i + 1 < tiles) {
+        load();
+        if (--tiles_left > 0) {
+          key += kChKeys;
+        } else if (walk_next(a, w)) {
+          key = w->s.tile * kChKeys + row_w;
+          tiles_left = w->s.n;
+          keys = w->s.req.keys;
+          ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+          head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
+        }
+        if (i + 2 < tiles) fetch_ids();
+      }
     }
-    cp_async_wait<0>();
   } else {
     regs_inc<kChSoftmaxRegs>();
     // ============================================================ softmax, queries, outputs
@@ -543,30 +487,32 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           const int qi = urow / a.group, qg = urow - qi * a.group;
           sees = w->s.req.keys;
           if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.q_len + qi + 1));
-          // ---- the query row, scaled into [1, 2)
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + static_cast<long long>(w->s.req.q0 + qi) * a.q_row +
-              static_cast<long long>(w->s.head * a.group + qg) * a.q_head);
-          uint4 raw[D / 8];
-          float amax = 0.f;
+          // ---- the warp's 32 query rows, scaled into [1, 2): kRow lanes take 16 bytes each of a row
+          constexpr int kRow = D / 8, kRowsIt = 32 / kRow;
+          const long long mine = live ? static_cast<long long>(w->s.req.q0 + qi) * a.q_row +
+                                            static_cast<long long>(w->s.head * a.group + qg) * a.q_head
+                                      : -1;
+          c = 0.f;
+#pragma unroll 4
+          for (int it = 0; it < 32 / kRowsIt; ++it) {
+            const int r = it * kRowsIt + lane / kRow, piece = lane % kRow;
+            const long long at = __shfl_sync(0xffffffffu, mine, r);
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (at >= 0) raw = __ldg(reinterpret_cast<const uint4*>(a.q + at) + piece);
+            float f[8], amax = 0.f;
+            unpack_bf16x8(raw, f);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            float f[8];
-            unpack_bf16x8(raw[i], f);
+            for (int e = 0; e < 8; e += 2) amax = max3f(amax, fabsf(f[e]), fabsf(f[e + 1]));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-          }
-          uint32_t ex = __float_as_uint(amax) >> 23;
-          ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
-          const float down = __uint_as_float((254u - ex) << 23);
-          c = a.c * __uint_as_float(ex << 23);
-          const uint32_t q_row = smem_u32(s_q) + h * G::kTileBytes + r_tile * 128;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            float f[8];
-            unpack_bf16x8(raw[i], f);
-            st_shared_v4(q_row + (i / 8) * (128 * 128) + (((i & 7) ^ (r_tile & 7)) << 4),
+            for (int o = 1; o < kRow; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            uint32_t ex = __float_as_uint(amax) >> 23;
+            ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
+            const float down = __uint_as_float((254u - ex) << 23), up = a.c * __uint_as_float(ex << 23);
+            const float theirs = __shfl_sync(0xffffffffu, up, (lane & (kRowsIt - 1)) * kRow);
+            if (lane / kRowsIt == it) c = theirs;  // the row of lane it * kRowsIt + ... is its own
+            const int row_in = warp % 4 * 32 + r;
+            st_shared_v4(smem_u32(s_q) + h * G::kTileBytes + row_in * 128 + (piece / 8) * (128 * 128) +
+                             (((piece & 7) ^ (row_in & 7)) << 4),
                          pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
                          pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
           }
@@ -595,54 +541,63 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
             mbar_arrive(smem_u32(&ctl->kv_empty[t % G::kSlots]));
             if (j > 0) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
           }
-          float s[128];
-          {
-            uint32_t r[4][32];
-#pragma unroll
-            for (int cb = 0; cb < 4; ++cb) tmem_ld32(t_s + cb * 32, r[cb]);
+          // Twice over the row's scores, 64 at a time: the maximum, then the probabilities.  (All 128
+          // in registers as one unrolled body did not fit the instruction cache beside the other
+          // roles' and left no registers for a second group of widening warps; 16 at a time, loaded one
+          // step ahead, took 2500 cycles a tile.)  Masked and not are two copies of the code: selects
+          // for a mask that mostly leaves all cost a third of the instructions.
+          const bool masked = holes || __any_sync(0xffffffffu, lim < kChKeys);
+          // bit i: the row sees key i of 16-key group g
+          auto seen16 = [&](int g) {
+            const int here = lim - 16 * g;
+            unsigned seen = here >= 16 ? 0xffffu : here <= 0 ? 0u : (1u << here) - 1u;
+            if (holes) {
+              const int key = (w->s.tile + j) * kChKeys + 16 * g;
+              const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+              if (key < w->s.req.keys &&
+                  static_cast<unsigned>(__ldg(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages))
+                seen = 0u;
+            }
+            return seen;
+          };
+          auto scores = [&](auto with_mask, int half, float (&s)[64]) {
+            uint32_t r[2][32];
+            tmem_ld32(t_s + half * 64, r[0]);
+            tmem_ld32(t_s + half * 64 + 32, r[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
+            for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(r[i / 32][i % 32]);
+            if constexpr (with_mask.value) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[cb * 32 + i] = __uint_as_float(r[cb][i]);
-          }
-          const bool masked = holes || __any_sync(0xffffffffu, lim < kChKeys);
-          if (masked) {
+              for (int g = 0; g < 4; ++g) {
+                const unsigned seen = seen16(4 * half + g);
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= lim) s[i] = -INFINITY;
-            if (holes) {
-              const int key0 = (w->s.tile + j) * kChKeys;
-              const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
-#pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                const int key = key0 + 16 * g;
-                if (key < w->s.req.keys &&
-                    static_cast<unsigned>(__ldg(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages)) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) s[16 * g + i] = -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i)
+                  if (!(seen >> i & 1u)) s[16 * g + i] = -INFINITY;
               }
             }
-          }
-          float mp[8];
+          };
+          auto maximum = [&](auto with_mask) {
+            float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              float s[64];
+              scores(with_mask, half, s);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mp[k] = fmaxf(s[2 * k], s[2 * k + 1]);
-#pragma unroll
-          for (int i = 16; i < 128; i += 2) mp[(i / 2) % 8] = max3f(mp[(i / 2) % 8], s[i], s[i + 1]);
-#pragma unroll
-          for (int k = 4; k >= 1; k /= 2)
-#pragma unroll
-            for (int i = 0; i < k; ++i) mp[i] = fmaxf(mp[i], mp[i + k]);
+              for (int i = 0; i < 64; i += 2) mp[i / 2 % 4] = max3f(mp[i / 2 % 4], s[i], s[i + 1]);
+            }
+            return fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+          };
+          float top = masked ? maximum(ChunkMasked<true>{}) : maximum(ChunkMasked<false>{});
           // the reference m: kDecBelow under the maximum, moved when that grew by 8 since
-          const float top = mp[0] * c;
+          top *= c;
           if (j == 0) {
             m = fmaxf(top - kDecBelow, m);
           } else if (__any_sync(0xffffffffu, top > m + kDecLazy)) {
             const float m_new = fmaxf(top - kDecBelow, m);
             const float alpha = ex2_mufu(m - m_new);
             uint32_t r[32];
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < D / 32; ++cb) {
               tmem_ld32(t_o + cb * 32, r);
               tmem_ld_wait();
@@ -657,8 +612,36 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
             l *= alpha;
             m = m_new;
           }
-          l += masked ? chunk_publish_p<true>(s, c, m, t_s, smem_u32(&ctl->p_full[h][0]), lane)
-                      : chunk_publish_p<false>(s, c, m, t_s, smem_u32(&ctl->p_full[h][0]), lane);
+          // P = 2^(s c - m) in f16 over S (columns already read), published in two parts of 64 keys
+          auto publish = [&](auto with_mask) {
+            float2 sum[4] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+            const float2 c2 = f32x2(c, c), nm = f32x2(-m, -m);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              float s[64];
+              scores(with_mask, half, s);
+              uint32_t p[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 x = fma_f32x2(f32x2(s[2 * i], s[2 * i + 1]), c2, nm);
+                float p0 = ex2_mufu(x.x), p1 = ex2_mufu(x.y);
+                if constexpr (with_mask.value) {  // whatever c is
+                  p0 = s[2 * i] == -INFINITY ? 0.f : p0;
+                  p1 = s[2 * i + 1] == -INFINITY ? 0.f : p1;
+                }
+                sum[i % 4] = add_f32x2(sum[i % 4], f32x2(p0, p1));
+                p[i] = pack_f16x2(p0, p1);
+              }
+              tmem_st32(t_s + 32 * half, p);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[h][half]));
+            }
+            sum[0] = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+            return sum[0].x + sum[0].y;
+          };
+          l += masked ? publish(ChunkMasked<true>{}) : publish(ChunkMasked<false>{});
         }
         if (!ok) break;
         // ---- O and the log-sum-exp, or the unit's partial sums
@@ -672,26 +655,49 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         const float inv = l == 0.f ? 0.f : a.v_descale / l;
         const size_t at = static_cast<size_t>(w->s.req.q0 + qi) * a.hq + w->s.head * a.group + qg;
         const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (unit_no > 0 ? 1 : 0)) * kChRows + row;
+        // Through shared memory, 128 bytes of each row at a time (64 bf16 columns, or 32 of a partial
+        // sum), so that whole lines go to memory; the buffer is where the warp's own query rows lay, which
+        // no MMA reads any more.  (Each lane storing its own row cost 3.4 us a unit.)
+        const uint32_t stage_row = smem_u32(s_q) + h * G::kTileBytes + r_tile * 128;
+        const uint8_t* const stage = s_q + h * G::kTileBytes + warp % 4 * 4096;
+        const long long out_at = !live ? -1 : static_cast<long long>(whole ? at : slot);
+        const int cols = whole ? 64 : 32;
+#pragma unroll 1
+        for (int col = 0; col < D; col += cols) {
+#pragma unroll 1
+          for (int cb = 0; cb < cols; cb += 32) {
+            uint32_t r[32];
+            tmem_ld32(t_o + col + cb, r);
+            tmem_ld_wait();
+            if (whole) {
 #pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t r[32];
-          tmem_ld32(t_o + cb * 32, r);
-          tmem_ld_wait();
-          if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + cb * 32);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t p[4];
+                for (int e = 0; e < 4; ++e)
+                  p[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv, __uint_as_float(r[8 * i + 2 * e + 1]) * inv);
+                st_shared_v4(stage_row + (((cb / 8 + i) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+              }
+            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                p[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv, __uint_as_float(r[8 * i + 2 * e + 1]) * inv);
-              dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
+              for (int i = 0; i < 8; ++i)
+                st_shared_v4(stage_row + ((i ^ (lane & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
             }
-          } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * D + cb * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
           }
+          __syncwarp();
+#pragma unroll 2
+          for (int it = 0; it < 8; ++it) {  // four rows at a time, eight lanes a row
+            const int r = it * 4 + lane / 8, piece = lane % 8;
+            const long long to = __shfl_sync(0xffffffffu, out_at, r);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+            if (to >= 0) {
+              if (whole)
+                reinterpret_cast<uint4*>(a.o + to * D + col)[piece] = y;
+              else
+                reinterpret_cast<uint4*>(a.part_o + to * D + col)[piece] = y;
+            }
+          }
+          __syncwarp();
         }
         if (live && whole) a.lse[at] = l == 0.f ? -INFINITY : m * kLn2F + logf(l);
         if (live && !whole) a.part_ml[slot] = make_float2(m, l);
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
   }
 
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kChMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -184,12 +184,11 @@ int launch_chunk(Kv4Args& a, void* workspace, cudaStream_t s) {
   static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "shared memory per CTA");
   static std::atomic<uint64_t> done{0};
   auto kern = kv4_chunk_kernel<D>;
-  if (!(done.load(std::memory_order_acquire))) {
-    // the warpgroups redistribute 512 x 128 registers: a build with fewer at launch would wait
-    // forever for the rest
+  if (!done.load(std::memory_order_acquire)) {
+    // a build with fewer registers at launch would wait forever for the ones to redistribute
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
-    if (attr.numRegs * 4 < 2 * kChSoftmaxRegs + kChWidenRegs + kChMmaRegs) return FA_ERR_UNSUPPORTED;
+    if (attr.numRegs < kChLaunchRegs) return FA_ERR_UNSUPPORTED;
   }
   if (int rc = opt_in_smem(kern, smem, done)) return rc;
   kern<<<n, kChThreads, smem, s>>>(a);
