@@ -23,9 +23,9 @@
 // Queries are scaled by a power of two per row into [1, 2) before they become f16, so the conversion
 // keeps bf16's 8 bits down to 2^-17 of the row's largest value.
 //
-// Split.  The work of all requests is one line of tiles (128 or 256 keys of one key head, for one
+// Split.  The work of all requests is one line of tiles (64 to 256 keys of one key head, for one
 // block of query rows); CTA i of n takes the i-th n-th of it, so ragged lengths balance by themselves and a
-// single long request fills the GPU.  In a tile each warp takes 32 keys (64 at head dim 64), in its own ring of
+// single long request fills the GPU.  In a tile each warp takes 16 to 64 keys, in its own ring of
 // cp.async stages, with its own softmax state: warps meet only at the end of a unit (one key head of
 // one block of rows).  A unit that crosses CTAs leaves partial sums (O, max, sum) in the workspace,
 // which a second kernel merges in a fixed order.
@@ -43,14 +43,15 @@ namespace exattn {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-// 16-key groups of a strip, one warp's share of a tile
-template <int D>
-__host__ __device__ constexpr int dec_groups() { return D == 128 ? 2 : 4; }
-template <int D>
-__host__ __device__ constexpr int dec_strip() { return 16 * dec_groups<D>(); }
-template <int D>
-__host__ __device__ constexpr int dec_tile() { return kDecWarps * dec_strip<D>(); }
-constexpr int kDecStages = 2;
+// 16-key groups of a strip, one warp's share of a tile: 32 keys at head dim 128, 64 at 64 (half the
+// work a key), 16 beside the 128 accumulators of 32 rows at 128 (with 32 keys registers were spilled).
+template <int D, int R>
+__host__ __device__ constexpr int dec_groups() { return D == 64 ? 4 : R == 32 ? 1 : 2; }
+template <int D, int R>
+__host__ __device__ constexpr int dec_strip() { return 16 * dec_groups<D, R>(); }
+template <int D, int R>
+__host__ __device__ constexpr int dec_tile() { return kDecWarps * dec_strip<D, R>(); }
+constexpr int kDecStages = 2;  // (3: no faster)
 constexpr float kLn2F = 0.6931471805599453f;
 // The reference m of a row's probabilities 2^(x - m) is set kDecBelow under the running maximum and
 // O and l are rescaled only when the maximum has grown by more than 8 (log2) since: P then lies
@@ -110,9 +111,9 @@ template <int R>
 __device__ __forceinline__ int kv4_blocks(const Kv4Args& a, const ReqShape& s) {
   return static_cast<int>((static_cast<long long>(s.q_len) * a.group + R - 1) / R);
 }
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ int kv4_tiles(const ReqShape& s) {
-  return max(1, (s.keys - 1) / dec_tile<D>() + 1);
+  return max(1, (s.keys - 1) / dec_tile<D, R>() + 1);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -201,7 +202,7 @@ __device__ __forceinline__ bool cursor_next(const Kv4Args& a, TileCursor& c) {
   while (++c.r < a.b) {
     const ReqShape s = kv4_request(a, c.r);
     c.blocks = kv4_blocks<R>(a, s);
-    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
+    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D, R>(s);
     c.req = s;
     if (c.blocks > 0) break;
   }
@@ -220,7 +221,7 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
     if (r >= a.b) return 0;
     const ReqShape s = kv4_request(a, r);
     c.blocks = kv4_blocks<R>(a, s);
-    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D>(s);
+    c.tiles = a.whole_tiles ? a.whole_tiles : kv4_tiles<D, R>(s);
     c.req = s;
     return static_cast<long long>(c.blocks) * a.hk * c.tiles;
   };
@@ -278,12 +279,12 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
   return n;
 }
 
-template <int D>
-__host__ __device__ constexpr int dec_strip_bytes() { return dec_strip<D>() * (D + D / 8); }
+template <int D, int R>
+__host__ __device__ constexpr int dec_strip_bytes() { return dec_strip<D, R>() * (D + D / 8); }
 
 template <int D, int NT>
 __host__ __device__ constexpr int dec_smem_bytes() {
-  return kDecWarps * kDecStages * dec_strip_bytes<D>() + kDecWarps * (D / 16) * NT * 32 * 16 +
+  return kDecWarps * kDecStages * dec_strip_bytes<D, 8 * NT>() + kDecWarps * (D / 16) * NT * 32 * 16 +
          NT * (D / 32) * 32 * 16;
 }
 
@@ -295,19 +296,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   constexpr int KW = D / 32;           // code words of a lane's share of a key
   constexpr int VW = D / 64;           // code words of a lane's share of a value
   constexpr int kCode = D / 2, kScale = D / 16;  // bytes of a row's codes and scales
-  constexpr int TG = dec_groups<D>(), kStrip = dec_strip<D>();
+  constexpr int TG = dec_groups<D, R>(), kStrip = dec_strip<D, R>();
   constexpr int kKs = kStrip * kCode, kV = kKs + kStrip * kScale, kVs = kV + kKs;
   constexpr unsigned kAll = (1u << TG) - 1;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ long long s_sum[kDecWarps];
   __shared__ TileCursor s_cur;
-  __shared__ float s_m[kDecWarps][R], s_l[kDecWarps][R], s_c[R];
+  __shared__ float s_m[kDecWarps][R], s_l[kDecWarps][R];
+  __shared__ __align__(8) float s_c[R];  // factors of the rows' scores
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g8 = lane / 4, t4 = lane % 4;
-  uint8_t* const ring = dec_smem + warp * (kDecStages * dec_strip_bytes<D>());
+  uint8_t* const ring = dec_smem + warp * (kDecStages * dec_strip_bytes<D, R>());
   // the warps' sums at the end of a unit, and its queries as the products' operand
-  float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D>());
+  float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D, R>());
   uint4* const s_q = reinterpret_cast<uint4*>(area + kDecWarps * MT * NT * 32);  // [nt][w][lane]
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -325,9 +327,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   // ---- loads: the strip's 16-key groups, one page id each, fetched a step ahead
   const unsigned page_bytes = static_cast<unsigned>(block_bytes) * 2u * static_cast<unsigned>(a.hk);
   constexpr int kPer = 16 * kCode / 512;  // 16-byte copies of a lane for one group's codes
-  // the lane's copy of the strip's scales: kScale copies for each of (K, V) x groups, 32 in all
-  static_assert(2 * TG * kScale == 32, "one copy of scales a lane");
-  const int sc_group = lane / kScale % TG, sc_kv = lane / (kScale * TG);
+  // the lane's copy of the strip's scales: kScale copies for each of (K, V) x groups, 32 or 16 in all
+  static_assert(2 * TG * kScale <= 32, "at most one copy of scales a lane");
+  const int sc_group = lane / kScale % TG, sc_kv = lane / (kScale * TG) & 1;
   const int sc_dst = (sc_kv ? kVs : kKs) + sc_group * 16 * kScale + (lane % kScale) * 16;
   const uint32_t ring_u32 = smem_u32(ring);
   const uint8_t *code_base, *scale_base;  // of the head, with the lane's offset
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   int ld_left = steps;
   unsigned seen = 0;  // TG bits a strip in flight: the group's page exists
   auto fetch_ids = [&]() {
-    const int key0 = ld.tile * dec_tile<D>() + warp * kStrip;
+    const int key0 = ld.tile * dec_tile<D, R>() + warp * kStrip;
 #pragma unroll
     for (int g = 0; g < TG; ++g) {
       const int key = key0 + 16 * g;
@@ -369,8 +371,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   auto issue = [&](int stage) {
     seen <<= TG;
     if (ld_left > 0) {
-      const uint32_t dst = ring_u32 + stage * dec_strip_bytes<D>();
-      const int key0 = ld.tile * dec_tile<D>() + warp * kStrip;
+      const uint32_t dst = ring_u32 + stage * dec_strip_bytes<D, R>();
+      const int key0 = ld.tile * dec_tile<D, R>() + warp * kStrip;
       uint32_t sc_n = 0;
       size_t sc_at = 0;
 #pragma unroll
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         }
         seen |= (ok ? 1u : 0u) << g;
       }
-      cp_async16(dst + sc_dst, scale_base + sc_at, sc_n);
+      if (2 * TG * kScale == 32 || lane < 2 * TG * kScale) cp_async16(dst + sc_dst, scale_base + sc_at, sc_n);
       if (--ld_left > 0) {
         if (cursor_next<D, R>(a, ld)) {
           set_head();
@@ -413,20 +415,23 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   for (int s = 0; s < kDecStages; ++s) issue(s);
 
   // ---- state of the unit at hand
-  ReqShape req;
-  float cs[NT][2];       // factor of each S^T column (query row)
-  int lim[NT][2];        // keys it sees
-  int min_lim = 0, max_lim = 0;
+  int min_lim = 0, max_lim = 0;  // fewest and most keys that a row of the unit sees
   float m[NT][2], l[NT][2], o[MT][NT][4];
   bool fresh = true, whole_start = cur.tile == 0;
   int unit_no = 0;
   int4 merge = make_int4(-1, 0, 0, 0);
 
   int stage = 0;
+  // keys that row `row` of the unit sees (a padding row: all)
+  auto row_keys = [&](int row) {
+    const int at = cur.block * R + row;
+    const int behind = a.causal && at < cur.req.q_len * a.group ? cur.req.q_len - at / a.group - 1 : 0;
+    return max(0, cur.req.keys - behind);
+  };
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      req = cur.req;
+      const ReqShape req = cur.req;
       const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
       // Warp nt turns eight rows into the operand for all warps: held in registers by each warp they
       // would cost 16 registers (of 128) per eight rows, and four conversions.
@@ -470,13 +475,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          cs[nt][cc] = s_c[nt * 8 + 2 * t4 + cc];
-          const int crow = row0 + nt * 8 + 2 * t4 + cc;
-          int k = req.keys;
-          if (a.causal && crow < rows) k = min(k, max(0, req.keys - req.q_len + crow / a.group + 1));
-          lim[nt][cc] = k;
+          const int row = nt * 8 + 2 * t4 + cc, k = row_keys(row);
           min_lim = min(min_lim, k);
-          if (crow < rows) max_lim = max(max_lim, k);
+          if (row0 + row < rows) max_lim = max(max_lim, k);
           m[nt][cc] = kDecNone;
           l[nt][cc] = 0.f;
         }
@@ -496,10 +497,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 
     cp_async_wait<kDecStages - 1>();
     __syncwarp();
-    const int key0 = cur.tile * dec_tile<D>() + warp * kStrip;
+    const int key0 = cur.tile * dec_tile<D, R>() + warp * kStrip;
     const unsigned have = (seen >> (TG * (kDecStages - 1))) & kAll;
     if (key0 < max_lim && have) {
-      const uint8_t* const st = ring + stage * dec_strip_bytes<D>();
+      const uint8_t* const st = ring + stage * dec_strip_bytes<D, R>();
       const bool full = key0 + kStrip <= min_lim && have == kAll;
       float x[TG][NT][4];
       // ---- S^T = K Q^T
@@ -544,7 +545,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            const float2 y = mul_f32x2(f32x2(x[tg][nt][e], x[tg][nt][e + 1]), f32x2(cs[nt][0], cs[nt][1]));
+            const float2 y = mul_f32x2(f32x2(x[tg][nt][e], x[tg][nt][e + 1]),
+                                       *reinterpret_cast<const float2*>(&s_c[nt * 8 + 2 * t4]));
             x[tg][nt][e] = y.x;
             x[tg][nt][e + 1] = y.y;
           }
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = tg * 16 + kv4_perm(2 * t4 + (e & 1)) + 8 * (e >> 1);
-            if (key0 + tok >= req.keys || !((have >> tg) & 1u)) b[tg][e] = 0u;
+            if (key0 + tok >= cur.req.keys || !((have >> tg) & 1u)) b[tg][e] = 0u;
           }
       }
 #pragma unroll
@@ -582,19 +584,28 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       const bool poisoned = __any_sync(0xffffffffu, any_nan_f16x2(sum_vs));
 
       if (!full || poisoned) {
+        bool nan[TG][2];
+#pragma unroll
+        for (int tg = 0; tg < TG; ++tg)
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr)
+            nan[tg][hr] = (st[kVs + (tg * 16 + kv4_perm(g8) + 8 * hr) * kScale] & 0x7fu) == 0x7fu;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int sees = row_keys(nt * 8 + 2 * t4 + cc) - key0;
+#pragma unroll
+            for (int tg = 0; tg < TG; ++tg)
+#pragma unroll
+              for (int hr = 0; hr < 2; ++hr) {
+                float& y = x[tg][nt][2 * hr + cc];
+                if (nan[tg][hr]) y = __uint_as_float(0x7fffffffu);
+                if (!((have >> tg) & 1u) || tg * 16 + kv4_perm(g8) + 8 * hr >= sees) y = -INFINITY;
+              }
+          }
 #pragma unroll
         for (int tg = 0; tg < TG; ++tg) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = tg * 16 + kv4_perm(g8) + 8 * (e >> 1);
-            const bool gone = !((have >> tg) & 1u);
-            const bool nan = (st[kVs + tok * kScale] & 0x7fu) == 0x7fu;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (nan) x[tg][nt][e] = __uint_as_float(0x7fffffffu);
-              if (gone || key0 + tok >= lim[nt][e & 1]) x[tg][nt][e] = -INFINITY;
-            }
-          }
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
             const float2 f = f16x2_to_f32x2(vs[tg][pr]);
@@ -715,6 +726,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       __syncthreads();  // (the one at the next unit's start keeps its sums out until all have read these)
       // Each warp adds up a quarter of the 16-dim tiles: the lanes' own places of all four warps.
       const bool complete = unit_ends && whole_start;
+      const ReqShape req = cur.req;
       const int head = cur.head, row0 = cur.block * R, rows = req.q_len * a.group;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0);
       constexpr int kMine = MT / kDecWarps;

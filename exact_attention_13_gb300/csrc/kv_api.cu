@@ -129,8 +129,8 @@ size_t kv4_workspace(int nt, int d) {
 // Tables of at most this many tiles: units are not split, which saves the merge kernel and the
 // workspace; a unit's tiles then run one after the other.
 constexpr int kWholeTiles = 4;
-int dec_whole_tiles(int d, int page, int width) {
-  const int tile = d == 64 ? dec_tile<64>() : dec_tile<128>();
+int dec_whole_tiles(int d, int nt, int page, int width) {
+  const int tile = d == 64 ? dec_tile<64, 8>() : nt == 4 ? dec_tile<128, 32>() : dec_tile<128, 8>();
   const long long tiles = (static_cast<long long>(page) * width + tile - 1) / tile;
   return tiles <= kWholeTiles ? static_cast<int>(tiles) : 0;
 }
@@ -352,7 +352,7 @@ size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_si
   if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
   if (!page_size_ok(page_size) || table_width < 1) return 0;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  return nt && dec_whole_tiles(d, page_size, table_width) ? 0 : kv4_workspace(nt, d);
+  return nt && dec_whole_tiles(d, nt, page_size, table_width) ? 0 : kv4_workspace(nt, d);
 }
 
 int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache,
@@ -370,7 +370,7 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
   if (static_cast<long long>(T) * Hq > 0x3fffffffll) return FA_ERR_UNSUPPORTED;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  const int whole = nt ? dec_whole_tiles(d, page_size, table_width) : 0;
+  const int whole = nt ? dec_whole_tiles(d, nt, page_size, table_width) : 0;
   if (!whole && (!workspace || workspace_bytes < kv4_workspace(nt, d))) return FA_ERR_INVALID_ARG;
   if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) ||
       !aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) ||
