@@ -160,14 +160,29 @@ __device__ __forceinline__ int walk_rows(const Kv4Args& a, const ChunkWalk* w) {
 __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, long long& total,
                                               long long& first, long long& last) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  ReqShape s;
-  long long per_head = 0;
+  ReqShape s{0, 0, 0};
+  long long per_head = 0;  // tiles of one key head of the thread's request
+  auto lane_request = [&](int l) {
+    return ReqShape{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
+                    __shfl_sync(0xffffffffu, s.keys, l)};
+  };
+  // A request a thread; those of many blocks (a block is 256 / group tokens) by the whole warp.
   auto cost = [&](int r) -> long long {
-    per_head = 0;
-    if (r >= a.b) return 0;
-    s = kv4_request(a, r);
+    constexpr int kAlone = 4;
+    s = r < a.b ? kv4_request(a, r) : ReqShape{0, 0, 0};
     const int blocks = chunk_blocks(a, s);
-    for (int b = 0; b < blocks; ++b) per_head += chunk_tiles(a, s, b);
+    per_head = 0;
+    if (blocks <= kAlone)
+      for (int b = 0; b < blocks; ++b) per_head += chunk_tiles(a, s, b);
+    for (unsigned many = __ballot_sync(0xffffffffu, blocks > kAlone); many; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      const ReqShape x = lane_request(l);
+      long long sum = 0;
+      for (int b = lane; b < chunk_blocks(a, x); b += 32) sum += chunk_tiles(a, x, b);
+#pragma unroll
+      for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == l) per_head = sum;
+    }
     return per_head * a.hk;
   };
   auto scan = [&](long long x) {
@@ -182,7 +197,7 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
     return x;
   };
   long long mine = 0, tiles = 0;
-  for (int r = threadIdx.x; r < a.b; r += kChThreads) mine += tiles = cost(r);
+  for (int r0 = 0; r0 < a.b; r0 += kChThreads) mine += tiles = cost(r0 + threadIdx.x);
   long long inc = scan(mine);
   total = 0;
   for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
@@ -200,17 +215,39 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
       all = base;
       for (int w = 0; w < kChThreads / 32; ++w) all += ctl->sum[w];
     }
-    if (first >= inc - tiles && first < inc) {
-      long long off = first - (inc - tiles);
-      ChunkSegment& c = ctl->start;
-      c.r = r0 + threadIdx.x;
-      c.req = s;
-      c.head = static_cast<int>(off / per_head);
-      off -= c.head * per_head;
-      c.block = 0;
-      while (off >= chunk_tiles(a, s, c.block)) off -= chunk_tiles(a, s, c.block++);
-      c.tile = static_cast<int>(off);
-      c.tiles = chunk_tiles(a, s, c.block);
+    const unsigned here = __ballot_sync(0xffffffffu, first >= inc - tiles && first < inc);
+    if (here) {
+      const int l = __ffs(here) - 1;
+      long long off = first - __shfl_sync(0xffffffffu, inc - tiles, l);
+      const long long head_tiles = __shfl_sync(0xffffffffu, per_head, l);
+      const ReqShape x = lane_request(l);
+      const int head = static_cast<int>(off / head_tiles);
+      off -= head * head_tiles;
+      // the block that holds tile `off` of the head, 32 blocks at a time
+      for (int b0 = 0;; b0 += 32) {
+        const int own = b0 + lane < chunk_blocks(a, x) ? chunk_tiles(a, x, b0 + lane) : 0;
+        long long upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, off < upto);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            ChunkSegment& c = ctl->start;
+            c.r = r0 + warp * 32 + l;
+            c.req = x;
+            c.head = head;
+            c.block = b0 + lane;
+            c.tile = static_cast<int>(off - (upto - own));
+            c.tiles = own;
+          }
+          break;
+        }
+        off -= __shfl_sync(0xffffffffu, upto, 31);
+        if (b0 > chunk_blocks(a, x)) break;  // (cannot be: off lies below the head's tiles)
+      }
     }
     base = all;
     if (first < base) break;
@@ -406,7 +443,8 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         }
       }
     };
-    const long long tiles = ctl->last - ctl->first;
+    // (test builds that inject a stall widen nothing: the first wait for a tile runs out)
+    const long long tiles = EXATTN_INJECT_STALL ? 0 : ctl->last - ctl->first;
     fetch_ids();
     // One copy of the code for the first loads and the later ones: the roles' loops together have to
     // stay in the instruction cache (a second copy of loads and conversions cost 8 %).
