@@ -34,6 +34,9 @@ bool power_of_two(float x) {
 
 bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
+// Tokens of one row of a page table: tiles and strips past the last one are still 32-bit numbers.
+bool width_ok(int width, int page) { return static_cast<long long>(width) * page <= 1ll << 30; }
+
 int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
@@ -268,7 +271,9 @@ int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_wid
   // other thread blocks read the old lengths and state while the new ones are written
   if (lens_out == lens || lens_out == new_lens || queue_state_out == queue_state)
     return FA_ERR_INVALID_ARG;
-  if (B > kPlanMaxBatch || !page_size_ok(page_size)) return FA_ERR_UNSUPPORTED;
+  if (B > kPlanMaxBatch || !page_size_ok(page_size) || !width_ok(table_width, page_size) ||
+      static_cast<long long>(B) * table_width > 0x7fffffffll)
+    return FA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(new_lens),
                         static_cast<const void*>(table), static_cast<const void*>(queue),
                         static_cast<const void*>(queue_state), static_cast<const void*>(lens_out),
@@ -329,7 +334,7 @@ int fa_kv4_append(const void* k, long long k_row_stride, long long k_head_stride
 
 int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slots, void* k, void* v,
                 int T, int Hkv, int d, float k_descale, float v_descale, void* stream) {
-  if (!k || !v || !slots || T < 1) return FA_ERR_INVALID_ARG;
+  if (!k || !v || k == v || !slots || T < 1) return FA_ERR_INVALID_ARG;
   if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return FA_ERR_MISALIGNED;
@@ -350,7 +355,7 @@ int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slot
 size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size,
                                   int table_width) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
-  if (!page_size_ok(page_size) || table_width < 1) return 0;
+  if (!page_size_ok(page_size) || table_width < 1 || !width_ok(table_width, page_size)) return 0;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
   return nt && dec_whole_tiles(d, nt, page_size, table_width) ? 0 : kv4_workspace(nt, d);
 }
@@ -360,7 +365,7 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
                const int* q_offsets, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
                int max_q, float scale, int causal, float k_descale, float v_descale,
                void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
-  if (!q || !table || !lens || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!q || !table || !lens || !o || !lse || o == q) return FA_ERR_INVALID_ARG;
   if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1)
     return FA_ERR_INVALID_ARG;
   if (!q_offsets && T % B) return FA_ERR_INVALID_ARG;
@@ -368,7 +373,8 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID_ARG;
   if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
-  if (static_cast<long long>(T) * Hq > 0x3fffffffll) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * Hq > 0x3fffffffll || !width_ok(table_width, page_size))
+    return FA_ERR_UNSUPPORTED;
   const int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
   const int whole = nt ? dec_whole_tiles(d, nt, page_size, table_width) : 0;
   if (!whole && (!workspace || workspace_bytes < kv4_workspace(nt, d))) return FA_ERR_INVALID_ARG;

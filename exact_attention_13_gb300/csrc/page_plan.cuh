@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   int head = a.state[0], count = a.state[1];
   count = min(max(count, 0), a.cap);
   head = static_cast<int>(static_cast<unsigned>(head) % static_cast<unsigned>(a.cap));
-  const int limit = static_cast<int>(min(static_cast<long long>(a.width) << a.page_shift, 0x7fffffffll));
+  const int limit = a.width << a.page_shift;  // at most 2^30
   // a request's length as far as its table row can hold it
   auto length = [&](int r) { return min(max(a.lens[r], 0), limit); };
   auto pages = [&](int tokens) { return tokens ? ((tokens - 1) >> a.page_shift) + 1 : 0; };
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   }
   for (int t = gthread; t < a.t; t += gthreads) {
     int pos = 0, slot = -1;
+    // (tokens that number 2^31 or more wrap: then a place may be found that is not the token's)
     if (t < total[0]) {
       int lo = 0, hi = a.b;  // the last request whose first token is at or before t
       while (hi - lo > 1) {
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       }
       const int len = length(lo);
       pos = len + (t - s_tok[lo]);
-      if (s_need[lo] >= 0) {
+      if (s_need[lo] >= 0 &&
+          static_cast<unsigned>(t - s_tok[lo]) < static_cast<unsigned>(s_tok[lo + 1] - s_tok[lo])) {
         const int p = pos >> a.page_shift, have = pages(len);
         const int id = p < have ? a.table[static_cast<long long>(lo) * a.width + p]
                                 : a.queue[ring(s_need[lo] + p - have)];

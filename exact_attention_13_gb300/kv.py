@@ -69,6 +69,8 @@ def _ints(t, shape, index, name):
     if (t.dtype is not _i32 or t.get_device() != index or t.shape != shape
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
+    if t.numel() > 0x7fffffff and len(shape) == 1:  # the library's sizes are 32 bits
+        raise ValueError(f"{name} has more than 2^31 - 1 entries")
 
 
 # ---------------------------------------------------------------------------------------------
@@ -201,8 +203,10 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
     include/exact_attention.h).  ``out``: a plan of the right sizes to write into; its ``lens`` and
     ``queue_state`` must not be this call's inputs."""
     index = lens.get_device()
-    if index < 0 or lens.dim() != 1 or table.dim() != 2 or queue.dim() != 1 or num_tokens < 0:
-        raise ValueError("lens and queue must be int32 CUDA vectors, table [B, width], num_tokens >= 0")
+    if (index < 0 or lens.dim() != 1 or table.dim() != 2 or queue.dim() != 1
+            or not 0 <= num_tokens < 2 ** 31):
+        raise ValueError("lens and queue must be int32 CUDA vectors, table [B, width], num_tokens in "
+                         "[0, 2^31)")
     B, width, cap = lens.shape[0], table.shape[1], queue.shape[0]
     _ints(lens, (B,), index, "lens")
     _ints(new_lens, (B,), index, "new_lens")

@@ -277,8 +277,12 @@ FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
  *                     slot -1 for tokens of refused requests; position 0 and slot -1 past the last
  *                     token.  num_tokens = 0: neither is written (they may be NULL)
  *   queue_state_out : {head, count} after the step
- *   page_size       : 16, 32, 64 or 128;  B <= 16384;  the tokens of a step number < 2^31
- * All arrays are device int32.  lens_out and queue_state_out may not be the inputs.  One launch,
+ *   num_tokens      : size of the packed batch, the refused requests' tokens included; tokens past
+ *                     it get no place, although their requests' lengths grow
+ *   page_size       : 16, 32, 64 or 128;  B <= 16384;  table_width * page_size <= 2^30;
+ *                     B * table_width < 2^31;  the tokens of a step number < 2^31
+ * All arrays are device int32.  No output may overlap an input or another output (lens_out and
+ * queue_state_out are refused when they are the inputs; the table and the ring are both).  One launch,
  * integers only: results do not depend on scheduling.
  */
 FA_API int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_width,
@@ -303,8 +307,8 @@ FA_API size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d);
  *   k, v      : device pointers, [T, Hkv, d] bf16 (16-byte aligned), last dimension contiguous, row
  *               and head strides in elements (multiples of 8, >= 0)
  *   cache     : device pointer (16-byte aligned)
- *   slots     : device int32 [T]; tokens whose slot lies outside the cache (-1) are skipped.  Of
- *               tokens with the same slot, which one's values each group keeps is undefined
+ *   slots     : device int32 [T]; tokens whose slot lies outside the cache (-1) are skipped.  What
+ *               a slot holds that several tokens of the call have is undefined, group by group
  *   d 64 or 128;  page_size 16, 32, 64 or 128;  num_pages * page_size < 2^31;  descales powers of
  *   two in [2^-61, 2^59]
  */
@@ -314,7 +318,7 @@ FA_API int fa_kv4_append(const void* k, long long k_row_stride, long long k_head
                          int Hkv, int d, float k_descale, float v_descale, void* stream);
 
 /* Read cached rows back as bf16 (exact): k, v are outputs [T, Hkv, d], contiguous, 16-byte
- * aligned; rows whose slot lies outside the cache are zeros.  Other arguments as fa_kv4_append. */
+ * aligned, not the same; rows whose slot lies outside the cache are zeros.  Other arguments as fa_kv4_append. */
 FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const int* slots, void* k,
                        void* v, int T, int Hkv, int d, float k_descale, float v_descale,
                        void* stream);
@@ -331,7 +335,8 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *                 page_size] are clamped; keys on a page id outside [0, num_pages) are not seen
  *   q_offsets   : device int32 [B + 1], not decreasing, or NULL: T / B queries each (T % B == 0).
  *                 Rows of q past q_offsets[B] are not read, their outputs left as they were
- *   o, lse      : outputs [T, Hq, d] bf16 (16-byte aligned) and [T, Hq] fp32
+ *   o, lse      : outputs [T, Hq, d] bf16 (16-byte aligned) and [T, Hq] fp32; they overlap no input
+ *                 (o = q is refused)
  *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks the
  *                 kernel: how many query rows share a pass over the cache
  *   scale       : softmax scale, finite and >= 0
@@ -339,7 +344,8 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *                 when that is 0), contents on entry do not matter; calls that may run at the same
  *                 time need one each
  *   dev_status  : as fa_fwd_opts.dev_status (NULL = the library's status word)
- *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30; d, page_size and descales as fa_kv4_append
+ *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30, table_width * page_size <= 2^30; d,
+ *                 page_size and descales as fa_kv4_append
  * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
  * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums
  * are merged in a fixed order: the same call gives the same bits.

@@ -283,6 +283,54 @@ def test_prompt_chunks_with_masked_places_and_missing_pages():
     check_on_gpu(q, cache, table, lens, offsets, d, max_q=200)
 
 
+def test_prompts_of_many_blocks():
+    """One prompt of 50 and one of 7 blocks of rows between short ones, on more and fewer key heads."""
+    d, page, lens, qlens = 64, 64, [90, 3300, 70, 800, 40], [40, 3200, 70, 440, 33]
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    for Hq, Hkv in ((4, 1), (4, 2)):
+        cache, table = make(lens, 52, page, Hkv, d)
+        check_on_gpu(queries(offsets[-1], Hq, d), cache, table, lens, offsets, d, max_q=3200)
+
+
+def test_prompt_chunks_at_once_captured_and_rows_outside():
+    """Calls of both kernels on two streams at once; a graph replayed on new data; rows before the
+    first request's and past the last one's are left as they are."""
+    d, page, Hq, Hkv, lens, qlens = 128, 32, 8, 2, [900, 200], [150, 40]
+    cache, table = make(lens, 29, page, Hkv, d)
+    offsets, tab, ln = ints([2, 152, 192]), ints(table), ints(lens)
+    q = queries(200, Hq, d)
+    q[:2] = math.nan
+    q[192:] = math.nan
+    want = check_on_gpu(q[2:192].contiguous(), cache, table, lens, [0, 150, 190], d, max_q=150)
+    dec_q = queries(2, Hq, d, seed=3)
+    dec = ea.kv4_fwd(dec_q, cache, tab, ln)
+    torch.cuda.synchronize()
+    got = []
+    for s in [torch.cuda.Stream() for _ in range(3)]:
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                o = torch.full((200, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+                lse = torch.full((200, Hq), 8.0, device="cuda")
+                ea.kv4_fwd(q, cache, tab, ln, q_offsets=offsets, max_q=150, out=o, lse=lse)
+                got.append((o, lse, ea.kv4_fwd(dec_q, cache, tab, ln)))
+    torch.cuda.synchronize()
+    for o, lse, x in got:
+        assert torch.equal(o[2:192], want[0]) and torch.equal(lse[2:192], want[1])
+        for rest in (slice(0, 2), slice(192, 200)):
+            assert (o[rest] == 7).all() and (lse[rest] == 8).all()
+        assert torch.equal(x[0], dec[0]) and torch.equal(x[1], dec[1])
+    static = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = ea.kv4_fwd(static, cache, tab, ln, q_offsets=offsets, max_q=150)
+    for sign in (1, -1):
+        static.copy_(sign * q)
+        graph.replay()
+        eager = ea.kv4_fwd(static, cache, tab, ln, q_offsets=offsets, max_q=150)
+        assert torch.equal(o[2:192], eager[0][2:192]) and torch.equal(lse[2:192], eager[1][2:192])
+    assert ea.device_status() == 0
+
+
 def test_scale_descales_and_large_scores():
     lens, d = [200, 77], 128
     cache, table = make(lens, 4, 64, 2, d)
@@ -404,6 +452,10 @@ def test_refusals():
                  (k, k[:1], cache, ints([0, 1])), (k.float(), k.float(), cache, ints([0, 1]))):
         with pytest.raises(ValueError):
             ea.kv4_append(*args)
+    with pytest.raises(ea.AttentionError):
+        ea.kv4_fwd(**ok, out=q)
+    with pytest.raises(ea.AttentionError):
+        ea.kv4_read(cache, ints([0, 1]), d, k=k, v=k)
     with pytest.raises(ValueError):
         ea.kv4_read(cache, ints([[0]]), d)
 

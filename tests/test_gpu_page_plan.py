@@ -58,6 +58,19 @@ def test_refused_requests_and_no_tokens():
     compare([0, 5], [-1, -1], np.array([[3], [4]]), [9, 9], [1, 0], 16, 0)
 
 
+def test_more_tokens_than_32_bits_hold():
+    """Beyond the documented sizes, but device data: places are still ones that the request has."""
+    big, page, width = 2 ** 31 - 1, 16, 4
+    new = [big, 1, 4, big, big, big, 20, 0, 3]
+    table = np.arange(100, 100 + 9 * width).reshape(9, width)
+    queue = np.arange(40)
+    cuda = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32).cuda()  # noqa: E731
+    out = ea.page_plan(cuda([5] * 9), cuda(new), cuda(table), cuda(queue), cuda([0, 40]), page, 3000)
+    slots = out.slots.cpu().numpy()
+    assert set(np.unique(slots[slots >= 0] // page)) <= set(range(40)) | set(range(100, 136))
+    assert out.lens.tolist() == [5, 6, 9, 5, 5, 5, 25, 5, 8]
+
+
 def test_many_steps_keep_every_page_once():
     rng = np.random.default_rng(5)
     B, page, width = 40, 16, 6

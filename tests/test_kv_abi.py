@@ -26,8 +26,8 @@ GOOD = {
                 1, 8, 128, P, 0, P, 128, 0, 1.0, None],
     "fa_page_plan": [P, P, P, 4, P, 16, P, 2, 16, 8, P + 64, P, P, P, P + 64, None],
     "fa_kv4_append": [P, 128, 128, P, 128, 128, P, 4, 16, P, 8, 1, 128, 1.0, 1.0, None],
-    "fa_kv4_read": [P, 4, 16, P, P, P, 8, 1, 128, 1.0, 1.0, None],
-    "fa_kv4_fwd": [P, 512, 128, P, 4, 16, P, 100, P, P, P, P, 8, 2, 4, 1, 128, 4, 0.1, 1, 1.0, 1.0, P,
+    "fa_kv4_read": [P, 4, 16, P, P, P + 64, 8, 1, 128, 1.0, 1.0, None],
+    "fa_kv4_fwd": [P, 512, 128, P, 4, 16, P, 100, P, P, P + 64, P, 8, 2, 4, 1, 128, 4, 0.1, 1, 1.0, 1.0, P,
                    1 << 30, None, None],
 }
 CASES = [
@@ -44,7 +44,8 @@ CASES = [
     ("fa_page_plan", dict(T=-1), BAD), ("fa_page_plan", dict(size=0), BAD),
     ("fa_page_plan", dict(lens_out=P), BAD), ("fa_page_plan", dict(state_out=P), BAD),
     ("fa_page_plan", dict(B=16385), UNS), ("fa_page_plan", dict(page=24), UNS),
-    ("fa_page_plan", dict(page=256), UNS), ("fa_page_plan", dict(table=P + 2), MIS),
+    ("fa_page_plan", dict(page=256), UNS), ("fa_page_plan", dict(width=1 << 27), UNS),
+    ("fa_page_plan", dict(B=16384, width=1 << 17), UNS), ("fa_page_plan", dict(table=P + 2), MIS),
     ("fa_kv4_append", dict(k=0), BAD), ("fa_kv4_append", dict(slots=0), BAD),
     ("fa_kv4_append", dict(cache=0), BAD), ("fa_kv4_append", dict(T=0), BAD),
     ("fa_kv4_append", dict(vr=-8), BAD), ("fa_kv4_append", dict(kd=3.0), BAD),
@@ -54,7 +55,7 @@ CASES = [
     ("fa_kv4_append", dict(cache=P + 8), MIS), ("fa_kv4_append", dict(kh=129), MIS),
     ("fa_kv4_read", dict(k=0), BAD), ("fa_kv4_read", dict(T=0), BAD),
     ("fa_kv4_read", dict(kd=0.3), BAD), ("fa_kv4_read", dict(page=48), UNS),
-    ("fa_kv4_read", dict(v=P + 4), MIS),
+    ("fa_kv4_read", dict(v=P + 4), MIS), ("fa_kv4_read", dict(v=P + 32, k=P + 32), BAD),
     ("fa_kv4_fwd", dict(q=0), BAD), ("fa_kv4_fwd", dict(lens=0), BAD),
     ("fa_kv4_fwd", dict(ws=0), BAD), ("fa_kv4_fwd", dict(ws_bytes=1024), BAD),
     ("fa_kv4_fwd", dict(T=0), BAD), ("fa_kv4_fwd", dict(Hq=3, Hkv=2), BAD),
@@ -65,6 +66,7 @@ CASES = [
     ("fa_kv4_fwd", dict(page=1024), UNS), ("fa_kv4_fwd", dict(T=1 << 29), UNS),
     ("fa_kv4_fwd", dict(q=P + 2), MIS), ("fa_kv4_fwd", dict(qr=100), MIS),
     ("fa_kv4_fwd", dict(lse=P + 2), MIS), ("fa_kv4_fwd", dict(ws=P + 8), MIS),
+    ("fa_kv4_fwd", dict(o=P), BAD), ("fa_kv4_fwd", dict(width=(1 << 26) + 1), UNS),
     ("fa_kv4_fwd", dict(status=P + 2), MIS), ("fa_kv4_fwd", dict(max_q=64, ws_bytes=1 << 20), BAD),
 ]
 
@@ -95,6 +97,8 @@ def test_sizes():
         assert ea.kv4_workspace_bytes(*bad, 64, 100) == 0
     assert ea.kv4_workspace_bytes(4, 2, 128, 1, 24, 100) == 0
     assert ea.kv4_workspace_bytes(4, 2, 128, 1, 64, 0) == 0
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 64, 1 << 24) > 0  # 2^30 tokens
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 64, (1 << 24) + 1) == 0
 
 
 def test_python_checks():
