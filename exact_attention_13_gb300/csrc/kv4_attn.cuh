@@ -74,7 +74,7 @@ struct Kv4Args {
   float* part_o;           // [2 n][R][d]
   float2* part_ml;         // [2 n][R] (max, sum)
   int* status;             // device status word (kv4_chunk.cuh)
-  int4* desc;              // [n] unit to merge: {first slot or -1, request, unit, last CTA}
+  int4* desc;              // [n] unit to merge (merge_desc), or x < 0
   long long q_len;
   int t, b, hq, hk, group, width, page_shift, pages;
   int causal;
@@ -91,8 +91,8 @@ __device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
   ReqShape s;
   long long q0, q1;
   if (a.q_offsets) {
-    q0 = __ldg(a.q_offsets + r);
-    q1 = __ldg(a.q_offsets + r + 1);
+    q0 = *(a.q_offsets + r);
+    q1 = *(a.q_offsets + r + 1);
   } else {
     q0 = a.q_len * r;
     q1 = q0 + a.q_len;
@@ -101,7 +101,7 @@ __device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
   s.q0 = static_cast<int>(min(max(q0, 0ll), static_cast<long long>(a.t)));
   s.q_len = static_cast<int>(min(max(q1, static_cast<long long>(s.q0)), static_cast<long long>(a.t))) - s.q0;
   const long long room = static_cast<long long>(a.width) << a.page_shift;
-  s.keys = static_cast<int>(min(static_cast<long long>(max(__ldg(a.lens + r), 0)), room));
+  s.keys = static_cast<int>(min(static_cast<long long>(max(*(a.lens + r), 0)), room));
   return s;
 }
 
@@ -188,6 +188,13 @@ __device__ __forceinline__ int share_of(long long total, int n, long long x) {
   }
   const long long q = total / n, more = total % n, longer = more * (q + 1);
   return static_cast<int>(x < longer ? x / (q + 1) : more + (x - longer) / q);
+}
+
+// A unit to be merged: its first partial sum's slot and the number of parts, its first query token, its
+// first row, its key head and its rows (<= 256).
+__device__ __forceinline__ int4 merge_desc(const ReqShape& req, int head, int row0, int rows, int slot,
+                                           int parts) {
+  return make_int4(slot | parts << 16, req.q0, row0, head | rows << 16);
 }
 
 // To the next tile; true when the next unit begins with it.
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   float4* const area = reinterpret_cast<float4*>(dec_smem + kDecWarps * kDecStages * dec_strip_bytes<D, R>());
   uint4* const s_q = reinterpret_cast<uint4*>(area + kDecWarps * MT * NT * 32);  // [nt][w][lane]
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_dependents();
   long long total, first, last;
   const int n_cta = kv4_my_range<D, R>(a, s_sum, &s_cur, total, first, last);
   if (static_cast<int>(blockIdx.x) >= n_cta) {
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         const __nv_bfloat16* p = a.q + static_cast<long long>(ld.req.q0 + qi) * a.q_row +
                                  static_cast<long long>(ld.head * a.group + qg) * a.q_head + line % kLines * 64;
         uint32_t unused;
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(unused) : "l"(p));
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(unused) : "l"(p));
       }
     }
   };
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       const int key = key0 + 16 * g;
       // groups that share a page share its id
       if (g > 0 && (key & (page_rows - 1)) != 0) id[g] = id[g - 1];
-      else id[g] = key < ld.req.keys ? __ldg(row_ids + (key >> a.page_shift)) : -1;
+      else id[g] = key < ld.req.keys ? *(row_ids + (key >> a.page_shift)) : -1;
     }
   };
   auto issue = [&](int stage) {
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         float amax = 0.f;
 #pragma unroll
         for (int w = 0; w < QW / 4; ++w) {
-          raw[w] = live ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0u, 0u, 0u, 0u);
+          raw[w] = live ? *(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0u, 0u, 0u, 0u);
           float f[8];
           unpack_bf16x8(raw[w], f);
 #pragma unroll
@@ -791,8 +798,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
       if (whole_start && !unit_ends) {
         // the unit begins here and ends in a later CTA: x is its last tile on the line
         const long long x = first + step + (cur.tiles - 1 - cur.tile);
-        merge = make_int4(unit_no > 0 ? 1 : 0, cur.r, cur.block * a.hk + cur.head,
-                          share_of(total, n_cta, x));
+        merge = merge_desc(req, head, row0, min(R, rows - row0), slot,
+                           share_of(total, n_cta, x) - static_cast<int>(blockIdx.x) + 1);
       }
       ++unit_no;
       fresh = true;
@@ -804,84 +811,200 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = merge;
 }
 
-// Merge of units that cross CTAs.  The blocks (i, *) share the rows of the unit that begins in CTA i
-// and ends later, if there is one.  Of a unit in few parts each warp takes rows of its own; of one
-// in many parts a block takes a row and its warps share the parts.  Always in the same order.  It is launched while the decode kernel still runs and
-// waits for its end.
-constexpr int kMergeThreads = 256;
+// Merge of units that cross CTAs, launched while the attention kernel still runs.  The blocks (i, *)
+// share the rows of the unit that begins in CTA i and ends in a later one, if there is one, or
+// (`ctas` > 0, where few of all CTAs begin such a unit) of the i-th one that there is.  Of a unit
+// in up to eight parts each warp takes rows of its own; of one in more parts a block takes a row
+// and its warps share the parts.  Always summed in the same order.  Its time is latency (descriptor,
+// then maxima and sums of the parts together): all loads of a row are in flight at once.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+
+template <int N>
+__device__ __forceinline__ void load_floats(const float* src, float (&y)[N]) {
+  if constexpr (N == 4)
+    *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
+  else
+    *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+}
+
+template <int D>
+struct MergeShared {
+  float m[kMergeWarps], l[kMergeWarps], o[kMergeWarps][D];
+};
 
 template <int D, int R>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Args a) {
-  constexpr int kWarps = kMergeThreads / 32, kPer = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 u = a.desc[blockIdx.x];
-  if (u.x < 0) return;
+__device__ __forceinline__ void kv4_merge_unit(const Kv4Args& a, const int4 u, MergeShared<D>& sh) {
+  constexpr int kPer = D / 32;
+  constexpr int kRows = R > 32 ? 4 : 1;  // rows that a warp takes at a time
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int parts = u.w - static_cast<int>(blockIdx.x) + 1;
-  const bool alone = parts <= kWarps;
-  const int sharing = alone ? 1 : kWarps;
-  const ReqShape req = kv4_request(a, u.y);
-  const int block = u.z / a.hk, head = u.z - block * a.hk;
-  const int rows = min(R, req.q_len * a.group - block * R);
-  const int step = alone ? kWarps * gridDim.y : gridDim.y;
-  for (int row = alone ? blockIdx.y * kWarps + warp : blockIdx.y; row < rows; row += step) {
-    auto slot = [&](int k) {  // part k: this CTA's, then the first of each later one
-      return static_cast<size_t>(2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? u.x : 0)) * R + row;
-    };
-    const int k0 = alone ? 0 : warp;
-    float big = kDecNone, sum = 0.f, acc[kPer];
+  const int first = u.x & 0xffff, parts = u.x >> 16, head = u.w & 0xffff, rows = u.w >> 16;
+  // part k of row 0: the first CTA's, then the first of each later one
+  auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? first : (first & ~1) + 2 * k) * R; };
+  auto store = [&](int row, float top, float sum, const float (&acc)[kPer]) {
+    const int at_row = u.z + row, qi = at_row / a.group, qg = at_row - qi * a.group;
+    const size_t to = static_cast<size_t>(u.y + qi) * a.hq + head * a.group + qg;
+    const float inv = sum == 0.f ? 0.f : a.v_descale / sum;
+    uint32_t p[kPer / 2];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    // running maximum: sums so far are rescaled when it grows
-#pragma unroll 8
-    for (int k = k0; k < parts; k += sharing) {
-      const float2 ml = a.part_ml[slot(k)];
-      const float* src = a.part_o + slot(k) * D + lane * kPer;
-      const float top = fmaxf(big, ml.x);
-      const float f = ex2_mufu(ml.x - top), g = ex2_mufu(big - top);
-      big = top;
-      sum = fmaf(sum, g, ml.y * f);
+    for (int e = 0; e < kPer / 2; ++e) p[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(a.o + to * D + lane * kPer) = make_uint2(p[0], p[1]);
+    else
+      *reinterpret_cast<uint32_t*>(a.o + to * D + lane * kPer) = p[0];
+    if (lane == 0) a.lse[to] = sum == 0.f ? -INFINITY : top * kLn2F + logf(sum);
+  };
+
+  if (parts <= kMergeWarps) {
+    constexpr int kAhead = kRows == 1 ? kMergeWarps : 2;  // parts whose sums are loaded together
+    for (int row0 = (blockIdx.y * kMergeWarps + warp) * kRows; row0 < rows; row0 += gridDim.y * kMergeWarps * kRows) {
+      const int n = min(kRows, rows - row0);
+      // lane 8 r + k: row r, part k
+      const int my_row = lane / 8, my_part = lane % 8;
+      float2 ml = make_float2(kDecNone, 0.f);
+      if (my_row < n && my_part < parts) ml = a.part_ml[slot(my_part) + row0 + my_row];
+      float acc[kRows][kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + i);
-        acc[i] = fmaf(acc[i], g, y.x * f);
-        acc[i + 1] = fmaf(acc[i + 1], g, y.y * f);
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[r][e] = 0.f;
+      float top = ml.x;
+#pragma unroll
+      for (int k0 = 0; k0 < kMergeWarps; k0 += kAhead) {
+        if (k0 >= parts) break;
+        float y[kAhead][kRows][kPer];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) y[k][r][e] = 0.f;
+            if (k0 + k < parts && r < n) load_floats(a.part_o + (slot(k0 + k) + row0 + r) * D + lane * kPer, y[k][r]);
+          }
+        if (k0 == 0) {
+#pragma unroll
+          for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          ml.x = ex2_mufu(ml.x - top);
+          ml.y *= ml.x;
+#pragma unroll
+          for (int o = 1; o < 8; o *= 2) ml.y += __shfl_xor_sync(0xffffffffu, ml.y, o);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const float f = __shfl_sync(0xffffffffu, ml.x, 8 * r + k0 + k);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[r][e] = fmaf(y[k][r][e], f, acc[r][e]);
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float t = __shfl_sync(0xffffffffu, top, 8 * r), sum = __shfl_sync(0xffffffffu, ml.y, 8 * r);
+        if (r < n) store(row0 + r, t, sum, acc[r]);
       }
     }
-    if (!alone) {
-      if (lane == 0) s_m[warp] = big;
-      __syncthreads();
-      const float own = big;
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    // the warp's parts warp, warp + 8, ...: 32 of them at a time, lane j part j
+    float top = kDecNone, sum = 0.f, acc[kPer];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) big = fmaxf(big, s_m[w]);
-      const float f = ex2_mufu(own - big);
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int k0 = warp; k0 < parts; k0 += 32 * kMergeWarps) {
+      const int mine = k0 + lane * kMergeWarps;
+      float2 ml = make_float2(kDecNone, 0.f);
+      if (mine < parts) ml = a.part_ml[slot(mine) + row];
+      float big = fmaxf(ml.x, top);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = acc[i] * f;
-      if (lane == 0) s_l[warp] = sum * f;
-      __syncthreads();
-      if (warp == 0) {
-        sum = 0.f;
+      for (int o = 1; o < 32; o *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const float f = ex2_mufu(ml.x - big), g = ex2_mufu(top - big);
+      ml.y *= f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+      for (int o = 1; o < 32; o *= 2) ml.y += __shfl_xor_sync(0xffffffffu, ml.y, o);
+      sum = fmaf(sum, g, ml.y);
+      top = big;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          sum += s_l[w];
+      for (int e = 0; e < kPer; ++e) acc[e] *= g;
+      const int here = min(32, (parts - k0 - 1) / kMergeWarps + 1);
+      for (int j0 = 0; j0 < here; j0 += 16) {
+        float y[16][kPer];
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) acc[i] += s_o[w][lane * kPer + i];
+        for (int j = 0; j < 16; ++j) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) y[j][e] = 0.f;
+          if (j0 + j < here) load_floats(a.part_o + (slot(k0 + (j0 + j) * kMergeWarps) + row) * D + lane * kPer, y[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(y[j][e], fj, acc[e]);
         }
       }
     }
-    if (alone || warp == 0) {
-      const int at_row = block * R + row, qi = at_row / a.group, qg = at_row - qi * a.group;
-      const size_t at = static_cast<size_t>(req.q0 + qi) * a.hq + head * a.group + qg;
-      const float inv = sum == 0.f ? 0.f : a.v_descale / sum;
+    if (lane == 0) sh.m[warp] = top;
+    __syncthreads();
+    const float own = top;
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2)
-        *reinterpret_cast<uint32_t*>(a.o + at * D + lane * kPer + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-      if (lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : big * kLn2F + logf(sum);
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, sh.m[w]);
+    const float f = ex2_mufu(own - top);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sh.o[warp][lane * kPer + e] = acc[e] * f;
+    if (lane == 0) sh.l[warp] = sum * f;
+    __syncthreads();
+    if (warp == 0) {
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        sum += sh.l[w];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] += sh.o[w][lane * kPer + e];
+      }
+      store(row, top, sum, acc);
     }
-    if (!alone) __syncthreads();
+    __syncthreads();
+  }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Args a, int ctas) {
+  __shared__ MergeShared<D> sh;
+  grid_launch_dependents();
+  grid_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  __shared__ int s_count[2][kMergeWarps], s_begins[2 * kMergeThreads];
+  int units = 1;
+  if (ctas > 0) {
+    int before[2];
+    unsigned begin[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = x * kMergeThreads + threadIdx.x;
+      begin[x] = __ballot_sync(0xffffffffu, i < ctas && a.desc[i].x >= 0);
+      if (lane == 0) s_count[x][warp] = __popc(begin[x]);
+    }
+    __syncthreads();
+    units = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        if (w == warp) before[x] = units;
+        units += s_count[x][w];
+      }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (begin[x] >> lane & 1u)
+        s_begins[before[x] + __popc(begin[x] & ((1u << lane) - 1u))] = x * kMergeThreads + threadIdx.x;
+    __syncthreads();
+    units = (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  }
+#pragma unroll 1
+  for (int x = 0; x < units; ++x) {
+    const int4 u = a.desc[ctas > 0 ? s_begins[blockIdx.x + x * gridDim.x] : blockIdx.x];
+    if (u.x >= 0) kv4_merge_unit<D, R>(a, u, sh);
   }
 }
 

@@ -125,18 +125,20 @@ struct Kv4Place {
 
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a) {
+  grid_launch_dependents();
+  grid_wait();
   using Index = Kv4Index<D, kKv4Group>;
   constexpr int kPieces = Index::kPieces;  // 8 or 4 neighbouring lanes hold one head vector
   const int id = blockIdx.x * kKv4Threads + threadIdx.x;
   const bool live = id < a.pieces;
   const Index ix(a, live ? id : a.pieces - 1);  // idle lanes repeat the last piece, for the votes
-  const int slot = __ldg(a.slots + ix.token);
+  const int slot = *(a.slots + ix.token);
   uint4 raw[2][2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const uint4* src = reinterpret_cast<const uint4*>(a.in[n] + ix.token * a.row[n] + ix.head * a.head[n]) + 2 * ix.p;
-    raw[n][0] = __ldg(src);
-    raw[n][1] = __ldg(src + 1);
+    raw[n][0] = *src;
+    raw[n][1] = *(src + 1);
   }
   const Kv4Place<D, kKv4Group> place(a, ix, slot);
   const unsigned mine = ((1u << kPieces) - 1u) << (threadIdx.x % 32 / kPieces * kPieces);
@@ -185,10 +187,12 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(const Kv4Rows a
 // Rows of invalid slots read as zeros.
 template <int D>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) {
+  grid_launch_dependents();
+  grid_wait();
   const int id = blockIdx.x * kKv4Threads + threadIdx.x;
   if (id >= a.pieces) return;
   const Kv4Index<D, 8> ix(a, id);
-  const Kv4Place<D, 8> place(a, ix, __ldg(a.slots + ix.token));
+  const Kv4Place<D, 8> place(a, ix, *(a.slots + ix.token));
   uint32_t codes[2] = {0u, 0u};
   uint8_t s8[2] = {0, 0};
   if (place.at >= 0) {

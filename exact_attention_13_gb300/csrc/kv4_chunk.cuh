@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
   ChunkCtrl* const ctl = reinterpret_cast<ChunkCtrl*>(s_ring + G::kSlots * G::kTileBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_dependents();
   {
     long long total, first, last;
     const int n_cta = chunk_my_range(a, ctl, total, first, last);
@@ -415,9 +415,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
     const uint8_t* head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
     int id[2];
     auto fetch_ids = [&]() {
-      id[0] = key < keys ? __ldg(ids + (key >> a.page_shift)) : -1;
+      id[0] = key < keys ? *(ids + (key >> a.page_shift)) : -1;
       id[1] = id[0];
-      if (a.page_shift == 4) id[1] = key + 16 < keys ? __ldg(ids + (key >> 4) + 1) : -1;
+      if (a.page_shift == 4) id[1] = key + 16 < keys ? *(ids + (key >> 4) + 1) : -1;
     };
     uint2 c0[kIt], c1[kIt];
     uint16_t sc[kIt], sc_values[kIt];
@@ -435,10 +435,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           c0[it] = c1[it] = make_uint2(0u, 0u);
           sc[it] = sc_values[it] = 0;
           if (ok) {  // (a page that is not there: zeros, and the scores are masked)
-            c0[it] = __ldg(reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + swap));
-            c1[it] = __ldg(reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + (swap ^ 8)));
-            sc[it] = __ldg(reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + (values ? block_bytes : 0)));
-            if (!values) sc_values[it] = __ldg(reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + block_bytes));
+            c0[it] = *reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + swap);
+            c1[it] = *reinterpret_cast<const uint2*>(codes + x * kRowsIt * kCode + (swap ^ 8));
+            sc[it] = *reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + (values ? block_bytes : 0));
+            if (!values) sc_values[it] = *reinterpret_cast<const uint16_t*>(scales + x * kRowsIt * kScale + block_bytes);
           }
         }
       }
@@ -512,8 +512,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         // the unit begins here and ends in a later CTA: x is its last tile on the line
         const long long x = ctl->last - w->left + w->s.tiles - 1, total = ctl->total;
         const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-        a.desc[blockIdx.x] = make_int4(unit_no > 0 ? 1 : 0, w->s.r, w->s.block * a.hk + w->s.head,
-                                       share_of(total, n_cta, x));
+        a.desc[blockIdx.x] = merge_desc(w->s.req, w->s.head, w->s.block * kChRows, min(kChRows, walk_rows(a, w)),
+                                        2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0),
+                                        share_of(total, n_cta, x) - static_cast<int>(blockIdx.x) + 1);
       }
       if (h == 0 || two) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
             const int r = it * kRowsIt + lane / kRow, piece = lane % kRow;
             const long long at = __shfl_sync(0xffffffffu, mine, r);
             uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= 0) raw = __ldg(reinterpret_cast<const uint4*>(a.q + at) + piece);
+            if (at >= 0) raw = *(reinterpret_cast<const uint4*>(a.q + at) + piece);
             float f[8], amax = 0.f;
             unpack_bf16x8(raw, f);
 #pragma unroll
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           const int key_end = min(w->s.req.keys, (w->s.tile + n) * kChKeys);
           const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
           for (int p = ((w->s.tile * kChKeys) >> a.page_shift) + lane; (p << a.page_shift) < key_end; p += 32)
-            holes |= static_cast<unsigned>(__ldg(ids + p)) >= static_cast<unsigned>(a.pages);
+            holes |= static_cast<unsigned>(*(ids + p)) >= static_cast<unsigned>(a.pages);
         }
         holes = __any_sync(0xffffffffu, holes);
         int lim = sees - w->s.tile * kChKeys;  // keys of the next tile that the row sees
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
               const int key = (w->s.tile + j) * kChKeys + 16 * g;
               const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;
               if (key < w->s.req.keys &&
-                  static_cast<unsigned>(__ldg(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages))
+                  static_cast<unsigned>(*(ids + (key >> a.page_shift))) >= static_cast<unsigned>(a.pages))
                 seen = 0u;
             }
             return seen;

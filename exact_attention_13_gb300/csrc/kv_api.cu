@@ -43,19 +43,41 @@ int log2_of(int x) {
   return s;
 }
 
-// Opt a kernel into `bytes` of dynamic shared memory, once per device.
+int launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// Set an attribute of a kernel, once per device.
 template <typename K>
-int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+int set_once(K kern, cudaFuncAttribute attribute, int value, std::atomic<uint64_t>& done) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxKvDevices) return FA_ERR_CUDA;
   if (done.load(std::memory_order_acquire) & (1ull << dev)) return FA_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return FA_ERR_CUDA;
+  if (cudaFuncSetAttribute(kern, attribute, value) != cudaSuccess) return FA_ERR_CUDA;
   done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   return FA_OK;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+template <typename K>
+int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  return set_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
+}
+
+// Launch a kernel that may begin while the one before it on the stream still runs (grid_wait in each).
+template <typename... Params, typename... Args>
+int launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, kern, args...) == cudaSuccess) return FA_OK;
+  (void)cudaGetLastError();
+  return FA_ERR_CUDA;
+}
 
 // ---------------------------------------------------------------------------------- rope
 int rope_tensor(RopeTensor& t, const void* x, const long long* xs, void* y, const long long* ys,
@@ -89,19 +111,15 @@ int cache_checks(const void* cache, int pages, int heads, int page, int d) {
 }
 
 // Append or read T tokens, in launches of fewer than 2^31 pieces (32-bit indices).
-template <typename K64, typename K128>
-int launch_rows(Kv4Rows a, int T, int heads, int d, int piece, K64 k64, K128 k128, cudaStream_t s) {
+int launch_rows(Kv4Rows a, int T, int heads, int d, int piece, void (*k64)(Kv4Rows), void (*k128)(Kv4Rows),
+                cudaStream_t s) {
   const int per_token = heads * (d / piece);
   const int most = ((1 << 30) / per_token);
   for (int t = 0; t < T; t += most) {
     const int n = T - t < most ? T - t : most;
     a.pieces = n * per_token;
     const unsigned grid = static_cast<unsigned>((a.pieces + kKv4Threads - 1) / kKv4Threads);
-    if (d == 64)
-      k64<<<grid, kKv4Threads, 0, s>>>(a);
-    else
-      k128<<<grid, kKv4Threads, 0, s>>>(a);
-    if (int rc = launched()) return rc;
+    if (int rc = launch_early(d == 64 ? k64 : k128, grid, kKv4Threads, 0, s, a)) return rc;
     a.slots += n;
     for (int i = 0; i < 2; ++i) {
       if (a.in[i]) a.in[i] += n * a.row[i];
@@ -145,19 +163,15 @@ void split_workspace(Kv4Args& a, void* workspace) {
   a.desc = reinterpret_cast<int4*>(a.part_ml + kv4_part_rows(NT));
 }
 
-// The merge of units that cross CTAs, launched while the first kernel runs.
 template <int D, int R>
-int launch_merge(const Kv4Args& a, int ctas, unsigned row_blocks, cudaStream_t s) {
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(ctas, row_blocks);
-  config.blockDim = dim3(kMergeThreads);
-  config.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &early;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kv4_merge_kernel<D, R>, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+int launch_merge(const Kv4Args& a, int ctas, cudaStream_t s) {
+  // Few units (at most one for eight CTAs): each may span many CTAs, and rows get blocks of their own
+  // (4 units of 8 rows in 114 parts each: 3.9 us instead of 7 with blocks for all CTAs; 128 units of 15
+  // rows: 2.4 us more than the other way).  Else eight rows a block, 64 of a prompt chunk (135 us
+  // for the whole call of 4 chunks of 512 tokens; 139 with eight).
+  const bool few = static_cast<long long>(a.b) * a.hk <= ctas / 8;
+  const dim3 grid = few ? dim3(ctas / 8, R > 32 ? 32 : R) : dim3(ctas, R > 32 ? R / 64 : R / 8);
+  return launch_early(kv4_merge_kernel<D, R>, grid, kMergeThreads, 0, s, a, few ? ctas : 0);
 }
 
 template <int D, int NT>
@@ -172,10 +186,8 @@ int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   kern<<<n, kDecThreads, smem, s>>>(a);
   if (int rc = launched()) return rc;
   if (a.whole_tiles) return FA_OK;
-  // Few units: each may span many CTAs, and rows get blocks of their own (one block for all rows of
-  // a unit that spans the whole GPU would take about 10 us); else a block takes all rows of its unit.
-  const unsigned row_blocks = static_cast<long long>(a.b) * a.hk <= n / 8 ? 8 * NT : 1;
-  return launch_merge<D, 8 * NT>(a, n, row_blocks, s);
+  static_assert(n <= 2 * kMergeThreads && 2 * n <= 0x7fff, "descriptors of the merge");
+  return launch_merge<D, 8 * NT>(a, n, s);
 }
 
 template <int D>
@@ -196,7 +208,7 @@ int launch_chunk(Kv4Args& a, void* workspace, cudaStream_t s) {
   if (int rc = opt_in_smem(kern, smem, done)) return rc;
   kern<<<n, kChThreads, smem, s>>>(a);
   if (int rc = launched()) return rc;
-  return launch_merge<D, kChRows>(a, n, kChRows / 8, s);
+  return launch_merge<D, kChRows>(a, n, s);
 }
 
 template <int D>
@@ -252,11 +264,9 @@ int fa_rope(const void* q, const long long* q_strides, void* q_out, const long l
                   static_cast<unsigned>((heads + a.heads_per_thread - 1) / a.heads_per_thread));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool il = flags & FA_ROPE_INTERLEAVED, inv = flags & FA_ROPE_INVERSE;
-  if (il && inv) rope_kernel<true, true><<<grid, kRopeThreads, 0, s>>>(a);
-  if (il && !inv) rope_kernel<true, false><<<grid, kRopeThreads, 0, s>>>(a);
-  if (!il && inv) rope_kernel<false, true><<<grid, kRopeThreads, 0, s>>>(a);
-  if (!il && !inv) rope_kernel<false, false><<<grid, kRopeThreads, 0, s>>>(a);
-  return launched();
+  auto kern = il ? inv ? rope_kernel<true, true> : rope_kernel<true, false>
+                 : inv ? rope_kernel<false, true> : rope_kernel<false, false>;
+  return launch_early(kern, grid, kRopeThreads, 0, s, a);
 }
 
 int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_width, int* queue,
@@ -292,9 +302,8 @@ int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_wid
   const long long items = num_tokens > 32ll * B ? num_tokens : 32ll * B;
   long long grid = (items + kPlanThreads - 1) / kPlanThreads;
   if (grid > kSms) grid = kSms;
-  page_plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, smem,
-                     static_cast<cudaStream_t>(stream)>>>(a);
-  return launched();
+  return launch_early(page_plan_kernel, static_cast<unsigned>(grid), kPlanThreads, smem,
+                static_cast<cudaStream_t>(stream), a);
 }
 
 size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d) {

@@ -18,6 +18,8 @@
 
 #include <cstdint>
 
+#include "rope.cuh"
+
 namespace exattn {
 
 constexpr int kPlanThreads = 512;
@@ -74,6 +76,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   __shared__ int warp_sums[kPlanThreads / 32][3];
   __shared__ int s_taken;
   if (threadIdx.x == 0) s_taken = 0;
+  grid_launch_dependents();
+  grid_wait();
 
   int head = a.state[0], count = a.state[1];
   count = min(max(count, 0), a.cap);

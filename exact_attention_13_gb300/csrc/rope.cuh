@@ -28,6 +28,15 @@ namespace exattn {
 
 constexpr int kRopeThreads = 128;
 
+// The kernels of a serving step follow each other at once: each is launched while the one before it
+// still runs (as soon as all of that one's blocks have started), and waits for its end and
+// its writes before it touches memory.  (Such a kernel's inputs may be written during its lifetime, so
+// the loads are ordinary ones, not those of the non-coherent path.)
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct RopeTensor {
   const __nv_bfloat16* x;
   __nv_bfloat16* y;
@@ -64,6 +73,8 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
 
 template <bool INTERLEAVED, bool INVERSE>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  grid_launch_dependents();
+  grid_wait();
   const int chunks = a.d / 16;
   const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const long long row = id / chunks;

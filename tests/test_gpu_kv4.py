@@ -430,6 +430,60 @@ def test_streams_and_two_captured_graphs():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_kernels_that_follow_each_other_across_streams(captured):
+    """plan, rope, append, read and attention, each of which may begin before the one before it has
+    ended, over forks and joins of two streams: the same bits as one after the other."""
+    d, page, T, Hq, Hkv = 128, 16, 300, 4, 2
+    B, width = 3, 40
+    table = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width).flip(0).contiguous()
+    queue, state = ints([0]), ints([0, 0])
+    k, v, q = (normal(T, h, d, seed=i).bfloat16().cuda() for i, h in enumerate((Hkv, Hkv, Hq)))
+    big = torch.randn(4096, 4096, device="cuda")
+    turns, m = ea.rope_turns(d)
+    side = torch.cuda.Stream()
+
+    def steps(two):
+        main, outs = torch.cuda.current_stream(), []
+        cache = torch.zeros(B * width, Hkv, 2, page * 9 * d // 16, dtype=torch.uint8, device="cuda")
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        for step in range(3):
+            plan = ea.page_plan(lens, lens, table, queue, state, page, T)
+            slots = (torch.arange(T, dtype=torch.int32, device="cuda") * (step + 1) % (B * width * page))
+            if two:
+                side.wait_stream(main)
+                with torch.cuda.stream(side):
+                    big @ big  # something long before the queries
+                    qr, _ = ea.rope(q, None, slots, turns, mscale=m)
+                kr, _ = ea.rope(k, None, slots, turns, mscale=m)
+                ea.kv4_append(kr, v, cache, slots)
+                main.wait_stream(side)
+            else:
+                qr, kr = ea.rope(q, k, slots, turns, mscale=m)
+                ea.kv4_append(kr, v, cache, slots)
+            rk, rv = ea.kv4_read(cache, slots, d)
+            o, lse = ea.kv4_fwd(qr, cache, table, torch.full((B,), 600, dtype=torch.int32, device="cuda"))
+            outs += [plan.slots, plan.lens, qr, kr, rk, rv, o, lse]
+        return outs
+
+    want = [x.clone() for x in steps(False)]
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            big @ big  # the library's own workspaces, before the capture
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            got = steps(True)
+        for _ in range(3):
+            graph.replay()
+    else:
+        got = steps(True)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
 def test_refusals():
     d, lens = 128, [5]
     cache, table = make(lens, 50, 16, 2, d)
