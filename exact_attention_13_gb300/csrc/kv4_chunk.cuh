@@ -36,8 +36,9 @@ constexpr int kChMmaWarp = 16;
 constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
 // 544 threads get 96 registers each at launch; the widening warpgroups give up what the softmax takes
-// (the MMA warp, alone in its warpgroup, keeps its 96).
-constexpr int kChLaunchRegs = 96, kChSoftmaxRegs = 136, kChWidenRegs = 56;
+// (the MMA warp, alone in its warpgroup, keeps its 96).  Four chunks of 512 tokens: 134.4 us with 136 and 56
+// registers, 131.0 with 128 and 64, 128.9 with 120 and 72, 130.8 with 112 and 80 (spilled registers either way).
+constexpr int kChLaunchRegs = 96, kChSoftmaxRegs = 120, kChWidenRegs = 72;
 static_assert(kChSoftmaxRegs + kChWidenRegs == 2 * kChLaunchRegs, "registers of the block at launch");
 
 __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {  // NaN: the other one
@@ -582,9 +583,11 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           }
           // Twice over the row's scores, 64 at a time: the maximum, then the probabilities.  (All 128
           // in registers as one unrolled body did not fit the instruction cache beside the other
-          // roles' and left no registers for a second group of widening warps; 16 at a time, loaded one
-          // step ahead, took 2500 cycles a tile.)  Masked and not are two copies of the code: selects
-          // for a mask that mostly leaves all cost a third of the instructions.
+          // roles'; 32 at a time: 134 us instead of 129; once over the scores, the reference moved
+          // between the halves and P published at the end: 148; S of 64 keys in two buffers a row
+          // tile, issued two steps ahead: 158, for Q is then read from shared memory twice as
+          // often.)  Masked and not are two copies of the code: selects for a mask that mostly leaves
+          // all cost a third of the instructions.
           const bool masked = holes || __any_sync(0xffffffffu, lim < kChKeys);
           // bit i: the row sees key i of 16-key group g
           auto seen16 = [&](int g) {
