@@ -29,6 +29,15 @@
 // cp.async stages, with its own softmax state: warps meet only at the end of a unit (one key head of
 // one block of rows).  A unit that crosses CTAs leaves partial sums (O, max, sum) in the workspace,
 // which a second kernel merges in a fixed order.
+//
+// Measured (2070 MHz, calls following each other).  64 requests of 500 to 8192 keys, 32 heads over 8, d 128:
+// 72 us, 321 MB at 4.5 TB/s; the slope over the length is 5.8 TB/s, about 11 us are start (lengths, page
+// ids and the first tiles follow each other from memory) and the units' begins and ends, 3 the merge.
+// 262144 keys of one request, 32 heads over 4: 37.8 us, 4.0 TB/s.  Up to 15 rows a key head, 24 heads
+// over 8, 16 requests: 50 us, 3.2 TB/s.  Instructions start in 56 % of the cycles (43 % beside 16 rows,
+// whose registers leave two warps a scheduler), the rest is waits for their fixed latencies.  Not
+// faster: loads to registers instead of the rings (100 us for the first case), four CTAs a SM, strips of
+// 64 keys at d 128, three stages, prefetches of page ids or of whole L2 lines.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -817,6 +826,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 // in up to eight parts each warp takes rows of its own; of one in more parts a block takes a row
 // and its warps share the parts.  Always summed in the same order.  Its time is latency (descriptor,
 // then maxima and sums of the parts together): all loads of a row are in flight at once.
+// It adds 3 us to a call for 64 requests, and 4 where the units of one are in 114 parts each.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
 template <int N>

@@ -18,7 +18,16 @@
 //
 // A CTA takes an equal share of the line of all tiles, as in kv4_attn.cuh; a unit that crosses CTAs
 // is merged from partial sums afterwards.  Units of one key head follow each other on the line, so
-// CTAs that run together read the same keys from L2.  Every mbarrier wait is bounded in time; one
+// CTAs that run together read the same keys from L2.
+//
+// Measured (2070 MHz).  One prompt of 65536 tokens, 8 heads over 1, d 128: 7.34 ms, 1199 TFLOP/s (0.62 of
+// cuBLAS bf16); four chunks of up to 512 tokens behind 4096 to 8192 keys, 32 heads over 8: 129 us,
+// 0.40 of it, 5 us of that the start, 18 the queries and outputs of the two or three shares of units a
+// CTA has, and 10 the merge.  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
+// tiles 2048 of them: S reads Q and K from shared memory at its full rate, beside which V is read and the
+// next tiles are written, and S of a row tile waits for its own softmax (2100 cycles) and P V.
+//
+// Every mbarrier wait is bounded in time; one
 // that runs out sets the CTA's abort flag and the status word, and all roles leave.
 #pragma once
 

@@ -131,7 +131,9 @@ int launch_rows(Kv4Rows a, int T, int heads, int d, int piece, void (*k64)(Kv4Ro
 }
 
 // ---------------------------------------------------------------------------------- attention
-// CTAs of one SM, by rows of a unit: 64 to 87 KB of shared memory and up to 168 (255) registers.
+// CTAs of one SM, by eights of rows of a unit: up to 168 registers a thread beside eight rows, 255
+// beside more.  (16 rows with three CTAs: 60 us instead of 50 for 16 requests of 15 rows, 57 with strips
+// of 16 keys; 8 rows with four: no gain.)
 constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 // Query rows that share a unit, in eights: the smallest of 8, 16 and 32 that hold the rows of one
@@ -297,8 +299,8 @@ int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_wid
   static std::atomic<uint64_t> done{0};
   if (int rc = opt_in_smem(page_plan_kernel, (3 * kPlanMaxBatch + 1) * 4, done)) return rc;
   // a warp per request and a thread per token, one CTA a SM at most: each repeats the scan over the
-  // lengths (1000 requests, 46,000 tokens: 15.8 us with four tokens a thread on a quarter of the
-  // CTAs; a single CTA for a small step)
+  // lengths (1000 requests, 46,000 tokens: 9.4 us; 15.8 with four tokens a thread on a quarter of
+  // the CTAs; a single CTA for a small step: 2.9 us)
   const long long items = num_tokens > 32ll * B ? num_tokens : 32ll * B;
   long long grid = (items + kPlanThreads - 1) / kPlanThreads;
   if (grid > kSms) grid = kSms;
