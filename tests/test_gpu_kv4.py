@@ -283,6 +283,42 @@ def test_prompt_chunks_with_masked_places_and_missing_pages():
     check_on_gpu(q, cache, table, lens, offsets, d, max_q=200)
 
 
+@pytest.mark.parametrize("d,B", [(64, 1200), (128, 545)])
+def test_many_requests_of_few_rows_as_chunks(d, B):
+    """``max_q`` only picks the kernel: more requests than a CTA has threads, most of a token or two,
+    some without tokens or keys, one long."""
+    rng = np.random.default_rng(B)
+    lens, qlens = rng.integers(0, 40, B), rng.integers(0, 3, B)
+    lens[B // 2], qlens[B // 2] = 900, 70
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    cache, table = make(lens.tolist(), 57, 16, 2, d)
+    check(queries(offsets[-1], 4, d), cache, table, lens.tolist(), offsets, d, max_q=70)
+
+
+def test_a_cache_of_more_than_4_gb():
+    """The same bits from pages past 2^32 bytes as from a small cache."""
+    d, page, Hq, Hkv, lens = 128, 128, 16, 8, [700, 200]
+    qlens = [3, 40]
+    width, offsets = 6, ints([0, 3, 43])
+    pages = 2 ** 32 // (2 * Hkv * page * 72) + 50
+    big = torch.empty((pages, Hkv, 2, page * 72), dtype=torch.uint8, device="cuda")
+    small = ea.kv4_cache(2 * width, Hkv, page, d)
+    high = torch.arange(pages - 2 * width, pages).view(2, width).flip(0)
+    assert int(high.min()) * 2 * Hkv * page * 72 > 2 ** 32
+    q, res = queries(43, Hq, d), []
+    for cache, table in ((small, torch.arange(2 * width).view(2, width)), (big, high)):
+        slots = torch.cat([table[b][torch.arange(n) // page] * page + torch.arange(n) % page
+                           for b, n in enumerate(lens)])
+        k, v = (normal(sum(lens), Hkv, d, seed=i).bfloat16().cuda() for i in (1, 2))
+        ea.kv4_append(k, v, cache, ints(slots))
+        res.append([*ea.kv4_read(cache, ints(slots), d)])
+        for max_q in (1, 4, 8, 40):
+            res[-1] += ea.kv4_fwd(q, cache, ints(table), ints(lens), q_offsets=offsets, max_q=max_q)
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+    assert not res[0][2].isnan().any()
+
+
 def test_prompts_of_many_blocks():
     """One prompt of 50 and one of 7 blocks of rows between short ones, on more and fewer key heads."""
     d, page, lens, qlens = 64, 64, [90, 3300, 70, 800, 40], [40, 3200, 70, 440, 33]
