@@ -69,7 +69,7 @@ def _ints(t, shape, index, name):
     if (t.dtype is not _i32 or t.get_device() != index or t.shape != shape
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
-    if t.numel() > 0x7fffffff and len(shape) == 1:  # the library's sizes are 32 bits
+    if shape[0] > 0x7fffffff:  # the library's sizes are 32 bits
         raise ValueError(f"{name} has more than 2^31 - 1 entries")
 
 
@@ -139,7 +139,9 @@ def _out_like(x, out, index, name):
     """`out`, or a new contiguous tensor like x, and its strides."""
     if out is None:
         out = torch.empty(x.shape, dtype=_bf16, device=x.device)
-    elif out.shape != x.shape:
+        s = out.stride()
+        return out, _strides(*s[:3]) if len(s) == 4 else _strides(0, s[1], s[0])
+    if out.shape != x.shape:
         raise ValueError(f"{name} must have its input's shape")
     return out, _heads(out, index, name)[1]
 
