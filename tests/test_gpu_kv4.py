@@ -64,6 +64,19 @@ def test_append_and_read_are_exact(d, page, H, T, kd, vd):
     assert same[~touched].all()  # nothing beside the rows was written
 
 
+def test_more_rows_than_one_launch_takes():
+    """2^24 + 5 tokens of 8 heads are more than 2^30 pieces: the last five go in a second launch."""
+    T, H, d, page = 2 ** 24 + 5, 8, 128, 16
+    cache = ea.kv4_cache(2, H, page, d)
+    rows = normal(1, H, d).bfloat16().cuda()
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    slots[0], slots[-3], slots[-1] = 4, 30, 17
+    ea.kv4_append(rows.expand(T, H, d), rows.expand(T, H, d), cache, slots)
+    small = ea.kv4_cache(2, H, page, d)
+    ea.kv4_append(rows.expand(3, H, d).contiguous(), rows.expand(3, H, d).contiguous(), small, ints([4, 30, 17]))
+    assert torch.equal(cache, small) and bool(cache.any())
+
+
 def test_extreme_values():
     d, page = 128, 16
     cache = ea.kv4_cache(1, 1, page, d)
@@ -401,6 +414,25 @@ def test_masked_places_hold_anything():
         rows = [0, 1, 2, 4, 5]
         assert torch.equal(o[rows], want[0][rows]) and torch.equal(lse[rows], want[1][rows])
         assert o[3].isnan().all() and lse[3].isnan().all()
+
+
+@pytest.mark.parametrize("max_q", [1, 8, 40])
+def test_infinite_and_nan_queries_stay_in_their_row(max_q):
+    d, lens, qlens = 128, [300, 90], [40, 5]
+    cache, table = make(lens, 5, 64, 2, d)
+    offsets = [0, 40, 45]
+    q = queries(45, 4, d)
+    args = (cache, ints(table), ints(lens), ints(offsets))
+    want = ea.kv4_fwd(q, *args, max_q=max_q)
+    bad = q.clone()
+    for row, head, value in ((0, 0, math.inf), (17, 3, -math.inf), (39, 1, math.nan), (44, 2, math.inf)):
+        bad[row, head, 7] = value
+    o, lse = ea.kv4_fwd(bad, *args, max_q=max_q)
+    hit = torch.zeros(45, 4, dtype=torch.bool)
+    hit[0, 0] = hit[17, 3] = hit[39, 1] = hit[44, 2] = True
+    assert torch.equal(o[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+    # a score of +inf leaves no finite softmax, nor does a NaN
+    assert o[hit].isnan().any(-1).all() and not lse[hit].isfinite().any()
 
 
 def test_bad_device_data_is_not_followed():

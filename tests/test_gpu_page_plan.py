@@ -33,7 +33,7 @@ def compare(lens, new, table, queue, state, page, T):
 
 @pytest.mark.parametrize("B,page,width,free,chunk", [
     (1, 16, 4, 3, 1), (8, 64, 8, 40, 1), (33, 16, 9, 150, 40), (600, 32, 5, 1000, 30),
-    (1025, 128, 2, 700, 100), (3, 16, 300, 20, 500),
+    (1025, 128, 2, 700, 100), (3, 16, 300, 20, 500), (16384, 16, 2, 9000, 4),
 ])
 def test_against_the_reference(B, page, width, free, chunk):
     rng = np.random.default_rng(B)
