@@ -6,7 +6,8 @@
 // free pages, and released pages go behind the free ones.  Request b is admitted iff its table row
 // is wide enough and need[b] = 0 or the running sum of need up to and with b is at most the number
 // of free pages; the running sum never falls, so the admitted takers are a prefix of the takers
-// and a request's first page is found from the exclusive sum alone.
+// and a request's first page is found from the exclusive sum alone.  A ring without room for all
+// released pages keeps the first cap - count of them; the rest are lost, none is free twice.
 //
 // One launch: every CTA computes the three prefix sums over all requests itself (B integers from
 // L2; a second launch or a device-wide barrier would cost more than the reads) and keeps them in
@@ -128,8 +129,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   };
   if (gthread == 0) {
     a.state_out[0] = ring(s_taken);
-    a.state_out[1] = static_cast<int>(min(static_cast<long long>(a.cap),
-                                          static_cast<long long>(count) - s_taken + total[2]));
+    // released pages count as far as they were stored: the places past `cap`, counted from the head, hold
+    // the pages that this step hands out
+    a.state_out[1] = count - s_taken + min(total[2], a.cap - count);
   }
   for (int r = gthread; r <= a.b; r += gthreads) {
     a.offsets[r] = s_tok[r];

@@ -264,8 +264,9 @@ FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
  * ceil(lens[b] / page_size)); it brings new_lens[b] tokens, or, with new_lens[b] < 0, it has ended
  * and its pages return to the free ones.
  *   queue, queue_state : ring of `queue_size` free page ids; queue_state = {head, count}: the free
- *                        pages are queue[(head + i) % queue_size], i < count.  The ring must have
- *                        room for every page there is
+ *                        pages are queue[(head + i) % queue_size], i < count.  The ring should have
+ *                        room for every page there is: of the pages that a step gets back it keeps
+ *                        the first queue_size - count (count as the step found it), the rest are lost
  * Requests take pages from the front in their order.  A request is refused (keeps its length and
  * pages, gets no slots) when its table row is too narrow, or when it needs pages and the sum of
  * all needs up to and with its own exceeds count.  Pages of ended requests become free behind the

@@ -103,3 +103,21 @@ def test_captured_into_a_graph_and_given_buffers():
         torch.cuda.synchronize()
         for g, w in zip([*out, ins[2], ins[3]], want):
             assert g.tolist() == w
+
+
+@pytest.mark.parametrize("cap", [4, 11, 60])
+def test_a_ring_without_room_for_every_page_gives_none_twice(cap):
+    """Pages come back to a ring that cannot hold them all: some are lost, no page is both free and a
+    request's, or free twice."""
+    rng = np.random.default_rng(cap)
+    B, page, width = 12, 16, 8
+    lens, table = rng.integers(0, width * page + 1, B), rng.permutation(B * width).reshape(B, width)
+    queue, state = [1000 + i for i in range(cap)], [cap // 2, cap]
+    for _ in range(12):
+        new = rng.integers(-1, 40, B)
+        got = compare(lens, new, table, queue, state, page, 500)
+        lens, state = got[0].cpu().numpy(), got[4].tolist()
+        table, queue = got[5].cpu().numpy(), got[6].tolist()
+        held = [p for b in range(B) for p in table[b, :-(-lens[b] // page)].tolist()]
+        idle = [queue[(state[0] + i) % cap] for i in range(state[1])]
+        assert len(set(held + idle)) == len(held + idle)

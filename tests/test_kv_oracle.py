@@ -133,3 +133,9 @@ def test_attention_matches_softmax():
     assert np.allclose(lse, s.logsumexp(-1).T, atol=1e-12)
     o, lse, *_ = kv.kv4_attention(q, cache, table, [2], [0, 3], d, 0.3, True)
     assert (o[0] == 0).all() and np.isneginf(lse[0]).all() and np.isfinite(lse[1:]).all()
+
+
+def test_page_plan_of_a_ring_too_small_gives_no_page_twice():
+    """1 takes two pages while 0 gives two back to a full ring: those are lost, 1's stay its own."""
+    out = kv.page_plan([32, 0], [-1, 32], [[10, 11], [0, 0]], [1, 2, 3, 4], [0, 4], 16, 32)
+    assert out[4] == [2, 2] and out[5][1] == [1, 2] and out[6] == [1, 2, 3, 4]
