@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         const int p = pos >> a.page_shift, have = pages(len);
         const int id = p < have ? a.table[static_cast<long long>(lo) * a.width + p]
                                 : a.queue[ring(s_need[lo] + p - have)];
-        slot = (id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        // an id that no cache has: its slot would wrap into another page
+        if (id >= 0 && id <= 0x7fffffff >> a.page_shift)
+          slot = (id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
       }
     }
     a.positions[t] = pos;

@@ -275,7 +275,8 @@ FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
  *   lens_out        : [B] lengths after the step (0 for ended requests)
  *   q_offsets       : [B + 1] first token of each request in the packed batch, and their number
  *   positions, slots: [num_tokens] position and cache slot (page * page_size + row) of each token;
- *                     slot -1 for tokens of refused requests; position 0 and slot -1 past the last
+ *                     slot -1 for tokens of refused requests and on page ids that no cache has
+ *                     (negative, or page_size * id >= 2^31); position 0 and slot -1 past the last
  *                     token.  num_tokens = 0: neither is written (they may be NULL)
  *   queue_state_out : {head, count} after the step
  *   num_tokens      : size of the packed batch, the refused requests' tokens included; tokens past

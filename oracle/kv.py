@@ -64,7 +64,8 @@ def page_plan(lens, new_lens, table, queue, state, page, num_tokens):
         offsets.append(offsets[-1] + add)
         for p in range(n, n + add):
             positions.append(p)
-            slots.append(table[b][p // page] * page + p % page if ok else -1)
+            slot = table[b][p // page] * page + p % page if ok else -1
+            slots.append(slot if 0 <= slot < 2 ** 31 else -1)
     back = back[:cap - count]  # what the ring has no room for is lost
     for i, p in enumerate(back):
         queue[(head + count + i) % cap] = p

@@ -121,3 +121,15 @@ def test_a_ring_without_room_for_every_page_gives_none_twice(cap):
         held = [p for b in range(B) for p in table[b, :-(-lens[b] // page)].tolist()]
         idle = [queue[(state[0] + i) % cap] for i in range(state[1])]
         assert len(set(held + idle)) == len(held + idle)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_page_ids_that_no_cache_has_give_no_slot(page):
+    """Ids in the table and in the ring whose slots would pass 31 bits and wrap into other pages."""
+    last = 2 ** 31 // page - 1  # the last page that slots can name
+    bad = [2 ** 32 // page, 2 ** 31 // page, -1, -2 ** 31, 2 ** 31 - 1, last]
+    table = np.array([[b, 3, 3] for b in bad] + [[3, 3, 3]])
+    lens, new = [5] * len(bad) + [0], [page] * len(bad) + [2 * page]
+    got = compare(lens, new, table, bad + [7] * 14, [0, 20], page, sum(new))
+    slots = got[3].cpu().numpy()
+    assert (slots[:5 * page] == -1).all() and slots.max() == 2 ** 31 - 1
