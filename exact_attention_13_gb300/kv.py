@@ -9,7 +9,10 @@ A serving step over a paged cache, all of it on the device:
     ea.kv4_append(k, v, cache, plan.slots)
     o, lse = ea.kv4_fwd(q, cache, table, plan.lens, plan.q_offsets, max_q=...)
 
-and in training, with the gradients of the rotated tensors turned back:
+A step without tokens (T = 0, as when all requests have just ended) passes through all of them: calls on
+no rows check their tensors and launch nothing.
+
+And in training, with the gradients of the rotated tensors turned back:
 
     qr, kr = ea.rope(q, k, positions, turns)                    # [B, H, N, d]
     o, lse = ea.fwd(qr, kr, v, causal=True)
@@ -173,6 +176,8 @@ def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = Fals
     if (turns.dtype is not torch.int64 or turns.dim() != 1 or turns.get_device() != index
             or not turns.is_contiguous()):
         raise ValueError(f"turns must be a contiguous int64 vector on cuda:{index}")
+    if B * N == 0:
+        return q_out, k_out
     _run("fa_rope", index, q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, kp, ks, ko, kos, Hk, B, N,
          d, positions.data_ptr(), N if per_batch else 0, turns.data_ptr(), 2 * turns.shape[0],
          (FA_ROPE_INTERLEAVED if interleaved else 0) | (FA_ROPE_INVERSE if inverse else 0),
@@ -270,6 +275,8 @@ def kv4_append(k, v, cache, slots, k_descale: float = 1.0, v_descale: float = 1.
     if heads != H or cache.get_device() != index:
         raise ValueError("the cache must have k's heads and device")
     _ints(slots, (T,), index, "slots")
+    if T == 0:
+        return
     _run("fa_kv4_append", index, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, cache.data_ptr(),
          pages, page, slots.data_ptr(), T, H, d, k_descale, v_descale)
 
@@ -292,6 +299,8 @@ def kv4_read(cache, slots, d: int, k_descale: float = 1.0, v_descale: float = 1.
         if (t.shape != shape or t.dtype is not _bf16 or t.get_device() != index
                 or not t.is_contiguous()):
             raise ValueError("k and v must be contiguous bf16 [T, H, d] tensors")
+    if T == 0:
+        return k, v
     _run("fa_kv4_read", index, cache.data_ptr(), pages, page, slots.data_ptr(), k.data_ptr(),
          v.data_ptr(), T, heads, d, k_descale, v_descale)
     return k, v
@@ -337,10 +346,6 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
         offsets = q_offsets.data_ptr()
     elif B < 1 or T % B:
         raise ValueError("without q_offsets T must be a multiple of B")
-    if max_q is None:
-        max_q = max(1, -(-T // max(B, 1)))
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=_bf16, device=q.device)
     elif (out.shape != q.shape or out.dtype is not _bf16 or out.get_device() != index
@@ -351,6 +356,12 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     elif (lse.shape != (T, Hq) or lse.dtype is not _f32 or lse.get_device() != index
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [T, Hq] tensor")
+    if T == 0:
+        return out, lse
+    if max_q is None:
+        max_q = max(1, -(-T // max(B, 1)))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
     scratch = None
     if workspace is None:
         size = kv4_workspace_bytes(Hq, Hkv, d, max_q, page, width)

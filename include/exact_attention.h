@@ -249,7 +249,7 @@ FA_API size_t fa_bwd_workspace_bytes(int B, int H, int N);
  *                     product with a position wraps to the exact fraction of a turn, so angles of
  *                     far positions keep fp32 accuracy.  Scalings for long contexts are made in
  *                     this table (and in mscale)
- *   d               : 64 or 128;  rotary_dim : a multiple of 16, <= d
+ *   B, N            : >= 1;  d : 64 or 128;  rotary_dim : a multiple of 16, <= d
  * Arithmetic is fp32 with one rounding to bf16.  Returns an fa_status; asynchronous like fa_fwd.
  */
 FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
@@ -311,7 +311,7 @@ FA_API size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d);
  *   cache     : device pointer (16-byte aligned)
  *   slots     : device int32 [T]; tokens whose slot lies outside the cache (-1) are skipped.  What
  *               a slot holds that several tokens of the call have is undefined, group by group
- *   d 64 or 128;  page_size 16, 32, 64 or 128;  num_pages * page_size < 2^31;  descales powers of
+ *   T >= 1;  d 64 or 128;  page_size 16, 32, 64 or 128;  num_pages * page_size < 2^31;  descales powers of
  *   two in [2^-61, 2^59]
  */
 FA_API int fa_kv4_append(const void* k, long long k_row_stride, long long k_head_stride,
@@ -346,7 +346,7 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *                 when that is 0), contents on entry do not matter; calls that may run at the same
  *                 time need one each
  *   dev_status  : as fa_fwd_opts.dev_status (NULL = the library's status word)
- *   sizes       : Hq a multiple of Hkv, T * Hq < 2^30, table_width * page_size <= 2^30; d,
+ *   sizes       : T and B >= 1, Hq a multiple of Hkv, T * Hq < 2^30, table_width * page_size <= 2^30; d,
  *                 page_size and descales as fa_kv4_append
  * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
  * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums

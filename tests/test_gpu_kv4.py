@@ -610,3 +610,33 @@ def test_a_serving_loop(d, page, Hq, Hkv):
         check(qr, cache, table.cpu().numpy(), plan.lens.tolist(), plan.q_offsets.tolist(), d, got=got)
         lens, state = plan.lens, plan.queue_state
     assert lens.tolist() == [36, 10, 23, 41]
+
+
+def test_a_step_without_tokens():
+    """All requests end: the plan gives their pages back and the other calls, on no rows, write nothing."""
+    d, page, Hq, Hkv = 128, 16, 8, 2
+    cache = ea.kv4_cache(6, Hkv, page, d)
+    cache.random_(0, 256, generator=torch.Generator("cuda").manual_seed(1))
+    before = cache.clone()
+    turns, _ = ea.rope_turns(d)
+    table, queue = ints([[0, 1, 2], [3, 4, 5]]), ints([9] * 6)
+    plan = ea.page_plan(ints([20, 40]), ints([-1, -1]), table, queue, ints([0, 0]), page, 0)
+    assert plan.lens.tolist() == [0, 0] and plan.q_offsets.tolist() == [0, 0, 0]
+    assert plan.queue_state.tolist() == [0, 5] and sorted(queue.tolist()) == [0, 1, 3, 4, 5, 9]
+    q, k = queries(0, Hq, d), queries(0, Hkv, d)
+    qr, kr = ea.rope(q, k, plan.positions, turns)
+    assert qr.shape == q.shape and kr.shape == k.shape
+    ea.kv4_append(kr, k, cache, plan.slots)
+    assert [x.shape for x in ea.kv4_read(cache, plan.slots, d)] == [k.shape, k.shape]
+    for kw in (dict(q_offsets=plan.q_offsets, max_q=max(-1, -1)), dict(q_offsets=plan.q_offsets, max_q=0), {}):
+        o, lse = ea.kv4_fwd(qr, cache, table, plan.lens, **kw)
+        assert o.shape == q.shape and lse.shape == (0, Hq)
+    assert torch.equal(cache, before)
+    for shape in ((2, 4, 0, d), (0, 4, 7, d)):  # training tensors of no rows
+        x = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        y, _ = ea.rope(x, x, torch.zeros(shape[2], dtype=torch.int32, device="cuda"), turns, inverse=True)
+        assert y.shape == x.shape
+    with pytest.raises(ValueError):
+        ea.kv4_fwd(q.float(), cache, table, plan.lens)
+    with pytest.raises(ValueError):
+        ea.kv4_append(k, k, cache, ints([1]))
