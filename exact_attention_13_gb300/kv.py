@@ -240,12 +240,18 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
 # the 4-bit cache
 # ---------------------------------------------------------------------------------------------
 def kv4_cache(num_pages: int, heads: int, page_size: int, d: int, device="cuda"):
-    """An empty 4-bit cache: uint8 zeros [num_pages, heads, 2, page_size * 9 d / 16]."""
+    """An empty 4-bit cache: uint8 zeros [num_pages, heads, 2, page_size * 9 d / 16].
+
+    The bytes alone do not tell pages of 128 tokens with d = 64 from pages of 64 tokens with d = 128 (or 64
+    from 32, 32 from 16).  The tensor returned here remembers its d, and calls with the other one are
+    refused; on its views and copies the caller has to keep to d."""
     total = int(_fn("fa_kv4_cache_bytes")(num_pages, heads, page_size, d))
     _need(total > 0, f"unsupported cache (pages {num_pages}, heads {heads}, page size {page_size},"
                      f" d {d})")
-    return torch.zeros((num_pages, heads, 2, total // (2 * num_pages * heads)), dtype=torch.uint8,
-                       device=device)
+    cache = torch.zeros((num_pages, heads, 2, total // (2 * num_pages * heads)), dtype=torch.uint8,
+                        device=device)
+    cache._kv4_d = d
+    return cache
 
 
 def _cache_shape(cache, d):
@@ -256,6 +262,8 @@ def _cache_shape(cache, d):
     page, rest = divmod(block * 16, 9 * d)
     if rest or two != 2 or cache.dtype is not torch.uint8 or not cache.is_contiguous():
         raise ValueError(f"cache must be a contiguous uint8 tensor as kv4_cache makes it for d = {d}")
+    if getattr(cache, "_kv4_d", d) != d:
+        raise ValueError(f"the cache was made for d = {cache._kv4_d}, not {d}")
     return pages, heads, page
 
 

@@ -300,7 +300,8 @@ FA_API int fa_page_plan(const int* lens, const int* new_lens, int* table, int ta
  *     value = code * scale * descale              (both roundings to nearest even, saturating)
  * descale is one power of two per tensor, the same in every call on the cache.  A head vector that
  * holds a NaN or an infinity reads back as NaN.  Slot s is row s % page_size of page s / page_size.
- * Bytes of such a cache; 0 for invalid arguments.
+ * The bytes do not tell (d 64, page_size 2 p) from (d 128, page_size p): all calls on a cache take those
+ * that it was made for.  Bytes of such a cache; 0 for invalid arguments.
  */
 FA_API size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d);
 

@@ -640,3 +640,13 @@ def test_a_step_without_tokens():
         ea.kv4_fwd(q.float(), cache, table, plan.lens)
     with pytest.raises(ValueError):
         ea.kv4_append(k, k, cache, ints([1]))
+
+
+def test_calls_with_the_other_head_dim_are_refused():
+    cache, slots = ea.kv4_cache(4, 2, 128, 64), ints([0])
+    wide = normal(1, 2, 128).bfloat16().cuda()
+    for call in (lambda: ea.kv4_read(cache, slots, 128), lambda: ea.kv4_append(wide, wide, cache, slots),
+                 lambda: ea.kv4_fwd(wide, cache, ints([[0]]), ints([1]))):
+        with pytest.raises(ValueError, match="made for d = 64"):
+            call()
+    assert ea.kv4_read(cache, slots, 64)[0].shape == (1, 2, 64)

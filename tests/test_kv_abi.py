@@ -118,3 +118,15 @@ def test_python_checks():
         ea.kv4_cache(2, 2, 20, 128, device="cpu")
     with pytest.raises(AttributeError):
         ea.no_such_name
+
+
+@pytest.mark.parametrize("page,d,other", [(128, 64, 128), (32, 64, 128), (64, 128, 64), (16, 128, 64)])
+def test_a_cache_is_read_with_its_own_head_dim(page, d, other):
+    """Both head dims divide its bytes: the other one would be read as pages of another size."""
+    from exact_attention_13_gb300 import kv
+
+    cache = ea.kv4_cache(3, 2, page, d, device="cpu")
+    assert kv._cache_shape(cache, d) == (3, 2, page)
+    with pytest.raises(ValueError, match=f"made for d = {d}"):
+        kv._cache_shape(cache, other)
+    assert kv._cache_shape(torch.empty_like(cache), d) == (3, 2, page)
