@@ -309,7 +309,8 @@ int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_wid
 }
 
 size_t fa_kv4_cache_bytes(int num_pages, int Hkv, int page_size, int d) {
-  if (num_pages < 1 || Hkv < 1 || !page_size_ok(page_size) || (d != 64 && d != 128)) return 0;
+  if (num_pages < 1 || Hkv < 1 || Hkv > 65535 || !page_size_ok(page_size) || (d != 64 && d != 128)) return 0;
+  if (static_cast<long long>(num_pages) * page_size > 0x7fffffffll) return 0;
   return static_cast<size_t>(num_pages) * Hkv * 2 * kv4_block_bytes(page_size, d);
 }
 

@@ -35,6 +35,7 @@ _bf16, _i32, _f32 = torch.bfloat16, torch.int32, torch.float32
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _bound = {}
+_most = 0x7fffffff  # the library's sizes are 32 bits, and ctypes drops what lies above them
 
 
 def _fn(name):
@@ -72,8 +73,8 @@ def _ints(t, shape, index, name):
     if (t.dtype is not _i32 or t.get_device() != index or t.shape != shape
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
-    if shape[0] > 0x7fffffff:  # the library's sizes are 32 bits
-        raise ValueError(f"{name} has more than 2^31 - 1 entries")
+    if shape[0] > _most or shape[-1] > _most:
+        raise ValueError(f"{name} has a side of more than 2^31 - 1 entries")
 
 
 # ---------------------------------------------------------------------------------------------
@@ -211,9 +212,9 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
     ``queue_state`` must not be this call's inputs."""
     index = lens.get_device()
     if (index < 0 or lens.dim() != 1 or table.dim() != 2 or queue.dim() != 1
-            or not 0 <= num_tokens < 2 ** 31):
+            or not 0 <= num_tokens <= _most or not 0 < page_size <= _most):
         raise ValueError("lens and queue must be int32 CUDA vectors, table [B, width], num_tokens in "
-                         "[0, 2^31)")
+                         "[0, 2^31), page_size in (0, 2^31)")
     B, width, cap = lens.shape[0], table.shape[1], queue.shape[0]
     _ints(lens, (B,), index, "lens")
     _ints(new_lens, (B,), index, "new_lens")
@@ -245,7 +246,9 @@ def kv4_cache(num_pages: int, heads: int, page_size: int, d: int, device="cuda")
     The bytes alone do not tell pages of 128 tokens with d = 64 from pages of 64 tokens with d = 128 (or 64
     from 32, 32 from 16).  The tensor returned here remembers its d, and calls with the other one are
     refused; on its views and copies the caller has to keep to d."""
-    total = int(_fn("fa_kv4_cache_bytes")(num_pages, heads, page_size, d))
+    total = 0
+    if all(0 < n <= _most for n in (num_pages, heads, page_size, d)):
+        total = int(_fn("fa_kv4_cache_bytes")(num_pages, heads, page_size, d))
     _need(total > 0, f"unsupported cache (pages {num_pages}, heads {heads}, page size {page_size},"
                      f" d {d})")
     cache = torch.zeros((num_pages, heads, 2, total // (2 * num_pages * heads)), dtype=torch.uint8,
@@ -318,7 +321,9 @@ def kv4_read(cache, slots, d: int, k_descale: float = 1.0, v_descale: float = 1.
 def kv4_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int, page_size: int, width: int) -> int:
     """Bytes of scratch ``kv4_fwd`` needs for tables of ``width`` pages, whatever the lengths are
     (0: none, when no key head's work is ever split)."""
-    return int(_fn("fa_kv4_fwd_workspace_bytes")(Hq, Hkv, d, max_q, page_size, width))
+    if max(Hq, Hkv, d, page_size, width) > _most:
+        return 0  # as for other invalid arguments
+    return int(_fn("fa_kv4_fwd_workspace_bytes")(Hq, Hkv, d, min(max_q, _most), page_size, width))
 
 
 def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, causal: bool = True,
@@ -368,6 +373,8 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
         return out, lse
     if max_q is None:
         max_q = max(1, -(-T // max(B, 1)))
+    elif max_q > _most:
+        max_q = _most
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     scratch = None

@@ -650,3 +650,11 @@ def test_calls_with_the_other_head_dim_are_refused():
         with pytest.raises(ValueError, match="made for d = 64"):
             call()
     assert ea.kv4_read(cache, slots, 64)[0].shape == (1, 2, 64)
+
+
+def test_the_largest_max_q():
+    """Any max_q from 1 on is correct, as documented, those past 32 bits too."""
+    d, lens, qlens = 64, [300, 90], [3, 2]
+    cache, table = make(lens, 5, 64, 2, d)
+    for max_q in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 1):
+        check(queries(5, 4, d), cache, table, lens, [0, 3, 5], d, max_q=max_q)

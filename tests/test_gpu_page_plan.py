@@ -133,3 +133,12 @@ def test_page_ids_that_no_cache_has_give_no_slot(page):
     got = compare(lens, new, table, bad + [7] * 14, [0, 20], page, sum(new))
     slots = got[3].cpu().numpy()
     assert (slots[:5 * page] == -1).all() and slots.max() == 2 ** 31 - 1
+
+
+def test_page_sizes_past_32_bits_are_refused():
+    cuda = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    args = cuda([0]), cuda([3]), cuda([[0, 0]]), cuda([3, 1]), cuda([0, 2])
+    for page in (2 ** 32 + 16, -16, 0):
+        with pytest.raises(ValueError):
+            ea.page_plan(*args, page, 3)
+    assert ea.page_plan(*args, 16, 3).slots.tolist() == [48, 49, 50]

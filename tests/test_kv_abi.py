@@ -130,3 +130,25 @@ def test_a_cache_is_read_with_its_own_head_dim(page, d, other):
     with pytest.raises(ValueError, match=f"made for d = {d}"):
         kv._cache_shape(cache, other)
     assert kv._cache_shape(torch.empty_like(cache), d) == (3, 2, page)
+
+
+def test_sizes_past_32_bits_are_refused_not_cut():
+    from exact_attention_13_gb300 import kv
+
+    for bad in ((2 ** 32 + 3, 2, 16, 64), (3, 2 ** 32 + 2, 16, 64), (3, 2, 2 ** 32 + 16, 64),
+                (3, 2, 16, 2 ** 32 + 64), (-1, 2, 16, 64)):
+        with pytest.raises(ValueError):
+            ea.kv4_cache(*bad, device="meta")
+    # sizes that the calls on a cache refuse: 2^31 slots, 65536 heads
+    for bad in ((2 ** 27, 1, 16, 64), (2 ** 24, 1, 128, 128), (1, 65536, 16, 64)):
+        assert ea.lib().fa_kv4_cache_bytes(*bad) == 0
+        with pytest.raises(ValueError):
+            ea.kv4_cache(*bad, device="meta")
+    assert ea.kv4_cache(2 ** 27 - 1, 1, 16, 64, device="meta").shape == (2 ** 27 - 1, 1, 2, 16 * 36)
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 2 ** 32 + 64, 100) == 0
+    assert ea.kv4_workspace_bytes(4, 2, 128, 1, 64, 2 ** 32 + 100) == 0
+    assert ea.kv4_workspace_bytes(4, 2, 128, 2 ** 40, 64, 100) == ea.kv4_workspace_bytes(4, 2, 128, 2 ** 20, 64, 100)
+    for shape in ((2 ** 31,), (1, 2 ** 32 + 4), (2, 2 ** 31)):
+        wide = torch.empty(shape, dtype=torch.int32, device="meta")
+        with pytest.raises(ValueError, match="2\\^31 - 1"):
+            kv._ints(wide, shape, wide.get_device(), "table")
