@@ -369,6 +369,9 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     elif (lse.shape != (T, Hq) or lse.dtype is not _f32 or lse.get_device() != index
           or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [T, Hq] tensor")
+    if status is not None and (status.dtype is not _i32 or status.get_device() != index
+                               or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor of one element on q's device")
     if T == 0:
         return out, lse
     if max_q is None:

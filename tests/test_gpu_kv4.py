@@ -658,3 +658,19 @@ def test_the_largest_max_q():
     cache, table = make(lens, 5, 64, 2, d)
     for max_q in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 1):
         check(queries(5, 4, d), cache, table, lens, [0, 3, 5], d, max_q=max_q)
+
+
+def test_a_status_word_elsewhere_is_refused():
+    """The kernel writes to it when a wait runs out: not to host memory, nor 4 bytes into fewer."""
+    d, lens = 64, [70]
+    cache, table = make(lens, 5, 64, 2, d)
+    q, args = queries(1, 4, d), (ints(table), ints(lens))
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int16).cuda(),
+                torch.zeros(0, dtype=torch.int32).cuda()):
+        with pytest.raises(ValueError, match="status"):
+            ea.kv4_fwd(q, cache, *args, status=bad)
+    word = torch.full((1,), 7, dtype=torch.int32).cuda()
+    for max_q in (1, 64):
+        a = ea.kv4_fwd(q, cache, *args, max_q=max_q, status=word)
+        b = ea.kv4_fwd(q, cache, *args, max_q=max_q)
+        assert torch.equal(a[0], b[0]) and word.item() == 7
