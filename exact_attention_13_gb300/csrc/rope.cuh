@@ -9,8 +9,9 @@
 // Angles.  p f_i in fp32 is off by up to 2^-24 p f_i radians: at position 2^17 already 2^-7.  The
 // step f_i is therefore held as a 64-bit fixed-point fraction of a turn (unit 2^-64 turn), and
 // p * step in wrapping 64-bit integer arithmetic IS the fractional part of the angle in turns:
-// the whole turns drop out of the product by themselves.  The step's rounding (2^-65 turn) times
-// p < 2^31 leaves at most 2^-34 turn; the top 32 bits, rounded to fp32, go to sincospif (2^-25 of
+// the whole turns drop out of the product by themselves.  The step's rounding (2^-65 turn in a table made
+// with enough digits; one made in doubles is off by up to 2^-55) times p < 2^31 leaves at most 2^-34
+// turn; the top 32 bits, rounded to fp32, go to sincospif (2^-25 of
 // half a turn).  Arithmetic is fp32, one rounding to bf16 at the end.
 //
 // One thread owns one row (batch, position) and one 16-value chunk of the head -- eight pairs, two

@@ -22,6 +22,7 @@ And in training, with the gradients of the rotated tensors turned back:
 from __future__ import annotations
 
 import ctypes
+import decimal
 import functools
 import math
 from typing import NamedTuple
@@ -80,6 +81,9 @@ def _ints(t, shape, index, name):
 # ---------------------------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------------------------
+_PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510")
+
+
 def rope_turns(rotary_dim: int, base: float = 10000.0, scaling: str | None = None,
                factor: float = 1.0, context: int = 4096, beta_fast: float = 32.0,
                beta_slow: float = 1.0, device="cuda"):
@@ -95,32 +99,38 @@ def rope_turns(rotary_dim: int, base: float = 10000.0, scaling: str | None = Non
       ``context``, f_i / factor where it turns less than ``beta_slow`` times, a linear ramp over the
       pairs between; mscale = 0.1 ln(factor) + 1
 
-    ``turns`` is int64, f_i / (2 pi) in units of 2^-64 turn."""
+    ``turns`` is int64, f_i / (2 pi) in units of 2^-64 turn, rounded to nearest: computed with 50 digits,
+    because the 53 bits of a double leave an error of up to 2^9 units."""
     _need(rotary_dim >= 2 and rotary_dim % 2 == 0, "rotary_dim must be even")
     _need(math.isfinite(base) and base >= 1 and math.isfinite(factor) and factor >= 1,
           "base and factor must be finite and >= 1")
-    r, mscale = rotary_dim, 1.0
-    if scaling == "base" and r > 2:
-        base = base * factor ** (r / (r - 2))
-    f = [base ** (-2.0 * i / r) for i in range(r // 2)]
-    if scaling == "linear":
-        f = [x / factor for x in f]
-    elif scaling == "parts":
-        _need(context >= 1 and base > 1 and beta_fast > beta_slow > 0,
-              "parts needs context >= 1, base > 1 and beta_fast > beta_slow > 0")
+    r, mscale = int(rotary_dim), 1.0
+    exact = decimal.Context(prec=50)
+    base_x, factor_x = decimal.Decimal(float(base)), decimal.Decimal(float(factor))
+    with decimal.localcontext(exact):
+        if scaling == "base" and r > 2:
+            base_x *= factor_x ** (decimal.Decimal(r) / (r - 2))
+        f = [base_x ** (decimal.Decimal(-2 * i) / r) for i in range(r // 2)]
+        if scaling == "linear":
+            f = [x / factor_x for x in f]
+        elif scaling == "parts":
+            _need(context >= 1 and base > 1 and beta_fast > beta_slow > 0,
+                  "parts needs context >= 1, base > 1 and beta_fast > beta_slow > 0")
 
-        def pair_that_turns(times):
-            return r * math.log(context / (times * 2 * math.pi)) / (2 * math.log(base))
+            def pair_that_turns(times):
+                return r * math.log(context / (times * 2 * math.pi)) / (2 * math.log(base))
 
-        lo = max(math.floor(pair_that_turns(beta_fast)), 0)
-        hi = min(math.ceil(pair_that_turns(beta_slow)), r - 1)
-        ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(r // 2)]
-        f = [x / factor * w + x * (1 - w) for x, w in zip(f, ramp)]
-        mscale = 0.1 * math.log(factor) + 1.0
-    else:
-        _need(scaling in (None, "base"), f"unknown scaling {scaling!r}")
-    unit = 2.0 ** 64 / (2 * math.pi)
-    return torch.tensor([round(x * unit) for x in f], dtype=torch.int64, device=device), mscale
+            lo = max(math.floor(pair_that_turns(beta_fast)), 0)
+            hi = min(math.ceil(pair_that_turns(beta_slow)), r - 1)
+            width = decimal.Decimal(hi - lo) if hi > lo else decimal.Decimal("1e-3")
+            ramp = [min(max((i - lo) / width, 0), 1) for i in range(r // 2)]
+            f = [x / factor_x * w + x * (1 - w) for x, w in zip(f, ramp)]
+            mscale = 0.1 * math.log(factor) + 1.0
+        else:
+            _need(scaling in (None, "base"), f"unknown scaling {scaling!r}")
+        unit = 2 ** 64 / (2 * _PI)
+        turns = [int((x * unit).to_integral_value(decimal.ROUND_HALF_EVEN)) for x in f]
+    return torch.tensor(turns, dtype=torch.int64, device=device), mscale
 
 
 def _heads(x, index, name):

@@ -139,3 +139,65 @@ def test_page_plan_of_a_ring_too_small_gives_no_page_twice():
     """1 takes two pages while 0 gives two back to a full ring: those are lost, 1's stay its own."""
     out = kv.page_plan([32, 0], [-1, 32], [[10, 11], [0, 0]], [1, 2, 3, 4], [0, 4], 16, 32)
     assert out[4] == [2, 2] and out[5][1] == [1, 2] and out[6] == [1, 2, 3, 4]
+
+
+def _pi_times(scale):
+    """floor(pi * scale), nearly: 16 atan(1/5) - 4 atan(1/239) in integers, with guard digits."""
+    guard = 10 ** 20
+
+    def atan_inverse(n):
+        term, total, k = scale * guard // n, 0, 0
+        while term:
+            total += (-term if k % 2 else term) // (2 * k + 1)
+            term //= n * n
+            k += 1
+        return total
+
+    return (16 * atan_inverse(5) - 4 * atan_inverse(239)) // guard
+
+
+def _root(x, n, one):
+    """The n-th root of x / one in units of 1 / one, by bisection in integers."""
+    lo, hi = 0, max(x, one) + 1
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        y = one
+        for _ in range(n):
+            y = y * mid // one
+        lo, hi = (mid, hi) if y <= x else (lo, mid)
+    return lo
+
+
+@pytest.mark.parametrize("r,base", [(128, 10000), (64, 500000), (16, 10000), (48, 10007)])
+@pytest.mark.parametrize("scaling,factor", [(None, 1), ("linear", 4), ("base", 8)])
+def test_rope_turns_are_right_to_their_last_bit(r, base, scaling, factor):
+    """Against roots and pi in integers of 60 digits: entries are the rounded f_i / (2 pi), so off by half a
+    unit of 2^-64 turn at most (and 2^-40 of one for the integers here)."""
+    one = 10 ** 60
+    turns = ea.rope_turns(r, base=base, scaling=scaling, factor=factor, device="cpu")[0].tolist()
+    ratio = one * one // _root(base * one, r // 2, one)  # f_1 / f_0 of the plain table
+    if scaling == "base":  # (base * factor^(r / (r - 2)))^(-2 / r) = base^(-2 / r) factor^(-2 / (r - 2))
+        ratio = ratio * one // _root(factor * one, (r - 2) // 2, one)
+    f, two_pi = one // (factor if scaling == "linear" else 1), 2 * _pi_times(one)
+    for t in turns:
+        units = f * one // two_pi * 2 ** 64
+        assert abs(t * one - units) <= one // 2 + one // 2 ** 40
+        f = f * ratio // one
+
+
+def test_rope_turns_by_parts_and_under_a_callers_decimal_context():
+    """Each entry by parts is the mean, with the ramp's weight, of the plain one and of the one divided by
+    the factor: three roundings.  The caller's precision is neither used nor changed."""
+    import decimal
+
+    with decimal.localcontext() as ctx:
+        ctx.prec = 3
+        plain = ea.rope_turns(128, device="cpu")[0].tolist()
+        parts = ea.rope_turns(128, scaling="parts", factor=8.0, context=4096, device="cpu")[0].tolist()
+        assert decimal.getcontext().prec == 3
+    assert plain == ea.rope_turns(128, device="cpu")[0].tolist()
+    at = lambda times: 128 * math.log(4096 / (times * 2 * math.pi)) / (2 * math.log(10000.0))  # noqa: E731
+    lo, hi = math.floor(at(32.0)), math.ceil(at(1.0))
+    for i, (x, y) in enumerate(zip(plain, parts)):
+        w = min(max(i - lo, 0), hi - lo)  # of hi - lo
+        assert abs(8 * (hi - lo) * y - x * (w + 8 * (hi - lo - w))) <= 8 * (hi - lo)
