@@ -674,3 +674,151 @@ def test_a_status_word_elsewhere_is_refused():
         a = ea.kv4_fwd(q, cache, *args, max_q=max_q, status=word)
         b = ea.kv4_fwd(q, cache, *args, max_q=max_q)
         assert torch.equal(a[0], b[0]) and word.item() == 7
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_each_call_waits_for_what_the_one_before_it_writes(captured):
+    """plan -> rope -> rope -> append -> read -> attention -> plan -> plan ..., each on the outputs of the ones before,
+    with no other kernel between them: the same bits as with a wait after every call.  All outputs hold
+    other values beforehand, so a kernel that reads too early takes those."""
+    d, page, Hq, Hkv, B, width = 128, 64, 16, 4, 64, 12
+    rng = np.random.default_rng(11)
+    news = [rng.integers(300, 500, B), np.ones(B, int), rng.integers(-1, 5, B), rng.integers(0, 9, B)]
+    sizes = [int(np.maximum(n, 0).sum()) + 1 for n in news]
+    new = [ints(n) for n in news]
+    q, k, v = ([queries(T, h, d, seed=40 * i + s) for s, T in enumerate(sizes)]
+               for i, h in enumerate((Hq, Hkv, Hkv)))
+    turns, m = ea.rope_turns(d)
+    queue0, big = ints(rng.permutation(B * width)), torch.randn(8192, 8192, device="cuda").bfloat16()
+    work = max(ea.kv4_workspace_bytes(Hq, Hkv, d, int(n.max()), page, width) for n in news)
+    bf16 = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    plan = lambda T: ea.PagePlan(*(torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+                                   for n in (B, B + 1, T, T, 2)))
+    state = [torch.empty(B, width, dtype=torch.int32, device="cuda"), torch.empty_like(queue0),
+             torch.empty(B * width, Hkv, 2, page * 9 * d // 16, dtype=torch.uint8, device="cuda")]
+    lens0, count0, ws = ints([0] * B), ints([0, B * width]), torch.empty(work, dtype=torch.uint8, device="cuda")
+    outs = [(plan(T), plan(0), bf16(T, Hq, d), bf16(T, Hkv, d), bf16(T, Hq, d), bf16(T, Hkv, d), bf16(T, Hkv, d),
+             bf16(T, Hq, d), torch.empty(T, Hq, device="cuda")) for T in sizes]
+
+    def reset():
+        state[0].fill_(0)
+        state[1].copy_(queue0)
+        state[2].fill_(255)
+        ws.fill_(255)
+        for step in outs:
+            for t in step:
+                for x in t if isinstance(t, tuple) else (t,):
+                    x.fill_(3 if x.dtype is torch.int32 else math.nan)
+
+    def chain(wait):
+        (table, queue, cache), lens, count = state, lens0, count0
+        for s, (p, p2, qr, kr, qb, ko, vo, o, lse) in enumerate(outs):
+            for call in (lambda: ea.page_plan(lens, new[s], table, queue, count, page, sizes[s], out=p),
+                         lambda: ea.rope(q[s], k[s], p.positions, turns, mscale=m, q_out=qr, k_out=kr),
+                         lambda: ea.rope(qr, None, p.positions, turns, inverse=True, q_out=qb),
+                         lambda: ea.kv4_append(kr, v[s], cache, p.slots),
+                         lambda: ea.kv4_read(cache, p.slots, d, k=ko, v=vo),
+                         lambda: ea.kv4_fwd(qr, cache, table, p.lens, p.q_offsets, max_q=int(news[s].max()),
+                                            out=o, lse=lse, workspace=ws),
+                         lambda: ea.page_plan(p.lens, lens0, table, queue, p.queue_state, page, 0, out=p2)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            lens, count = p2.lens, p2.queue_state
+
+    def results():
+        torch.cuda.synchronize()
+        flat = [x for step in outs for t in step for x in (t if isinstance(t, tuple) else (t,))]
+        return [x.view(torch.uint8).clone() for x in flat + state]
+
+    reset()
+    chain(True)
+    want = results()
+    assert outs[-1][0].lens.sum() > 0 and not outs[0][7][:-1].isnan().any()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain(False)
+    for _ in range(3):
+        reset()
+        if captured:
+            graph.replay()
+        else:
+            for _ in range(8):  # the host runs ahead meanwhile
+                big @ big
+            chain(False)
+        for x, y in zip(results(), want):
+            assert torch.equal(x, y)
+
+
+def test_rows_on_both_sides_of_a_launch_border():
+    """An append takes 2^30 / 64 tokens of 8 heads of 128 in a launch, a read 2^30 / 128: rows around those
+    borders, on rows that differ (windows of one buffer, 8 values apart)."""
+    H, d, page, T = 8, 128, 16, 2 ** 24 + 5
+    flat = torch.randn(8 * T + 2 * H * d, device="cuda").bfloat16()
+    k = flat.as_strided((T, H, d), (8, 128, 1))
+    v = flat[8:].as_strided((T, H, d), (8, 64, 1))
+    at = [0, 2 ** 23 - 1, 2 ** 23, 2 ** 23 + 1, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 1, T - 1]
+    where = torch.tensor(at).cuda()
+    cache, small = ea.kv4_cache(2, H, page, d), ea.kv4_cache(2, H, page, d)
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    own = ints([4, 30, 17, 0, 9, 31, 2, 16])
+    slots[where] = own
+    ea.kv4_append(k, v, cache, slots)
+    ea.kv4_append(k[where].contiguous(), v[where].contiguous(), small, own)
+    assert torch.equal(cache, small) and len({bytes(x) for x in small[:, 0, 0].cpu().numpy()}) == 2
+    want = ea.kv4_read(small, own, d)
+    T = 2 ** 23 + 9  # two launches
+    slots = slots[:T].contiguous()
+    got = ea.kv4_read(cache, slots, d)
+    inside = where[where < T]
+    for x, y in zip(got, want):
+        assert torch.equal(x[inside], y[:len(inside)])
+        x[inside] = 0
+        assert not any(bool(part.view(torch.int32).any()) for part in x.split(2 ** 20))
+    del got, x
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,max_q,Hq", [(129, 1, 4), (300, 1, 4), (129, 8, 2), (300, 8, 4)])
+def test_more_requests_than_threads_with_split_units(d, B, max_q, Hq):
+    """The line of work found in pieces of 128 requests, beside units that cross CTAs: lengths of nothing
+    to thousands, requests without queries."""
+    rng = np.random.default_rng(B + max_q)
+    page, width = 32, 130
+    lens = rng.integers(0, 200, B)
+    lens[rng.integers(0, B, 6)] = 0
+    lens[[3, 127, 128, B - 1]] = 4100, 1, 3000, 2500
+    qlens = rng.integers(0, max_q + 1, B)
+    qlens[[3, 127, 128, B - 1]] = max_q
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    cache, table = make(lens.tolist(), width, page, 1, d)
+    size = ea.kv4_workspace_bytes(Hq, 1, d, max_q, page, width)
+    assert size > 0
+    ws = torch.full((size,), 255, dtype=torch.uint8).cuda()
+    check_on_gpu(queries(offsets[-1], Hq, d), cache, table, lens.tolist(), offsets, d, max_q=max_q, workspace=ws)
+
+
+def test_strides_past_32_bits():
+    """Queries, keys and values whose rows lie 2^26 values apart: the last ones beyond 2^32."""
+    d, page, Hq, Hkv, T, far = 64, 16, 4, 2, 70, 2 ** 26
+    flat = torch.empty((T - 1) * far + (Hq + 2 * Hkv) * d, dtype=torch.bfloat16, device="cuda")
+    rows = flat.as_strided((T, Hq + 2 * Hkv, d), (far, d, 1))
+    near = queries(T, Hq + 2 * Hkv, d)
+    rows.copy_(near)
+    turns, _ = ea.rope_turns(d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    res = []
+    for x in (near, rows):
+        q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        cache = ea.kv4_cache(5, Hkv, page, d)
+        ea.rope(q, k, pos, turns, q_out=q, k_out=k)
+        ea.kv4_append(k, v, cache, pos)
+        res.append([q.clone(), k.clone(), cache])
+        for max_q in (1, 8, T):
+            res[-1] += ea.kv4_fwd(q, cache, pos[None, :5].contiguous(), ints([T]), max_q=max_q)
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+    del flat, rows, q, k, v, x
+    torch.cuda.empty_cache()
