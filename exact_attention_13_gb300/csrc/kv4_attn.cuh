@@ -92,8 +92,10 @@ struct Kv4Args {
   float v_descale;
 };
 
+// A request's first row, its rows that there are, its keys, and its queries: more than the rows where its
+// offsets reach past the end of q (a batch cut short).  The causal mask goes by the queries.
 struct ReqShape {
-  int q0, q_len, keys;
+  int q0, q_len, keys, queries;
 };
 
 __device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
@@ -108,7 +110,9 @@ __device__ __forceinline__ ReqShape kv4_request(const Kv4Args& a, int r) {
   }
   // offsets and lengths are device data: keep what they address inside the buffers
   s.q0 = static_cast<int>(min(max(q0, 0ll), static_cast<long long>(a.t)));
-  s.q_len = static_cast<int>(min(max(q1, static_cast<long long>(s.q0)), static_cast<long long>(a.t))) - s.q0;
+  q1 = max(q1, static_cast<long long>(s.q0));
+  s.q_len = static_cast<int>(min(q1, static_cast<long long>(a.t))) - s.q0;
+  s.queries = static_cast<int>(q1) - s.q0;
   const long long room = static_cast<long long>(a.width) << a.page_shift;
   s.keys = static_cast<int>(min(static_cast<long long>(max(*(a.lens + r), 0)), room));
   return s;
@@ -233,7 +237,7 @@ __device__ __forceinline__ int kv4_my_range(const Kv4Args& a, long long* s_sum, 
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   TileCursor c;
   auto cost = [&](int r) -> long long {
-    c = TileCursor{r, 0, 0, 0, 0, 1, {0, 0, 0}};
+    c = TileCursor{r, 0, 0, 0, 0, 1, {0, 0, 0, 0}};
     if (r >= a.b) return 0;
     const ReqShape s = kv4_request(a, r);
     c.blocks = kv4_blocks<R>(a, s);
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   // keys that row `row` of the unit sees (a padding row: all)
   auto row_keys = [&](int row) {
     const int at = cur.block * R + row;
-    const int behind = a.causal && at < cur.req.q_len * a.group ? cur.req.q_len - at / a.group - 1 : 0;
+    const int behind = a.causal && at < cur.req.q_len * a.group ? cur.req.queries - at / a.group - 1 : 0;
     return max(0, cur.req.keys - behind);
   };
   for (int step = 0; step < steps; ++step) {

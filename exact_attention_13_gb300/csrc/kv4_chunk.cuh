@@ -114,7 +114,7 @@ __device__ __forceinline__ int chunk_tiles(const Kv4Args& a, const ReqShape& s, 
   int seen = s.keys;
   if (a.causal) {
     const int last_row = min(s.q_len * a.group, (block + 1) * kChRows) - 1;
-    seen = max(0, s.keys - s.q_len + last_row / a.group + 1);
+    seen = max(0, s.keys - s.queries + last_row / a.group + 1);
   }
   return max(1, (min(seen, s.keys) - 1) / kChKeys + 1);
 }
@@ -170,16 +170,16 @@ __device__ __forceinline__ int walk_rows(const Kv4Args& a, const ChunkWalk* w) {
 __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, long long& total,
                                               long long& first, long long& last) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  ReqShape s{0, 0, 0};
+  ReqShape s{0, 0, 0, 0};
   long long per_head = 0;  // tiles of one key head of the thread's request
   auto lane_request = [&](int l) {
     return ReqShape{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
-                    __shfl_sync(0xffffffffu, s.keys, l)};
+                    __shfl_sync(0xffffffffu, s.keys, l), __shfl_sync(0xffffffffu, s.queries, l)};
   };
   // A request a thread; those of many blocks (a block is 256 / group tokens) by the whole warp.
   auto cost = [&](int r) -> long long {
     constexpr int kAlone = 4;
-    s = r < a.b ? kv4_request(a, r) : ReqShape{0, 0, 0};
+    s = r < a.b ? kv4_request(a, r) : ReqShape{0, 0, 0, 0};
     const int blocks = chunk_blocks(a, s);
     per_head = 0;
     if (blocks <= kAlone)
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           const bool live = row < walk_rows(a, w);
           const int qi = urow / a.group, qg = urow - qi * a.group;
           sees = w->s.req.keys;
-          if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.q_len + qi + 1));
+          if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.queries + qi + 1));
           // ---- the warp's 32 query rows, scaled into [1, 2): kRow lanes take 16 bytes each of a row
           constexpr int kRow = D / 8, kRowsIt = 32 / kRow;
           const long long mine = live ? static_cast<long long>(w->s.req.q0 + qi) * a.q_row +

@@ -337,7 +337,8 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *   table, lens : device int32, [B, table_width] and [B].  Lengths outside [0, table_width *
  *                 page_size] are clamped; keys on a page id outside [0, num_pages) are not seen
  *   q_offsets   : device int32 [B + 1], not decreasing, or NULL: T / B queries each (T % B == 0).
- *                 Rows of q past q_offsets[B] are not read, their outputs left as they were
+ *                 Rows of q past q_offsets[B] are not read, their outputs left as they were.  Offsets
+ *                 past T: the rows that there are, each at its place among all n queries
  *   o, lse      : outputs [T, Hq, d] bf16 (16-byte aligned) and [T, Hq] fp32; they overlap no input
  *                 (o = q is refused)
  *   max_q       : about the most queries of a request; any value >= 1 is correct, it picks the

@@ -136,7 +136,8 @@ def unblock(raw, page, d):
 def kv4_attention(q, cache, table, lens, q_offsets, d, scale, causal, k_descale=1.0, v_descale=1.0):
     """q [T, Hq, d] fp64, cache bytes [P, Hkv, 2, :]; returns O [T, Hq, d], LSE [T, Hq], and for
     tolerances, per row, the sums of p |v| and of |v| and the largest sum |q k| of a visible key.
-    Rows past the last request keep NaN."""
+    Rows past the last request keep NaN; of a request that reaches past the T rows there are the first are
+    computed, at the places in the cache that they have among all of its rows."""
     T, Hq, _ = q.shape
     P, Hkv = cache.shape[:2]
     page = cache.shape[3] * 16 // (9 * d)
@@ -156,7 +157,7 @@ def kv4_attention(q, cache, table, lens, q_offsets, d, scale, causal, k_descale=
                 there[j0:j0 + m] = True
                 for dst, kv, ds in ((k, 0, k_descale), (v, 1, v_descale)):
                     dst[j0:j0 + m] = dequantise(*unblock(cache[p, h, kv], page, d), ds)[:m]
-            for i in range(rows):
+            for i in range(min(rows, T - int(q_offsets[b]))):
                 t = int(q_offsets[b]) + i
                 seen = there & (np.arange(n) <= (n - rows + i if causal else n))
                 for g in range(Hq // Hkv):

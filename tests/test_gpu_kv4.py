@@ -822,3 +822,17 @@ def test_strides_past_32_bits():
         assert torch.equal(x, y)
     del flat, rows, q, k, v, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d,max_q,qlens,T", [(64, 1, [2, 9, 3], 7), (128, 8, [2, 8, 3], 3), (128, 4, [3, 8, 3], 12),
+                                             (128, 150, [40, 150, 60], 150), (64, 150, [40, 150, 60], 245)])
+def test_a_batch_cut_short_keeps_its_rows_places(d, max_q, qlens, T):
+    """A plan of fewer tokens than the requests bring: the rows that there are see the keys up to their own, not
+    those of the rows cut off."""
+    lens = [130, 400, 90]
+    cache, table = make(lens, 8, 64, 2, d)
+    offsets = np.concatenate([[0], np.cumsum(qlens)]).tolist()
+    assert T < offsets[-1]
+    q = queries(offsets[-1], 4, d)
+    check(q[:T].contiguous(), cache, table, lens, offsets, d, max_q=max_q)
+    check(q, cache, table, lens, offsets, d, max_q=max_q)
