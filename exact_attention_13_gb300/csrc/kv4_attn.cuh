@@ -5,14 +5,15 @@
 // over the keys j < len of the row's request (causal: j <= len - q_len + i, the new tokens being the
 // last of the cache).  A row that sees no key gets O = 0 and LSE = -inf.
 //
-// What bounds it.  Each cached value is 4.5 bits and meets 8 query rows or fewer: the floor is the
-// cache's bytes over HBM.  At 6.7 TB/s an SM has to widen about 41 values a clock, and its ALU and
-// FMA pipes each start 64 lanes a clock, so conversions are counted in instructions per value:
+// What bounds it.  Each cached value is 4.5 bits and meets 8, 16 or 32 query rows (NT = 1, 2, 4 eights):
+// the floor is the cache's bytes over HBM.  At 6.7 TB/s an SM has to widen about 41 values a clock, and its
+// ALU and FMA pipes each start 64 lanes a clock, so conversions are counted in instructions per value
+// (beside 8 rows; beside 16 and 32 the products and the latencies weigh more, see below):
 //  * one cvt widens two e2m1 codes to f16 and one f16x2 multiply applies their scales (code * scale
 //    is exact in f16), one instruction a value in all;
 //  * the products run as mma.m16n8k16 with the CACHE as the 16-row operand, straight from the
 //    registers that widened it: S^T = K Q^T and O^T = V^T P^T, queries in the 8-wide operand.  The
-//    tensor core then does 8 products a value (queries as the 16-row operand: 16, half of them
+//    tensor core then does 8 NT products a value (8 queries as the 16-row operand: 16, half of them
 //    padding).  tcgen05 takes its wide operand from shared or tensor memory only: each widened value
 //    would be written and read there again, 4 bytes of on-chip traffic for each half byte of HBM;
 //  * the contraction index of a product may be permuted freely, so each lane owns 16 or 32
@@ -21,7 +22,9 @@
 //    before they are widened, 4 logic instructions for 16 values;
 //  * P^T leaves the S^T accumulators in the layout that movmatrix transposes into the operand's.
 // Queries are scaled by a power of two per row into [1, 2) before they become f16, so the conversion
-// keeps bf16's 8 bits down to 2^-17 of the row's largest value.
+// keeps bf16's 8 bits down to 2^-17 of the row's largest value.  P is rounded to f16 (2^-11 of each
+// probability at most, beside the 2^-8 of a bf16 output): against 64 bits outputs are as far off as with P in
+// fp32 (1.7e-3 in norm either way), and single ones differ from those by a bf16 step.
 //
 // Split.  The work of all requests is one line of tiles (64 to 256 keys of one key head, for one
 // block of query rows); CTA i of n takes the i-th n-th of it, so ragged lengths balance by themselves and a
@@ -31,11 +34,14 @@
 // which a second kernel merges in a fixed order.
 //
 // Measured (2070 MHz, calls following each other).  64 requests of 500 to 8192 keys, 32 heads over 8, d 128:
-// 72 us, 321 MB at 4.5 TB/s; the slope over the length is 5.8 TB/s, about 11 us are start (lengths, page
-// ids and the first tiles follow each other from memory) and the units' begins and ends, 3 the merge.
-// 262144 keys of one request, 32 heads over 4: 37.8 us, 4.0 TB/s.  Up to 15 rows a key head, 24 heads
-// over 8, 16 requests: 50 us, 3.2 TB/s.  Instructions start in 56 % of the cycles (43 % beside 16 rows,
-// whose registers leave two warps a scheduler), the rest is waits for their fixed latencies.  Not
+// 72 us, 284 MB at 3.9 TB/s; 64 of 4096 keys each 65 us, 303 MB at 4.7.  The slope over the length is
+// 5.8 TB/s; what comes on top is fixed: 13 us beside equal lengths, 23 beside ragged ones, of it the start
+// (lengths, page ids and the first tiles follow each other from memory), the units' begins and ends, and 3
+// for the merge.  262144 keys of one request, 32 heads over 4: 37.7 us, 4.0 TB/s, 12 of it fixed.  Up to 15
+// rows a key head, 24 heads over 8, 16 requests: 50 us, 145 MB at 2.9 TB/s.  64 requests of 4096 keys (floor
+// 46 us): 66 us with 8 rows a key head, 91 with 16, 163 with 32 (NT = 4: 255 registers, some spilled).
+// Beside 8 rows instructions start in 56 % of the cycles, beside 16 in 43 % (their registers leave two warps
+// a scheduler); the rest is waits for the instructions' fixed latencies.  Not
 // faster: loads to registers instead of the rings (100 us for the first case), four CTAs a SM, strips of
 // 64 keys at d 128, three stages, prefetches of page ids or of whole L2 lines.
 #pragma once

@@ -20,10 +20,12 @@
 // is merged from partial sums afterwards.  Units of one key head follow each other on the line, so
 // CTAs that run together read the same keys from L2.
 //
-// Measured (2070 MHz).  One prompt of 65536 tokens, 8 heads over 1, d 128: 7.34 ms, 1199 TFLOP/s (0.62 of
-// cuBLAS bf16); four chunks of up to 512 tokens behind 4096 to 8192 keys, 32 heads over 8: 129 us,
-// 0.40 of it, 5 us of that the start, 18 the queries and outputs of the two or three shares of units a
-// CTA has, and 10 the merge.  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
+// Measured (2070 MHz).  One prompt of 65536 tokens, 8 heads over 1, d 128: 7.32 ms, 1202 TFLOP/s (0.62 of
+// cuBLAS bf16); four chunks of up to 512 tokens behind 4096 to 8192 keys, 32 heads over 8: 129.5 us for
+// 116 GFLOP, 897 TFLOP/s (0.46), 5 us of that the start, 18 the queries and outputs of the two or three
+// shares of units a CTA has, and 10 the merge.  Units of at most 128 rows have one row tile: the other's
+// warps and accumulators idle, and its chain S, softmax, P V, S runs alone (64 requests of 4096 keys with 36
+// to 128 rows a key head: 231 to 238 us, their bytes take 47 to 50).  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
 // tiles 2048 of them: S reads Q and K from shared memory at its full rate, beside which V is read and the
 // next tiles are written, and S of a row tile waits for its own softmax (2100 cycles) and P V.
 //
@@ -46,7 +48,7 @@ constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
 // 544 threads get 96 registers each at launch; the widening warpgroups give up what the softmax takes
 // (the MMA warp, alone in its warpgroup, keeps its 96).  Four chunks of 512 tokens: 134.4 us with 136 and 56
-// registers, 131.0 with 128 and 64, 128.9 with 120 and 72, 130.8 with 112 and 80 (spilled registers either way).
+// registers, 131.0 with 128 and 64, 128.9 with 120 and 72, 130.8 with 112 and 80 (a register or a few spilled each time).
 constexpr int kChLaunchRegs = 96, kChSoftmaxRegs = 120, kChWidenRegs = 72;
 static_assert(kChSoftmaxRegs + kChWidenRegs == 2 * kChLaunchRegs, "registers of the block at launch");
 

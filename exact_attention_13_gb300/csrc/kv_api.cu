@@ -299,7 +299,7 @@ int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_wid
   static std::atomic<uint64_t> done{0};
   if (int rc = opt_in_smem(page_plan_kernel, (3 * kPlanMaxBatch + 1) * 4, done)) return rc;
   // a warp per request and a thread per token, one CTA a SM at most: each repeats the scan over the
-  // lengths (1000 requests, 46,000 tokens: 9.4 us; 15.8 with four tokens a thread on a quarter of
+  // lengths (1000 requests, 46,000 tokens, some ended: 9.4 us; 15.8 with four tokens a thread on a quarter of
   // the CTAs; a single CTA for a small step: 2.9 us)
   const long long items = num_tokens > 32ll * B ? num_tokens : 32ll * B;
   long long grid = (items + kPlanThreads - 1) / kPlanThreads;

@@ -216,9 +216,9 @@ def page_plan(lens, new_lens, table, queue, queue_state, page_size: int, num_tok
     ``lens`` [B]: cached tokens; ``new_lens`` [B]: tokens each request brings, or -1 for one that
     has ended; ``table`` [B, width]: page ids, extended in place; ``queue`` [capacity] and
     ``queue_state`` [2] = (head, count): ring of free pages, released pages are appended in place.
-    All int32.  ``num_tokens``: size of the packed batch, padding included.  Requests that do not
-    get their pages keep their length and get slots of -1 (see fa_page_plan in
-    include/exact_attention.h).  ``out``: a plan of the right sizes to write into; its ``lens`` and
+    All int32, B from 1 to 16384.  ``num_tokens``: size of the packed batch, padding included.  Requests that
+    do not get their pages keep their length and get slots of -1; what attention gives for their tokens means
+    nothing (see fa_page_plan in include/exact_attention.h).  ``out``: a plan of the right sizes to write into; its ``lens`` and
     ``queue_state`` must not be this call's inputs."""
     index = lens.get_device()
     if (index < 0 or lens.dim() != 1 or table.dim() != 2 or queue.dim() != 1
@@ -283,7 +283,9 @@ def _cache_shape(cache, d):
 def kv4_append(k, v, cache, slots, k_descale: float = 1.0, v_descale: float = 1.0):
     """Quantise k and v (bf16 [T, H, d], last dimension contiguous) and write them into the cache
     at ``slots`` (int32 [T]; rows with a slot outside the cache, such as -1, are skipped).  Descales
-    are powers of two: values are stored divided by them."""
+    are powers of two: values are stored divided by them.  A group of 16 values keeps its precision where its
+    largest, so divided, lies between 0.1 and 2688 (6 times e4m3's normal range); below the scale gets coarse,
+    below 0.006 the group is stored as zeros, above 2688 it saturates."""
     index = k.get_device()
     if (k.dtype is not _bf16 or v.dtype is not _bf16 or k.dim() != 3 or k.shape != v.shape
             or index < 0 or v.get_device() != index):
@@ -346,7 +348,10 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     are; request b's queries are rows q_offsets[b] .. q_offsets[b + 1) (int32 [B + 1]), or T / B rows
     each without ``q_offsets``.  ``causal``: the queries are the last tokens of the cache.
     ``max_q``: about the most queries of a request (default T / B, rounded up); it only picks the
-    kernel (how many rows share a pass over the cache).  Rows of q past the last request's are left as they are.
+    kernel (how many rows share a pass over the cache), one for all requests of the call.  Rows of ``out`` and
+    ``lse`` past the last request's are left as they are (not initialised in tensors made here).  Rows of
+    tokens without a slot, such as those of a request that ``page_plan`` refused, mean nothing: their keys are
+    not in the cache, and they see what it held before.
     ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes or more, not shared by calls that may run
     at the same time; without it torch allocates one.  ``status``: as in ``fwd``."""
     index = q.get_device()

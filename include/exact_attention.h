@@ -281,7 +281,7 @@ FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
  *   queue_state_out : {head, count} after the step
  *   num_tokens      : size of the packed batch, the refused requests' tokens included; tokens past
  *                     it get no place, although their requests' lengths grow
- *   page_size       : 16, 32, 64 or 128;  B <= 16384;  table_width * page_size <= 2^30;
+ *   page_size       : 16, 32, 64 or 128;  1 <= B <= 16384;  table_width * page_size <= 2^30;
  *                     B * table_width < 2^31;  the tokens of a step number < 2^31
  * All arrays are device int32.  No output may overlap an input or another output (lens_out and
  * queue_state_out are refused when they are the inputs; the table and the ring are both).  One launch,
@@ -350,6 +350,9 @@ FA_API int fa_kv4_read(const void* cache, int num_pages, int page_size, const in
  *   dev_status  : as fa_fwd_opts.dev_status (NULL = the library's status word)
  *   sizes       : T and B >= 1, Hq a multiple of Hkv, T * Hq < 2^30, table_width * page_size <= 2^30; d,
  *                 page_size and descales as fa_kv4_append
+ * Queries enter the products as f16 scaled by a power of two per row: values below 2^-17 of a row's largest
+ * lose bits, below 2^-26 they count as zero.  Probabilities are rounded to f16; sums are fp32.  A row whose
+ * token has no slot (a request that fa_page_plan refused) means nothing: its key is not in the cache.
  * A key or value vector that is NaN makes the rows that see it NaN (O and LSE); rows that do not
  * see it, and whatever lies in the pages past a request's length, have no effect.  Partial sums
  * are merged in a fixed order: the same call gives the same bits.
