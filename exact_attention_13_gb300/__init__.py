@@ -11,7 +11,8 @@ fallback: if the library is missing or fails to load, importing ``lib()`` raises
 
 ``kv.py`` adds what stands around attention in training and serving: rotary positions (``rope``),
 pages and slots from request lengths (``page_plan``), a paged 4-bit key/value cache (``kv4_cache``,
-``kv4_append``, ``kv4_read``) and attention over it (``kv4_fwd``).
+``kv4_append``, ``kv4_read``) and attention over it (``kv4_fwd``).  ``tree.py`` checks trees of drafted
+tokens over that cache: ``tree_plan``, ``kv4_tree_fwd``, ``tree_accept`` and ``kv4_move``.
 """
 from __future__ import annotations
 
@@ -387,16 +388,19 @@ def debug_exp2(x, mode: int):
     return y
 
 
-# Rotary positions, page planning, the 4-bit cache and attention over it: functions of kv.py, loaded
-# on first use (that module imports torch, this one does not).
-_KV_NAMES = ("rope", "rope_turns", "page_plan", "PagePlan", "kv4_cache", "kv4_append", "kv4_read",
-             "kv4_fwd", "kv4_workspace_bytes")
+# Rotary positions, page planning, the 4-bit cache and attention over it (kv.py), trees of drafted tokens
+# (tree.py): loaded on first use (those modules import torch, this one does not).
+_KV_NAMES = ("rope", "rope_turns", "rope_axes", "rope_axis_pairs", "page_plan", "PagePlan", "kv4_cache",
+             "kv4_append", "kv4_read", "kv4_fwd", "kv4_workspace_bytes")
+_TREE_NAMES = ("tree_plan", "TreePlan", "tree_accept", "TreeAccept", "kv4_move", "kv4_tree_fwd",
+               "kv4_tree_workspace_bytes")
 
 
 def __getattr__(name):
-    if name in _KV_NAMES:
-        from . import kv
+    if name in _KV_NAMES or name in _TREE_NAMES:
+        from . import kv, tree
 
         globals().update({n: getattr(kv, n) for n in _KV_NAMES})
+        globals().update({n: getattr(tree, n) for n in _TREE_NAMES})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

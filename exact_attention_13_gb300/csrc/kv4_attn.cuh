@@ -96,6 +96,8 @@ struct Kv4Args {
   int whole_tiles;         // > 0: units are not split, each counts as this many tiles
   float c;                 // scale * log2(e) * key descale
   float v_descale;
+  const uint32_t* tree;    // [T, words]: the nodes that a query sees among its request's (TREE)
+  int words;
 };
 
 // A request's first row, its rows that there are, its keys, and its queries: more than the rows where its
@@ -314,7 +316,7 @@ __host__ __device__ constexpr int dec_smem_bytes() {
          NT * (D / 32) * 32 * 16;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE = false>
 __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kernel(const Kv4Args a) {
   constexpr int R = 8 * NT;            // query rows of a unit
   constexpr int MT = D / 16;           // 16-dim tiles of O^T
@@ -448,9 +450,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
   int4 merge = make_int4(-1, 0, 0, 0);
 
   int stage = 0;
-  // keys that row `row` of the unit sees (a padding row: all)
+  // keys that row `row` of the unit sees, one behind the other (a padding row: all; of a tree those before it)
   auto row_keys = [&](int row) {
     const int at = cur.block * R + row;
+    if constexpr (TREE) return at < cur.req.q_len * a.group ? max(0, cur.req.keys - cur.req.queries) : cur.req.keys;
     const int behind = a.causal && at < cur.req.q_len * a.group ? cur.req.queries - at / a.group - 1 : 0;
     return max(0, cur.req.keys - behind);
   };
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
         for (int cc = 0; cc < 2; ++cc) {
           const int row = nt * 8 + 2 * t4 + cc, k = row_keys(row);
           min_lim = min(min_lim, k);
-          if (row0 + row < rows) max_lim = max(max_lim, k);
+          if (row0 + row < rows) max_lim = max(max_lim, TREE ? req.keys : k);
           m[nt][cc] = kDecNone;
           l[nt][cc] = 0.f;
         }
@@ -621,13 +624,22 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2) kv4_decode_kerne
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int sees = row_keys(nt * 8 + 2 * t4 + cc) - key0;
+            const int at = cur.block * R + nt * 8 + 2 * t4 + cc;
+            // whether the row sees its tree's node at key `key` (past those that it sees all)
+            auto node_seen = [&](int key) {
+              const int m = key0 + key - (cur.req.keys - cur.req.queries);
+              if (!TREE || m < 0 || key0 + key >= cur.req.keys || m >= 32 * a.words || at >= cur.req.q_len * a.group)
+                return false;
+              return (a.tree[static_cast<size_t>(cur.req.q0 + at / a.group) * a.words + m / 32] >> (m % 32) & 1u) != 0u;
+            };
 #pragma unroll
             for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
               for (int hr = 0; hr < 2; ++hr) {
                 float& y = x[tg][nt][2 * hr + cc];
                 if (nan[tg][hr]) y = __uint_as_float(0x7fffffffu);
-                if (!((have >> tg) & 1u) || tg * 16 + kv4_perm(g8) + 8 * hr >= sees) y = -INFINITY;
+                const int key = tg * 16 + kv4_perm(g8) + 8 * hr;
+                if (!((have >> tg) & 1u) || (key >= sees && !node_seen(key))) y = -INFINITY;
               }
           }
 #pragma unroll

@@ -1,4 +1,4 @@
-// kv4_cache.cuh -- the paged 4-bit key/value cache: layout, write, read back.
+// kv4_cache.cuh -- the paged 4-bit key/value cache: layout, write, read back, move of rows.
 //
 // Format.  A head vector is cut into groups of 16 values; a group holds one e4m3 scale and 16 e2m1
 // codes (the magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6), 4.5 bits a value:
@@ -33,6 +33,7 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "rope.cuh"
 #include "sm103_ptx.cuh"
@@ -218,6 +219,68 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) 
       f[2 * j + 1] = two.y * s;
     }
     reinterpret_cast<uint4*>(a.out[n])[id] = pack_bf16x8(f);
+  }
+}
+
+// Rows of one cache, or of the caches of all layers, to other slots: of request r, row sources[i] to
+// slots[i] for its first counts[r] rows i, in their order.  A row is D / 16 bytes of scales and eight times as
+// much of codes: nine pieces of that size, of which a thread takes one, of the keys or the values of one head,
+// through all of the request's rows.  Eight rows are read before they are written; in a path of accepted
+// nodes, whose sources rise and lie at or behind their destinations, no source is then written before it is
+// read.  Bound by latency (count, slots, row), for large steps by short pieces of lines.
+constexpr int kMoveLayers = 256;  // caches of one launch (their addresses are the kernel's arguments)
+constexpr int kMoveAhead = 8;
+
+struct Kv4MoveArgs {
+  uint8_t* cache[kMoveLayers];
+  const int* sources;   // [T]
+  const int* slots;     // [T]
+  const int* offsets;   // [B + 1]
+  const int* counts;    // [B]
+  int t, b, heads, page_shift, pages;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKv4Threads) kv4_move_kernel(const __grid_constant__ Kv4MoveArgs a) {
+  using Piece = typename std::conditional<D == 128, uint2, uint32_t>::type;
+  constexpr int kPieces = 9;
+  static_assert(sizeof(Piece) == D / kKv4Group, "a row of scales is one piece");
+  grid_launch_dependents();
+  grid_wait();
+  unsigned id = blockIdx.x * kKv4Threads + threadIdx.x;
+  const unsigned piece = id % kPieces;
+  id /= kPieces;
+  const unsigned r = id / (2u * a.heads), vec = id - r * (2u * a.heads);  // 2 head + (0 keys, 1 values)
+  if (r >= static_cast<unsigned>(a.b)) return;
+  const int first = min(max(a.offsets[r], 0), a.t);
+  const int n = min(a.counts[r], min(max(a.offsets[r + 1], first), a.t) - first);
+  const int rows = 1 << a.page_shift, block = kv4_block_bytes(rows, D);
+  uint8_t* const base = a.cache[blockIdx.y] + static_cast<size_t>(vec) * block +
+                        (piece < 8 ? piece * sizeof(Piece) : static_cast<unsigned>(rows) * (D / 2));
+  const unsigned step = piece < 8 ? D / 2 : D / kKv4Group;
+  const size_t page_bytes = static_cast<size_t>(block) * 2u * a.heads;
+  auto place = [&](int slot) {
+    return reinterpret_cast<Piece*>(base + static_cast<size_t>(slot >> a.page_shift) * page_bytes +
+                                    static_cast<unsigned>(slot & (rows - 1)) * step);
+  };
+  auto there = [&](int slot) { return slot >= 0 && (slot >> a.page_shift) < a.pages; };
+  for (int i0 = 0; i0 < n; i0 += kMoveAhead) {
+    int from[kMoveAhead], to[kMoveAhead];
+    Piece x[kMoveAhead];
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i) {
+      const bool live = i0 + i < n;
+      from[i] = live ? a.sources[first + i0 + i] : -1;
+      to[i] = live ? a.slots[first + i0 + i] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i) {
+      if (from[i] == to[i] || !there(from[i]) || !there(to[i])) to[i] = -1;
+      if (to[i] >= 0) x[i] = *place(from[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveAhead; ++i)
+      if (to[i] >= 0) *place(to[i]) = x[i];
   }
 }
 

@@ -12,72 +12,14 @@
 #include "kv4_attn.cuh"
 #include "kv4_cache.cuh"
 #include "kv4_chunk.cuh"
+#include "kv_host.cuh"
 #include "page_plan.cuh"
 #include "rope.cuh"
+#include "tree_plan.cuh"
 
 namespace exattn {
 
-int* library_status_ptr(int dev);  // fa_api.cu
-
 namespace {
-
-constexpr int kSms = 152;
-constexpr int kMaxKvDevices = 64;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool power_of_two(float x) {
-  if (!(x > 0.f) || !std::isfinite(x)) return false;
-  int e = 0;
-  return std::frexp(x, &e) == 0.5f && e >= -60 && e <= 60;
-}
-
-bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
-
-// Tokens of one row of a page table: tiles and strips past the last one are still 32-bit numbers.
-bool width_ok(int width, int page) { return static_cast<long long>(width) * page <= 1ll << 30; }
-
-int log2_of(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
-
-int launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
-
-// Set an attribute of a kernel, once per device.
-template <typename K>
-int set_once(K kern, cudaFuncAttribute attribute, int value, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxKvDevices) return FA_ERR_CUDA;
-  if (done.load(std::memory_order_acquire) & (1ull << dev)) return FA_OK;
-  if (cudaFuncSetAttribute(kern, attribute, value) != cudaSuccess) return FA_ERR_CUDA;
-  done.fetch_or(1ull << dev, std::memory_order_acq_rel);
-  return FA_OK;
-}
-
-template <typename K>
-int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
-  return set_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
-}
-
-// Launch a kernel that may begin while the one before it on the stream still runs (grid_wait in each).
-template <typename... Params, typename... Args>
-int launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t config{};
-  config.gridDim = grid;
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &early;
-  config.numAttrs = 1;
-  if (cudaLaunchKernelEx(&config, kern, args...) == cudaSuccess) return FA_OK;
-  (void)cudaGetLastError();
-  return FA_ERR_CUDA;
-}
 
 // ---------------------------------------------------------------------------------- rope
 int rope_tensor(RopeTensor& t, const void* x, const long long* xs, void* y, const long long* ys,
@@ -102,14 +44,51 @@ int rope_tensor(RopeTensor& t, const void* x, const long long* xs, void* y, cons
   return FA_OK;
 }
 
-// ---------------------------------------------------------------------------------- cache
-int cache_checks(const void* cache, int pages, int heads, int page, int d) {
-  if (!cache || pages < 1 || heads < 1) return FA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || !page_size_ok(page) || heads > 65535) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(pages) * page > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
-  return aligned(cache, 16) ? FA_OK : FA_ERR_MISALIGNED;
+// fa_rope, and (a.axes given) fa_rope_axes.
+int launch_rope(RopeArgs& a, const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                int Hq, const void* k, const long long* k_strides, void* k_out, const long long* k_out_strides,
+                int Hk, int B, int N, int d, const int* positions, long long positions_batch_stride,
+                const long long* turns, int rotary_dim, int flags, float mscale, void* stream) {
+  if (!positions || !turns || B < 1 || N < 1 || Hq < 1 || Hk < 0 || positions_batch_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  if (flags & ~(FA_ROPE_INTERLEAVED | FA_ROPE_INVERSE)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > d || rotary_dim % 16) return FA_ERR_UNSUPPORTED;
+  if (!aligned(positions, 4) || !aligned(turns, 8)) return FA_ERR_MISALIGNED;
+  if (int rc = rope_tensor(a.t[0], q, q_strides, q_out, q_out_strides, Hq)) return rc;
+  if (int rc = rope_tensor(a.t[1], k, k_strides, k_out, k_out_strides, Hk)) return rc;
+  a.positions = positions;
+  a.turns = turns;
+  a.pos_batch = positions_batch_stride;
+  a.rows = static_cast<long long>(B) * N;
+  a.n = N;
+  a.d = d;
+  a.r = rotary_dim;
+  a.mscale = mscale;
+  const long long blocks = (a.rows * (d / 16) + kRopeThreads - 1) / kRopeThreads;
+  if (blocks > 0x7fffffffll || static_cast<long long>(Hq) + Hk > 65535) return FA_ERR_UNSUPPORTED;
+  // Heads per thread: four, whose loads are in flight together.  (B2 H32+32 N8192 d128 takes 78.7 us
+  // with 4, 79.9 with 8, 81.1 with 16 and 89.5 with all 64: the angles that more heads would share
+  // cost less than the longer blocks' last wave.)  Fewer where that leaves less than eight blocks a
+  // SM, as in a decode step.
+  const int heads = Hq + Hk;
+  a.heads_per_thread = 4;
+  while (a.heads_per_thread > 1 &&
+         blocks * ((heads + a.heads_per_thread - 1) / a.heads_per_thread) < 8 * kSms)
+    a.heads_per_thread /= 2;
+  const dim3 grid(static_cast<unsigned>(blocks),
+                  static_cast<unsigned>((heads + a.heads_per_thread - 1) / a.heads_per_thread));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool il = flags & FA_ROPE_INTERLEAVED, inv = flags & FA_ROPE_INVERSE;
+  auto kern = a.axes ? il ? inv ? rope_kernel<true, true, true> : rope_kernel<true, false, true>
+                          : inv ? rope_kernel<false, true, true> : rope_kernel<false, false, true>
+                     : il ? inv ? rope_kernel<true, true, false> : rope_kernel<true, false, false>
+                          : inv ? rope_kernel<false, true, false> : rope_kernel<false, false, false>;
+  return launch_early(kern, grid, kRopeThreads, 0, s, a);
 }
 
+// ---------------------------------------------------------------------------------- cache
 // Append or read T tokens, in launches of fewer than 2^31 pieces (32-bit indices).
 int launch_rows(Kv4Rows a, int T, int heads, int d, int piece, void (*k64)(Kv4Rows), void (*k128)(Kv4Rows),
                 cudaStream_t s) {
@@ -176,14 +155,14 @@ int launch_merge(const Kv4Args& a, int ctas, cudaStream_t s) {
   return launch_early(kv4_merge_kernel<D, R>, grid, kMergeThreads, 0, s, a, few ? ctas : 0);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE = false>
 int launch_decode(Kv4Args& a, void* workspace, cudaStream_t s) {
   constexpr int n = kv4_ctas(NT);
   if (!a.whole_tiles) split_workspace<D, NT>(a, workspace);
   constexpr int smem = dec_smem_bytes<D, NT>();
   static_assert(dec_ctas_per_sm(NT) * (smem + 2048) <= 228 * 1024, "shared memory per SM");
   static std::atomic<uint64_t> done{0};
-  auto kern = kv4_decode_kernel<D, NT>;
+  auto kern = kv4_decode_kernel<D, NT, TREE>;
   if (int rc = opt_in_smem(kern, smem, done)) return rc;
   kern<<<n, kDecThreads, smem, s>>>(a);
   if (int rc = launched()) return rc;
@@ -233,42 +212,26 @@ int fa_rope(const void* q, const long long* q_strides, void* q_out, const long l
             const long long* k_out_strides, int Hk, int B, int N, int d, const int* positions,
             long long positions_batch_stride, const long long* turns, int rotary_dim, int flags,
             float mscale, void* stream) {
-  if (!positions || !turns || B < 1 || N < 1 || Hq < 1 || Hk < 0 || positions_batch_stride < 0)
-    return FA_ERR_INVALID_ARG;
-  if (flags & ~(FA_ROPE_INTERLEAVED | FA_ROPE_INVERSE)) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if (rotary_dim < 16 || rotary_dim > d || rotary_dim % 16) return FA_ERR_UNSUPPORTED;
-  if (!aligned(positions, 4) || !aligned(turns, 8)) return FA_ERR_MISALIGNED;
-  RopeArgs a;
-  if (int rc = rope_tensor(a.t[0], q, q_strides, q_out, q_out_strides, Hq)) return rc;
-  if (int rc = rope_tensor(a.t[1], k, k_strides, k_out, k_out_strides, Hk)) return rc;
-  a.positions = positions;
-  a.turns = turns;
-  a.pos_batch = positions_batch_stride;
-  a.rows = static_cast<long long>(B) * N;
-  a.n = N;
-  a.d = d;
-  a.r = rotary_dim;
-  a.mscale = mscale;
-  const long long blocks = (a.rows * (d / 16) + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > 0x7fffffffll || static_cast<long long>(Hq) + Hk > 65535) return FA_ERR_UNSUPPORTED;
-  // Heads per thread: four, whose loads are in flight together.  (B2 H32+32 N8192 d128 takes 78.7 us
-  // with 4, 79.9 with 8, 81.1 with 16 and 89.5 with all 64: the angles that more heads would share
-  // cost less than the longer blocks' last wave.)  Fewer where that leaves less than eight blocks a
-  // SM, as in a decode step.
-  const int heads = Hq + Hk;
-  a.heads_per_thread = 4;
-  while (a.heads_per_thread > 1 &&
-         blocks * ((heads + a.heads_per_thread - 1) / a.heads_per_thread) < 8 * kSms)
-    a.heads_per_thread /= 2;
-  const dim3 grid(static_cast<unsigned>(blocks),
-                  static_cast<unsigned>((heads + a.heads_per_thread - 1) / a.heads_per_thread));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool il = flags & FA_ROPE_INTERLEAVED, inv = flags & FA_ROPE_INVERSE;
-  auto kern = il ? inv ? rope_kernel<true, true> : rope_kernel<true, false>
-                 : inv ? rope_kernel<false, true> : rope_kernel<false, false>;
-  return launch_early(kern, grid, kRopeThreads, 0, s, a);
+  RopeArgs a{};
+  return launch_rope(a, q, q_strides, q_out, q_out_strides, Hq, k, k_strides, k_out, k_out_strides, Hk, B, N, d,
+                     positions, positions_batch_stride, turns, rotary_dim, flags, mscale, stream);
+}
+
+int fa_rope_axes(const void* q, const long long* q_strides, void* q_out, const long long* q_out_strides,
+                 int Hq, const void* k, const long long* k_strides, void* k_out,
+                 const long long* k_out_strides, int Hk, int B, int N, int d, const int* positions,
+                 int num_axes, long long positions_axis_stride, long long positions_batch_stride,
+                 const unsigned char* axes, const long long* turns, int rotary_dim, int flags, float mscale,
+                 void* stream) {
+  if (!axes || num_axes < 1 || positions_axis_stride < 0) return FA_ERR_INVALID_ARG;
+  if (num_axes > kRopeAxes) return FA_ERR_UNSUPPORTED;
+  if (!aligned(axes, 8)) return FA_ERR_MISALIGNED;
+  RopeArgs a{};
+  a.axes = axes;
+  a.n_axes = num_axes;
+  a.pos_axis = positions_axis_stride;
+  return launch_rope(a, q, q_strides, q_out, q_out_strides, Hq, k, k_strides, k_out, k_out_strides, Hk, B, N, d,
+                     positions, positions_batch_stride, turns, rotary_dim, flags, mscale, stream);
 }
 
 int fa_page_plan(const int* lens, const int* new_lens, int* table, int table_width, int* queue,
@@ -428,6 +391,150 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return d == 64 ? launch_kv4<64>(a, nt, workspace, s) : launch_kv4<128>(a, nt, workspace, s);
+}
+
+int fa_tree_plan(const int* parents, const int* q_offsets, const int* lens, int B, int T, int words, int* positions,
+                 unsigned* seen, void* stream) {
+  if (!parents || !q_offsets || !lens || !positions || !seen || B < 1 || T < 1 || words < 1) return FA_ERR_INVALID_ARG;
+  if (words > kTreeWords || B > kPlanMaxBatch || static_cast<long long>(T) * words > 0x7fffffffll)
+    return FA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(q_offsets),
+                        static_cast<const void*>(lens), static_cast<const void*>(positions),
+                        static_cast<const void*>(seen)})
+    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  const TreePlanArgs a{parents, q_offsets, lens, positions, seen, B, T, words};
+  return launch_early(tree_plan_kernel, static_cast<unsigned>(B + 1), kTreeThreads, 0,
+                      static_cast<cudaStream_t>(stream), a);
+}
+
+int fa_tree_accept(const int* parents, const unsigned* seen, int words, const int* tokens, const int* choices,
+                   const int* lens, const int* new_lens, const int* q_offsets, const int* slots, const int* table,
+                   int table_width, int* queue, int queue_size, const int* queue_state, int B, int page_size, int T,
+                   int* lens_out, int* counts, int* path, int* next_tokens, int* sources, int* queue_state_out,
+                   void* stream) {
+  if (!lens || !new_lens || !q_offsets || !table || !queue || !queue_state || !lens_out || !counts || !next_tokens ||
+      !queue_state_out)
+    return FA_ERR_INVALID_ARG;
+  if (T > 0 && (!parents || !seen || !tokens || !choices || !slots || !path || !sources)) return FA_ERR_INVALID_ARG;
+  if (B < 1 || T < 0 || words < 1 || table_width < 1 || queue_size < 1) return FA_ERR_INVALID_ARG;
+  // other thread blocks, and the second kernel, read the old lengths and state
+  if (lens_out == lens || lens_out == new_lens || queue_state_out == queue_state) return FA_ERR_INVALID_ARG;
+  if (words > kTreeWords || B > kPlanMaxBatch || !page_size_ok(page_size) || !width_ok(table_width, page_size) ||
+      static_cast<long long>(B) * table_width > 0x7fffffffll || static_cast<long long>(T) * words > 0x7fffffffll)
+    return FA_ERR_UNSUPPORTED;
+  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(seen),
+                        static_cast<const void*>(tokens), static_cast<const void*>(choices),
+                        static_cast<const void*>(lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(q_offsets), static_cast<const void*>(slots),
+                        static_cast<const void*>(table), static_cast<const void*>(queue),
+                        static_cast<const void*>(queue_state), static_cast<const void*>(lens_out),
+                        static_cast<const void*>(counts), static_cast<const void*>(path),
+                        static_cast<const void*>(next_tokens), static_cast<const void*>(sources),
+                        static_cast<const void*>(queue_state_out)})
+    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  const TreeAcceptArgs a{parents, seen,   tokens, choices,     lens,     new_lens,        q_offsets, slots,
+                         table,   queue,  queue_state, lens_out, counts, path,            next_tokens, sources,
+                         queue_state_out, B,      T,      words,       table_width, queue_size, log2_of(page_size)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (int rc = launch_early(tree_accept_kernel, static_cast<unsigned>(B + 1), kTreeThreads, 0, s, a)) return rc;
+  static std::atomic<uint64_t> done{0};
+  if (int rc = opt_in_smem(tree_release_kernel, kPlanMaxBatch * 4, done)) return rc;
+  long long grid = (32ll * B + kPlanThreads - 1) / kPlanThreads;  // a warp a request
+  if (grid > kSms) grid = kSms;
+  return launch_early(tree_release_kernel, static_cast<unsigned>(grid), kPlanThreads, B * 4, s, a);
+}
+
+int fa_kv4_move(void* const* caches, int num_caches, int num_pages, int page_size, int Hkv, int d, const int* sources,
+                const int* slots, const int* q_offsets, const int* counts, int T, int B, void* stream) {
+  if (!caches || !sources || !slots || !q_offsets || !counts || num_caches < 1 || T < 1 || B < 1)
+    return FA_ERR_INVALID_ARG;
+  if (num_caches > kMoveLayers) return FA_ERR_UNSUPPORTED;
+  if (!aligned(sources, 4) || !aligned(slots, 4) || !aligned(q_offsets, 4) || !aligned(counts, 4))
+    return FA_ERR_MISALIGNED;
+  Kv4MoveArgs a{};
+  for (int i = 0; i < num_caches; ++i) {
+    if (int rc = cache_checks(caches[i], num_pages, Hkv, page_size, d)) return rc;
+    a.cache[i] = static_cast<uint8_t*>(caches[i]);
+  }
+  a.sources = sources;
+  a.slots = slots;
+  a.offsets = q_offsets;
+  a.counts = counts;
+  a.t = T;
+  a.b = B;
+  a.heads = Hkv;
+  a.page_shift = log2_of(page_size);
+  a.pages = num_pages;
+  const long long pieces = 18ll * Hkv * B;  // threads of a cache
+  if (pieces > 0x7fffffffll - kKv4Threads) return FA_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((pieces + kKv4Threads - 1) / kKv4Threads), static_cast<unsigned>(num_caches));
+  return launch_early(d == 64 ? kv4_move_kernel<64> : kv4_move_kernel<128>, grid, kKv4Threads, 0,
+                      static_cast<cudaStream_t>(stream), a);
+}
+
+size_t fa_kv4_tree_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size, int table_width) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
+  if (!page_size_ok(page_size) || table_width < 1 || !width_ok(table_width, page_size)) return 0;
+  int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
+  if (nt == 0) nt = 4;
+  return dec_whole_tiles(d, nt, page_size, table_width) ? 0 : kv4_workspace(nt, d);
+}
+
+int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache, int num_pages,
+                    int page_size, const int* table, int table_width, const int* lens, const int* q_offsets,
+                    const unsigned* seen, int words, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
+                    int max_q, float scale, float k_descale, float v_descale, void* workspace, size_t workspace_bytes,
+                    int* dev_status, void* stream) {
+  if (!q || !table || !lens || !q_offsets || !seen || !o || !lse || o == q) return FA_ERR_INVALID_ARG;
+  if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1 || words < 1)
+    return FA_ERR_INVALID_ARG;
+  if (q_row_stride < 0 || q_head_stride < 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID_ARG;
+  if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
+  if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
+  if (static_cast<long long>(T) * Hq > 0x3fffffffll || !width_ok(table_width, page_size) || words > kTreeWords)
+    return FA_ERR_UNSUPPORTED;
+  int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
+  if (nt == 0) nt = 4;
+  const int whole = dec_whole_tiles(d, nt, page_size, table_width);
+  if (!whole && (!workspace || workspace_bytes < kv4_workspace(nt, d))) return FA_ERR_INVALID_ARG;
+  if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) || !aligned(seen, 4) ||
+      !aligned(workspace, 16) || !aligned(dev_status, 4))
+    return FA_ERR_MISALIGNED;
+  const double c = static_cast<double>(scale) * 1.4426950408889634 * k_descale;
+  if (!(c <= 3.0e38)) return FA_ERR_INVALID_ARG;
+  Kv4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = table;
+  a.lens = lens;
+  a.q_offsets = q_offsets;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.t = T;
+  a.b = B;
+  a.hq = Hq;
+  a.hk = Hkv;
+  a.group = Hq / Hkv;
+  a.width = table_width;
+  a.page_shift = log2_of(page_size);
+  a.pages = num_pages;
+  a.whole_tiles = whole;
+  a.c = static_cast<float>(c);
+  a.v_descale = v_descale;
+  a.tree = seen;
+  a.words = words;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    return nt == 1   ? launch_decode<64, 1, true>(a, workspace, s)
+           : nt == 2 ? launch_decode<64, 2, true>(a, workspace, s)
+                     : launch_decode<64, 4, true>(a, workspace, s);
+  return nt == 1   ? launch_decode<128, 1, true>(a, workspace, s)
+         : nt == 2 ? launch_decode<128, 2, true>(a, workspace, s)
+                   : launch_decode<128, 4, true>(a, workspace, s);
 }
 
 }  // extern "C"

@@ -18,6 +18,10 @@
 // 16-byte loads and stores per head -- and walks over a range of heads, so its eight angles are
 // computed once.  The D / 16 chunks of a row sit in neighbouring lanes: a warp moves whole
 // 128-byte lines.  Bound by memory: 537 MB (B 2, 32 + 32 heads, N 8192, d 128) take 78.8 us, 6.8 TB/s.
+//
+// Several axes (AXES): the tokens of images and video have a position on each of up to four axes (time,
+// height, width), and each pair turns by its own axis's: p is p_{axis(i)}.  A row's positions are loaded once
+// a thread, the eight pairs' axes as one word, and each pair selects its position.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -56,7 +60,11 @@ struct RopeArgs {
   int d, r;
   float mscale;
   int heads_per_thread;
+  const uint8_t* axes;        // [r / 2] axis of each pair; positions of axis x lie x * pos_axis on
+  long long pos_axis;
+  int n_axes;                 // 1 .. kRopeAxes
 };
+constexpr int kRopeAxes = 4;
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& raw, float (&f)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -72,7 +80,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-template <bool INTERLEAVED, bool INVERSE>
+template <bool INTERLEAVED, bool INVERSE, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   grid_launch_dependents();
   grid_wait();
@@ -90,10 +98,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 
   float cs[8], sn[8];
   if (rotate) {
-    const unsigned long long p =
-        static_cast<unsigned long long>(static_cast<long long>(a.positions[batch * a.pos_batch + n]));
+    const int* at = a.positions + batch * a.pos_batch + n;
+    int pos[AXES ? kRopeAxes : 1];
+    uint2 axes = make_uint2(0u, 0u);
+    pos[0] = at[0];
+    if constexpr (AXES) {
+#pragma unroll
+      for (int x = 1; x < kRopeAxes; ++x) pos[x] = x < a.n_axes ? at[x * a.pos_axis] : pos[0];
+      axes = *reinterpret_cast<const uint2*>(a.axes + chunk * 8);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      int mine = pos[0];
+      if constexpr (AXES) {  // (an axis that there is not: the first one)
+        const uint32_t axis = ((i < 4 ? axes.x : axes.y) >> (i % 4 * 8)) & 0xffu;
+#pragma unroll
+        for (int x = 1; x < kRopeAxes; ++x) mine = axis == static_cast<uint32_t>(x) ? pos[x] : mine;
+      }
+      const unsigned long long p = static_cast<unsigned long long>(static_cast<long long>(mine));
       const unsigned long long turn = p * static_cast<unsigned long long>(a.turns[chunk * 8 + i]);
       // fraction of a turn in [-1/2, 1/2), as half turns
       const float half_turns = __int2float_rn(static_cast<int>(turn >> 32)) * 0x1p-31f;

@@ -1,0 +1,269 @@
+// tree_plan.cuh -- bookkeeping of trees of drafted tokens: positions and masks before the step that checks
+// them, and what of them is accepted after it.
+//
+// A request brings n nodes behind its len cached tokens; node i hangs on node parent(i) < i of the same
+// request, or (parent -1) on the last cached token.  With A(i) = {i} and A(parent(i)), the nodes on the way
+// up from i,
+//     position(i) = len + |A(i)| - 1,      node i sees the cached tokens and the nodes of A(i).
+// A(i) is kept as bits, 32 nodes a word.
+//
+// Plan.  A block takes a request; its nodes' bits and pointers lie in shared memory and double their reach
+// each round: A(i) |= A(up(i)), up(i) = up(up(i)), so a chain of n nodes takes log2(n) rounds instead of n
+// dependent loads.  Rounds end when every pointer has left the tree.
+//
+// Acceptance.  choice(i) is the token that the model chose behind node i.  Node 0 of a request holds the token
+// that was chosen before, and is good; another one is good if its token is its parent's choice (of several
+// such children the first).  A node is accepted iff all of A(i) is good, that is, iff A(i) without the good
+// nodes is empty: no walk down the tree.  The accepted nodes are a path, and node i's place on it is
+// |A(i)| - 1.  A second kernel, launched while the first runs, gives back the pages behind the new lengths: it
+// needs the sums over all requests.
+//
+// Integers only: results do not depend on scheduling (the one atomic is a minimum).
+#pragma once
+
+#include <cstdint>
+
+#include "page_plan.cuh"
+#include "rope.cuh"
+
+namespace exattn {
+
+constexpr int kTreeThreads = 128;
+constexpr int kTreeNodes = 256;  // nodes of a request that others can see, 32 a word
+constexpr int kTreeWords = kTreeNodes / 32;
+
+// A request's first node and the nodes there are of it (offsets are device data: kept inside the buffers).
+struct TreeShape {
+  int first, n;
+};
+__device__ __forceinline__ TreeShape tree_shape(const int* offsets, int r, int t) {
+  const int first = min(max(offsets[r], 0), t);
+  return {first, min(max(offsets[r + 1], first), t) - first};
+}
+
+struct TreePlanArgs {
+  const int* parents;    // [T]
+  const int* offsets;    // [B + 1]
+  const int* lens;       // [B]
+  int* positions;        // [T]
+  uint32_t* seen;        // [T, words]
+  int b, t, words;
+};
+
+__global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const TreePlanArgs a) {
+  __shared__ uint32_t s_seen[kTreeNodes][kTreeWords + 1];
+  __shared__ int s_up[kTreeNodes];
+  grid_launch_dependents();
+  grid_wait();
+  const int tid = threadIdx.x, r = blockIdx.x;
+  if (r >= a.b) {  // rows behind the last request
+    const int from = min(max(a.offsets[a.b], 0), a.t), step = (gridDim.x - a.b) * kTreeThreads;
+    for (int t = from + (r - a.b) * kTreeThreads + tid; t < a.t; t += step) {
+      a.positions[t] = 0;
+      for (int w = 0; w < a.words; ++w) a.seen[static_cast<size_t>(t) * a.words + w] = 0u;
+    }
+    return;
+  }
+  const TreeShape s = tree_shape(a.offsets, r, a.t);
+  const int n = min(s.n, 32 * a.words);  // nodes that have bits
+  const int len = a.lens[r];
+  auto parent = [&](int i) {
+    const int p = a.parents[s.first + i];
+    return p < i ? p : -1;
+  };
+  constexpr int kPer = kTreeNodes / kTreeThreads;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * kTreeThreads + tid;
+    if (i < n) {
+      s_up[i] = parent(i);
+      for (int w = 0; w < a.words; ++w) s_seen[i][w] = w == i / 32 ? 1u << (i % 32) : 0u;
+    }
+  }
+  // (at most log2(n) rounds: pointers fall by doubling distances)
+  while (true) {
+    int up[kPer], next[kPer];
+    uint32_t more[kPer][kTreeWords];
+    bool any = false;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int i = x * kTreeThreads + tid;
+      up[x] = i < n ? s_up[i] : -1;
+      if (up[x] >= 0) {
+        any = true;
+        next[x] = s_up[up[x]];
+#pragma unroll
+        for (int w = 0; w < kTreeWords; ++w)
+          if (w < a.words) more[x][w] = s_seen[up[x]][w];
+      }
+    }
+    if (!__syncthreads_or(any)) break;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int i = x * kTreeThreads + tid;
+      if (up[x] >= 0) {
+        s_up[i] = next[x];
+#pragma unroll
+        for (int w = 0; w < kTreeWords; ++w)
+          if (w < a.words) s_seen[i][w] |= more[x][w];
+      }
+    }
+  }
+  for (int i = tid; i < s.n; i += kTreeThreads) {
+    // a node past the bits is seen by none: it takes those of the nodes above it that have some
+    int j = i, depth = -1;
+    while (j >= n) {
+      ++depth;
+      j = parent(j);
+    }
+    uint32_t* const out = a.seen + static_cast<size_t>(s.first + i) * a.words;
+    for (int w = 0; w < a.words; ++w) {
+      const uint32_t bits = j >= 0 ? s_seen[j][w] : 0u;
+      depth += __popc(bits);
+      out[w] = bits;
+    }
+    a.positions[s.first + i] = static_cast<int>(static_cast<unsigned>(len) + static_cast<unsigned>(depth));
+  }
+}
+
+struct TreeAcceptArgs {
+  const int* parents;    // [T]
+  const uint32_t* seen;  // [T, words]
+  const int* tokens;     // [T]
+  const int* choices;    // [T]
+  const int* lens;       // [B] before the step
+  const int* after;      // [B] with the nodes
+  const int* offsets;    // [B + 1]
+  const int* slots;      // [T]
+  const int* table;      // [B, width]
+  int* queue;            // [cap]
+  const int* state;      // {head, count}
+  int* lens_out;         // [B]
+  int* counts;           // [B]
+  int* path;             // [T]
+  int* next;             // [B]
+  int* sources;          // [T]
+  int* state_out;        // {head, count}
+  int b, t, words, width, cap, page_shift;
+};
+
+__global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcceptArgs a) {
+  __shared__ int s_choice[kTreeNodes], s_slot[kTreeNodes], s_first[kTreeNodes], s_path[kTreeNodes];
+  __shared__ uint32_t s_good[kTreeWords];
+  grid_launch_dependents();
+  grid_wait();
+  const int tid = threadIdx.x, lane = tid % 32, r = blockIdx.x;
+  if (r >= a.b) {
+    const int from = min(max(a.offsets[a.b], 0), a.t), step = (gridDim.x - a.b) * kTreeThreads;
+    for (int t = from + (r - a.b) * kTreeThreads + tid; t < a.t; t += step) a.path[t] = a.sources[t] = -1;
+    return;
+  }
+  const TreeShape s = tree_shape(a.offsets, r, a.t);
+  const int before = a.lens[r], after = a.after[r];
+  const int n = after > before ? min(s.n, 32 * a.words) : 0;  // a refused request has no places
+  constexpr int kPer = kTreeNodes / kTreeThreads;
+  int parent[kPer], token[kPer];
+  uint32_t seen[kPer][kTreeWords];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * kTreeThreads + tid;
+    if (i < n) {
+      parent[x] = a.parents[s.first + i];
+      token[x] = a.tokens[s.first + i];
+      s_choice[i] = a.choices[s.first + i];
+      s_slot[i] = a.slots[s.first + i];
+      s_first[i] = kTreeNodes;
+      s_path[i] = 0;
+#pragma unroll
+      for (int w = 0; w < kTreeWords; ++w)
+        seen[x][w] = w < a.words ? a.seen[static_cast<size_t>(s.first + i) * a.words + w] : 0u;
+    }
+  }
+  __syncthreads();
+  bool hit[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * kTreeThreads + tid;
+    hit[x] = i < n && parent[x] >= 0 && parent[x] < i && token[x] == s_choice[parent[x]];
+    if (hit[x]) atomicMin(&s_first[parent[x]], i);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * kTreeThreads + tid;
+    const bool good = (i == 0 && n > 0) || (hit[x] && s_first[parent[x]] == i);
+    const unsigned word = __ballot_sync(0xffffffffu, good);
+    if (lane == 0) s_good[i / 32] = word;
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * kTreeThreads + tid;
+    bool on = i < n;
+    int place = -1;
+    if (on) {
+#pragma unroll
+      for (int w = 0; w < kTreeWords; ++w) {
+        on = on && (seen[x][w] & ~s_good[w]) == 0u;
+        place += __popc(seen[x][w]);
+      }
+      if (on && place >= 0) s_path[place] = i;
+    }
+    count += __syncthreads_count(on);
+  }
+  for (int i = tid; i < s.n; i += kTreeThreads) {
+    const int node = i < count ? min(max(s_path[i], 0), n - 1) : -1;
+    a.path[s.first + i] = node;
+    a.sources[s.first + i] = node >= 0 ? s_slot[node] : -1;
+  }
+  if (tid == 0) {
+    a.counts[r] = count;
+    a.next[r] = count > 0 ? s_choice[min(max(s_path[count - 1], 0), n - 1)] : -1;
+    a.lens_out[r] = min(before, after) + count;
+  }
+}
+
+// The pages behind the new lengths go behind the free ones of the ring, in the requests' order (as in
+// page_plan_kernel: every CTA sums over all requests itself).
+__global__ void __launch_bounds__(kPlanThreads) tree_release_kernel(const TreeAcceptArgs a) {
+  extern __shared__ int plan_smem[];
+  int* const s_back = plan_smem;  // [b] first place of a request's released pages
+  __shared__ int warp_sums[kPlanThreads / 32][3];
+  grid_launch_dependents();
+  grid_wait();
+  const int head = static_cast<int>(static_cast<unsigned>(a.state[0]) % static_cast<unsigned>(a.cap));
+  const int count = min(max(a.state[1], 0), a.cap);
+  const int limit = a.width << a.page_shift;  // at most 2^30
+  auto pages = [&](int tokens) { return tokens > 0 ? ((min(tokens, limit) - 1) >> a.page_shift) + 1 : 0; };
+  auto back = [&](int r) { return max(pages(a.after[r]) - pages(a.lens_out[r]), 0); };
+  const int per = (a.b + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(a.b, static_cast<int>(threadIdx.x) * per), r1 = min(a.b, r0 + per);
+  int v[3] = {0, 0, 0}, total[3];
+  for (int r = r0; r < r1; ++r) v[0] += back(r);
+  block_scan3(v, total, warp_sums);
+  for (int r = r0; r < r1; ++r) {
+    s_back[r] = v[0];
+    v[0] += back(r);
+  }
+  __syncthreads();
+  const int gthread = blockIdx.x * kPlanThreads + threadIdx.x, gthreads = gridDim.x * kPlanThreads;
+  const int lane = threadIdx.x % 32;
+  if (gthread == 0) {
+    a.state_out[0] = head;
+    a.state_out[1] = count + min(total[0], a.cap - count);
+  }
+  for (int r = gthread / 32; r < a.b; r += gthreads / 32) {
+    const int n = back(r), keep = pages(a.lens_out[r]);
+    const int* const row = a.table + static_cast<long long>(r) * a.width;
+    for (int i = lane; i < n; i += 32) {
+      const long long at = static_cast<long long>(count) + s_back[r] + i;
+      if (at >= a.cap) continue;  // a ring without room for all keeps the first ones
+      const unsigned x = static_cast<unsigned>(head) + static_cast<unsigned>(at), cap = static_cast<unsigned>(a.cap);
+      a.queue[x >= cap ? x - cap : x] = row[keep + i];
+    }
+  }
+}
+
+}  // namespace exattn

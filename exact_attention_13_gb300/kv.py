@@ -196,6 +196,62 @@ def rope(q, k, positions, turns, interleaved: bool = False, inverse: bool = Fals
     return q_out, k_out
 
 
+def rope_axis_pairs(sections, cycled: bool = False, device="cuda"):
+    """The axis of each pair for ``rope_axes``: uint8 [sum(sections)].
+
+    ``sections``: how many pairs each axis has, up to four axes, as (16, 24, 24) for time, height and width
+    at a rotary dim of 128.  The axes take their pairs one section behind the other, or, ``cycled``, in turn
+    until their sections are used up (0, 1, 2, 0, 1, 2, ...)."""
+    left = [int(n) for n in sections]
+    _need(1 <= len(left) <= 4 and all(n >= 0 for n in left) and 0 < sum(left) <= 64,
+          "sections must be the pairs of one to four axes, 64 in all at most")
+    if cycled:
+        pairs = [a for i in range(max(left)) for a, n in enumerate(left) if i < n]
+    else:
+        pairs = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(pairs, dtype=torch.uint8, device=device)
+
+
+def rope_axes(q, k, positions, turns, axes, interleaved: bool = False, inverse: bool = False,
+              mscale: float = 1.0, q_out=None, k_out=None):
+    """Rotary positions with several axes (the time, height and width of image and video tokens): as
+    ``rope``, but pair i turns by position ``axes[i]`` of its token.
+
+    ``positions``: int32 [A, N] or [A, B, N] ([A, T] for packed tokens), A from 1 to 4; text tokens have the
+    same position on all axes.  ``axes``: uint8 [rotary_dim / 2], as ``rope_axis_pairs`` makes it (an axis
+    that there is not counts as the first).  ``turns``: from ``rope_turns``, or any table that gives each pair its own
+    frequency.  ``inverse``: the gradients of q and k from those of the outputs."""
+    index = q.get_device()
+    (B, Hq, N, d), qs = _heads(q, index, "q")
+    q_out, qos = _out_like(q, q_out, index, "q_out")
+    if k is None:
+        k_out, Hk, kp, ko, ks, kos = None, 0, None, None, None, None
+    else:
+        (Bk, Hk, Nk, dk), ks = _heads(k, index, "k")
+        if Bk != B or Nk != N or dk != d or k.dim() != q.dim():
+            raise ValueError("k must be like q but for its heads")
+        k_out, kos = _out_like(k, k_out, index, "k_out")
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    shape = positions.shape
+    per_batch = len(shape) == 3
+    if not 2 <= len(shape) <= 3 or not 1 <= shape[0] <= 4:
+        raise ValueError("positions must be [axes, N] or [axes, B, N] with one to four axes")
+    _ints(positions, (shape[0], B, N) if per_batch else (shape[0], N), index, "positions")
+    if (turns.dtype is not torch.int64 or turns.dim() != 1 or turns.get_device() != index
+            or not turns.is_contiguous()):
+        raise ValueError(f"turns must be a contiguous int64 vector on cuda:{index}")
+    if (axes.dtype is not torch.uint8 or axes.shape != turns.shape or axes.get_device() != index
+            or not axes.is_contiguous()):
+        raise ValueError(f"axes must be a contiguous uint8 vector as long as turns on cuda:{index}")
+    if B * N == 0:
+        return q_out, k_out
+    _run("fa_rope_axes", index, q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, kp, ks, ko, kos, Hk, B, N, d,
+         positions.data_ptr(), shape[0], B * N if per_batch else N, N if per_batch else 0, axes.data_ptr(),
+         turns.data_ptr(), 2 * turns.shape[0],
+         (FA_ROPE_INTERLEAVED if interleaved else 0) | (FA_ROPE_INVERSE if inverse else 0), mscale)
+    return q_out, k_out
+
+
 # ---------------------------------------------------------------------------------------------
 # page planning
 # ---------------------------------------------------------------------------------------------

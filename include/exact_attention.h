@@ -259,6 +259,24 @@ FA_API int fa_rope(const void* q, const long long* q_strides, void* q_out,
                    const long long* turns, int rotary_dim, int flags, float mscale, void* stream);
 
 /*
+ * Rotary positions with several axes (time, height and width of image and video tokens): as fa_rope, but each
+ * token has a position on each of num_axes axes and pair i turns by position[axes[i]] * f_i.
+ *   positions : device int32; the position of row n of batch b on axis x lies at
+ *               x * positions_axis_stride + b * positions_batch_stride + n (strides >= 0; 0: shared)
+ *   num_axes  : 1 to 4
+ *   axes      : device uint8 [rotary_dim / 2] (8-byte aligned), the axis of each pair; an axis >= num_axes
+ *               counts as axis 0
+ * The rest, the gradient (FA_ROPE_INVERSE) included, as fa_rope.
+ */
+FA_API int fa_rope_axes(const void* q, const long long* q_strides, void* q_out,
+                        const long long* q_out_strides, int Hq, const void* k,
+                        const long long* k_strides, void* k_out, const long long* k_out_strides,
+                        int Hk, int B, int N, int d, const int* positions, int num_axes,
+                        long long positions_axis_stride, long long positions_batch_stride,
+                        const unsigned char* axes, const long long* turns, int rotary_dim, int flags,
+                        float mscale, void* stream);
+
+/*
  * One step of a paged cache's bookkeeping, on the device: which request gets which pages, and
  * where each new token goes.  Request b holds lens[b] tokens in the pages table[b, 0 ..
  * ceil(lens[b] / page_size)); it brings new_lens[b] tokens, or, with new_lens[b] < 0, it has ended
@@ -368,6 +386,83 @@ FA_API int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_st
  * tables: no key head's work is split), and for invalid arguments. */
 FA_API size_t fa_kv4_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size,
                                          int table_width);
+
+/*
+ * Trees of drafted tokens.  A request's new tokens are the nodes 0 .. n - 1 of a tree behind its lens[b] cached
+ * ones: node i hangs on node parents[i] < i of the same request, or (any other value, such as -1) on the last
+ * cached token.  Positions are lens[b] + depth (0 for a node on the last cached token).  In `seen`, bit j % 32 of
+ * word j / 32 of node i's row is set iff j is i or lies on i's way up.
+ *   parents   : device int32 [T], packed by request
+ *   q_offsets : device int32 [B + 1], not decreasing: first node of each request (rows past T do not count)
+ *   words     : 1 to 8, words of a row of `seen`.  Nodes from 32 * words on have no bit: they are seen by none,
+ *               and their rows hold the bits of the nodes above them that have one
+ *   positions : output [T];  seen : output [T, words].  Rows past q_offsets[B]: position 0 and no bits
+ *   sizes     : 1 <= B <= 16384, T >= 1, T * words < 2^31
+ * No output may overlap an input.  One launch, integers only.
+ */
+FA_API int fa_tree_plan(const int* parents, const int* q_offsets, const int* lens, int B, int T,
+                        int words, int* positions, unsigned* seen, void* stream);
+
+/*
+ * Attention of the nodes of such trees over the paged 4-bit cache, which holds them already: request b's nodes are
+ * rows q_offsets[b] .. q_offsets[b + 1) of q and the last tokens of its lens[b] cached ones, in their order.  A node
+ * sees the cached tokens before its tree (j < lens[b] - n) and node m (token lens[b] - n + m) iff bit m % 32 of
+ * word m / 32 of its row of `seen` is set.  Nodes from 32 * words on are not seen.  Any mask of bits will do; a row
+ * that sees nothing gets O = 0 and LSE = -inf.
+ *   seen      : device [T, words] (4-byte aligned), words from 1 to 8
+ *   q_offsets : as fa_kv4_fwd, not NULL
+ *   workspace : fa_kv4_tree_fwd_workspace_bytes(...) bytes, as fa_kv4_fwd's
+ * Everything else as fa_kv4_fwd.
+ */
+FA_API int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stride,
+                           const void* cache, int num_pages, int page_size, const int* table,
+                           int table_width, const int* lens, const int* q_offsets,
+                           const unsigned* seen, int words, void* o, float* lse, int T, int B, int Hq,
+                           int Hkv, int d, int max_q, float scale, float k_descale, float v_descale,
+                           void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+FA_API size_t fa_kv4_tree_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size,
+                                              int table_width);
+
+/*
+ * What a step accepts of its trees.  choices[t] is the token that the model chose behind node t.  Node 0 of a
+ * request is accepted (its token was chosen before), and every child of an accepted node whose token equals its
+ * parent's choice (of several such children the one with the lowest number): a path down the tree.
+ *   parents, seen, words, q_offsets : as for and from fa_tree_plan (`seen` that belongs to other parents gives
+ *                   meaningless rows, but no access outside the buffers).  Nodes without a bit are not accepted
+ *   tokens, choices : device int32 [T]
+ *   lens, new_lens  : device int32 [B]: lengths before the step, and with all nodes (0 for ended requests).  A request
+ *                   whose length did not grow (refused, ended, no nodes) accepts nothing
+ *   slots         : device int32 [T]: the nodes' slots
+ *   table, queue, queue_size, queue_state, page_size : as fa_page_plan, after it.  Pages that new_lens needs and
+ *                   the accepted length does not go back to the ring, behind the free ones, in the requests' order
+ *   lens_out      : [B] min(lens, new_lens) + accepted nodes;  counts : [B] accepted nodes
+ *   path          : [T] a request's accepted nodes in their order in its first rows, -1 in the others
+ *   next_tokens   : [B] choice of the last accepted node, -1 where none is
+ *   sources       : [T] slots of the nodes of `path`, -1 in the other rows
+ *   queue_state_out : {head, count} after the step
+ *   sizes         : as fa_tree_plan; T = 0 is a step without nodes (arrays of T entries may be NULL)
+ * All arrays are device int32.  No output may overlap an input or another output (lens_out and queue_state_out
+ * are refused when they are the inputs; the ring is both).  Two launches, integers only.
+ */
+FA_API int fa_tree_accept(const int* parents, const unsigned* seen, int words, const int* tokens,
+                          const int* choices, const int* lens, const int* new_lens,
+                          const int* q_offsets, const int* slots, const int* table, int table_width,
+                          int* queue, int queue_size, const int* queue_state, int B, int page_size,
+                          int T, int* lens_out, int* counts, int* path, int* next_tokens,
+                          int* sources, int* queue_state_out, void* stream);
+
+/*
+ * Move rows of paged 4-bit caches: for request b and i < counts[b], the keys and values of all heads at slot
+ * sources[q_offsets[b] + i] to slot slots[q_offsets[b] + i], in each of num_caches caches (one a layer).
+ *   caches  : HOST array of num_caches (1 to 256) device pointers to different caches of one shape
+ *   sources, slots : device int32 [T]; rows with one outside the cache are skipped
+ *   q_offsets, counts : device int32 [B + 1] and [B]
+ * No source may be the slot of an earlier row of its request, or of any row of another: what is moved then is
+ * undefined (fa_tree_accept's never are).  18 * Hkv * B < 2^31 - 128; the rest as fa_kv4_append.  One launch.
+ */
+FA_API int fa_kv4_move(void* const* caches, int num_caches, int num_pages, int page_size, int Hkv,
+                       int d, const int* sources, const int* slots, const int* q_offsets,
+                       const int* counts, int T, int B, void* stream);
 
 /*
  * Read, and if `clear` is nonzero reset to FA_OK, the library's status word on the current
