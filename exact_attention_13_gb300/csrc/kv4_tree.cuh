@@ -1,0 +1,993 @@
+// kv4_tree.cuh -- attention of trees of drafted tokens over the paged 4-bit cache.
+//
+// The operation of kv4_attn.cuh with another mask: a node sees the keys before its request's tree, and of the
+// tree's keys those whose bit is set in its row of `seen`.  Units of N = 16, 32, 64 or 128 query rows (one key
+// head of one request, rows ordered by node, then by head of the group).
+//
+// Both products take the widened cache as the 128-row operand of tcgen05.mma, out of tensor memory:
+//     S^T [128 keys x N] = K [128 x d] Q^T,      O^T [d x N] += V^T [d x 128 keys] P^T
+// so the tensor core does N products a cached value (query rows as the 128-row operand: 128, mostly padding),
+// and the widened tiles, four times the cache's bytes, go from registers to tensor memory without
+// a write and a read of shared memory.  What is left there a tile is the codes (written once by the bulk copies, read
+// once), Q^T (N x d, read by the product) and P^T (128 x N).
+//
+// Layouts.  An A operand in tensor memory is one lane a row and 32 bits of two neighbouring contraction indices a
+// column.  Contraction indices and rows may be permuted freely, so the tiles are stored with the 16x128b shape:
+// thread (g, t) = (lane / 4, lane % 4) writes rows g and g + 8, columns 4 n + t.
+//   K: column 4 n + t holds dims t d/4 + 2 n and the next one: a thread reads d/4 neighbouring codes of a row.
+//      Row m holds key 16 (t' + 4 (n' % 2)) + 2 (n' / 2) + e with m = 8 n' + 2 t' + e.
+//   V^T: column 4 n + t holds keys 16 (t + 4 (n % 2)) + 2 (n / 2) and the next one, that is, contraction index k holds
+//      the key of row m = k of K: a thread of the softmax writes P of its own key to row m of P^T.  Row 32 q + 8 i + g
+//      is dim 32 q + 4 g + i (d = 128; for d = 64 row 32 q + 8 i + g, i < 2, is dim 16 q + 2 g + i and the other rows
+//      are not used): a thread needs 4 neighbouring codes, 16 bits, of each of its keys.  For d = 128 a warp loads eight
+//      keys' 16 bytes at a time, one key of each group of 16 (whose codes are padded to other banks), and movmatrix
+//      transposes the 8 x 8 matrix of 16-bit pieces.
+//
+// Softmax.  A thread has one key and N/2 rows, so a row's sum runs over threads: each keeps partial sums of its
+// keys, added up at the end of a unit.  The maximum would be one reduction a tile, row and warp; instead the
+// reference m of a row is moved only when some score of the tile lies more than 2^15 above it (kDecLazy): a
+// maximum over the thread's own scores and one barrier with a vote decide, and mostly nothing else happens.
+//
+// Roles (one CTA a SM):
+//   8 or 16 warps  softmax: lanes 32 (w % 4) .. + 31 (keys; dims of O^T), the w / 4-th part of the rows; outputs
+//   4 and 4        widen K and V^T
+//   1              issues the MMAs:  S(t + 1) | PV(t) | S(t + 2) | ...
+//   1              copies codes and scales into a ring of tiles
+//   2              queries, masks and places of the rows of the next unit, while this one runs
+// The split over CTAs and the merge of units that cross them are those of kv4_attn.cuh.
+//
+// Every mbarrier wait is bounded in time; one that runs out sets the CTA's abort flag and the status word, and
+// all roles leave.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "fa_fwd_kernel.cuh"
+#include "kv4_attn.cuh"
+#include "kv4_chunk.cuh"
+#include "tree_plan.cuh"
+
+namespace exattn {
+
+constexpr int kTrKeys = 128;
+constexpr int kTrFlags = 32;  // tiles whose flags are kept: more than are ever between copies and softmax
+
+template <int D, int N>
+struct TreeGeo {
+  // a stage of the ring: codes of K, of V (16 keys at a time, padded by 16 bytes), scales of K, of V
+  static constexpr int kGroup = 16 * D / 2, kVGroup = kGroup + 16, kScales = 16 * D / 16;
+  static constexpr int kV = 8 * kGroup, kKs = kV + 8 * kVGroup, kVs = kKs + 8 * kScales, kStage = kVs + 8 * kScales;
+  static constexpr int kStages = N == 128 ? 6 : 8;
+  static constexpr int kBufs = N == 128 ? 1 : 2;        // of K, V^T and P^T
+  static constexpr int kQBytes = N * D * 2;             // boxes of 64 dims, 128 bytes a row
+  static constexpr int kPBytes = (N + 63) / 64 * 128 * 128;
+  static constexpr int kCols = N < 32 ? 32 : N;         // columns between accumulators
+  static constexpr int kO = 2 * kCols, kK = 3 * kCols, kVt = kK + kBufs * (D / 2);
+  static_assert(kVt + kBufs * 64 <= 512, "tensor memory");
+  static constexpr uint32_t kIdescS = instr_desc(128, N, 0, false, false);
+  static constexpr uint32_t kIdescPV = instr_desc(128, N, 0, false, true);
+  // warps: softmax, then 4 that widen K, 4 that widen V^T, and 4 others
+  static constexpr int kSoft = N == 64 ? 16 : 8;
+  static constexpr int kWidenWarp = kSoft, kMmaWarp = kSoft + 8, kCopyWarp = kSoft + 9, kQueryWarp = kSoft + 10;
+  static constexpr int kThreads = 32 * (kSoft + 12);
+  static constexpr int kParts = kSoft / 4;              // of the rows; a softmax thread has one
+  static constexpr int kCol = N / kParts;               // rows of a softmax thread
+  static constexpr int kChunk = kCol < 32 ? kCol : 32;
+  // registers a thread at launch, and how the warpgroups share them
+  static constexpr int kLaunchRegs = kSoft == 16 ? 72 : 96, kSoftRegs = kSoft == 16 ? 72 : 120;
+  static constexpr int kWidenRegs = kSoft == 16 ? 72 : 80, kOtherRegs = kSoft == 16 ? 72 : 80;
+  static_assert(32 * kSoft * kSoftRegs + 256 * kWidenRegs + 128 * kOtherRegs == kThreads * kLaunchRegs,
+                "registers of the block at launch");
+};
+
+// A share of a unit: tiles [tile, tile + n) of its `tiles`; n = 0: there are no more.
+struct TreeSeg {
+  int r, head, block, tile, n, tiles;
+  ReqShape req;
+};
+struct TreeWalk {
+  TreeSeg s;
+  int blocks;
+  long long left;  // tiles of the CTA's share from s.tile on (units, when they are not split)
+};
+
+template <int N>
+struct TreeRows {          // of one unit, written by the query warps
+  TreeSeg seg;
+  float c;                 // factor of the scores
+  int out[N];              // row of o and lse, -1: padding
+  uint32_t seen[N][kTreeWords + 1];
+};
+
+template <int N>
+struct TreeCtrl {
+  uint64_t ring_full[8], ring_empty[8];
+  uint64_t k_full[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], o_empty, drain;
+  uint32_t tmem_base;
+  int abort;
+  int flags[kTrFlags];     // bit g: 16-key group g of the tile is there; -1: no more tiles
+  long long sum[32];
+  long long total, first, last;
+  TreeSeg start;
+  TreeRows<N> rows[2];
+  alignas(16) float nm[N];  // minus the reference of a row's probabilities
+  float alpha[N];
+  float top[4][N];          // of each quarter's keys: maxima, and in the end sums
+  alignas(16) uint32_t scales[4][8][20];  // V's scales of a widening warp, as pairs of keys
+};
+
+template <int D, int N>
+constexpr int tree_smem_bytes() {
+  using G = TreeGeo<D, N>;
+  return 2 * G::kQBytes + G::kBufs * G::kPBytes + G::kStages * G::kStage + static_cast<int>(sizeof(TreeCtrl<N>)) + 1024;
+}
+
+// ---- small PTX
+// As mbar_try_wait, suspended for up to about `ns`.
+__device__ __forceinline__ uint32_t mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return done;
+}
+constexpr uint32_t kTrTryNs = 200000;
+// The largest of the warp's values (NaN: the others).
+__device__ __forceinline__ float warp_max(float v) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
+}
+// An arrival on `bar` when the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Barrier over `threads` threads that tells whether any of them votes yes.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool vote) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+               "barrier.cta.red.or.pred.aligned q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(any)
+               : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(vote))
+               : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void bar_wait(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+#define EXATTN_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define EXATTN_W4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+// N consecutive columns of the thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns of one load");
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : EXATTN_R4(r, 0), EXATTN_R4(r, 4)
+                 : "r"(taddr));
+  if constexpr (N == 16)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : EXATTN_R4(r, 0), EXATTN_R4(r, 4), EXATTN_R4(r, 8), EXATTN_R4(r, 12)
+                 : "r"(taddr));
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 EXATTN_W4(r, 0), EXATTN_W4(r, 4)
+                 : "memory");
+  if constexpr (N == 16) tmem_st16(taddr, r);
+  if constexpr (N == 32) tmem_st32(taddr, r);
+}
+// 16 lanes from the address's on, 32 columns: r[2 n + i] to row lane / 4 + 8 i, column 4 n + lane % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+               "%14, %15, %16};" ::"r"(taddr),
+               EXATTN_W4(r, 0), EXATTN_W4(r, 4), EXATTN_W4(r, 8), EXATTN_W4(r, 12)
+               : "memory");
+}
+#undef EXATTN_R4
+#undef EXATTN_W4
+
+// ---- the line of tiles
+template <int N>
+__device__ __forceinline__ int tree_blocks(const Kv4Args& a, const ReqShape& s) {
+  return static_cast<int>((static_cast<long long>(s.q_len) * a.group + N - 1) / N);
+}
+__device__ __forceinline__ int tree_tiles(const ReqShape& s) { return max(1, (s.keys - 1) / kTrKeys + 1); }
+
+// The next segment of a warp's walk (every lane does the same); s.n = 0 at the end of the share.
+template <int N>
+__device__ __forceinline__ void tree_next(const Kv4Args& a, TreeWalk& w) {
+  w.left -= a.whole_tiles ? 1 : w.s.n;
+  w.s.n = 0;
+  if (w.left <= 0) return;
+  w.s.tile = 0;
+  if (++w.s.head == a.hk) {
+    w.s.head = 0;
+    if (++w.s.block == w.blocks) {
+      w.s.block = 0;
+      do {
+        ++w.s.r;
+        w.s.req = kv4_request(a, w.s.r);
+        w.blocks = tree_blocks<N>(a, w.s.req);
+      } while (w.blocks == 0 && w.s.r + 1 < a.b);
+      w.s.tiles = tree_tiles(w.s.req);
+    }
+  }
+  w.s.n = a.whole_tiles ? w.s.tiles : static_cast<int>(min(static_cast<long long>(w.s.tiles), w.left));
+}
+template <int N>
+__device__ __forceinline__ TreeWalk tree_walk(const Kv4Args& a, const TreeCtrl<N>* ctl) {
+  TreeWalk w;
+  w.s = ctl->start;
+  w.blocks = tree_blocks<N>(a, w.s.req);
+  w.left = ctl->last - ctl->first;
+  w.s.n = a.whole_tiles ? w.s.tiles : static_cast<int>(min(static_cast<long long>(w.s.tiles - w.s.tile), w.left));
+  return w;
+}
+
+// The CTA's share [first, last) of the line of `total` tiles (units, when they are not split); fills ctl->start.
+// Returns the number of CTAs that have work.
+template <int N, int THREADS>
+__device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  ReqShape s{0, 0, 0, 0};
+  int per = 1;
+  auto cost = [&](int r) -> long long {
+    if (r >= a.b) return 0;
+    s = kv4_request(a, r);
+    per = a.whole_tiles ? 1 : tree_tiles(s);
+    return static_cast<long long>(tree_blocks<N>(a, s)) * a.hk * per;
+  };
+  auto scan = [&](long long x) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) ctl->sum[warp] = x;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < warp; ++w) x += ctl->sum[w];
+    return x;
+  };
+  long long mine = 0, tiles = 0;
+  for (int r = tid; r < a.b; r += THREADS) mine += tiles = cost(r);
+  long long inc = scan(mine), total = 0;
+#pragma unroll 1
+  for (int w = 0; w < THREADS / 32; ++w) total += ctl->sum[w];
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= n) return n;
+  const long long first = share_begin(total, n, blockIdx.x), last = share_begin(total, n, blockIdx.x + 1);
+  long long base = 0;
+  for (int r0 = 0; r0 < a.b; r0 += THREADS) {
+    long long all = total;
+    if (a.b > THREADS) {
+      __syncthreads();
+      tiles = cost(r0 + tid);
+      inc = scan(tiles) + base;
+      all = base;
+#pragma unroll 1
+      for (int w = 0; w < THREADS / 32; ++w) all += ctl->sum[w];
+    }
+    if (first >= inc - tiles && first < inc) {
+      const long long off = first - (inc - tiles);
+      // (64-bit divisions take about 100 instructions)
+      const int u = off <= 0x7fffffffll ? static_cast<int>(off) / per : static_cast<int>(off / per);
+      const int block = u / a.hk;
+      ctl->start = TreeSeg{r0 + tid,
+                           u - block * a.hk,
+                           block,
+                           a.whole_tiles ? 0 : static_cast<int>(off - static_cast<long long>(u) * per),
+                           0,
+                           tree_tiles(s),
+                           s};
+      ctl->total = total;
+      ctl->first = first;
+      ctl->last = last;
+    }
+    base = all;
+    if (first < base) break;
+  }
+  __syncthreads();
+  return n;
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(const Kv4Args a) {
+  using G = TreeGeo<D, N>;
+  extern __shared__ __align__(1024) uint8_t tr_smem[];
+  uint8_t* const smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const s_q = smem;
+  uint8_t* const s_p = smem + 2 * G::kQBytes;
+  uint8_t* const s_ring = s_p + G::kBufs * G::kPBytes;
+  static_assert(G::kStages * G::kStage % 16 == 0 && G::kQBytes % 1024 == 0, "alignment");
+  TreeCtrl<N>* const ctl = reinterpret_cast<TreeCtrl<N>*>(s_ring + G::kStages * G::kStage);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  grid_launch_dependents();
+  const int n_cta = tree_my_range<N, G::kThreads>(a, ctl);
+  if (static_cast<int>(blockIdx.x) >= n_cta) {
+    if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  if (warp == G::kMmaWarp) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(smem_u32(&ctl->ring_full[i]), 33);  // the copying warp's lanes, and its flags
+      mbar_init(smem_u32(&ctl->ring_empty[i]), 8);  // one arrival per widening warp
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->k_full[i]), 4);
+      mbar_init(smem_u32(&ctl->v_full[i]), 4);
+      mbar_init(smem_u32(&ctl->s_full[i]), 1);
+      mbar_init(smem_u32(&ctl->s_empty[i]), G::kSoft);  // one arrival per softmax warp
+      mbar_init(smem_u32(&ctl->p_full[i]), G::kSoft);
+      mbar_init(smem_u32(&ctl->pv_done[i]), 1);
+      mbar_init(smem_u32(&ctl->q_full[i]), 2);   // one arrival per query warp
+      mbar_init(smem_u32(&ctl->q_empty[i]), 1 + G::kSoft);  // the unit's last S, and the softmax warps
+    }
+    mbar_init(smem_u32(&ctl->o_empty), G::kSoft);
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int* const abort_flag = &ctl->abort;
+  // For the number-th completion, counted from 0.  A try suspends the warp for a while; the first that fails starts the
+  // clock, and a wait that runs out raises the CTA's abort flag (small code: there are 20 copies of it).
+  auto wait = [&](uint64_t& bar, int number) -> bool {
+    const uint32_t at = smem_u32(&bar), parity = static_cast<uint32_t>(number) & 1u;
+    uint64_t limit = 0;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait_for(at, parity, kTrTryNs))) {
+      const uint64_t now = globaltimer_ns();
+      if (limit == 0) limit = now + kWaitLimitNs;
+      if (__any_sync(0xffffffffu, *abort_flag || now > limit)) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp >= G::kMmaWarp) {
+    if constexpr (G::kOtherRegs < G::kLaunchRegs) regs_dec<G::kOtherRegs>();
+    if (warp == G::kMmaWarp) {
+      // ============================================================ MMA issuer
+      const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
+      const uint64_t p_desc = smem_desc(smem_u32(s_p), 128 * 128, 1024, kSwizzle128B);
+      int u_s = -1, left_s = 0;  // the unit that S works on, and its tiles to come
+      int u_v = -1, left_v = 0;
+      bool ok = true, more = true;
+      // S of tile t; false at the end of the tiles (or on abort: ok is false then)
+      auto issue_s = [&](int t) -> bool {
+        if (left_s == 0) {
+          ++u_s;
+          ok = wait(ctl->q_full[u_s & 1], u_s >> 1);
+          if (!ok) return false;
+          left_s = ctl->rows[u_s & 1].seg.n;
+          if (left_s == 0) return false;
+        }
+        --left_s;
+        ok = wait(ctl->k_full[t % G::kBufs], t / G::kBufs);
+        if (ok && t >= 2) ok = wait(ctl->s_empty[t & 1], (t >> 1) - 1);
+        if (!ok) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t qd = q_desc + (u_s & 1) * (G::kQBytes >> 4);
+          const uint32_t k = tmem + G::kK + t % G::kBufs * (D / 2), s = tmem + (t & 1) * G::kCols;
+          mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 0u, k, qd);
+          if constexpr (D == 128)
+            mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 1u, k + 32, qd + (N * 128 >> 4));
+          tc_commit(smem_u32(&ctl->s_full[t & 1]));
+          if (left_s == 0) tc_commit(smem_u32(&ctl->q_empty[u_s & 1]));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int t) {
+        bool begins = false;
+        if (left_v == 0) {
+          ++u_v;
+          left_v = ctl->rows[u_v & 1].seg.n;
+          begins = true;
+          if (u_v > 0) ok = wait(ctl->o_empty, u_v - 1);
+        }
+        --left_v;
+        ok = ok && wait(ctl->v_full[t % G::kBufs], t / G::kBufs) && wait(ctl->p_full[t % G::kBufs], t / G::kBufs);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_chain_ts_off<8, 0, 128, 8, 16, 24, 32, 40, 48, 56>(
+              tmem + G::kO, G::kIdescPV, begins ? 0u : 1u, tmem + G::kVt + t % G::kBufs * 64,
+              p_desc + t % G::kBufs * (G::kPBytes >> 4));
+          tc_commit(smem_u32(&ctl->pv_done[t & 1]));
+        }
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (int t = -1; more && ok; ++t) {  // (one copy of the code)
+        more = issue_s(t + 1);
+        if (ok && t >= 0) issue_pv(t);
+      }
+      // nothing this warp issued may still run when the TMEM is released
+      __syncwarp();
+      if (elect_one()) tc_commit(smem_u32(&ctl->drain));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    } else if (warp == G::kCopyWarp) {
+      // ============================================================ copies of the cache
+      // 16 bytes a lane and copy.  Groups of 16 keys on pages that are not there are not copied: their scores are
+      // masked, and whatever lies in the ring is a number after widening.
+      TreeWalk w = tree_walk<N>(a, ctl);
+      const int page_rows = 1 << a.page_shift;
+      const int block_bytes = kv4_block_bytes(page_rows, D);
+      const size_t page_bytes = static_cast<size_t>(block_bytes) * 2u * a.hk;
+      // scales: kJoin groups a copy, kLanes lanes for the keys' and for the values' of each
+      constexpr int kLanes = G::kScales / 16, kJoin = 16 / kLanes;
+      const int sc_group = lane / (2 * kLanes), sc_kv = lane / kLanes & 1, sc_at = lane % kLanes * 16;
+      const uint32_t ring = smem_u32(s_ring);
+      const uint32_t sc_dst = ring + (sc_kv ? G::kVs : G::kKs) + sc_group * G::kScales + sc_at;
+      const size_t sc_from = (sc_kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * (D / 2) + sc_at;
+      int t = 0;
+      bool ok = true;
+      while (w.s.n > 0 && ok && !EXATTN_INJECT_STALL) {
+        const int* const ids = a.table + static_cast<size_t>(w.s.r) * a.width;
+        const uint8_t* const head = a.cache + static_cast<size_t>(w.s.head) * 2 * block_bytes;
+        int key = w.s.tile * kTrKeys + lane % 8 * 16;  // lanes g, g + 8, ...: group g
+        int id = key < w.s.req.keys ? ids[key >> a.page_shift] : -1;
+        for (int i = 0; i < w.s.n; ++i, ++t) {
+          const int next = key + kTrKeys;
+          const int id_next = i + 1 < w.s.n && next < w.s.req.keys ? ids[next >> a.page_shift] : -1;
+          const int slot = t % G::kStages;
+          if (t >= G::kStages) ok = wait(ctl->ring_empty[slot], t / G::kStages - 1);
+          if (!ok) break;
+          const bool there = static_cast<unsigned>(id) < static_cast<unsigned>(a.pages);
+          const int flags = static_cast<int>(__ballot_sync(0xffffffffu, there) & 0xffu);
+          const size_t page_at = there ? static_cast<size_t>(id) * page_bytes : 0;
+          const int row = key & (page_rows - 1);
+          const uint32_t stage = slot * G::kStage;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const size_t at = __shfl_sync(0xffffffffu, page_at, g);
+            const uint8_t* const k = head + at + __shfl_sync(0xffffffffu, row, g) * (D / 2) + lane * 16;
+            const uint32_t dst = ring + stage + g * G::kGroup + lane * 16;
+            if (flags >> g & 1) {
+#pragma unroll
+              for (int x = 0; x < G::kGroup; x += 512) {
+                cp_async16(dst + x, k + x, 16u);
+                cp_async16(dst + G::kV + g * (G::kVGroup - G::kGroup) + x, k + block_bytes + x, 16u);
+              }
+            }
+          }
+#pragma unroll
+          for (int g0 = 0; g0 < 8; g0 += kJoin) {
+            const int g = g0 + sc_group;
+            const size_t at = __shfl_sync(0xffffffffu, page_at, g);
+            const int sc_row = __shfl_sync(0xffffffffu, row, g);
+            if (flags >> g & 1) cp_async16(sc_dst + stage + g0 * G::kScales, head + at + sc_row * (D / 16) + sc_from, 16u);
+          }
+          const uint32_t bar = smem_u32(&ctl->ring_full[slot]);
+          cp_async_arrive(bar);
+          if (lane == 0) {
+            ctl->flags[t % kTrFlags] = flags;
+            mbar_arrive(bar);
+          }
+          key = next;
+          id = id_next;
+        }
+        if (ok) tree_next<N>(a, w);
+      }
+      if (ok) ok = t < G::kStages || wait(ctl->ring_empty[t % G::kStages], t / G::kStages - 1);
+      if (ok && !EXATTN_INJECT_STALL) {  // (a test build delivers nothing: the first waits run out)
+        const uint32_t bar = smem_u32(&ctl->ring_full[t % G::kStages]);
+        if (lane == 0) {
+          ctl->flags[t % kTrFlags] = -1;
+          mbar_arrive(bar);
+        }
+        mbar_arrive(bar);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();  // copies under way land before the CTA's shared memory goes away
+    } else {
+      // ============================================================ queries, masks and places of a unit's rows
+      // A thread takes d/4 dims of a row: 8 of each quarter, which are four chunks of the operand.
+      TreeWalk w = tree_walk<N>(a, ctl);
+      constexpr int kLanes = D / 32, kRowsIt = 32 / kLanes;
+      const int part = lane % kLanes, self = warp - G::kQueryWarp;
+      for (int u = 0;; ++u) {
+        if (u >= 2 && !wait(ctl->q_empty[u & 1], (u >> 1) - 1)) break;
+        TreeRows<N>& rows = ctl->rows[u & 1];
+        if (self == 0 && lane == 0) rows.seg = w.s;
+        if (w.s.n > 0) {
+          const int live = w.s.req.q_len * a.group - w.s.block * N;
+          uint8_t* const q = s_q + (u & 1) * G::kQBytes;
+          const __nv_bfloat16* const q_head = a.q + static_cast<long long>(w.s.req.q0) * a.q_row +
+                                              static_cast<long long>(w.s.head) * a.group * a.q_head;
+          auto row_at = [&](int row) {  // row of the unit
+            const int at = w.s.block * N + row, node = at / a.group;
+            return q_head + static_cast<long long>(node) * a.q_row +
+                   static_cast<long long>(at - node * a.group) * a.q_head;
+          };
+          // One power of two for all rows brings the largest finite value into [2^14, 2^15): f16 then holds bf16's 8
+          // bits down to 2^-31 of it (2^-17 of a row's own largest, as long as that is not below 2^-14 of the unit's),
+          // and the softmax needs no factor for each row.  Each of the two warps looks at all rows.
+          __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+          const int rows_there = min(live, N);
+#pragma unroll 4
+          for (int x = lane; x < rows_there * (D / 8); x += 32) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(row_at(x / (D / 8)) + x % (D / 8) * 8);
+            const __nv_bfloat162* const v = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // (infinities and NaN: 0 x + |x| is NaN, and the maximum the other one)
+              top = __hmax2(top, __hfma2(v[e], __float2bfloat162_rn(0.f), __habs2(v[e])));
+          }
+          const float amax = warp_max(fmaxf(__low2float(top), __high2float(top)));
+          const uint32_t down_ex = min(268u - (__float_as_uint(amax) >> 23), 253u);
+          const float down = __uint_as_float(down_ex << 23);
+          if (self == 0 && lane == 0) rows.c = a.c * __uint_as_float((254u - down_ex) << 23);
+#pragma unroll 2
+          for (int row0 = self * kRowsIt; row0 < N; row0 += 2 * kRowsIt) {
+            const int row = row0 + lane / kLanes, at = w.s.block * N + row;
+            const int node = at / a.group, head = w.s.head * a.group + at - node * a.group;
+            const __nv_bfloat16* const src = row_at(row) + 8 * part;
+            uint32_t h[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+              if (row < live) raw = *reinterpret_cast<const uint4*>(src + x * (D / 4));
+              float f[8];
+              unpack_bf16x8(raw, f);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int chunk = 4 * part + e;
+              st_shared_v4(smem_u32(q) + chunk / 8 * (N * 128) + row * 128 + ((chunk % 8 ^ (row & 7)) << 4), h[0][e],
+                           h[1][e], h[2][e], h[3][e]);
+            }
+            if (part == 0) rows.out[row] = row < live ? (w.s.req.q0 + node) * a.hq + head : -1;
+            for (int x = part; x < a.words; x += kLanes)
+              rows.seen[row][x] = row < live ? a.tree[static_cast<size_t>(w.s.req.q0 + node) * a.words + x] : 0u;
+          }
+          fence_proxy_async_smem();  // the MMAs read the queries through the async proxy
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[u & 1]));
+        if (w.s.n == 0) break;
+        tree_next<N>(a, w);
+      }
+    }
+  } else if (warp >= G::kWidenWarp + 4) {
+    if constexpr (G::kWidenRegs < G::kLaunchRegs) regs_dec<G::kWidenRegs>();
+    // ============================================================ widening the values
+    const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
+    uint32_t(*const s_scale)[20] = ctl->scales[q];
+    const uint32_t t_v = tmem + (static_cast<uint32_t>(32 * q) << 16) + G::kVt;
+    for (int t = 0;; ++t) {
+      const int slot = t % G::kStages;
+      if (!wait(ctl->ring_full[slot], t / G::kStages) || ctl->flags[t % kTrFlags] < 0) break;
+      const uint8_t* const st = s_ring + slot * G::kStage;
+      // scales of the warp's dims (one or two groups of 16) for pairs of keys: lane 8 x + y takes those of
+      // columns 4 n + x, n = 2 y and 2 y + 1.  A value vector that is not a number (NaN scales) is zero here: its
+      // key's scores are NaN, and rows that do not see the key multiply it by zero.
+      {
+        const int x = lane / 8, n = 2 * (lane % 8);  // keys 16 x + n and the next, and those 64 on
+        const uint8_t* const p = st + G::kVs + (16 * x + n) * (D / 16);
+        if constexpr (D == 128) {
+          uint32_t b[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint16_t*>(p + (i / 2 * 64 + i % 2) * 8 + 2 * q);
+          uint32_t y[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t both = __byte_perm(b[2 * i], b[2 * i + 1], 0x5140);  // (k0 d0, k1 d0, k0 d1, k1 d1)
+            y[0][i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both)), 0u);
+            y[1][i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both >> 16)), 0u);
+          }
+          *reinterpret_cast<uint2*>(&s_scale[x][n]) = make_uint2(y[0][0], y[0][1]);
+          *reinterpret_cast<uint2*>(&s_scale[4 + x][n]) = make_uint2(y[1][0], y[1][1]);
+        } else {
+          uint32_t y[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            y[i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(p[256 * i + q] | p[256 * i + 4 + q] << 8)), 0u);
+          *reinterpret_cast<uint2*>(&s_scale[x][n]) = make_uint2(y[0], y[1]);
+        }
+      }
+      __syncwarp();
+      const uint32_t* const my_scale = s_scale[D == 128 ? g8 / 4 * 4 + t4 : t4];
+      if (t >= G::kBufs && !wait(ctl->pv_done[(t - G::kBufs) & 1], (t - G::kBufs) >> 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // 8 columns of the thread
+        uint32_t sc[8];
+        *reinterpret_cast<uint4*>(sc) = *reinterpret_cast<const uint4*>(my_scale + 8 * b);
+        *reinterpret_cast<uint4*>(sc + 4) = *reinterpret_cast<const uint4*>(my_scale + 8 * b + 4);
+        uint32_t r0[16];
+        if constexpr (D == 128) {
+          // lane 4 r + x loads bytes 4 x .. of the key in group r / 2 + 4 (r % 2): column 2 t + i of the matrix is
+          // column n + i of thread t
+          const uint8_t* const p = st + G::kV + (g8 / 2 + 4 * (g8 % 2)) * G::kVGroup + 16 * q + 4 * t4;
+          uint32_t r1[16];
+#pragma unroll
+          for (int n = 0; n < 8; n += 2) {
+            const uint8_t* const row = p + (8 * b + n) * (D / 2);
+            const uint32_t xa = movmatrix_trans(*reinterpret_cast<const uint32_t*>(row));
+            const uint32_t xb = movmatrix_trans(*reinterpret_cast<const uint32_t*>(row + D / 2));
+            uint32_t even[4], odd[4];  // dims 0, 2 of column n, then of n + 1; dims 1, 3
+            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
+            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              r0[2 * (n + e)] = mul_f16x2(even[2 * e], sc[n + e]);
+              r0[2 * (n + e) + 1] = mul_f16x2(odd[2 * e], sc[n + e]);
+              r1[2 * (n + e)] = mul_f16x2(even[2 * e + 1], sc[n + e]);
+              r1[2 * (n + e) + 1] = mul_f16x2(odd[2 * e + 1], sc[n + e]);
+            }
+          }
+          tmem_st_16x128b_x8(t_v + (16u << 16) + t % G::kBufs * 64 + b * 32, r1);
+        } else {
+          const uint8_t* const p = st + G::kV + t4 * G::kVGroup + 8 * q + g8;
+#pragma unroll
+          for (int n = 0; n < 8; n += 4) {
+            uint32_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              x[e] = p[e / 2 % 2 * 4 * G::kVGroup + (8 * b + n + e / 4 * 2 + e % 2) * (D / 2)];
+            const uint32_t xa = x[0] | x[2] << 8 | x[4] << 16 | x[6] << 24, xb = x[1] | x[3] << 8 | x[5] << 16 | x[7] << 24;
+            uint32_t even[4], odd[4];
+            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
+            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              r0[2 * (n + e)] = mul_f16x2(even[e], sc[n + e]);
+              r0[2 * (n + e) + 1] = mul_f16x2(odd[e], sc[n + e]);
+            }
+          }
+        }
+        tmem_st_16x128b_x8(t_v + t % G::kBufs * 64 + b * 32, r0);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ctl->ring_empty[slot]));
+        mbar_arrive(smem_u32(&ctl->v_full[t % G::kBufs]));
+      }
+    }
+  } else if (warp >= G::kWidenWarp) {
+    if constexpr (G::kWidenRegs < G::kLaunchRegs) regs_dec<G::kWidenRegs>();
+    // ============================================================ widening the keys
+    const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
+    const int row_in = 4 * q + (g8 & 1), group = g8 / 2;  // row + 2 hh, group + 4 i
+    const uint32_t t_k = tmem + (static_cast<uint32_t>(32 * q) << 16) + G::kK;
+    for (int t = 0;; ++t) {
+      const int slot = t % G::kStages;
+      if (!wait(ctl->ring_full[slot], t / G::kStages) || ctl->flags[t % kTrFlags] < 0) break;
+      const uint8_t* const st = s_ring + slot * G::kStage;
+      const uint8_t* const codes = st + group * G::kGroup + row_in * (D / 2) + t4 * (D / 8);
+      const uint8_t* const scale = st + G::kKs + (16 * group + row_in) * (D / 16) + t4 * (D / 64);
+      if (t >= G::kBufs && !wait(ctl->s_full[(t - G::kBufs) & 1], (t - G::kBufs) >> 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t w[2][4], sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int code_at = i * 4 * G::kGroup + 2 * hh * (D / 2), scale_at = (i * 64 + 2 * hh) * (D / 16);
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint4*>(w[i]) = *reinterpret_cast<const uint4*>(codes + code_at);
+            sc[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale + scale_at));
+            // a value vector that is not a number makes its key's scores NaN
+            sc[i] = fma_f16x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale + scale_at + (G::kVs - G::kKs))), 0u,
+                              sc[i]);
+          } else {
+            *reinterpret_cast<uint2*>(w[i]) = *reinterpret_cast<const uint2*>(codes + code_at);
+            sc[i] = e4m3x2_to_f16x2(scale[scale_at]);
+            sc[i] = fma_f16x2(e4m3x2_to_f16x2(scale[scale_at + (G::kVs - G::kKs)]), 0u, sc[i]);
+          }
+        }
+#pragma unroll
+        for (int part = 0; part < D / 64; ++part) {
+          uint32_t r[16];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t h[4];
+              unpack_e2m1x8(w[i][2 * part + x], h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                r[2 * (4 * x + e) + i] = part ? mul_f16x2_hi(h[e], sc[i]) : mul_f16x2_lo(h[e], sc[i]);
+            }
+          tmem_st_16x128b_x8(t_k + (static_cast<uint32_t>(16 * hh) << 16) + t % G::kBufs * (D / 2) + part * 32, r);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ctl->ring_empty[slot]));
+        mbar_arrive(smem_u32(&ctl->k_full[t % G::kBufs]));
+      }
+    }
+  } else {
+    if constexpr (G::kSoftRegs > G::kLaunchRegs) regs_inc<G::kSoftRegs>();
+    // ============================================================ softmax, outputs
+    constexpr int H = G::kCol, C = G::kChunk;
+    const int g = warp / 4, q = warp % 4, m_row = 32 * q + lane, tid = threadIdx.x % 128;
+    const int my_group = m_row % 8 / 2 + 4 * (m_row / 8 % 2);  // of 16 keys
+    const int my_key = 16 * my_group + 2 * (m_row / 16) + (m_row & 1);
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t t_s = tmem + lanes + g * H, t_o = tmem + lanes + G::kO + g * H;
+    float* const s_nm = ctl->nm + g * H;
+    float* const s_alpha = ctl->alpha + g * H;
+    const uint32_t p_row = smem_u32(s_p) + m_row * 128;
+    const int bar = 1 + g;
+    int t = 0, unit_no = 0;
+    bool ok = true;
+    if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // The four warps of a half meet at barriers that no time limit ends, so they leave together: a warp whose wait
+    // has run out goes on to the next vote.
+    for (int u = 0;; ++u) {
+      ok = wait(ctl->q_full[u & 1], u >> 1);
+      if (tid < H) s_nm[tid] = -kDecNone;
+      if (bar_any(bar, 128, !ok)) break;
+      const TreeRows<N>& rows = ctl->rows[u & 1];
+      const int n = rows.seg.n;
+      if (n == 0) break;
+      bool leave = false;
+      const float c = rows.c;
+      const int keys = rows.seg.req.keys, before = keys - rows.seg.req.queries, tile0 = rows.seg.tile;
+      float l[H];
+      constexpr bool kNmRegs = H <= 16;  // the references in registers
+      float nmr[kNmRegs ? H : 1];
+#pragma unroll
+      for (int i = 0; i < H; ++i) l[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < (kNmRegs ? H : 1); ++i) nmr[i] = -kDecNone;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, ++t) {
+        ok = ok && wait(ctl->s_full[t & 1], t >> 1);
+        const int key = (tile0 + j) * kTrKeys + my_key;
+        const int flags = ctl->flags[t % kTrFlags];
+        const bool clean = flags == 0xff && (tile0 + j + 1) * kTrKeys <= before;
+        const bool there = key < keys && (flags >> my_group & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < H / C; ++cc) {
+          const uint32_t t_here = t_s + (t & 1) * G::kCols + cc * C;
+          float x[C];
+          auto scores = [&]() {
+            uint32_t r[C];
+            tmem_ld_cols<C>(t_here, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < C; ++i) x[i] = __uint_as_float(r[i]);
+          };
+          // bit i: row i of the chunk sees the thread's key
+          uint32_t see = ~0u;
+          if (!clean) {
+            const int node = key - before, word = node >> 5;
+            see = there && (node < 0 || word < a.words) ? ~0u : 0u;
+            if (node >= 0 && see) {
+              see = 0u;
+#pragma unroll 1
+              for (int i = 0; i < C; ++i) see |= (rows.seen[g * H + cc * C + i][word] >> (node & 31) & 1u) << i;
+            }
+          }
+          auto mask = [&]() {
+            if (clean) return;
+#pragma unroll
+            for (int i = 0; i < C; ++i) x[i] = see >> i & 1u ? x[i] : -INFINITY;
+          };
+          // scores in units of the exponent, relative to the rows' references
+          auto relative = [&]() {
+#pragma unroll
+            for (int i = 0; i < C; i += 4) {
+              float4 nm;
+              if constexpr (kNmRegs)
+                nm = make_float4(nmr[i], nmr[i + 1], nmr[i + 2], nmr[i + 3]);
+              else
+                nm = *reinterpret_cast<const float4*>(s_nm + cc * C + i);
+              const float2 y = fma_f32x2(f32x2(x[i], x[i + 1]), f32x2(c, c), f32x2(nm.x, nm.y));
+              const float2 z = fma_f32x2(f32x2(x[i + 2], x[i + 3]), f32x2(c, c), f32x2(nm.z, nm.w));
+              x[i] = y.x;
+              x[i + 1] = y.y;
+              x[i + 2] = z.x;
+              x[i + 3] = z.y;
+            }
+          };
+#pragma unroll 1
+          for (bool moved = false;; moved = true) {
+            scores();
+            relative();
+            mask();
+            float big = x[0];
+#pragma unroll
+            for (int i = 1; i + 1 < C; i += 2) big = max3f(big, x[i], x[i + 1]);
+            big = fmaxf(big, x[C - 1]);
+            if (moved || !bar_any(bar, 128, big > kDecLazy || !ok)) break;
+            // ---- some row's reference moves: maxima of all rows over the tile's keys
+#pragma unroll 1
+            for (int i0 = 0; i0 < C; i0 += 8) {
+              uint32_t r[8];
+              tmem_ld_cols<8>(t_here + i0, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float v = warp_max(see >> (i0 + i) & 1u ? __uint_as_float(r[i]) * c : -INFINITY);
+                if (lane == 0) ctl->top[q][g * H + cc * C + i0 + i] = v;
+              }
+            }
+            bar_wait(bar, 128);
+            if (tid < C) {
+              const int col = g * H + cc * C + tid;
+              float v = fmaxf(fmaxf(ctl->top[0][col], ctl->top[1][col]), fmaxf(ctl->top[2][col], ctl->top[3][col]));
+              const float m = -s_nm[cc * C + tid];
+              v = fmaxf(v - kDecBelow, m);
+              s_alpha[cc * C + tid] = ex2_mufu(m - v);
+              s_nm[cc * C + tid] = -v;
+            }
+            if (j > 0 && ok) ok = wait(ctl->pv_done[(t - 1) & 1], (t - 1) >> 1);
+            leave = bar_any(bar, 128, !ok);
+            if (leave) break;
+            if constexpr (kNmRegs) {
+#pragma unroll
+              for (int i = 0; i < H; ++i) nmr[i] = s_nm[i];
+            }
+            if (j > 0) {
+              tc_fence_after();
+              uint32_t r[C];
+              tmem_ld_cols<C>(t_o + cc * C, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < C; ++i) {
+                const float f = s_alpha[cc * C + i];
+                r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                l[cc * C + i] *= f;
+              }
+              tmem_st_cols<C>(t_o + cc * C, r);
+              tmem_st_wait();
+            }
+          }
+          if (leave) break;
+          if (cc == H / C - 1) {  // S has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->s_empty[t & 1]));
+          }
+          if (cc == 0 && t >= G::kBufs && ok) ok = wait(ctl->pv_done[(t - G::kBufs) & 1], (t - G::kBufs) >> 1);
+          const uint32_t dst = p_row + t % G::kBufs * G::kPBytes;
+#pragma unroll
+          for (int i = 0; i < C; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int y = i + 2 * e;
+              const float2 p = f32x2(ex2_mufu(x[y]), ex2_mufu(x[y + 1]));
+              const float2 sum = add_f32x2(f32x2(l[cc * C + y], l[cc * C + y + 1]), p);
+              l[cc * C + y] = sum.x;
+              l[cc * C + y + 1] = sum.y;
+              w[e] = pack_f16x2(p.x, p.y);
+            }
+            const int col = g * H + cc * C + i;
+            st_shared_v4(dst + col / 64 * (128 * 128) + ((col / 8 % 8 ^ (m_row & 7)) << 4), w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (leave) break;
+        fence_proxy_async_smem();
+        tc_fence_before();  // (O may have been rescaled)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[t % G::kBufs]));
+      }
+      if (leave) break;
+      // ---- the rows' sums over all keys: lanes exchange halves until each holds a row's sum of its warp
+#pragma unroll
+      for (int cc = 0; cc < H / C; ++cc) {
+        float v[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = l[cc * C + i];
+#pragma unroll
+        for (int o = C / 2; o >= 1; o /= 2) {
+          const bool high = lane & o;
+#pragma unroll
+          for (int i = 0; i < o; ++i) {
+            const float keep = high ? v[i + o] : v[i], send = high ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+#pragma unroll
+        for (int o = C; o < 32; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        if (lane < C) ctl->top[q][g * H + cc * C + lane] = v[0];
+      }
+      if (bar_any(bar, 128, !ok)) break;
+      const bool whole = n == rows.seg.tiles;
+      const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (unit_no > 0 ? 1 : 0)) * N;
+      if (tid < H) {
+        const int col = g * H + tid;
+        const float sum = (ctl->top[0][col] + ctl->top[1][col]) + (ctl->top[2][col] + ctl->top[3][col]);
+        const float m = -s_nm[tid];
+        const int at = rows.out[col];
+        // nothing seen: O = 0 (a NaN sum stays NaN)
+        s_alpha[tid] = sum == 0.f ? 0.f : a.v_descale / sum;
+        if (at >= 0) {
+          if (whole)
+            a.lse[at] = sum == 0.f ? -INFINITY : m * kLn2F + logf(sum);
+          else
+            a.part_ml[slot + col] = make_float2(m, sum);
+        }
+      }
+      if (threadIdx.x == 0 && rows.seg.tile == 0 && !whole) {
+        // the unit begins here and ends in a later CTA: x is its last tile on the line
+        const long long left = ctl->last - ctl->first - t + n;  // tiles of the share from the segment's first on
+        const long long x = ctl->last - left + rows.seg.tiles - 1;
+        const int row0 = rows.seg.block * N;
+        a.desc[blockIdx.x] = merge_desc(rows.seg.req, rows.seg.head, row0, min(N, rows.seg.req.q_len * a.group - row0),
+                                        2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0),
+                                        share_of(ctl->total, n_cta, x) - static_cast<int>(blockIdx.x) + 1);
+      }
+      ok = wait(ctl->pv_done[(t - 1) & 1], (t - 1) >> 1);
+      if (bar_any(bar, 128, !ok)) break;
+      tc_fence_after();
+      // ---- O: the thread's lane is a dim, its columns are rows
+      const bool has_dim = D == 128 || lane < 16;
+      const int dim = D == 128 ? 32 * q + 4 * (lane % 8) + lane / 8 : 16 * q + 2 * (lane % 8) + lane / 8;
+#pragma unroll
+      for (int cc = 0; cc < H / C; ++cc) {
+        uint32_t r[C];
+        tmem_ld_cols<C>(t_o + cc * C, r);
+        tmem_ld_wait();
+        if (cc == H / C - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->o_empty));
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const int col = g * H + cc * C + i, at = rows.out[col];
+          if (at < 0 || !has_dim) continue;
+          if (whole)
+            a.o[static_cast<size_t>(at) * D + dim] = __float2bfloat16_rn(__uint_as_float(r[i]) * s_alpha[cc * C + i]);
+          else
+            a.part_o[(slot + col) * D + dim] = __uint_as_float(r[i]);
+        }
+      }
+      ++unit_no;
+      bar_wait(bar, 128);  // the next unit writes s_alpha and s_nm
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->q_empty[u & 1]));
+    }
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0 && ctl->abort) atomicExch(a.status, kStatusTimeout);
+  if (warp == G::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace exattn

@@ -15,7 +15,6 @@
 #include "kv_host.cuh"
 #include "page_plan.cuh"
 #include "rope.cuh"
-#include "tree_plan.cuh"
 
 namespace exattn {
 
@@ -142,17 +141,6 @@ void split_workspace(Kv4Args& a, void* workspace) {
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + kv4_part_rows(NT) * D);
   a.desc = reinterpret_cast<int4*>(a.part_ml + kv4_part_rows(NT));
-}
-
-template <int D, int R>
-int launch_merge(const Kv4Args& a, int ctas, cudaStream_t s) {
-  // Few units (at most one for eight CTAs): each may span many CTAs, and rows get blocks of their own
-  // (4 units of 8 rows in 114 parts each: 3.9 us instead of 7 with blocks for all CTAs; 128 units of 15
-  // rows: 2.4 us more than the other way).  Else eight rows a block, 64 of a prompt chunk (135 us
-  // for the whole call of 4 chunks of 512 tokens; 139 with eight).
-  const bool few = static_cast<long long>(a.b) * a.hk <= ctas / 8;
-  const dim3 grid = few ? dim3(ctas / 8, R > 32 ? 32 : R) : dim3(ctas, R > 32 ? R / 64 : R / 8);
-  return launch_early(kv4_merge_kernel<D, R>, grid, kMergeThreads, 0, s, a, few ? ctas : 0);
 }
 
 template <int D, int NT, bool TREE = false>
@@ -393,57 +381,6 @@ int fa_kv4_fwd(const void* q, long long q_row_stride, long long q_head_stride, c
   return d == 64 ? launch_kv4<64>(a, nt, workspace, s) : launch_kv4<128>(a, nt, workspace, s);
 }
 
-int fa_tree_plan(const int* parents, const int* q_offsets, const int* lens, int B, int T, int words, int* positions,
-                 unsigned* seen, void* stream) {
-  if (!parents || !q_offsets || !lens || !positions || !seen || B < 1 || T < 1 || words < 1) return FA_ERR_INVALID_ARG;
-  if (words > kTreeWords || B > kPlanMaxBatch || static_cast<long long>(T) * words > 0x7fffffffll)
-    return FA_ERR_UNSUPPORTED;
-  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(q_offsets),
-                        static_cast<const void*>(lens), static_cast<const void*>(positions),
-                        static_cast<const void*>(seen)})
-    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
-  const TreePlanArgs a{parents, q_offsets, lens, positions, seen, B, T, words};
-  return launch_early(tree_plan_kernel, static_cast<unsigned>(B + 1), kTreeThreads, 0,
-                      static_cast<cudaStream_t>(stream), a);
-}
-
-int fa_tree_accept(const int* parents, const unsigned* seen, int words, const int* tokens, const int* choices,
-                   const int* lens, const int* new_lens, const int* q_offsets, const int* slots, const int* table,
-                   int table_width, int* queue, int queue_size, const int* queue_state, int B, int page_size, int T,
-                   int* lens_out, int* counts, int* path, int* next_tokens, int* sources, int* queue_state_out,
-                   void* stream) {
-  if (!lens || !new_lens || !q_offsets || !table || !queue || !queue_state || !lens_out || !counts || !next_tokens ||
-      !queue_state_out)
-    return FA_ERR_INVALID_ARG;
-  if (T > 0 && (!parents || !seen || !tokens || !choices || !slots || !path || !sources)) return FA_ERR_INVALID_ARG;
-  if (B < 1 || T < 0 || words < 1 || table_width < 1 || queue_size < 1) return FA_ERR_INVALID_ARG;
-  // other thread blocks, and the second kernel, read the old lengths and state
-  if (lens_out == lens || lens_out == new_lens || queue_state_out == queue_state) return FA_ERR_INVALID_ARG;
-  if (words > kTreeWords || B > kPlanMaxBatch || !page_size_ok(page_size) || !width_ok(table_width, page_size) ||
-      static_cast<long long>(B) * table_width > 0x7fffffffll || static_cast<long long>(T) * words > 0x7fffffffll)
-    return FA_ERR_UNSUPPORTED;
-  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(seen),
-                        static_cast<const void*>(tokens), static_cast<const void*>(choices),
-                        static_cast<const void*>(lens), static_cast<const void*>(new_lens),
-                        static_cast<const void*>(q_offsets), static_cast<const void*>(slots),
-                        static_cast<const void*>(table), static_cast<const void*>(queue),
-                        static_cast<const void*>(queue_state), static_cast<const void*>(lens_out),
-                        static_cast<const void*>(counts), static_cast<const void*>(path),
-                        static_cast<const void*>(next_tokens), static_cast<const void*>(sources),
-                        static_cast<const void*>(queue_state_out)})
-    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
-  const TreeAcceptArgs a{parents, seen,   tokens, choices,     lens,     new_lens,        q_offsets, slots,
-                         table,   queue,  queue_state, lens_out, counts, path,            next_tokens, sources,
-                         queue_state_out, B,      T,      words,       table_width, queue_size, log2_of(page_size)};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (int rc = launch_early(tree_accept_kernel, static_cast<unsigned>(B + 1), kTreeThreads, 0, s, a)) return rc;
-  static std::atomic<uint64_t> done{0};
-  if (int rc = opt_in_smem(tree_release_kernel, kPlanMaxBatch * 4, done)) return rc;
-  long long grid = (32ll * B + kPlanThreads - 1) / kPlanThreads;  // a warp a request
-  if (grid > kSms) grid = kSms;
-  return launch_early(tree_release_kernel, static_cast<unsigned>(grid), kPlanThreads, B * 4, s, a);
-}
-
 int fa_kv4_move(void* const* caches, int num_caches, int num_pages, int page_size, int Hkv, int d, const int* sources,
                 const int* slots, const int* q_offsets, const int* counts, int T, int B, void* stream) {
   if (!caches || !sources || !slots || !q_offsets || !counts || num_caches < 1 || T < 1 || B < 1)
@@ -470,71 +407,6 @@ int fa_kv4_move(void* const* caches, int num_caches, int num_pages, int page_siz
   const dim3 grid(static_cast<unsigned>((pieces + kKv4Threads - 1) / kKv4Threads), static_cast<unsigned>(num_caches));
   return launch_early(d == 64 ? kv4_move_kernel<64> : kv4_move_kernel<128>, grid, kKv4Threads, 0,
                       static_cast<cudaStream_t>(stream), a);
-}
-
-size_t fa_kv4_tree_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int page_size, int table_width) {
-  if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
-  if (!page_size_ok(page_size) || table_width < 1 || !width_ok(table_width, page_size)) return 0;
-  int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  if (nt == 0) nt = 4;
-  return dec_whole_tiles(d, nt, page_size, table_width) ? 0 : kv4_workspace(nt, d);
-}
-
-int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache, int num_pages,
-                    int page_size, const int* table, int table_width, const int* lens, const int* q_offsets,
-                    const unsigned* seen, int words, void* o, float* lse, int T, int B, int Hq, int Hkv, int d,
-                    int max_q, float scale, float k_descale, float v_descale, void* workspace, size_t workspace_bytes,
-                    int* dev_status, void* stream) {
-  if (!q || !table || !lens || !q_offsets || !seen || !o || !lse || o == q) return FA_ERR_INVALID_ARG;
-  if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || table_width < 1 || max_q < 1 || words < 1)
-    return FA_ERR_INVALID_ARG;
-  if (q_row_stride < 0 || q_head_stride < 0) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_INVALID_ARG;
-  if (!power_of_two(k_descale) || !power_of_two(v_descale)) return FA_ERR_INVALID_ARG;
-  if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
-  if (static_cast<long long>(T) * Hq > 0x3fffffffll || !width_ok(table_width, page_size) || words > kTreeWords)
-    return FA_ERR_UNSUPPORTED;
-  int nt = dec_row_eights(static_cast<long long>(max_q) * (Hq / Hkv));
-  if (nt == 0) nt = 4;
-  const int whole = dec_whole_tiles(d, nt, page_size, table_width);
-  if (!whole && (!workspace || workspace_bytes < kv4_workspace(nt, d))) return FA_ERR_INVALID_ARG;
-  if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
-      !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) || !aligned(seen, 4) ||
-      !aligned(workspace, 16) || !aligned(dev_status, 4))
-    return FA_ERR_MISALIGNED;
-  const double c = static_cast<double>(scale) * 1.4426950408889634 * k_descale;
-  if (!(c <= 3.0e38)) return FA_ERR_INVALID_ARG;
-  Kv4Args a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_row = q_row_stride;
-  a.q_head = q_head_stride;
-  a.cache = static_cast<const uint8_t*>(cache);
-  a.table = table;
-  a.lens = lens;
-  a.q_offsets = q_offsets;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  a.t = T;
-  a.b = B;
-  a.hq = Hq;
-  a.hk = Hkv;
-  a.group = Hq / Hkv;
-  a.width = table_width;
-  a.page_shift = log2_of(page_size);
-  a.pages = num_pages;
-  a.whole_tiles = whole;
-  a.c = static_cast<float>(c);
-  a.v_descale = v_descale;
-  a.tree = seen;
-  a.words = words;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64)
-    return nt == 1   ? launch_decode<64, 1, true>(a, workspace, s)
-           : nt == 2 ? launch_decode<64, 2, true>(a, workspace, s)
-                     : launch_decode<64, 4, true>(a, workspace, s);
-  return nt == 1   ? launch_decode<128, 1, true>(a, workspace, s)
-         : nt == 2 ? launch_decode<128, 2, true>(a, workspace, s)
-                   : launch_decode<128, 4, true>(a, workspace, s);
 }
 
 }  // extern "C"

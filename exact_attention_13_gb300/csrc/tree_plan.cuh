@@ -23,7 +23,7 @@
 
 #include <cstdint>
 
-#include "page_plan.cuh"
+#include "block_scan.cuh"
 #include "rope.cuh"
 
 namespace exattn {
