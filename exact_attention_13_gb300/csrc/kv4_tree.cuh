@@ -28,12 +28,12 @@
 // reference m of a row is moved only when some score of the tile lies more than 2^15 above it (kDecLazy): a
 // maximum over the thread's own scores and one barrier with a vote decide, and mostly nothing else happens.
 //
-// Roles (one CTA a SM):
-//   8 or 16 warps  softmax: lanes 32 (w % 4) .. + 31 (keys; dims of O^T), the w / 4-th part of the rows; outputs
-//   4 and 4        widen K and V^T
-//   1              issues the MMAs:  S(t + 1) | PV(t) | S(t + 2) | ...
-//   1              copies codes and scales into a ring of tiles
-//   2              queries, masks and places of the rows of the next unit, while this one runs
+// Roles (640 threads, one CTA a SM):
+//   warps 0-7    softmax: lanes 32 (w % 4) .. + 31 (keys; dims of O^T), rows N/2 (w / 4) .. + N/2 - 1; outputs
+//   warps 8-11   widen K,  warps 12-15 widen V^T
+//   warp  16     issues the MMAs:  S(0) S(1) | PV(t) S(t + 2) | ...
+//   warp  17     copies codes and scales into a ring of tiles
+//   warps 18-19  queries, masks and places of the rows of the next unit, while this one runs
 // The split over CTAs and the merge of units that cross them are those of kv4_attn.cuh.
 //
 // Every mbarrier wait is bounded in time; one that runs out sets the CTA's abort flag and the status word, and
@@ -51,7 +51,13 @@
 
 namespace exattn {
 
+constexpr int kTrThreads = 640;
 constexpr int kTrKeys = 128;
+constexpr int kTrMmaWarp = 16, kTrCopyWarp = 17, kTrQueryWarp = 18;
+// 640 threads get 96 registers each at launch; softmax 256 x 120 + widening 256 x 80 + the others 128 x 80
+constexpr int kTrLaunchRegs = 96, kTrSoftmaxRegs = 120, kTrWidenRegs = 80, kTrOtherRegs = 80;
+static_assert(256 * kTrSoftmaxRegs + 256 * kTrWidenRegs + 128 * kTrOtherRegs == kTrThreads * kTrLaunchRegs,
+              "registers of the block at launch");
 constexpr int kTrFlags = 32;  // tiles whose flags are kept: more than are ever between copies and softmax
 
 template <int D, int N>
@@ -59,8 +65,8 @@ struct TreeGeo {
   // a stage of the ring: codes of K, of V (16 keys at a time, padded by 16 bytes), scales of K, of V
   static constexpr int kGroup = 16 * D / 2, kVGroup = kGroup + 16, kScales = 16 * D / 16;
   static constexpr int kV = 8 * kGroup, kKs = kV + 8 * kVGroup, kVs = kKs + 8 * kScales, kStage = kVs + 8 * kScales;
-  static constexpr int kStages = N == 128 ? 6 : 8;
-  static constexpr int kBufs = N == 128 ? 1 : 2;        // of K, V^T and P^T
+  static constexpr int kStages = N == 128 ? 4 : 8;
+  static constexpr int kBufs = N == 128 ? 1 : 2;        // of K and V^T
   static constexpr int kQBytes = N * D * 2;             // boxes of 64 dims, 128 bytes a row
   static constexpr int kPBytes = (N + 63) / 64 * 128 * 128;
   static constexpr int kCols = N < 32 ? 32 : N;         // columns between accumulators
@@ -68,18 +74,8 @@ struct TreeGeo {
   static_assert(kVt + kBufs * 64 <= 512, "tensor memory");
   static constexpr uint32_t kIdescS = instr_desc(128, N, 0, false, false);
   static constexpr uint32_t kIdescPV = instr_desc(128, N, 0, false, true);
-  // warps: softmax, then 4 that widen K, 4 that widen V^T, and 4 others
-  static constexpr int kSoft = N == 64 ? 16 : 8;
-  static constexpr int kWidenWarp = kSoft, kMmaWarp = kSoft + 8, kCopyWarp = kSoft + 9, kQueryWarp = kSoft + 10;
-  static constexpr int kThreads = 32 * (kSoft + 12);
-  static constexpr int kParts = kSoft / 4;              // of the rows; a softmax thread has one
-  static constexpr int kCol = N / kParts;               // rows of a softmax thread
-  static constexpr int kChunk = kCol < 32 ? kCol : 32;
-  // registers a thread at launch, and how the warpgroups share them
-  static constexpr int kLaunchRegs = kSoft == 16 ? 72 : 96, kSoftRegs = kSoft == 16 ? 72 : 120;
-  static constexpr int kWidenRegs = kSoft == 16 ? 72 : 80, kOtherRegs = kSoft == 16 ? 72 : 80;
-  static_assert(32 * kSoft * kSoftRegs + 256 * kWidenRegs + 128 * kOtherRegs == kThreads * kLaunchRegs,
-                "registers of the block at launch");
+  static constexpr int kHalf = N / 2;                   // rows of a softmax thread
+  static constexpr int kChunk = kHalf < 32 ? kHalf : 32;
 };
 
 // A share of a unit: tiles [tile, tile + n) of its `tiles`; n = 0: there are no more.
@@ -96,7 +92,7 @@ struct TreeWalk {
 template <int N>
 struct TreeRows {          // of one unit, written by the query warps
   TreeSeg seg;
-  float c;                 // factor of the scores
+  float c[2];              // factors of the halves' scores
   int out[N];              // row of o and lse, -1: padding
   uint32_t seen[N][kTreeWords + 1];
 };
@@ -104,7 +100,7 @@ struct TreeRows {          // of one unit, written by the query warps
 template <int N>
 struct TreeCtrl {
   uint64_t ring_full[8], ring_empty[8];
-  uint64_t k_full[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t k_full[2], v_full[2], s_full[2], p_full[2], pv_done[2];
   uint64_t q_full[2], q_empty[2], o_empty, drain;
   uint32_t tmem_base;
   int abort;
@@ -122,23 +118,10 @@ struct TreeCtrl {
 template <int D, int N>
 constexpr int tree_smem_bytes() {
   using G = TreeGeo<D, N>;
-  return 2 * G::kQBytes + G::kBufs * G::kPBytes + G::kStages * G::kStage + static_cast<int>(sizeof(TreeCtrl<N>)) + 1024;
+  return 2 * G::kQBytes + 2 * G::kPBytes + G::kStages * G::kStage + static_cast<int>(sizeof(TreeCtrl<N>)) + 1024;
 }
 
 // ---- small PTX
-// As mbar_try_wait, suspended for up to about `ns`.
-__device__ __forceinline__ uint32_t mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(ns)
-      : "memory");
-  return done;
-}
-constexpr uint32_t kTrTryNs = 200000;
 // The largest of the warp's values (NaN: the others).
 __device__ __forceinline__ float warp_max(float v) {
   float y;
@@ -239,7 +222,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const Kv4Args& a, const TreeCtrl<N
 
 // The CTA's share [first, last) of the line of `total` tiles (units, when they are not split); fills ctl->start.
 // Returns the number of CTAs that have work.
-template <int N, int THREADS>
+template <int N>
 __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   ReqShape s{0, 0, 0, 0};
@@ -263,23 +246,23 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
     return x;
   };
   long long mine = 0, tiles = 0;
-  for (int r = tid; r < a.b; r += THREADS) mine += tiles = cost(r);
+  for (int r = tid; r < a.b; r += kTrThreads) mine += tiles = cost(r);
   long long inc = scan(mine), total = 0;
 #pragma unroll 1
-  for (int w = 0; w < THREADS / 32; ++w) total += ctl->sum[w];
+  for (int w = 0; w < kTrThreads / 32; ++w) total += ctl->sum[w];
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   if (static_cast<int>(blockIdx.x) >= n) return n;
   const long long first = share_begin(total, n, blockIdx.x), last = share_begin(total, n, blockIdx.x + 1);
   long long base = 0;
-  for (int r0 = 0; r0 < a.b; r0 += THREADS) {
+  for (int r0 = 0; r0 < a.b; r0 += kTrThreads) {
     long long all = total;
-    if (a.b > THREADS) {
+    if (a.b > kTrThreads) {
       __syncthreads();
       tiles = cost(r0 + tid);
       inc = scan(tiles) + base;
       all = base;
 #pragma unroll 1
-      for (int w = 0; w < THREADS / 32; ++w) all += ctl->sum[w];
+      for (int w = 0; w < kTrThreads / 32; ++w) all += ctl->sum[w];
     }
     if (first >= inc - tiles && first < inc) {
       const long long off = first - (inc - tiles);
@@ -305,25 +288,25 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a) {
   using G = TreeGeo<D, N>;
   extern __shared__ __align__(1024) uint8_t tr_smem[];
   uint8_t* const smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const s_q = smem;
   uint8_t* const s_p = smem + 2 * G::kQBytes;
-  uint8_t* const s_ring = s_p + G::kBufs * G::kPBytes;
+  uint8_t* const s_ring = s_p + 2 * G::kPBytes;
   static_assert(G::kStages * G::kStage % 16 == 0 && G::kQBytes % 1024 == 0, "alignment");
   TreeCtrl<N>* const ctl = reinterpret_cast<TreeCtrl<N>*>(s_ring + G::kStages * G::kStage);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   grid_launch_dependents();
-  const int n_cta = tree_my_range<N, G::kThreads>(a, ctl);
+  const int n_cta = tree_my_range<N>(a, ctl);
   if (static_cast<int>(blockIdx.x) >= n_cta) {
     if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  if (warp == G::kMmaWarp) {
+  if (warp == kTrMmaWarp) {
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish();
   }
@@ -336,13 +319,12 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
       mbar_init(smem_u32(&ctl->k_full[i]), 4);
       mbar_init(smem_u32(&ctl->v_full[i]), 4);
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
-      mbar_init(smem_u32(&ctl->s_empty[i]), G::kSoft);  // one arrival per softmax warp
-      mbar_init(smem_u32(&ctl->p_full[i]), G::kSoft);
+      mbar_init(smem_u32(&ctl->p_full[i]), 8);   // one arrival per softmax warp
       mbar_init(smem_u32(&ctl->pv_done[i]), 1);
       mbar_init(smem_u32(&ctl->q_full[i]), 2);   // one arrival per query warp
-      mbar_init(smem_u32(&ctl->q_empty[i]), 1 + G::kSoft);  // the unit's last S, and the softmax warps
+      mbar_init(smem_u32(&ctl->q_empty[i]), 9);  // the unit's last S, and the softmax warps
     }
-    mbar_init(smem_u32(&ctl->o_empty), G::kSoft);
+    mbar_init(smem_u32(&ctl->o_empty), 8);
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -352,13 +334,13 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   volatile int* const abort_flag = &ctl->abort;
-  // For the number-th completion, counted from 0.  A try suspends the warp for a while; the first that fails starts the
-  // clock, and a wait that runs out raises the CTA's abort flag (small code: there are 20 copies of it).
+  // For the number-th completion, counted from 0.  The first try that fails starts the clock, and a wait that runs out
+  // raises the CTA's abort flag (small code: there are 20 copies of it).
   auto wait = [&](uint64_t& bar, int number) -> bool {
     const uint32_t at = smem_u32(&bar), parity = static_cast<uint32_t>(number) & 1u;
     uint64_t limit = 0;
 #pragma unroll 1
-    while (!__all_sync(0xffffffffu, mbar_try_wait_for(at, parity, kTrTryNs))) {
+    while (!__all_sync(0xffffffffu, mbar_try_wait(at, parity))) {
       const uint64_t now = globaltimer_ns();
       if (limit == 0) limit = now + kWaitLimitNs;
       if (__any_sync(0xffffffffu, *abort_flag || now > limit)) {
@@ -369,29 +351,21 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
     return true;
   };
 
-  if (warp >= G::kMmaWarp) {
-    if constexpr (G::kOtherRegs < G::kLaunchRegs) regs_dec<G::kOtherRegs>();
-    if (warp == G::kMmaWarp) {
+  if (warp >= kTrMmaWarp) {
+    regs_dec<kTrOtherRegs>();
+    if (warp == kTrMmaWarp) {
       // ============================================================ MMA issuer
       const uint64_t q_desc = smem_desc(smem_u32(s_q), 16, 1024, kSwizzle128B);
       const uint64_t p_desc = smem_desc(smem_u32(s_p), 128 * 128, 1024, kSwizzle128B);
+      // S(t + 2) is issued behind PV(t): what it overwrites, S(t), has been read when P(t) is there, so the step waits for
+      // P(t), V(t) and K(t + 2) at once (a wait takes 150 cycles even if nothing is left to wait for), and S(t + 1) runs
+      // under the softmax of tile t.  Its completion, behind PV(t)'s, tells the softmax that P's buffer is free.
       int u_s = -1, left_s = 0;  // the unit that S works on, and its tiles to come
       int u_v = -1, left_v = 0;
-      bool ok = true, more = true;
-      // S of tile t; false at the end of the tiles (or on abort: ok is false then)
-      auto issue_s = [&](int t) -> bool {
-        if (left_s == 0) {
-          ++u_s;
-          ok = wait(ctl->q_full[u_s & 1], u_s >> 1);
-          if (!ok) return false;
-          left_s = ctl->rows[u_s & 1].seg.n;
-          if (left_s == 0) return false;
-        }
-        --left_s;
-        ok = wait(ctl->k_full[t % G::kBufs], t / G::kBufs);
-        if (ok && t >= 2) ok = wait(ctl->s_empty[t & 1], (t >> 1) - 1);
-        if (!ok) return false;
+      bool ok = true;
+      auto issue_s = [&](int t) {
         tc_fence_after();
+        --left_s;
         if (elect_one()) {
           const uint64_t qd = q_desc + (u_s & 1) * (G::kQBytes >> 4);
           const uint32_t k = tmem + G::kK + t % G::kBufs * (D / 2), s = tmem + (t & 1) * G::kCols;
@@ -402,32 +376,53 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
           if (left_s == 0) tc_commit(smem_u32(&ctl->q_empty[u_s & 1]));
         }
         __syncwarp();
-        return true;
       };
-      auto issue_pv = [&](int t) {
-        bool begins = false;
-        if (left_v == 0) {
-          ++u_v;
-          left_v = ctl->rows[u_v & 1].seg.n;
-          begins = true;
-          if (u_v > 0) ok = wait(ctl->o_empty, u_v - 1);
-        }
-        --left_v;
-        ok = ok && wait(ctl->v_full[t % G::kBufs], t / G::kBufs) && wait(ctl->p_full[t % G::kBufs], t / G::kBufs);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_chain_ts_off<8, 0, 128, 8, 16, 24, 32, 40, 48, 56>(
-              tmem + G::kO, G::kIdescPV, begins ? 0u : 1u, tmem + G::kVt + t % G::kBufs * 64,
-              p_desc + t % G::kBufs * (G::kPBytes >> 4));
-          tc_commit(smem_u32(&ctl->pv_done[t & 1]));
-        }
-        __syncwarp();
-      };
+      int pv = 0, s_next = 0;
 #pragma unroll 1
-      for (int t = -1; more && ok; ++t) {  // (one copy of the code)
-        more = issue_s(t + 1);
-        if (ok && t >= 0) issue_pv(t);
+      for (bool more = true; ok && (more || pv < s_next);) {
+        // (the first two passes issue S only)
+        const bool with_pv = s_next - pv == 2 || !more, in_unit = more && left_s > 0;
+        bool k_there = false;
+        if (with_pv) {
+          bool begins = false;
+          if (left_v == 0) {
+            ++u_v;
+            left_v = ctl->rows[u_v & 1].seg.n;
+            begins = true;
+            if (u_v > 0) ok = wait(ctl->o_empty, u_v - 1);
+          }
+          --left_v;
+          uint64_t &bp = ctl->p_full[pv & 1], &bv = ctl->v_full[pv % G::kBufs];
+          uint64_t& bk = in_unit ? ctl->k_full[s_next % G::kBufs] : bv;
+          const int nk = in_unit ? s_next / G::kBufs : pv / G::kBufs;
+          if (ok) {
+            k_there = __all_sync(0xffffffffu, mbar_try_wait3(smem_u32(&bp), (pv >> 1) & 1, smem_u32(&bv),
+                                                             pv / G::kBufs & 1, smem_u32(&bk), nk & 1));
+            if (!k_there) ok = wait(bp, pv >> 1) && wait(bv, pv / G::kBufs);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_chain_ts_off<8, 0, 128, 8, 16, 24, 32, 40, 48, 56>(
+                tmem + G::kO, G::kIdescPV, begins ? 0u : 1u, tmem + G::kVt + pv % G::kBufs * 64,
+                p_desc + (pv & 1) * (G::kPBytes >> 4));
+            tc_commit(smem_u32(&ctl->pv_done[pv & 1]));
+          }
+          __syncwarp();
+          ++pv;
+        }
+        if (!more) continue;
+        if (!in_unit) {
+          ++u_s;
+          ok = wait(ctl->q_full[u_s & 1], u_s >> 1);
+          if (!ok) break;
+          left_s = ctl->rows[u_s & 1].seg.n;
+          more = left_s > 0;
+          if (!more) continue;
+        }
+        if (!(k_there && in_unit)) ok = wait(ctl->k_full[s_next % G::kBufs], s_next / G::kBufs);
+        if (!ok) break;
+        issue_s(s_next++);
       }
       // nothing this warp issued may still run when the TMEM is released
       __syncwarp();
@@ -435,7 +430,7 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
-    } else if (warp == G::kCopyWarp) {
+    } else if (warp == kTrCopyWarp) {
       // ============================================================ copies of the cache
       // 16 bytes a lane and copy.  Groups of 16 keys on pages that are not there are not copied: their scores are
       // masked, and whatever lies in the ring is a number after widening.
@@ -511,32 +506,50 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
       cp_async_wait<0>();  // copies under way land before the CTA's shared memory goes away
     } else {
       // ============================================================ queries, masks and places of a unit's rows
-      // A thread takes d/4 dims of a row: 8 of each quarter, which are four chunks of the operand.
+      // A warp takes half of the rows (one half of the softmax warps has the same), as they are, by 16 bytes to where
+      // the row's operand lies, and turns them into it in place.
       TreeWalk w = tree_walk<N>(a, ctl);
-      constexpr int kLanes = D / 32, kRowsIt = 32 / kLanes;
-      const int part = lane % kLanes, self = warp - G::kQueryWarp;
+      constexpr int R = N / 2, kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = (R + 31) / 32;
+      const int self = warp - kTrQueryWarp;
       for (int u = 0;; ++u) {
         if (u >= 2 && !wait(ctl->q_empty[u & 1], (u >> 1) - 1)) break;
         TreeRows<N>& rows = ctl->rows[u & 1];
         if (self == 0 && lane == 0) rows.seg = w.s;
         if (w.s.n > 0) {
-          const int live = w.s.req.q_len * a.group - w.s.block * N;
-          uint8_t* const q = s_q + (u & 1) * G::kQBytes;
-          const __nv_bfloat16* const q_head = a.q + static_cast<long long>(w.s.req.q0) * a.q_row +
-                                              static_cast<long long>(w.s.head) * a.group * a.q_head;
-          auto row_at = [&](int row) {  // row of the unit
-            const int at = w.s.block * N + row, node = at / a.group;
-            return q_head + static_cast<long long>(node) * a.q_row +
-                   static_cast<long long>(at - node * a.group) * a.q_head;
+          long long from[kOffsets];  // of rows lane, lane + 32; -1: padding
+#pragma unroll
+          for (int x = 0; x < kOffsets; ++x) {
+            const int row = self * R + x * 32 + lane, at = w.s.block * N + row;
+            const int node = at / a.group, head = w.s.head * a.group + at - node * a.group, token = w.s.req.q0 + node;
+            const bool live = x * 32 + lane < R && at < w.s.req.q_len * a.group;
+            from[x] = live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1;
+            if (x * 32 + lane < R) {
+              rows.out[row] = live ? token * a.hq + head : -1;
+#pragma unroll 1
+              for (int y = 0; y < a.words; ++y)
+                rows.seen[row][y] = live ? a.tree[static_cast<size_t>(token) * a.words + y] : 0u;
+            }
+          }
+          uint8_t* const q = s_q + (u & 1) * G::kQBytes + self * R * 128;
+          auto piece_at = [&](int row, int piece) {
+            return piece / 8 * (N * 128) + row * 128 + ((piece % 8 ^ (row & 7)) << 4);
           };
+#pragma unroll
+          for (int row0 = 0; row0 < R; row0 += kRowsIt) {
+            const int row = row0 + lane / kPieces, piece = lane % kPieces;
+            const long long at = __shfl_sync(0xffffffffu, from[row0 / 32], row % 32);
+            cp_async16(smem_u32(q) + piece_at(row, piece), a.q + (at < 0 ? 0 : at + piece * 8), at < 0 ? 0u : 16u);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          __syncwarp();
           // One power of two for all rows brings the largest finite value into [2^14, 2^15): f16 then holds bf16's 8
-          // bits down to 2^-31 of it (2^-17 of a row's own largest, as long as that is not below 2^-14 of the unit's),
-          // and the softmax needs no factor for each row.  Each of the two warps looks at all rows.
+          // bits down to 2^-31 of it (2^-17 of a row's own largest, as long as that is not below 2^-14 of the
+          // half's), and the softmax needs no factor for each row.
           __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-          const int rows_there = min(live, N);
 #pragma unroll 4
-          for (int x = lane; x < rows_there * (D / 8); x += 32) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(row_at(x / (D / 8)) + x % (D / 8) * 8);
+          for (int row0 = 0; row0 < R; row0 += kRowsIt) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(q + piece_at(row0 + lane / kPieces, lane % kPieces));
             const __nv_bfloat162* const v = reinterpret_cast<const __nv_bfloat162*>(&raw);
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // (infinities and NaN: 0 x + |x| is NaN, and the maximum the other one)
@@ -545,31 +558,29 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
           const float amax = warp_max(fmaxf(__low2float(top), __high2float(top)));
           const uint32_t down_ex = min(268u - (__float_as_uint(amax) >> 23), 253u);
           const float down = __uint_as_float(down_ex << 23);
-          if (self == 0 && lane == 0) rows.c = a.c * __uint_as_float((254u - down_ex) << 23);
-#pragma unroll 2
-          for (int row0 = self * kRowsIt; row0 < N; row0 += 2 * kRowsIt) {
-            const int row = row0 + lane / kLanes, at = w.s.block * N + row;
-            const int node = at / a.group, head = w.s.head * a.group + at - node * a.group;
-            const __nv_bfloat16* const src = row_at(row) + 8 * part;
+          if (lane == 0) rows.c[self] = a.c * __uint_as_float((254u - down_ex) << 23);
+          // a lane takes d/4 dims of a row, 8 of each quarter, which are four chunks of the operand
+          constexpr int kLanes = D / 32;
+          const int part = lane % kLanes;
+#pragma unroll 1
+          for (int row0 = 0; row0 < R; row0 += 32 / kLanes) {
+            const int row = row0 + lane / kLanes;
             uint32_t h[4][4];
+            if (row < R) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-              if (row < live) raw = *reinterpret_cast<const uint4*>(src + x * (D / 4));
-              float f[8];
-              unpack_bf16x8(raw, f);
+              for (int x = 0; x < 4; ++x) {
+                float f[8];
+                unpack_bf16x8(*reinterpret_cast<const uint4*>(q + piece_at(row, x * kLanes + part)), f);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+                for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+              }
             }
+            __syncwarp();
+            if (row < R) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int chunk = 4 * part + e;
-              st_shared_v4(smem_u32(q) + chunk / 8 * (N * 128) + row * 128 + ((chunk % 8 ^ (row & 7)) << 4), h[0][e],
-                           h[1][e], h[2][e], h[3][e]);
+              for (int e = 0; e < 4; ++e)
+                st_shared_v4(smem_u32(q) + piece_at(row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
             }
-            if (part == 0) rows.out[row] = row < live ? (w.s.req.q0 + node) * a.hq + head : -1;
-            for (int x = part; x < a.words; x += kLanes)
-              rows.seen[row][x] = row < live ? a.tree[static_cast<size_t>(w.s.req.q0 + node) * a.words + x] : 0u;
           }
           fence_proxy_async_smem();  // the MMAs read the queries through the async proxy
         }
@@ -579,8 +590,8 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
         tree_next<N>(a, w);
       }
     }
-  } else if (warp >= G::kWidenWarp + 4) {
-    if constexpr (G::kWidenRegs < G::kLaunchRegs) regs_dec<G::kWidenRegs>();
+  } else if (warp >= 12) {
+    regs_dec<kTrWidenRegs>();
     // ============================================================ widening the values
     const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
     uint32_t(*const s_scale)[20] = ctl->scales[q];
@@ -677,8 +688,8 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
         mbar_arrive(smem_u32(&ctl->v_full[t % G::kBufs]));
       }
     }
-  } else if (warp >= G::kWidenWarp) {
-    if constexpr (G::kWidenRegs < G::kLaunchRegs) regs_dec<G::kWidenRegs>();
+  } else if (warp >= 8) {
+    regs_dec<kTrWidenRegs>();
     // ============================================================ widening the keys
     const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
     const int row_in = 4 * q + (g8 & 1), group = g8 / 2;  // row + 2 hh, group + 4 i
@@ -734,9 +745,9 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
       }
     }
   } else {
-    if constexpr (G::kSoftRegs > G::kLaunchRegs) regs_inc<G::kSoftRegs>();
+    regs_inc<kTrSoftmaxRegs>();
     // ============================================================ softmax, outputs
-    constexpr int H = G::kCol, C = G::kChunk;
+    constexpr int H = G::kHalf, C = G::kChunk;
     const int g = warp / 4, q = warp % 4, m_row = 32 * q + lane, tid = threadIdx.x % 128;
     const int my_group = m_row % 8 / 2 + 4 * (m_row / 8 % 2);  // of 16 keys
     const int my_key = 16 * my_group + 2 * (m_row / 16) + (m_row & 1);
@@ -759,10 +770,10 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
       const int n = rows.seg.n;
       if (n == 0) break;
       bool leave = false;
-      const float c = rows.c;
+      const float c = rows.c[g];
       const int keys = rows.seg.req.keys, before = keys - rows.seg.req.queries, tile0 = rows.seg.tile;
       float l[H];
-      constexpr bool kNmRegs = H <= 16;  // the references in registers
+      constexpr bool kNmRegs = H <= 32;  // the references in registers
       float nmr[kNmRegs ? H : 1];
 #pragma unroll
       for (int i = 0; i < H; ++i) l[i] = 0.f;
@@ -874,13 +885,7 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
             }
           }
           if (leave) break;
-          if (cc == H / C - 1) {  // S has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->s_empty[t & 1]));
-          }
-          if (cc == 0 && t >= G::kBufs && ok) ok = wait(ctl->pv_done[(t - G::kBufs) & 1], (t - G::kBufs) >> 1);
-          const uint32_t dst = p_row + t % G::kBufs * G::kPBytes;
+          const uint32_t dst = p_row + t % 2 * G::kPBytes;
 #pragma unroll
           for (int i = 0; i < C; i += 8) {
             uint32_t w[4];
@@ -899,9 +904,9 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
         }
         if (leave) break;
         fence_proxy_async_smem();
-        tc_fence_before();  // (O may have been rescaled)
+        tc_fence_before();  // S has been read (and O perhaps rescaled)
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[t % G::kBufs]));
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[t & 1]));
       }
       if (leave) break;
       // ---- the rows' sums over all keys: lanes exchange halves until each holds a row's sum of its warp
@@ -984,7 +989,7 @@ __global__ void __launch_bounds__(TreeGeo<D, N>::kThreads, 1) kv4_tree_kernel(co
 
   __syncthreads();
   if (threadIdx.x == 0 && ctl->abort) atomicExch(a.status, kStatusTimeout);
-  if (warp == G::kMmaWarp) {
+  if (warp == kTrMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -50,10 +50,10 @@ int launch_tree(Kv4Args& a, void* workspace, cudaStream_t s) {
     // a build with fewer registers at launch would wait forever for the ones to redistribute
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
-    if (attr.numRegs < TreeGeo<D, N>::kLaunchRegs) return FA_ERR_UNSUPPORTED;
+    if (attr.numRegs < kTrLaunchRegs) return FA_ERR_UNSUPPORTED;
   }
   if (int rc = opt_in_smem(kern, taken, done)) return rc;
-  kern<<<kSms, TreeGeo<D, N>::kThreads, taken, s>>>(a);
+  kern<<<kSms, kTrThreads, taken, s>>>(a);
   if (int rc = launched()) return rc;
   return a.whole_tiles ? FA_OK : launch_merge<D, N>(a, kSms, s);
 }
