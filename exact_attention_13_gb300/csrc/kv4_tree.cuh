@@ -1,7 +1,7 @@
 // kv4_tree.cuh -- attention of trees of drafted tokens over the paged 4-bit cache.
 //
 // The operation of kv4_attn.cuh with another mask: a node sees the keys before its request's tree, and of the
-// tree's keys those whose bit is set in its row of `seen`.  Units of N = 16, 32, 64 or 128 query rows (one key
+// tree's keys those whose bit is set in its row of `seen`.  Units of N = 16, 32 or 64 query rows (one key
 // head of one request, rows ordered by node, then by head of the group).
 //
 // Both products take the widened cache as the 128-row operand of tcgen05.mma, out of tensor memory:
@@ -30,10 +30,10 @@
 //
 // Roles (640 threads, one CTA a SM):
 //   warps 0-7    softmax: lanes 32 (w % 4) .. + 31 (keys; dims of O^T), rows N/2 (w / 4) .. + N/2 - 1; outputs
-//   warps 8-11   widen K,  warps 12-15 widen V^T
+//   warps 8-15   widen K and V^T: two warps share 32 rows of both
 //   warp  16     issues the MMAs:  S(0) S(1) | PV(t) S(t + 2) | ...
-//   warp  17     copies codes and scales into a ring of tiles
-//   warps 18-19  queries, masks and places of the rows of the next unit, while this one runs
+//   warps 17, 18 copy codes and scales of K and of V into a ring of tiles
+//   warp  19     queries, masks and places of the rows of the next unit, while this one runs
 // The split over CTAs and the merge of units that cross them are those of kv4_attn.cuh.
 //
 // Every mbarrier wait is bounded in time; one that runs out sets the CTA's abort flag and the status word, and
@@ -53,7 +53,7 @@ namespace exattn {
 
 constexpr int kTrThreads = 640;
 constexpr int kTrKeys = 128;
-constexpr int kTrMmaWarp = 16, kTrCopyWarp = 17, kTrQueryWarp = 18;
+constexpr int kTrMmaWarp = 16, kTrCopyWarp = 17, kTrQueryWarp = 19;
 // 640 threads get 96 registers each at launch; softmax 256 x 120 + widening 256 x 80 + the others 128 x 80
 constexpr int kTrLaunchRegs = 96, kTrSoftmaxRegs = 120, kTrWidenRegs = 80, kTrOtherRegs = 80;
 static_assert(256 * kTrSoftmaxRegs + 256 * kTrWidenRegs + 128 * kTrOtherRegs == kTrThreads * kTrLaunchRegs,
@@ -65,17 +65,15 @@ struct TreeGeo {
   // a stage of the ring: codes of K, of V (16 keys at a time, padded by 16 bytes), scales of K, of V
   static constexpr int kGroup = 16 * D / 2, kVGroup = kGroup + 16, kScales = 16 * D / 16;
   static constexpr int kV = 8 * kGroup, kKs = kV + 8 * kVGroup, kVs = kKs + 8 * kScales, kStage = kVs + 8 * kScales;
-  static constexpr int kStages = N == 128 ? 4 : 8;
-  static constexpr int kBufs = N == 128 ? 1 : 2;        // of K and V^T
+  static constexpr int kStages = 8;
   static constexpr int kQBytes = N * D * 2;             // boxes of 64 dims, 128 bytes a row
-  static constexpr int kPBytes = (N + 63) / 64 * 128 * 128;
+  static constexpr int kPBytes = 128 * 128;             // a row of 128 bytes a key
   static constexpr int kCols = N < 32 ? 32 : N;         // columns between accumulators
-  static constexpr int kO = 2 * kCols, kK = 3 * kCols, kVt = kK + kBufs * (D / 2);
-  static_assert(kVt + kBufs * 64 <= 512, "tensor memory");
+  static constexpr int kO = 2 * kCols, kK = 3 * kCols, kVt = kK + 2 * (D / 2);
+  static_assert(kVt + 2 * 64 <= 512, "tensor memory");
   static constexpr uint32_t kIdescS = instr_desc(128, N, 0, false, false);
   static constexpr uint32_t kIdescPV = instr_desc(128, N, 0, false, true);
   static constexpr int kHalf = N / 2;                   // rows of a softmax thread
-  static constexpr int kChunk = kHalf < 32 ? kHalf : 32;
 };
 
 // A share of a unit: tiles [tile, tile + n) of its `tiles`; n = 0: there are no more.
@@ -92,7 +90,7 @@ struct TreeWalk {
 template <int N>
 struct TreeRows {          // of one unit, written by the query warps
   TreeSeg seg;
-  float c[2];              // factors of the halves' scores
+  float c;                 // factor of the scores
   int out[N];              // row of o and lse, -1: padding
   uint32_t seen[N][kTreeWords + 1];
 };
@@ -112,7 +110,7 @@ struct TreeCtrl {
   alignas(16) float nm[N];  // minus the reference of a row's probabilities
   float alpha[N];
   float top[4][N];          // of each quarter's keys: maxima, and in the end sums
-  alignas(16) uint32_t scales[4][8][20];  // V's scales of a widening warp, as pairs of keys
+  alignas(16) uint32_t scales[8][8][12];  // V's scales of a widening warp, as pairs of keys
 };
 
 template <int D, int N>
@@ -122,6 +120,22 @@ constexpr int tree_smem_bytes() {
 }
 
 // ---- small PTX
+// Whether three phases have all completed; does not wait.
+__device__ __forceinline__ uint32_t mbar_test3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2,
+                                               uint32_t p2) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred q0, q1, q2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q0, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q1, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q2, [%5], %6;\n\t"
+      "and.pred q0, q0, q1;\n\tand.pred q0, q0, q2;\n\t"
+      "selp.u32 %0, 1, 0, q0;\n\t}"
+      : "=r"(done)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2)
+      : "memory");
+  return done;
+}
 // The largest of the warp's values (NaN: the others).
 __device__ __forceinline__ float warp_max(float v) {
   float y;
@@ -312,16 +326,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(smem_u32(&ctl->ring_full[i]), 33);  // the copying warp's lanes, and its flags
+      mbar_init(smem_u32(&ctl->ring_full[i]), 65);  // the copying warps' lanes, and the flags
       mbar_init(smem_u32(&ctl->ring_empty[i]), 8);  // one arrival per widening warp
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctl->k_full[i]), 4);
-      mbar_init(smem_u32(&ctl->v_full[i]), 4);
+      mbar_init(smem_u32(&ctl->k_full[i]), 8);
+      mbar_init(smem_u32(&ctl->v_full[i]), 8);
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
       mbar_init(smem_u32(&ctl->p_full[i]), 8);   // one arrival per softmax warp
       mbar_init(smem_u32(&ctl->pv_done[i]), 1);
-      mbar_init(smem_u32(&ctl->q_full[i]), 2);   // one arrival per query warp
+      mbar_init(smem_u32(&ctl->q_full[i]), 1);
       mbar_init(smem_u32(&ctl->q_empty[i]), 9);  // the unit's last S, and the softmax warps
     }
     mbar_init(smem_u32(&ctl->o_empty), 8);
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         --left_s;
         if (elect_one()) {
           const uint64_t qd = q_desc + (u_s & 1) * (G::kQBytes >> 4);
-          const uint32_t k = tmem + G::kK + t % G::kBufs * (D / 2), s = tmem + (t & 1) * G::kCols;
+          const uint32_t k = tmem + G::kK + (t & 1) * (D / 2), s = tmem + (t & 1) * G::kCols;
           mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 0u, k, qd);
           if constexpr (D == 128)
             mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 1u, k + 32, qd + (N * 128 >> 4));
@@ -392,19 +406,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
             if (u_v > 0) ok = wait(ctl->o_empty, u_v - 1);
           }
           --left_v;
-          uint64_t &bp = ctl->p_full[pv & 1], &bv = ctl->v_full[pv % G::kBufs];
-          uint64_t& bk = in_unit ? ctl->k_full[s_next % G::kBufs] : bv;
-          const int nk = in_unit ? s_next / G::kBufs : pv / G::kBufs;
+          uint64_t &bp = ctl->p_full[pv & 1], &bv = ctl->v_full[pv & 1];
+          uint64_t& bk = in_unit ? ctl->k_full[s_next & 1] : bv;
+          const int nk = in_unit ? s_next >> 1 : pv >> 1;
           if (ok) {
-            k_there = __all_sync(0xffffffffu, mbar_try_wait3(smem_u32(&bp), (pv >> 1) & 1, smem_u32(&bv),
-                                                             pv / G::kBufs & 1, smem_u32(&bk), nk & 1));
-            if (!k_there) ok = wait(bp, pv >> 1) && wait(bv, pv / G::kBufs);
+            k_there = __all_sync(0xffffffffu, mbar_test3(smem_u32(&bp), pv >> 1 & 1, smem_u32(&bv), pv >> 1 & 1,
+                                                         smem_u32(&bk), nk & 1));
+            if (!k_there) ok = wait(bp, pv >> 1) && wait(bv, pv >> 1);
           }
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             mma_chain_ts_off<8, 0, 128, 8, 16, 24, 32, 40, 48, 56>(
-                tmem + G::kO, G::kIdescPV, begins ? 0u : 1u, tmem + G::kVt + pv % G::kBufs * 64,
+                tmem + G::kO, G::kIdescPV, begins ? 0u : 1u, tmem + G::kVt + (pv & 1) * 64,
                 p_desc + (pv & 1) * (G::kPBytes >> 4));
             tc_commit(smem_u32(&ctl->pv_done[pv & 1]));
           }
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           more = left_s > 0;
           if (!more) continue;
         }
-        if (!(k_there && in_unit)) ok = wait(ctl->k_full[s_next % G::kBufs], s_next / G::kBufs);
+        if (!(k_there && in_unit)) ok = wait(ctl->k_full[s_next & 1], s_next >> 1);
         if (!ok) break;
         issue_s(s_next++);
       }
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
-    } else if (warp == kTrCopyWarp) {
+    } else if (warp < kTrQueryWarp) {
       // ============================================================ copies of the cache
       // 16 bytes a lane and copy.  Groups of 16 keys on pages that are not there are not copied: their scores are
       // masked, and whatever lies in the ring is a number after widening.
@@ -438,17 +452,20 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       const int page_rows = 1 << a.page_shift;
       const int block_bytes = kv4_block_bytes(page_rows, D);
       const size_t page_bytes = static_cast<size_t>(block_bytes) * 2u * a.hk;
-      // scales: kJoin groups a copy, kLanes lanes for the keys' and for the values' of each
-      constexpr int kLanes = G::kScales / 16, kJoin = 16 / kLanes;
-      const int sc_group = lane / (2 * kLanes), sc_kv = lane / kLanes & 1, sc_at = lane % kLanes * 16;
+      const int self = warp - kTrCopyWarp;  // 0: keys, 1: values
+      // scales: kJoin groups a copy, kLanes lanes each
+      constexpr int kLanes = G::kScales / 16, kJoin = 32 / kLanes;
+      const int sc_group = lane / kLanes, sc_at = lane % kLanes * 16;
       const uint32_t ring = smem_u32(s_ring);
-      const uint32_t sc_dst = ring + (sc_kv ? G::kVs : G::kKs) + sc_group * G::kScales + sc_at;
-      const size_t sc_from = (sc_kv ? block_bytes : 0) + static_cast<size_t>(page_rows) * (D / 2) + sc_at;
+      const uint32_t sc_dst = ring + (self ? G::kVs : G::kKs) + sc_group * G::kScales + sc_at;
+      const uint32_t code_dst = ring + (self ? G::kV : 0) + lane * 16;
+      const uint32_t group_step = self ? G::kVGroup : G::kGroup;
+      const size_t sc_from = static_cast<size_t>(page_rows) * (D / 2) + sc_at;
       int t = 0;
       bool ok = true;
       while (w.s.n > 0 && ok && !EXATTN_INJECT_STALL) {
         const int* const ids = a.table + static_cast<size_t>(w.s.r) * a.width;
-        const uint8_t* const head = a.cache + static_cast<size_t>(w.s.head) * 2 * block_bytes;
+        const uint8_t* const head = a.cache + static_cast<size_t>(2 * w.s.head + self) * block_bytes;
         int key = w.s.tile * kTrKeys + lane % 8 * 16;  // lanes g, g + 8, ...: group g
         int id = key < w.s.req.keys ? ids[key >> a.page_shift] : -1;
         for (int i = 0; i < w.s.n; ++i, ++t) {
@@ -464,27 +481,22 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           const uint32_t stage = slot * G::kStage;
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            const size_t at = __shfl_sync(0xffffffffu, page_at, g);
-            const uint8_t* const k = head + at + __shfl_sync(0xffffffffu, row, g) * (D / 2) + lane * 16;
-            const uint32_t dst = ring + stage + g * G::kGroup + lane * 16;
+            const uint8_t* const from = head + __shfl_sync(0xffffffffu, page_at + row * (D / 2), g) + lane * 16;
             if (flags >> g & 1) {
 #pragma unroll
-              for (int x = 0; x < G::kGroup; x += 512) {
-                cp_async16(dst + x, k + x, 16u);
-                cp_async16(dst + G::kV + g * (G::kVGroup - G::kGroup) + x, k + block_bytes + x, 16u);
-              }
+              for (int x = 0; x < G::kGroup; x += 512) cp_async16(code_dst + stage + g * group_step + x, from + x, 16u);
             }
           }
+          const size_t scale_at = page_at + row * (D / 16);
 #pragma unroll
           for (int g0 = 0; g0 < 8; g0 += kJoin) {
             const int g = g0 + sc_group;
-            const size_t at = __shfl_sync(0xffffffffu, page_at, g);
-            const int sc_row = __shfl_sync(0xffffffffu, row, g);
-            if (flags >> g & 1) cp_async16(sc_dst + stage + g0 * G::kScales, head + at + sc_row * (D / 16) + sc_from, 16u);
+            const uint8_t* const from = head + __shfl_sync(0xffffffffu, scale_at, g) + sc_from;
+            if (flags >> g & 1) cp_async16(sc_dst + stage + g0 * G::kScales, from, 16u);
           }
           const uint32_t bar = smem_u32(&ctl->ring_full[slot]);
           cp_async_arrive(bar);
-          if (lane == 0) {
+          if (self == 0 && lane == 0) {
             ctl->flags[t % kTrFlags] = flags;
             mbar_arrive(bar);
           }
@@ -496,7 +508,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       if (ok) ok = t < G::kStages || wait(ctl->ring_empty[t % G::kStages], t / G::kStages - 1);
       if (ok && !EXATTN_INJECT_STALL) {  // (a test build delivers nothing: the first waits run out)
         const uint32_t bar = smem_u32(&ctl->ring_full[t % G::kStages]);
-        if (lane == 0) {
+        if (self == 0 && lane == 0) {
           ctl->flags[t % kTrFlags] = -1;
           mbar_arrive(bar);
         }
@@ -506,36 +518,34 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       cp_async_wait<0>();  // copies under way land before the CTA's shared memory goes away
     } else {
       // ============================================================ queries, masks and places of a unit's rows
-      // A warp takes half of the rows (one half of the softmax warps has the same), as they are, by 16 bytes to where
-      // the row's operand lies, and turns them into it in place.
+      // The rows come as they are, by 16 bytes to where the row's operand lies, and are turned into it in place.
       TreeWalk w = tree_walk<N>(a, ctl);
-      constexpr int R = N / 2, kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = (R + 31) / 32;
-      const int self = warp - kTrQueryWarp;
+      constexpr int kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = (N + 31) / 32;
       for (int u = 0;; ++u) {
         if (u >= 2 && !wait(ctl->q_empty[u & 1], (u >> 1) - 1)) break;
         TreeRows<N>& rows = ctl->rows[u & 1];
-        if (self == 0 && lane == 0) rows.seg = w.s;
+        if (lane == 0) rows.seg = w.s;
         if (w.s.n > 0) {
           long long from[kOffsets];  // of rows lane, lane + 32; -1: padding
 #pragma unroll
           for (int x = 0; x < kOffsets; ++x) {
-            const int row = self * R + x * 32 + lane, at = w.s.block * N + row;
+            const int row = x * 32 + lane, at = w.s.block * N + row;
             const int node = at / a.group, head = w.s.head * a.group + at - node * a.group, token = w.s.req.q0 + node;
-            const bool live = x * 32 + lane < R && at < w.s.req.q_len * a.group;
+            const bool live = row < N && at < w.s.req.q_len * a.group;
             from[x] = live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1;
-            if (x * 32 + lane < R) {
+            if (row < N) {
               rows.out[row] = live ? token * a.hq + head : -1;
 #pragma unroll 1
               for (int y = 0; y < a.words; ++y)
                 rows.seen[row][y] = live ? a.tree[static_cast<size_t>(token) * a.words + y] : 0u;
             }
           }
-          uint8_t* const q = s_q + (u & 1) * G::kQBytes + self * R * 128;
+          uint8_t* const q = s_q + (u & 1) * G::kQBytes;
           auto piece_at = [&](int row, int piece) {
             return piece / 8 * (N * 128) + row * 128 + ((piece % 8 ^ (row & 7)) << 4);
           };
 #pragma unroll
-          for (int row0 = 0; row0 < R; row0 += kRowsIt) {
+          for (int row0 = 0; row0 < N; row0 += kRowsIt) {
             const int row = row0 + lane / kPieces, piece = lane % kPieces;
             const long long at = __shfl_sync(0xffffffffu, from[row0 / 32], row % 32);
             cp_async16(smem_u32(q) + piece_at(row, piece), a.q + (at < 0 ? 0 : at + piece * 8), at < 0 ? 0u : 16u);
@@ -545,10 +555,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           __syncwarp();
           // One power of two for all rows brings the largest finite value into [2^14, 2^15): f16 then holds bf16's 8
           // bits down to 2^-31 of it (2^-17 of a row's own largest, as long as that is not below 2^-14 of the
-          // half's), and the softmax needs no factor for each row.
+          // unit's), and the softmax needs no factor for each row.
           __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll 4
-          for (int row0 = 0; row0 < R; row0 += kRowsIt) {
+          for (int row0 = 0; row0 < N; row0 += kRowsIt) {
             const uint4 raw = *reinterpret_cast<const uint4*>(q + piece_at(row0 + lane / kPieces, lane % kPieces));
             const __nv_bfloat162* const v = reinterpret_cast<const __nv_bfloat162*>(&raw);
 #pragma unroll
@@ -558,15 +568,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           const float amax = warp_max(fmaxf(__low2float(top), __high2float(top)));
           const uint32_t down_ex = min(268u - (__float_as_uint(amax) >> 23), 253u);
           const float down = __uint_as_float(down_ex << 23);
-          if (lane == 0) rows.c[self] = a.c * __uint_as_float((254u - down_ex) << 23);
+          if (lane == 0) rows.c = a.c * __uint_as_float((254u - down_ex) << 23);
           // a lane takes d/4 dims of a row, 8 of each quarter, which are four chunks of the operand
           constexpr int kLanes = D / 32;
           const int part = lane % kLanes;
 #pragma unroll 1
-          for (int row0 = 0; row0 < R; row0 += 32 / kLanes) {
+          for (int row0 = 0; row0 < N; row0 += 32 / kLanes) {
             const int row = row0 + lane / kLanes;
             uint32_t h[4][4];
-            if (row < R) {
+            if (row < N) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 float f[8];
@@ -576,7 +586,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
               }
             }
             __syncwarp();
-            if (row < R) {
+            if (row < N) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 st_shared_v4(smem_u32(q) + piece_at(row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
@@ -590,134 +600,49 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         tree_next<N>(a, w);
       }
     }
-  } else if (warp >= 12) {
-    regs_dec<kTrWidenRegs>();
-    // ============================================================ widening the values
-    const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
-    uint32_t(*const s_scale)[20] = ctl->scales[q];
-    const uint32_t t_v = tmem + (static_cast<uint32_t>(32 * q) << 16) + G::kVt;
-    for (int t = 0;; ++t) {
-      const int slot = t % G::kStages;
-      if (!wait(ctl->ring_full[slot], t / G::kStages) || ctl->flags[t % kTrFlags] < 0) break;
-      const uint8_t* const st = s_ring + slot * G::kStage;
-      // scales of the warp's dims (one or two groups of 16) for pairs of keys: lane 8 x + y takes those of
-      // columns 4 n + x, n = 2 y and 2 y + 1.  A value vector that is not a number (NaN scales) is zero here: its
-      // key's scores are NaN, and rows that do not see the key multiply it by zero.
-      {
-        const int x = lane / 8, n = 2 * (lane % 8);  // keys 16 x + n and the next, and those 64 on
-        const uint8_t* const p = st + G::kVs + (16 * x + n) * (D / 16);
-        if constexpr (D == 128) {
-          uint32_t b[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint16_t*>(p + (i / 2 * 64 + i % 2) * 8 + 2 * q);
-          uint32_t y[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t both = __byte_perm(b[2 * i], b[2 * i + 1], 0x5140);  // (k0 d0, k1 d0, k0 d1, k1 d1)
-            y[0][i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both)), 0u);
-            y[1][i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both >> 16)), 0u);
-          }
-          *reinterpret_cast<uint2*>(&s_scale[x][n]) = make_uint2(y[0][0], y[0][1]);
-          *reinterpret_cast<uint2*>(&s_scale[4 + x][n]) = make_uint2(y[1][0], y[1][1]);
-        } else {
-          uint32_t y[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            y[i] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(p[256 * i + q] | p[256 * i + 4 + q] << 8)), 0u);
-          *reinterpret_cast<uint2*>(&s_scale[x][n]) = make_uint2(y[0], y[1]);
-        }
-      }
-      __syncwarp();
-      const uint32_t* const my_scale = s_scale[D == 128 ? g8 / 4 * 4 + t4 : t4];
-      if (t >= G::kBufs && !wait(ctl->pv_done[(t - G::kBufs) & 1], (t - G::kBufs) >> 1)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {  // 8 columns of the thread
-        uint32_t sc[8];
-        *reinterpret_cast<uint4*>(sc) = *reinterpret_cast<const uint4*>(my_scale + 8 * b);
-        *reinterpret_cast<uint4*>(sc + 4) = *reinterpret_cast<const uint4*>(my_scale + 8 * b + 4);
-        uint32_t r0[16];
-        if constexpr (D == 128) {
-          // lane 4 r + x loads bytes 4 x .. of the key in group r / 2 + 4 (r % 2): column 2 t + i of the matrix is
-          // column n + i of thread t
-          const uint8_t* const p = st + G::kV + (g8 / 2 + 4 * (g8 % 2)) * G::kVGroup + 16 * q + 4 * t4;
-          uint32_t r1[16];
-#pragma unroll
-          for (int n = 0; n < 8; n += 2) {
-            const uint8_t* const row = p + (8 * b + n) * (D / 2);
-            const uint32_t xa = movmatrix_trans(*reinterpret_cast<const uint32_t*>(row));
-            const uint32_t xb = movmatrix_trans(*reinterpret_cast<const uint32_t*>(row + D / 2));
-            uint32_t even[4], odd[4];  // dims 0, 2 of column n, then of n + 1; dims 1, 3
-            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
-            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              r0[2 * (n + e)] = mul_f16x2(even[2 * e], sc[n + e]);
-              r0[2 * (n + e) + 1] = mul_f16x2(odd[2 * e], sc[n + e]);
-              r1[2 * (n + e)] = mul_f16x2(even[2 * e + 1], sc[n + e]);
-              r1[2 * (n + e) + 1] = mul_f16x2(odd[2 * e + 1], sc[n + e]);
-            }
-          }
-          tmem_st_16x128b_x8(t_v + (16u << 16) + t % G::kBufs * 64 + b * 32, r1);
-        } else {
-          const uint8_t* const p = st + G::kV + t4 * G::kVGroup + 8 * q + g8;
-#pragma unroll
-          for (int n = 0; n < 8; n += 4) {
-            uint32_t x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              x[e] = p[e / 2 % 2 * 4 * G::kVGroup + (8 * b + n + e / 4 * 2 + e % 2) * (D / 2)];
-            const uint32_t xa = x[0] | x[2] << 8 | x[4] << 16 | x[6] << 24, xb = x[1] | x[3] << 8 | x[5] << 16 | x[7] << 24;
-            uint32_t even[4], odd[4];
-            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
-            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              r0[2 * (n + e)] = mul_f16x2(even[e], sc[n + e]);
-              r0[2 * (n + e) + 1] = mul_f16x2(odd[e], sc[n + e]);
-            }
-          }
-        }
-        tmem_st_16x128b_x8(t_v + t % G::kBufs * 64 + b * 32, r0);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&ctl->ring_empty[slot]));
-        mbar_arrive(smem_u32(&ctl->v_full[t % G::kBufs]));
-      }
-    }
   } else if (warp >= 8) {
     regs_dec<kTrWidenRegs>();
-    // ============================================================ widening the keys
-    const int q = warp % 4, g8 = lane / 4, t4 = lane % 4;
-    const int row_in = 4 * q + (g8 & 1), group = g8 / 2;  // row + 2 hh, group + 4 i
-    const uint32_t t_k = tmem + (static_cast<uint32_t>(32 * q) << 16) + G::kK;
-    for (int t = 0;; ++t) {
-      const int slot = t % G::kStages;
-      if (!wait(ctl->ring_full[slot], t / G::kStages) || ctl->flags[t % kTrFlags] < 0) break;
-      const uint8_t* const st = s_ring + slot * G::kStage;
-      const uint8_t* const codes = st + group * G::kGroup + row_in * (D / 2) + t4 * (D / 8);
-      const uint8_t* const scale = st + G::kKs + (16 * group + row_in) * (D / 16) + t4 * (D / 64);
-      if (t >= G::kBufs && !wait(ctl->s_full[(t - G::kBufs) & 1], (t - G::kBufs) >> 1)) break;
+    // ============================================================ widening
+    // Of lanes 32 q .. + 31 the warp has 16 keys of K (rows 16 half ..) and, of V^T, all dims of half of the columns
+    // (n = 8 half .. + 7).  In pass i it widens K(i) and V(i - 1): S(i - 1), issued behind PV(i - 3), frees both.
+    const int q = warp % 4, half = (warp - 8) / 4, g8 = lane / 4, t4 = lane % 4;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t t_k = tmem + lanes + (static_cast<uint32_t>(16 * half) << 16) + G::kK;
+    const uint32_t t_v = tmem + lanes + G::kVt + 32 * half;
+    // K: rows g8 and g8 + 8 are keys in groups g8 / 2 and g8 / 2 + 4, d/4 codes each
+    const int k_row = 4 * q + 2 * half + (g8 & 1);
+    const int k_codes = g8 / 2 * G::kGroup + k_row * (D / 2) + t4 * (D / 8);
+    const int k_scale = G::kKs + (16 * (g8 / 2) + k_row) * (D / 16) + t4 * (D / 64);
+    // V: the matrix of columns n and n + 1 has the keys of all groups in one row; lane 4 r + x loads bytes 4 x .. of the
+    // key in group r / 2 + 4 (r % 2), and the transposed matrix's columns 2 t + i are columns n + i of thread t
+    const int v_codes = D == 128 ? G::kV + (g8 / 2 + 4 * (g8 % 2)) * G::kVGroup + 8 * half * (D / 2) + 16 * q + 4 * t4
+                                 : G::kV + t4 * G::kVGroup + 8 * half * (D / 2) + 8 * q + g8;
+    // scales of the warp's dims (one or two groups of 16) as pairs of keys: lane 8 x + y takes column 4 n + x,
+    // n = 8 half + y: rows 2 (n / 2) and the next of group x + 4 (n % 2)
+    const int v_scale = G::kVs + (16 * (lane / 8 + 4 * (lane % 2)) + 8 * half + lane % 8 / 2 * 2) * (D / 16) +
+                        (D == 128 ? 2 * q : q);
+    uint32_t(*const s_scale)[12] = ctl->scales[warp - 8];
+    const uint32_t* const my_scale = s_scale[D == 128 ? g8 / 4 * 4 + t4 : t4];
+    for (int i = 0;; ++i) {
+      if (!wait(ctl->ring_full[i % G::kStages], i / G::kStages)) break;
+      const bool end = ctl->flags[i % kTrFlags] < 0;
+      if (i > 0 && !wait(ctl->s_full[(i - 1) & 1], (i - 1) >> 1)) break;
       tc_fence_after();
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
+      if (!end) {
+        const uint8_t* const st = s_ring + i % G::kStages * G::kStage;
         uint32_t w[2][4], sc[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int code_at = i * 4 * G::kGroup + 2 * hh * (D / 2), scale_at = (i * 64 + 2 * hh) * (D / 16);
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t* const codes = st + k_codes + e * 4 * G::kGroup;
+          const uint8_t* const scale = st + k_scale + e * 64 * (D / 16);
+          // (a value vector that is not a number makes its key's scores NaN)
           if constexpr (D == 128) {
-            *reinterpret_cast<uint4*>(w[i]) = *reinterpret_cast<const uint4*>(codes + code_at);
-            sc[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale + scale_at));
-            // a value vector that is not a number makes its key's scores NaN
-            sc[i] = fma_f16x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale + scale_at + (G::kVs - G::kKs))), 0u,
-                              sc[i]);
+            *reinterpret_cast<uint4*>(w[e]) = *reinterpret_cast<const uint4*>(codes);
+            sc[e] = fma_f16x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale + (G::kVs - G::kKs))), 0u,
+                              e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scale)));
           } else {
-            *reinterpret_cast<uint2*>(w[i]) = *reinterpret_cast<const uint2*>(codes + code_at);
-            sc[i] = e4m3x2_to_f16x2(scale[scale_at]);
-            sc[i] = fma_f16x2(e4m3x2_to_f16x2(scale[scale_at + (G::kVs - G::kKs)]), 0u, sc[i]);
+            *reinterpret_cast<uint2*>(w[e]) = *reinterpret_cast<const uint2*>(codes);
+            sc[e] = fma_f16x2(e4m3x2_to_f16x2(scale[G::kVs - G::kKs]), 0u, e4m3x2_to_f16x2(*scale));
           }
         }
 #pragma unroll
@@ -726,28 +651,90 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t h[4];
-              unpack_e2m1x8(w[i][2 * part + x], h);
+              unpack_e2m1x8(w[e][2 * part + x], h);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                r[2 * (4 * x + e) + i] = part ? mul_f16x2_hi(h[e], sc[i]) : mul_f16x2_lo(h[e], sc[i]);
+              for (int y = 0; y < 4; ++y)
+                r[2 * (4 * x + y) + e] = part ? mul_f16x2_hi(h[y], sc[e]) : mul_f16x2_lo(h[y], sc[e]);
             }
-          tmem_st_16x128b_x8(t_k + (static_cast<uint32_t>(16 * hh) << 16) + t % G::kBufs * (D / 2) + part * 32, r);
+          tmem_st_16x128b_x8(t_k + (i & 1) * (D / 2) + part * 32, r);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->k_full[i & 1]));
+      }
+      if (i > 0) {
+        const int t = i - 1, slot = t % G::kStages;
+        const uint8_t* const st = s_ring + slot * G::kStage;
+        // A value vector that is not a number (NaN scales) is zero: its key's scores are NaN, and rows that do not see
+        // the key multiply it by zero.
+        const uint8_t* const scale = st + v_scale;
+        if constexpr (D == 128) {
+          const uint32_t both = __byte_perm(*reinterpret_cast<const uint16_t*>(scale),
+                                            *reinterpret_cast<const uint16_t*>(scale + D / 16), 0x5140);
+          s_scale[lane / 8][lane % 8] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both)), 0u);
+          s_scale[4 + lane / 8][lane % 8] = max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(both >> 16)), 0u);
+        } else {
+          s_scale[lane / 8][lane % 8] =
+              max_f16x2(e4m3x2_to_f16x2(static_cast<uint16_t>(scale[0] | scale[D / 16] << 8)), 0u);
+        }
+        __syncwarp();
+        uint32_t sv[8], r0[16];
+        *reinterpret_cast<uint4*>(sv) = *reinterpret_cast<const uint4*>(my_scale);
+        *reinterpret_cast<uint4*>(sv + 4) = *reinterpret_cast<const uint4*>(my_scale + 4);
+        const uint8_t* const p = st + v_codes;
+        if constexpr (D == 128) {
+          uint32_t r1[16];
+#pragma unroll
+          for (int n = 0; n < 8; n += 2) {
+            const uint32_t xa = movmatrix_trans(*reinterpret_cast<const uint32_t*>(p + n * (D / 2)));
+            const uint32_t xb = movmatrix_trans(*reinterpret_cast<const uint32_t*>(p + (n + 1) * (D / 2)));
+            uint32_t even[4], odd[4];  // dims 0, 2 of column n, then of n + 1; dims 1, 3
+            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
+            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              r0[2 * (n + e)] = mul_f16x2(even[2 * e], sv[n + e]);
+              r0[2 * (n + e) + 1] = mul_f16x2(odd[2 * e], sv[n + e]);
+              r1[2 * (n + e)] = mul_f16x2(even[2 * e + 1], sv[n + e]);
+              r1[2 * (n + e) + 1] = mul_f16x2(odd[2 * e + 1], sv[n + e]);
+            }
+          }
+          tmem_st_16x128b_x8(t_v + (16u << 16) + (t & 1) * 64, r1);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 8; n += 4) {
+            uint32_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = p[e / 2 % 2 * 4 * G::kVGroup + (n + e / 4 * 2 + e % 2) * (D / 2)];
+            const uint32_t xa = x[0] | x[2] << 8 | x[4] << 16 | x[6] << 24, xb = x[1] | x[3] << 8 | x[5] << 16 | x[7] << 24;
+            uint32_t even[4], odd[4];
+            unpack_e2m1x8((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), even);
+            unpack_e2m1x8(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), odd);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              r0[2 * (n + e)] = mul_f16x2(even[e], sv[n + e]);
+              r0[2 * (n + e) + 1] = mul_f16x2(odd[e], sv[n + e]);
+            }
+          }
+        }
+        tmem_st_16x128b_x8(t_v + (t & 1) * 64, r0);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->ring_empty[slot]));
+          mbar_arrive(smem_u32(&ctl->v_full[t & 1]));
         }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&ctl->ring_empty[slot]));
-        mbar_arrive(smem_u32(&ctl->k_full[t % G::kBufs]));
-      }
+      if (end) break;
     }
   } else {
     regs_inc<kTrSoftmaxRegs>();
     // ============================================================ softmax, outputs
-    constexpr int H = G::kHalf, C = G::kChunk;
+    constexpr int H = G::kHalf;
     const int g = warp / 4, q = warp % 4, m_row = 32 * q + lane, tid = threadIdx.x % 128;
     const int my_group = m_row % 8 / 2 + 4 * (m_row / 8 % 2);  // of 16 keys
     const int my_key = 16 * my_group + 2 * (m_row / 16) + (m_row & 1);
@@ -770,15 +757,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       const int n = rows.seg.n;
       if (n == 0) break;
       bool leave = false;
-      const float c = rows.c[g];
+      const float c = rows.c;
       const int keys = rows.seg.req.keys, before = keys - rows.seg.req.queries, tile0 = rows.seg.tile;
-      float l[H];
-      constexpr bool kNmRegs = H <= 32;  // the references in registers
-      float nmr[kNmRegs ? H : 1];
+      float l[H], nm[H];
 #pragma unroll
-      for (int i = 0; i < H; ++i) l[i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < (kNmRegs ? H : 1); ++i) nmr[i] = -kDecNone;
+      for (int i = 0; i < H; ++i) {
+        l[i] = 0.f;
+        nm[i] = -kDecNone;
+      }
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++t) {
         ok = ok && wait(ctl->s_full[t & 1], t >> 1);
@@ -787,122 +773,107 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         const bool clean = flags == 0xff && (tile0 + j + 1) * kTrKeys <= before;
         const bool there = key < keys && (flags >> my_group & 1);
         tc_fence_after();
+        const uint32_t t_here = t_s + (t & 1) * G::kCols;
+        float x[H];
+        auto scores = [&]() {
+          uint32_t r[H];
+          tmem_ld_cols<H>(t_here, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int cc = 0; cc < H / C; ++cc) {
-          const uint32_t t_here = t_s + (t & 1) * G::kCols + cc * C;
-          float x[C];
-          auto scores = [&]() {
-            uint32_t r[C];
-            tmem_ld_cols<C>(t_here, r);
+          for (int i = 0; i < H; ++i) x[i] = __uint_as_float(r[i]);
+        };
+        // bit i: row i of the chunk sees the thread's key
+        uint32_t see = ~0u;
+        if (!clean) {
+          const int node = key - before, word = node >> 5;
+          see = there && (node < 0 || word < a.words) ? ~0u : 0u;
+          if (node >= 0 && see) {
+            see = 0u;
+#pragma unroll 1
+            for (int i = 0; i < H; ++i) see |= (rows.seen[g * H + i][word] >> (node & 31) & 1u) << i;
+          }
+        }
+        auto mask = [&]() {
+          if (clean) return;
+#pragma unroll
+          for (int i = 0; i < H; ++i) x[i] = see >> i & 1u ? x[i] : -INFINITY;
+        };
+        // scores in units of the exponent, relative to the rows' references
+        auto relative = [&]() {
+#pragma unroll
+          for (int i = 0; i < H; i += 2) {
+            const float2 y = fma_f32x2(f32x2(x[i], x[i + 1]), f32x2(c, c), f32x2(nm[i], nm[i + 1]));
+            x[i] = y.x;
+            x[i + 1] = y.y;
+          }
+        };
+#pragma unroll 1
+        for (bool moved = false;; moved = true) {
+          scores();
+          relative();
+          mask();
+          float big = x[0];
+#pragma unroll
+          for (int i = 1; i + 1 < H; i += 2) big = max3f(big, x[i], x[i + 1]);
+          big = fmaxf(big, x[H - 1]);
+          if (moved || !bar_any(bar, 128, big > kDecLazy || !ok)) break;
+          // ---- some row's reference moves: maxima of all rows over the tile's keys
+#pragma unroll 1
+          for (int i0 = 0; i0 < H; i0 += 8) {
+            uint32_t r[8];
+            tmem_ld_cols<8>(t_here + i0, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = __uint_as_float(r[i]);
-          };
-          // bit i: row i of the chunk sees the thread's key
-          uint32_t see = ~0u;
-          if (!clean) {
-            const int node = key - before, word = node >> 5;
-            see = there && (node < 0 || word < a.words) ? ~0u : 0u;
-            if (node >= 0 && see) {
-              see = 0u;
-#pragma unroll 1
-              for (int i = 0; i < C; ++i) see |= (rows.seen[g * H + cc * C + i][word] >> (node & 31) & 1u) << i;
+            for (int i = 0; i < 8; ++i) {
+              const float v = warp_max(see >> (i0 + i) & 1u ? __uint_as_float(r[i]) * c : -INFINITY);
+              if (lane == 0) ctl->top[q][g * H + i0 + i] = v;
             }
           }
-          auto mask = [&]() {
-            if (clean) return;
-#pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = see >> i & 1u ? x[i] : -INFINITY;
-          };
-          // scores in units of the exponent, relative to the rows' references
-          auto relative = [&]() {
-#pragma unroll
-            for (int i = 0; i < C; i += 4) {
-              float4 nm;
-              if constexpr (kNmRegs)
-                nm = make_float4(nmr[i], nmr[i + 1], nmr[i + 2], nmr[i + 3]);
-              else
-                nm = *reinterpret_cast<const float4*>(s_nm + cc * C + i);
-              const float2 y = fma_f32x2(f32x2(x[i], x[i + 1]), f32x2(c, c), f32x2(nm.x, nm.y));
-              const float2 z = fma_f32x2(f32x2(x[i + 2], x[i + 3]), f32x2(c, c), f32x2(nm.z, nm.w));
-              x[i] = y.x;
-              x[i + 1] = y.y;
-              x[i + 2] = z.x;
-              x[i + 3] = z.y;
-            }
-          };
-#pragma unroll 1
-          for (bool moved = false;; moved = true) {
-            scores();
-            relative();
-            mask();
-            float big = x[0];
-#pragma unroll
-            for (int i = 1; i + 1 < C; i += 2) big = max3f(big, x[i], x[i + 1]);
-            big = fmaxf(big, x[C - 1]);
-            if (moved || !bar_any(bar, 128, big > kDecLazy || !ok)) break;
-            // ---- some row's reference moves: maxima of all rows over the tile's keys
-#pragma unroll 1
-            for (int i0 = 0; i0 < C; i0 += 8) {
-              uint32_t r[8];
-              tmem_ld_cols<8>(t_here + i0, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float v = warp_max(see >> (i0 + i) & 1u ? __uint_as_float(r[i]) * c : -INFINITY);
-                if (lane == 0) ctl->top[q][g * H + cc * C + i0 + i] = v;
-              }
-            }
-            bar_wait(bar, 128);
-            if (tid < C) {
-              const int col = g * H + cc * C + tid;
-              float v = fmaxf(fmaxf(ctl->top[0][col], ctl->top[1][col]), fmaxf(ctl->top[2][col], ctl->top[3][col]));
-              const float m = -s_nm[cc * C + tid];
-              v = fmaxf(v - kDecBelow, m);
-              s_alpha[cc * C + tid] = ex2_mufu(m - v);
-              s_nm[cc * C + tid] = -v;
-            }
-            if (j > 0 && ok) ok = wait(ctl->pv_done[(t - 1) & 1], (t - 1) >> 1);
-            leave = bar_any(bar, 128, !ok);
-            if (leave) break;
-            if constexpr (kNmRegs) {
-#pragma unroll
-              for (int i = 0; i < H; ++i) nmr[i] = s_nm[i];
-            }
-            if (j > 0) {
-              tc_fence_after();
-              uint32_t r[C];
-              tmem_ld_cols<C>(t_o + cc * C, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < C; ++i) {
-                const float f = s_alpha[cc * C + i];
-                r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                l[cc * C + i] *= f;
-              }
-              tmem_st_cols<C>(t_o + cc * C, r);
-              tmem_st_wait();
-            }
+          bar_wait(bar, 128);
+          if (tid < H) {
+            const int col = g * H + tid;
+            float v = fmaxf(fmaxf(ctl->top[0][col], ctl->top[1][col]), fmaxf(ctl->top[2][col], ctl->top[3][col]));
+            const float m = -s_nm[tid];
+            v = fmaxf(v - kDecBelow, m);
+            s_alpha[tid] = ex2_mufu(m - v);
+            s_nm[tid] = -v;
           }
+          if (j > 0 && ok) ok = wait(ctl->pv_done[(t - 1) & 1], (t - 1) >> 1);
+          leave = bar_any(bar, 128, !ok);
           if (leave) break;
-          const uint32_t dst = p_row + t % 2 * G::kPBytes;
 #pragma unroll
-          for (int i = 0; i < C; i += 8) {
-            uint32_t w[4];
+          for (int i = 0; i < H; ++i) nm[i] = s_nm[i];
+          if (j > 0) {
+            tc_fence_after();
+            uint32_t r[H];
+            tmem_ld_cols<H>(t_o, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int y = i + 2 * e;
-              const float2 p = f32x2(ex2_mufu(x[y]), ex2_mufu(x[y + 1]));
-              const float2 sum = add_f32x2(f32x2(l[cc * C + y], l[cc * C + y + 1]), p);
-              l[cc * C + y] = sum.x;
-              l[cc * C + y + 1] = sum.y;
-              w[e] = pack_f16x2(p.x, p.y);
+            for (int i = 0; i < H; ++i) {
+              const float f = s_alpha[i];
+              r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+              l[i] *= f;
             }
-            const int col = g * H + cc * C + i;
-            st_shared_v4(dst + col / 64 * (128 * 128) + ((col / 8 % 8 ^ (m_row & 7)) << 4), w[0], w[1], w[2], w[3]);
+            tmem_st_cols<H>(t_o, r);
+            tmem_st_wait();
           }
         }
         if (leave) break;
+        const uint32_t dst = p_row + (t & 1) * G::kPBytes;
+#pragma unroll
+        for (int i = 0; i < H; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int y = i + 2 * e;
+            const float2 p = f32x2(ex2_mufu(x[y]), ex2_mufu(x[y + 1]));
+            const float2 sum = add_f32x2(f32x2(l[y], l[y + 1]), p);
+            l[y] = sum.x;
+            l[y + 1] = sum.y;
+            w[e] = pack_f16x2(p.x, p.y);
+          }
+          st_shared_v4(dst + (((g * H + i) / 8 ^ (m_row & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();  // S has been read (and O perhaps rescaled)
         __syncwarp();
@@ -911,23 +882,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       if (leave) break;
       // ---- the rows' sums over all keys: lanes exchange halves until each holds a row's sum of its warp
 #pragma unroll
-      for (int cc = 0; cc < H / C; ++cc) {
-        float v[C];
+      for (int o = H / 2; o >= 1; o /= 2) {
+        const bool high = lane & o;
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = l[cc * C + i];
-#pragma unroll
-        for (int o = C / 2; o >= 1; o /= 2) {
-          const bool high = lane & o;
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const float keep = high ? v[i + o] : v[i], send = high ? v[i] : v[i + o];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
+        for (int i = 0; i < o; ++i) {
+          const float keep = high ? l[i + o] : l[i], send = high ? l[i] : l[i + o];
+          l[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-#pragma unroll
-        for (int o = C; o < 32; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        if (lane < C) ctl->top[q][g * H + cc * C + lane] = v[0];
       }
+#pragma unroll
+      for (int o = H; o < 32; o *= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      if (lane < H) ctl->top[q][g * H + lane] = l[0];
       if (bar_any(bar, 128, !ok)) break;
       const bool whole = n == rows.seg.tiles;
       const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (unit_no > 0 ? 1 : 0)) * N;
@@ -960,25 +925,20 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       // ---- O: the thread's lane is a dim, its columns are rows
       const bool has_dim = D == 128 || lane < 16;
       const int dim = D == 128 ? 32 * q + 4 * (lane % 8) + lane / 8 : 16 * q + 2 * (lane % 8) + lane / 8;
+      uint32_t r[H];
+      tmem_ld_cols<H>(t_o, r);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->o_empty));
 #pragma unroll
-      for (int cc = 0; cc < H / C; ++cc) {
-        uint32_t r[C];
-        tmem_ld_cols<C>(t_o + cc * C, r);
-        tmem_ld_wait();
-        if (cc == H / C - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->o_empty));
-        }
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const int col = g * H + cc * C + i, at = rows.out[col];
-          if (at < 0 || !has_dim) continue;
-          if (whole)
-            a.o[static_cast<size_t>(at) * D + dim] = __float2bfloat16_rn(__uint_as_float(r[i]) * s_alpha[cc * C + i]);
-          else
-            a.part_o[(slot + col) * D + dim] = __uint_as_float(r[i]);
-        }
+      for (int i = 0; i < H; ++i) {
+        const int col = g * H + i, at = rows.out[col];
+        if (at < 0 || !has_dim) continue;
+        if (whole)
+          a.o[static_cast<size_t>(at) * D + dim] = __float2bfloat16_rn(__uint_as_float(r[i]) * s_alpha[i]);
+        else
+          a.part_o[(slot + col) * D + dim] = __uint_as_float(r[i]);
       }
       ++unit_no;
       bar_wait(bar, 128);  // the next unit writes s_alpha and s_nm

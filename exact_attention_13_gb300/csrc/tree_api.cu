@@ -17,8 +17,8 @@ namespace exattn {
 
 namespace {
 
-// Query rows that share a unit: the smallest of 16, 32, 64 and 128 that hold the rows of one key head.
-int tree_rows(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Query rows that share a unit: the smallest of 16, 32 and 64 that hold the rows of one key head.
+int tree_rows(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 size_t tree_workspace(int n, int d) {
   const size_t rows = static_cast<size_t>(2) * kSms * n;
@@ -62,8 +62,7 @@ template <int D>
 int launch_tree_rows(Kv4Args& a, int n, void* workspace, cudaStream_t s) {
   return n == 16   ? launch_tree<D, 16>(a, workspace, s)
          : n == 32 ? launch_tree<D, 32>(a, workspace, s)
-         : n == 64 ? launch_tree<D, 64>(a, workspace, s)
-                   : launch_tree<D, 128>(a, workspace, s);
+                   : launch_tree<D, 64>(a, workspace, s);
 }
 
 }  // namespace
