@@ -88,11 +88,13 @@ struct TreeWalk {
 };
 
 template <int N>
+constexpr int kRowWords = (N + 31) / 32;
+template <int N>
 struct TreeRows {          // of one unit, written by the query warps
   TreeSeg seg;
   float c;                 // factor of the scores
   int out[N];              // row of o and lse, -1: padding
-  uint32_t seen[N][kTreeWords + 1];
+  uint32_t seen[kTreeNodes][kRowWords<N>];  // rows that see a node
 };
 
 template <int N>
@@ -193,6 +195,22 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
                EXATTN_W4(r, 0), EXATTN_W4(r, 4), EXATTN_W4(r, 8), EXATTN_W4(r, 12)
                : "memory");
 }
+// 16 lanes from the address's on: r[2 n + i] from row lane / 4 + 8 i, column 4 n + lane % 4.
+template <int N>
+__device__ __forceinline__ void tmem_ld_16x128b(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "registers of one load");
+  if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x2.b32 {%0, %1, %2, %3}, [%4];" : EXATTN_R4(r, 0) : "r"(taddr));
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : EXATTN_R4(r, 0), EXATTN_R4(r, 4)
+                 : "r"(taddr));
+  if constexpr (N == 16)
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : EXATTN_R4(r, 0), EXATTN_R4(r, 4), EXATTN_R4(r, 8), EXATTN_R4(r, 12)
+                 : "r"(taddr));
+}
 #undef EXATTN_R4
 #undef EXATTN_W4
 
@@ -265,7 +283,10 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
 #pragma unroll 1
   for (int w = 0; w < kTrThreads / 32; ++w) total += ctl->sum[w];
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  if (static_cast<int>(blockIdx.x) >= n) return n;
+  if (static_cast<int>(blockIdx.x) >= n) {
+    __syncthreads();
+    return n;
+  }
   const long long first = share_begin(total, n, blockIdx.x), last = share_begin(total, n, blockIdx.x + 1);
   long long base = 0;
   for (int r0 = 0; r0 < a.b; r0 += kTrThreads) {
@@ -315,11 +336,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   grid_launch_dependents();
-  const int n_cta = tree_my_range<N>(a, ctl);
-  if (static_cast<int>(blockIdx.x) >= n_cta) {
-    if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
   if (warp == kTrMmaWarp) {
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish();
@@ -344,9 +360,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
     fence_mbar_init();
   }
   tc_fence_before();
-  __syncthreads();
+  const int n_cta = tree_my_range<N>(a, ctl);  // (ends with a barrier)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  if (static_cast<int>(blockIdx.x) >= n_cta) {
+    if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (warp == kTrMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
   volatile int* const abort_flag = &ctl->abort;
   // For the number-th completion, counted from 0.  The first try that fails starts the clock, and a wait that runs out
   // raises the CTA's abort flag (small code: there are 20 copies of it).
@@ -533,21 +554,28 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
             const int node = at / a.group, head = w.s.head * a.group + at - node * a.group, token = w.s.req.q0 + node;
             const bool live = row < N && at < w.s.req.q_len * a.group;
             from[x] = live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1;
-            if (row < N) {
-              rows.out[row] = live ? token * a.hq + head : -1;
+            if (row < N) rows.out[row] = live ? token * a.hq + head : -1;
+            // the lane's row of bits, a word at a time, becomes a bit of each node's word
 #pragma unroll 1
-              for (int y = 0; y < a.words; ++y)
-                rows.seen[row][y] = live ? a.tree[static_cast<size_t>(token) * a.words + y] : 0u;
+            for (int y = 0; 32 * y < min(w.s.req.queries, 32 * a.words); ++y) {
+              const uint32_t bits = live ? a.tree[static_cast<size_t>(token) * a.words + y] : 0u;
+              uint32_t mine = 0u;
+#pragma unroll 4
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t node = __ballot_sync(0xffffffffu, bits >> e & 1u);
+                mine = lane == e ? node : mine;
+              }
+              rows.seen[32 * y + lane][x] = mine;
             }
           }
           uint8_t* const q = s_q + (u & 1) * G::kQBytes;
           auto piece_at = [&](int row, int piece) {
             return piece / 8 * (N * 128) + row * 128 + ((piece % 8 ^ (row & 7)) << 4);
           };
-#pragma unroll
+#pragma unroll 4
           for (int row0 = 0; row0 < N; row0 += kRowsIt) {
             const int row = row0 + lane / kPieces, piece = lane % kPieces;
-            const long long at = __shfl_sync(0xffffffffu, from[row0 / 32], row % 32);
+            const long long at = __shfl_sync(0xffffffffu, kOffsets > 1 && row0 >= 32 ? from[kOffsets - 1] : from[0], row % 32);
             cp_async16(smem_u32(q) + piece_at(row, piece), a.q + (at < 0 ? 0 : at + piece * 8), at < 0 ? 0u : 16u);
           }
           cp_async_commit();
@@ -759,6 +787,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       bool leave = false;
       const float c = rows.c;
       const int keys = rows.seg.req.keys, before = keys - rows.seg.req.queries, tile0 = rows.seg.tile;
+      const int clean_tiles = before / kTrKeys - tile0;  // whose keys all rows see, if their pages are there
       float l[H], nm[H];
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -768,10 +797,6 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++t) {
         ok = ok && wait(ctl->s_full[t & 1], t >> 1);
-        const int key = (tile0 + j) * kTrKeys + my_key;
-        const int flags = ctl->flags[t % kTrFlags];
-        const bool clean = flags == 0xff && (tile0 + j + 1) * kTrKeys <= before;
-        const bool there = key < keys && (flags >> my_group & 1);
         tc_fence_after();
         const uint32_t t_here = t_s + (t & 1) * G::kCols;
         float x[H];
@@ -782,16 +807,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
 #pragma unroll
           for (int i = 0; i < H; ++i) x[i] = __uint_as_float(r[i]);
         };
-        // bit i: row i of the chunk sees the thread's key
+        // bit i: row i of the half sees the thread's key
         uint32_t see = ~0u;
+        const int flags = ctl->flags[t % kTrFlags];
+        const bool clean = j < clean_tiles && flags == 0xff;
         if (!clean) {
-          const int node = key - before, word = node >> 5;
-          see = there && (node < 0 || word < a.words) ? ~0u : 0u;
-          if (node >= 0 && see) {
+          const int key = (tile0 + j) * kTrKeys + my_key, node = key - before;
+          if (key >= keys || !(flags >> my_group & 1) || node >= 32 * a.words)
             see = 0u;
-#pragma unroll 1
-            for (int i = 0; i < H; ++i) see |= (rows.seen[g * H + i][word] >> (node & 31) & 1u) << i;
-          }
+          else if (node >= 0)
+            see = rows.seen[node][g * H / 32] >> (g * H % 32);
         }
         auto mask = [&]() {
           if (clean) return;
@@ -922,23 +947,41 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       ok = wait(ctl->pv_done[(t - 1) & 1], (t - 1) >> 1);
       if (bar_any(bar, 128, !ok)) break;
       tc_fence_after();
-      // ---- O: the thread's lane is a dim, its columns are rows
-      const bool has_dim = D == 128 || lane < 16;
-      const int dim = D == 128 ? 32 * q + 4 * (lane % 8) + lane / 8 : 16 * q + 2 * (lane % 8) + lane / 8;
-      uint32_t r[H];
-      tmem_ld_cols<H>(t_o, r);
+      // ---- O: rows g8 and g8 + 8 of the 32 lanes, and the two 16 further on, are four neighbouring dims (two for
+      // d = 64) of columns 4 n + t4
+      const int g8 = lane / 4, t4 = lane % 4;
+      constexpr int kDims = D / 32;
+      uint32_t lo[H / 2], hi[D == 128 ? H / 2 : 1];
+      tmem_ld_16x128b<H / 2>(t_o, lo);
+      if constexpr (D == 128) tmem_ld_16x128b<H / 2>(t_o + (16u << 16), hi);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->o_empty));
+      const int dim = D / 4 * q + kDims * g8;
 #pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const int col = g * H + i, at = rows.out[col];
-        if (at < 0 || !has_dim) continue;
-        if (whole)
-          a.o[static_cast<size_t>(at) * D + dim] = __float2bfloat16_rn(__uint_as_float(r[i]) * s_alpha[i]);
-        else
-          a.part_o[(slot + col) * D + dim] = __uint_as_float(r[i]);
+      for (int n4 = 0; n4 < H / 4; ++n4) {
+        const int col = g * H + 4 * n4 + t4, at = rows.out[col];
+        float y[4] = {__uint_as_float(lo[2 * n4]), __uint_as_float(lo[2 * n4 + 1]), 0.f, 0.f};
+        if constexpr (D == 128) {
+          y[2] = __uint_as_float(hi[2 * n4]);
+          y[3] = __uint_as_float(hi[2 * n4 + 1]);
+        }
+        if (at < 0) continue;
+        if (whole) {
+          const float f = s_alpha[4 * n4 + t4];
+          __nv_bfloat16* const to = a.o + static_cast<size_t>(at) * D + dim;
+          if constexpr (D == 128)
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
+          else
+            *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(y[0] * f, y[1] * f);
+        } else {
+          float* const to = a.part_o + (slot + col) * D + dim;
+          if constexpr (D == 128)
+            *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+          else
+            *reinterpret_cast<float2*>(to) = make_float2(y[0], y[1]);
+        }
       }
       ++unit_no;
       bar_wait(bar, 128);  // the next unit writes s_alpha and s_nm
