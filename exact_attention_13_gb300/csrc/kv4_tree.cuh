@@ -84,7 +84,7 @@ struct TreeSeg {
 struct TreeWalk {
   TreeSeg s;
   int blocks;
-  long long left;  // tiles of the CTA's share from s.tile on (units, when they are not split)
+  long long left;  // of the CTA's share behind the segment
 };
 
 template <int N>
@@ -107,6 +107,7 @@ struct TreeCtrl {
   int flags[kTrFlags];     // bit g: 16-key group g of the tile is there; -1: no more tiles
   long long sum[32];
   long long total, first, last;
+  int extra, skip;         // what a unit counts more on the line, and how much of that the share begins with
   TreeSeg start;
   TreeRows<N> rows[2];
   alignas(16) float nm[N];  // minus the reference of a row's probabilities
@@ -221,10 +222,27 @@ __device__ __forceinline__ int tree_blocks(const Kv4Args& a, const ReqShape& s) 
 }
 __device__ __forceinline__ int tree_tiles(const ReqShape& s) { return max(1, (s.keys - 1) / kTrKeys + 1); }
 
+// On the line of tiles that the CTAs share a unit counts `extra` more than it has, at its front: queries, first
+// reference, sums and outputs take the time of that many tiles (64 requests of 500 to 8192 keys, up to 64 rows: 187 us with
+// 0, XXX with 4).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
+// have few tiles each, spreading them is worth more.  Units that are not split count 1.
+__device__ __forceinline__ int tree_extra(const Kv4Args& a, long long tiles) {
+  return !a.whole_tiles && tiles >= 16ll * gridDim.x ? 4 : 0;
+}
+// Tiles of the walk's unit that its share has, from s.tile on, after `skip` of the line in front of them.
+__device__ __forceinline__ void tree_take(const Kv4Args& a, TreeWalk& w, int skip) {
+  if (a.whole_tiles) {
+    w.s.n = w.left > 0 ? w.s.tiles : 0;
+    w.left -= 1;
+  } else {
+    w.left -= skip;
+    w.s.n = static_cast<int>(max(0ll, min(static_cast<long long>(w.s.tiles - w.s.tile), w.left)));
+    w.left -= w.s.n;
+  }
+}
 // The next segment of a warp's walk (every lane does the same); s.n = 0 at the end of the share.
 template <int N>
-__device__ __forceinline__ void tree_next(const Kv4Args& a, TreeWalk& w) {
-  w.left -= a.whole_tiles ? 1 : w.s.n;
+__device__ __forceinline__ void tree_next(const Kv4Args& a, const TreeCtrl<N>* ctl, TreeWalk& w) {
   w.s.n = 0;
   if (w.left <= 0) return;
   w.s.tile = 0;
@@ -240,7 +258,7 @@ __device__ __forceinline__ void tree_next(const Kv4Args& a, TreeWalk& w) {
       w.s.tiles = tree_tiles(w.s.req);
     }
   }
-  w.s.n = a.whole_tiles ? w.s.tiles : static_cast<int>(min(static_cast<long long>(w.s.tiles), w.left));
+  tree_take(a, w, ctl->extra);
 }
 template <int N>
 __device__ __forceinline__ TreeWalk tree_walk(const Kv4Args& a, const TreeCtrl<N>* ctl) {
@@ -248,23 +266,26 @@ __device__ __forceinline__ TreeWalk tree_walk(const Kv4Args& a, const TreeCtrl<N
   w.s = ctl->start;
   w.blocks = tree_blocks<N>(a, w.s.req);
   w.left = ctl->last - ctl->first;
-  w.s.n = a.whole_tiles ? w.s.tiles : static_cast<int>(min(static_cast<long long>(w.s.tiles - w.s.tile), w.left));
+  tree_take(a, w, ctl->skip);
   return w;
 }
 
-// The CTA's share [first, last) of the line of `total` tiles (units, when they are not split); fills ctl->start.
-// Returns the number of CTAs that have work.
+// The CTA's share [first, last) of the line of `total`; fills ctl->start.  Returns the number of CTAs that have work.
 template <int N>
 __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   ReqShape s{0, 0, 0, 0};
-  int per = 1;
+  int per = 1, extra = 0;
+  long long units = 0;  // of the thread's requests
   auto cost = [&](int r) -> long long {
     if (r >= a.b) return 0;
     s = kv4_request(a, r);
-    per = a.whole_tiles ? 1 : tree_tiles(s);
-    return static_cast<long long>(tree_blocks<N>(a, s)) * a.hk * per;
+    per = a.whole_tiles ? 1 : tree_tiles(s) + extra;
+    const long long u = static_cast<long long>(tree_blocks<N>(a, s)) * a.hk;
+    units += u;
+    return u * per;
   };
+  // inclusive scan over the block; ctl->sum keeps the warps' sums until the next barrier
   auto scan = [&](long long x) {
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -277,11 +298,23 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
     for (int w = 0; w < warp; ++w) x += ctl->sum[w];
     return x;
   };
+  auto all_sum = [&]() {
+    long long x = 0;
+#pragma unroll 1
+    for (int w = 0; w < kTrThreads / 32; ++w) x += ctl->sum[w];
+    return x;
+  };
   long long mine = 0, tiles = 0;
   for (int r = tid; r < a.b; r += kTrThreads) mine += tiles = cost(r);
-  long long inc = scan(mine), total = 0;
-#pragma unroll 1
-  for (int w = 0; w < kTrThreads / 32; ++w) total += ctl->sum[w];
+  long long inc = scan(mine), total = all_sum();
+  extra = tree_extra(a, total);
+  if (extra > 0) {  // the line again, with what each unit counts more
+    per += extra;
+    tiles += extra * units;  // (up to one request a thread: the scan below is the line itself)
+    __syncthreads();
+    inc = scan(mine + extra * units);
+    total = all_sum();
+  }
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   if (static_cast<int>(blockIdx.x) >= n) {
     __syncthreads();
@@ -295,22 +328,17 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
       __syncthreads();
       tiles = cost(r0 + tid);
       inc = scan(tiles) + base;
-      all = base;
-#pragma unroll 1
-      for (int w = 0; w < kTrThreads / 32; ++w) all += ctl->sum[w];
+      all = base + all_sum();
     }
     if (first >= inc - tiles && first < inc) {
       const long long off = first - (inc - tiles);
       // (64-bit divisions take about 100 instructions)
       const int u = off <= 0x7fffffffll ? static_cast<int>(off) / per : static_cast<int>(off / per);
       const int block = u / a.hk;
-      ctl->start = TreeSeg{r0 + tid,
-                           u - block * a.hk,
-                           block,
-                           a.whole_tiles ? 0 : static_cast<int>(off - static_cast<long long>(u) * per),
-                           0,
-                           tree_tiles(s),
-                           s};
+      const int at = a.whole_tiles ? 0 : static_cast<int>(off - static_cast<long long>(u) * per);
+      ctl->start = TreeSeg{r0 + tid, u - block * a.hk, block, max(0, at - extra), 0, tree_tiles(s), s};
+      ctl->skip = max(0, extra - at);
+      ctl->extra = extra;
       ctl->total = total;
       ctl->first = first;
       ctl->last = last;
@@ -524,7 +552,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           key = next;
           id = id_next;
         }
-        if (ok) tree_next<N>(a, w);
+        if (ok) tree_next<N>(a, ctl, w);
       }
       if (ok) ok = t < G::kStages || wait(ctl->ring_empty[t % G::kStages], t / G::kStages - 1);
       if (ok && !EXATTN_INJECT_STALL) {  // (a test build delivers nothing: the first waits run out)
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[u & 1]));
         if (w.s.n == 0) break;
-        tree_next<N>(a, w);
+        tree_next<N>(a, ctl, w);
       }
     }
   } else if (warp >= 8) {
@@ -936,9 +964,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         }
       }
       if (threadIdx.x == 0 && rows.seg.tile == 0 && !whole) {
-        // the unit begins here and ends in a later CTA: x is its last tile on the line
-        const long long left = ctl->last - ctl->first - t + n;  // tiles of the share from the segment's first on
-        const long long x = ctl->last - left + rows.seg.tiles - 1;
+        // the unit begins here and ends in a later CTA: x is its last tile on the line (its first n end the share)
+        const long long x = ctl->last - n + rows.seg.tiles - 1;
         const int row0 = rows.seg.block * N;
         a.desc[blockIdx.x] = merge_desc(rows.seg.req, rows.seg.head, row0, min(N, rows.seg.req.q_len * a.group - row0),
                                         2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0),
