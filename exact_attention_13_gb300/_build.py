@@ -13,7 +13,7 @@ SOURCES = [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "kv_api.cu"),
            os.path.join(CSRC, "tree_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "fa_fwd_kernel.cuh", "fa_quant.cuh", "fa_bwd_kernel.cuh", "sm103_ptx.cuh", "rope.cuh",
-    "page_plan.cuh", "kv4_cache.cuh", "kv4_attn.cuh", "kv4_chunk.cuh", "kv_host.cuh", "kv4_tree.cuh",
+    "page_plan.cuh", "kv4_cache.cuh", "kv4_attn.cuh", "kv4_chunk.cuh", "kv_host.cuh", "kv4_launch.cuh", "kv4_tree.cuh",
     "tree_plan.cuh", "block_scan.cuh")] + [
     os.path.join(ROOT, "include", "exact_attention.h")]
 

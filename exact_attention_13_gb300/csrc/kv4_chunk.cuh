@@ -268,7 +268,7 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   return n;
 }
 
-template <int D>
+template <int D, bool TREE = false>
 __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args a) {
   using G = ChunkGeo<D>;
   extern __shared__ __align__(1024) uint8_t ch_smem[];
@@ -531,13 +531,21 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       if (h == 0 || two) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
         float c;   // factor of the row's scores
-        int sees;  // keys that the row sees
+        int sees;  // keys that the row sees, one behind the other
+        const uint32_t* bits = nullptr;  // TREE: the tree's nodes that it sees
         {
           const int row = h * 128 + r_tile, urow = w->s.block * kChRows + row;
           const bool live = row < walk_rows(a, w);
           const int qi = urow / a.group, qg = urow - qi * a.group;
           sees = w->s.req.keys;
-          if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.queries + qi + 1));
+          if constexpr (TREE) {
+            if (live) {
+              sees = max(0, sees - w->s.req.queries);
+              bits = a.tree + static_cast<size_t>(w->s.req.q0 + qi) * a.words;
+            }
+          } else {
+            if (a.causal && live) sees = min(sees, max(0, sees - w->s.req.queries + qi + 1));
+          }
           // ---- the warp's 32 query rows, scaled into [1, 2): kRow lanes take 16 bytes each of a row
           constexpr int kRow = D / 8, kRowsIt = 32 / kRow;
           const long long mine = live ? static_cast<long long>(w->s.req.q0 + qi) * a.q_row +
@@ -604,6 +612,13 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           auto seen16 = [&](int g) {
             const int here = lim - 16 * g;
             unsigned seen = here >= 16 ? 0xffffu : here <= 0 ? 0u : (1u << here) - 1u;
+            if (TREE && here < 16 && bits) {  // and nodes node .. node + 15, as far as there are keys and bits
+              const int key = (w->s.tile + j) * kChKeys + 16 * g, node = key - (w->s.req.keys - w->s.req.queries);
+              const int word = node >> 5, keys = min(max(w->s.req.keys - key, 0), 16);
+              const uint32_t lo = word >= 0 && word < a.words ? bits[word] : 0u;
+              const uint32_t hi = word >= -1 && word + 1 < a.words ? bits[word + 1] : 0u;
+              seen |= __funnelshift_r(lo, hi, node & 31) & ((1u << keys) - 1u);
+            }
             if (holes) {
               const int key = (w->s.tile + j) * kChKeys + 16 * g;
               const int* ids = a.table + static_cast<size_t>(w->s.r) * a.width;

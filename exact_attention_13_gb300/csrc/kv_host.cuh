@@ -8,7 +8,6 @@
 #include <cstdint>
 
 #include "../../include/exact_attention.h"
-#include "kv4_attn.cuh"
 
 namespace exattn {
 
@@ -79,17 +78,6 @@ int cache_checks(const void* cache, int pages, int heads, int page, int d) {
   if ((d != 64 && d != 128) || !page_size_ok(page) || heads > 65535) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(pages) * page > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
   return aligned(cache, 16) ? FA_OK : FA_ERR_MISALIGNED;
-}
-
-template <int D, int R>
-int launch_merge(const Kv4Args& a, int ctas, cudaStream_t s) {
-  // Few units (at most one for eight CTAs): each may span many CTAs, and rows get blocks of their own
-  // (4 units of 8 rows in 114 parts each: 3.9 us instead of 7 with blocks for all CTAs; 128 units of 15
-  // rows: 2.4 us more than the other way).  Else eight rows a block, 64 of a prompt chunk (135 us
-  // for the whole call of 4 chunks of 512 tokens; 139 with eight).
-  const bool few = static_cast<long long>(a.b) * a.hk <= ctas / 8;
-  const dim3 grid = few ? dim3(ctas / 8, R > 32 ? 32 : R) : dim3(ctas, R > 32 ? R / 64 : R / 8);
-  return launch_early(kv4_merge_kernel<D, R>, grid, kMergeThreads, 0, s, a, few ? ctas : 0);
 }
 
 }  // namespace

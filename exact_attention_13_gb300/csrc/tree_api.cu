@@ -9,6 +9,7 @@
 #include <initializer_list>
 
 #include "../../include/exact_attention.h"
+#include "kv4_launch.cuh"
 #include "kv4_tree.cuh"
 #include "kv_host.cuh"
 #include "tree_plan.cuh"
@@ -17,19 +18,23 @@ namespace exattn {
 
 namespace {
 
-// Query rows that share a unit: the smallest of 16, 32 and 64 that hold the rows of one key head.
-int tree_rows(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// The kernel for `rows` query rows of a key head: 8 or 16 (kv4_attn.cuh, every value widened in registers), units of 32
+// or 64 (kv4_tree.cuh) or of 256 (kv4_chunk.cuh).  TABLE
+int tree_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 64 : 256; }
 
 size_t tree_workspace(int n, int d) {
+  if (n <= 16) return kv4_workspace(n / 8, d);
+  if (n == 256) return kv4_workspace(0, d);
   const size_t rows = static_cast<size_t>(2) * kSms * n;
   return (rows * (d * 4 + 8) + kSms * 16 + 255) / 256 * 256;
 }
 
 // Tables of at most this many tiles: units are not split, which saves the merge kernel and the workspace.
 constexpr int kTreeWholeTiles = 4;
-int tree_whole_tiles(int page, int width) {
+int tree_whole_tiles(int n, int d, int page, int width) {
+  if (n <= 16) return dec_whole_tiles(d, n / 8, page, width);
   const long long tiles = (static_cast<long long>(page) * width + kTrKeys - 1) / kTrKeys;
-  return tiles <= kTreeWholeTiles ? static_cast<int>(tiles) : 0;
+  return n < 256 && tiles <= kTreeWholeTiles ? static_cast<int>(tiles) : 0;
 }
 
 template <int D, int N>
@@ -60,9 +65,11 @@ int launch_tree(Kv4Args& a, void* workspace, cudaStream_t s) {
 
 template <int D>
 int launch_tree_rows(Kv4Args& a, int n, void* workspace, cudaStream_t s) {
-  return n == 16   ? launch_tree<D, 16>(a, workspace, s)
-         : n == 32 ? launch_tree<D, 32>(a, workspace, s)
-                   : launch_tree<D, 64>(a, workspace, s);
+  return n == 8     ? launch_decode<D, 1, true>(a, workspace, s)
+         : n == 16  ? launch_decode<D, 2, true>(a, workspace, s)
+         : n == 32  ? launch_tree<D, 32>(a, workspace, s)
+         : n == 64  ? launch_tree<D, 64>(a, workspace, s)
+                    : launch_chunk<D, true>(a, workspace, s);
 }
 
 }  // namespace
@@ -127,7 +134,7 @@ size_t fa_kv4_tree_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q, int pa
   if (Hq < 1 || Hkv < 1 || Hq % Hkv || max_q < 1 || (d != 64 && d != 128)) return 0;
   if (!page_size_ok(page_size) || table_width < 1 || !width_ok(table_width, page_size)) return 0;
   const int n = tree_rows(static_cast<long long>(max_q) * (Hq / Hkv));
-  return tree_whole_tiles(page_size, table_width) ? 0 : tree_workspace(n, d);
+  return tree_whole_tiles(n, d, page_size, table_width) ? 0 : tree_workspace(n, d);
 }
 
 int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stride, const void* cache, int num_pages,
@@ -144,7 +151,7 @@ int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stri
   if (int rc = cache_checks(cache, num_pages, Hkv, page_size, d)) return rc;
   if (static_cast<long long>(T) * Hq > 0x3fffffffll || !width_ok(table_width, page_size) || words > kTreeWords)
     return FA_ERR_UNSUPPORTED;
-  const int n = tree_rows(static_cast<long long>(max_q) * (Hq / Hkv)), whole = tree_whole_tiles(page_size, table_width);
+  const int n = tree_rows(static_cast<long long>(max_q) * (Hq / Hkv)), whole = tree_whole_tiles(n, d, page_size, table_width);
   if (!whole && (!workspace || workspace_bytes < tree_workspace(n, d))) return FA_ERR_INVALID_ARG;
   if (q_row_stride % 8 || q_head_stride % 8 || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4) || !aligned(seen, 4) ||
@@ -176,7 +183,7 @@ int fa_kv4_tree_fwd(const void* q, long long q_row_stride, long long q_head_stri
   a.tree = seen;
   a.words = words;
   a.status = dev_status;
-  if (!a.status) {
+  if (!a.status && n > 16) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxKvDevices) return FA_ERR_CUDA;
     a.status = library_status_ptr(dev);
