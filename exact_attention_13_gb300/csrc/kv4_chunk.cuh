@@ -102,6 +102,7 @@ struct ChunkCtrl {
   int abort;
   long long sum[kChThreads / 32];
   long long total, first, last;
+  int extra, skip;  // what a unit counts more on the line, and how much of that the share begins with
   ChunkSegment start;
   ChunkWalk walk[kChThreads / 32];
 };
@@ -130,18 +131,19 @@ __device__ __forceinline__ void walk_begin(const Kv4Args& a, ChunkWalk* w, const
   if (threadIdx.x % 32 == 0) {
     w->s = ctl->start;
     w->blocks = chunk_blocks(a, w->s.req);
-    w->left = ctl->last - ctl->first;
+    w->left = ctl->last - ctl->first - ctl->skip;
     w->s.n = static_cast<int>(min(static_cast<long long>(w->s.tiles - w->s.tile), w->left));
   }
   __syncwarp();
 }
 
 // To the next segment; false at the end of the share.
-__device__ __forceinline__ bool walk_next(const Kv4Args& a, ChunkWalk* w) {
+__device__ __forceinline__ bool walk_next(const Kv4Args& a, ChunkWalk* w, const ChunkCtrl* ctl) {
   __syncwarp();
   if (threadIdx.x % 32 == 0) {
     w->left -= w->s.n;
     if (w->left > 0) {
+      w->left -= ctl->extra;
       w->s.tile = 0;
       if (++w->s.block == w->blocks) {
         w->s.block = 0;
@@ -169,11 +171,21 @@ __device__ __forceinline__ int walk_rows(const Kv4Args& a, const ChunkWalk* w) {
 
 // The CTA's share [first, last) of the line of `total` tiles; fills ctl->start.  Returns the number
 // of CTAs that have work.
+//
+// Trees of drafted tokens (TREE): a unit counts kChTreeExtra tiles more than it has, at its front, where the CTAs have
+// many tiles each: queries and outputs take the time of that many.  A share that ends among them leaves the
+// whole unit to the next one.  64 requests of 500 to 8192 keys, 8 key heads, d 128, 256 rows each: 401 us with 0, 355
+// with 2, 317 with 4, 299 with 7, 309 with 12; of 16 to 2048 keys 216, 169, 139, 122, 132; with 128 rows 5 is 1 % better
+// than 7 on the first and 7 % worse on the second.
+constexpr int kChTreeExtra = 7;
+template <bool TREE>
 __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, long long& total,
                                               long long& first, long long& last) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ReqShape s{0, 0, 0, 0};
   long long per_head = 0;  // tiles of one key head of the thread's request
+  int extra = 0;
+  long long blocks_seen = 0;  // of the thread's requests
   auto lane_request = [&](int l) {
     return ReqShape{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
                     __shfl_sync(0xffffffffu, s.keys, l), __shfl_sync(0xffffffffu, s.queries, l)};
@@ -195,6 +207,10 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
       for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == l) per_head = sum;
     }
+    if constexpr (TREE) {
+      per_head += static_cast<long long>(extra) * blocks;
+      blocks_seen += blocks;
+    }
     return per_head * a.hk;
   };
   auto scan = [&](long long x) {
@@ -213,6 +229,18 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   long long inc = scan(mine);
   total = 0;
   for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
+  if constexpr (TREE) {
+    if (total >= 16ll * gridDim.x) {  // the line again (up to one request a thread; more: below)
+      extra = kChTreeExtra;
+      const int blocks = chunk_blocks(a, s);
+      per_head += static_cast<long long>(extra) * blocks;
+      tiles += static_cast<long long>(extra) * blocks * a.hk;
+      __syncthreads();
+      inc = scan(mine + extra * blocks_seen * a.hk);
+      total = 0;
+      for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
+    }
+  }
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   if (static_cast<int>(blockIdx.x) >= n) return n;
   first = share_begin(total, n, blockIdx.x);
@@ -237,7 +265,7 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
       off -= head * head_tiles;
       // the block that holds tile `off` of the head, 32 blocks at a time
       for (int b0 = 0;; b0 += 32) {
-        const int own = b0 + lane < chunk_blocks(a, x) ? chunk_tiles(a, x, b0 + lane) : 0;
+        const int own = b0 + lane < chunk_blocks(a, x) ? chunk_tiles(a, x, b0 + lane) + extra : 0;
         long long upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -252,8 +280,11 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
             c.req = x;
             c.head = head;
             c.block = b0 + lane;
-            c.tile = static_cast<int>(off - (upto - own));
-            c.tiles = own;
+            const int at = static_cast<int>(off - (upto - own));
+            c.tile = max(0, at - extra);
+            c.tiles = own - extra;
+            ctl->extra = extra;
+            ctl->skip = max(0, extra - at);
           }
           break;
         }
@@ -282,7 +313,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
   grid_launch_dependents();
   {
     long long total, first, last;
-    const int n_cta = chunk_my_range(a, ctl, total, first, last);
+    const int n_cta = chunk_my_range<TREE>(a, ctl, total, first, last);
     if (static_cast<int>(blockIdx.x) >= n_cta) {
       if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
       return;
@@ -386,7 +417,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         ok = step(h, j == 0, j + 1 < n);
         if (h == (two ? 1 : 0)) t += 2;
       }
-    } while (ok && walk_next(a, w));
+    } while (ok && walk_next(a, w, ctl));
     // nothing this warp issued may still run when the TMEM is released
     __syncwarp();
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
@@ -456,12 +487,12 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       }
     };
     // (test builds that inject a stall widen nothing: the first wait for a tile runs out)
-    const long long tiles = EXATTN_INJECT_STALL ? 0 : ctl->last - ctl->first;
+    bool more = !EXATTN_INJECT_STALL;
     fetch_ids();
     // One copy of the code for the first loads and the later ones: the roles' loops together have to
     // stay in the instruction cache (a second copy of loads and conversions cost 8 %).
 #pragma unroll 1
-    for (long long i = -1; i < tiles; ++i) {
+    for (long long i = -1;; ++i) {
       if (i >= 0) {
         const long long t = 2 * i + (values ? 1 : 0);
         const int slot = static_cast<int>(t % G::kSlots);
@@ -491,19 +522,20 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->kv_full[slot]));
       }
-      if (i + 1 < tiles) {
-        load();
-        if (--tiles_left > 0) {
-          key += kChKeys;
-        } else if (walk_next(a, w)) {
-          key = w->s.tile * kChKeys + row_w;
-          tiles_left = w->s.n;
-          keys = w->s.req.keys;
-          ids = a.table + static_cast<size_t>(w->s.r) * a.width;
-          head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
-        }
-        if (i + 2 < tiles) fetch_ids();
+      if (!more) break;
+      load();
+      if (--tiles_left > 0) {
+        key += kChKeys;
+      } else {
+        more = walk_next(a, w, ctl);
+        if (!more) continue;
+        key = w->s.tile * kChKeys + row_w;
+        tiles_left = w->s.n;
+        keys = w->s.req.keys;
+        ids = a.table + static_cast<size_t>(w->s.r) * a.width;
+        head = a.cache + static_cast<size_t>(w->s.head) * 2 * block_bytes;
       }
+      fetch_ids();
     }
   } else {
     regs_inc<kChSoftmaxRegs>();
@@ -774,7 +806,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         t += 2 * n;
       }
       ++unit_no;
-    } while (walk_next(a, w));
+    } while (walk_next(a, w, ctl));
   }
 
   __syncthreads();

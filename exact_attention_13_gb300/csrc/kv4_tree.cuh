@@ -1,14 +1,14 @@
 // kv4_tree.cuh -- attention of trees of drafted tokens over the paged 4-bit cache.
 //
 // The operation of kv4_attn.cuh with another mask: a node sees the keys before its request's tree, and of the
-// tree's keys those whose bit is set in its row of `seen`.  Units of N = 16, 32 or 64 query rows (one key
-// head of one request, rows ordered by node, then by head of the group).
+// tree's keys those whose bit is set in its row of `seen`.  Units of N = 32 or 64 query rows (one key head of
+// one request, rows ordered by node, then by head of the group).
 //
 // Both products take the widened cache as the 128-row operand of tcgen05.mma, out of tensor memory:
 //     S^T [128 keys x N] = K [128 x d] Q^T,      O^T [d x N] += V^T [d x 128 keys] P^T
 // so the tensor core does N products a cached value (query rows as the 128-row operand: 128, mostly padding),
 // and the widened tiles, four times the cache's bytes, go from registers to tensor memory without
-// a write and a read of shared memory.  What is left there a tile is the codes (written once by the bulk copies, read
+// a write and a read of shared memory.  What is left there a tile is the codes (written once by asynchronous copies, read
 // once), Q^T (N x d, read by the product) and P^T (128 x N).
 //
 // Layouts.  An A operand in tensor memory is one lane a row and 32 bits of two neighbouring contraction indices a
@@ -35,6 +35,18 @@
 //   warps 17, 18 copy codes and scales of K and of V into a ring of tiles
 //   warp  19     queries, masks and places of the rows of the next unit, while this one runs
 // The split over CTAs and the merge of units that cross them are those of kv4_attn.cuh.
+//
+// Copies go by 16 bytes a lane: a bulk copy takes its issuer about 90 cycles whatever its size, and a tile has 32
+// pieces.  The two issue orders that would overlap more (PV and S from warps of their own; three steps in
+// flight with 24 warps) were not faster.
+//
+// Measured (64 requests of 4096 keys, 8 key heads, d 128: 302 MB of cache, 44 us at 6.8 TB/s): 120 us for 32 rows of a
+// key head, 148 us for 64; 1800 to 2050 cycles a tile of 128 keys, of which the copies are
+// 800.  Bound by neither memory nor the tensor core (0.37, 0.25 of their rates with 32 and 64 rows) but by the hand-offs
+// copy - widen - S - softmax - PV of the tiles and, three to four times a CTA, of the units: with copies, widening,
+// exponentials and MMAs all left out the waits and the units' work alone take 71 and 97 us.  What was worth the
+// most on the way (64 rows, 269 us at first): masks by node in shared memory instead of by row (a word a
+// row and tile before), code small enough for the instruction cache, one exponent for all rows' queries.
 //
 // Every mbarrier wait is bounded in time; one that runs out sets the CTA's abort flag and the status word, and
 // all roles leave.
@@ -68,12 +80,12 @@ struct TreeGeo {
   static constexpr int kStages = 8;
   static constexpr int kQBytes = N * D * 2;             // boxes of 64 dims, 128 bytes a row
   static constexpr int kPBytes = 128 * 128;             // a row of 128 bytes a key
-  static constexpr int kCols = N < 32 ? 32 : N;         // columns between accumulators
-  static constexpr int kO = 2 * kCols, kK = 3 * kCols, kVt = kK + 2 * (D / 2);
+  static constexpr int kO = 2 * N, kK = 3 * N, kVt = kK + 2 * (D / 2);  // columns behind the two S
   static_assert(kVt + 2 * 64 <= 512, "tensor memory");
   static constexpr uint32_t kIdescS = instr_desc(128, N, 0, false, false);
   static constexpr uint32_t kIdescPV = instr_desc(128, N, 0, false, true);
   static constexpr int kHalf = N / 2;                   // rows of a softmax thread
+  static_assert(N == 32 || N == 64, "rows of a unit");
 };
 
 // A share of a unit: tiles [tile, tile + n) of its `tiles`; n = 0: there are no more.
@@ -88,13 +100,11 @@ struct TreeWalk {
 };
 
 template <int N>
-constexpr int kRowWords = (N + 31) / 32;
-template <int N>
 struct TreeRows {          // of one unit, written by the query warps
   TreeSeg seg;
   float c;                 // factor of the scores
   int out[N];              // row of o and lse, -1: padding
-  uint32_t seen[kTreeNodes][kRowWords<N>];  // rows that see a node
+  uint32_t seen[kTreeNodes][N / 32];  // rows that see a node
 };
 
 template <int N>
@@ -169,7 +179,7 @@ __device__ __forceinline__ void bar_wait(int id, int threads) {
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
   static_assert(N == 8 || N == 16 || N == 32, "columns of one load");
-  if constexpr (N == 8)
+  if constexpr (N == 8)  // (maxima of eight rows at a time)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : EXATTN_R4(r, 0), EXATTN_R4(r, 4)
                  : "r"(taddr));
@@ -182,10 +192,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
-  if constexpr (N == 8)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 EXATTN_W4(r, 0), EXATTN_W4(r, 4)
-                 : "memory");
+  static_assert(N == 16 || N == 32, "columns of one store");
   if constexpr (N == 16) tmem_st16(taddr, r);
   if constexpr (N == 32) tmem_st32(taddr, r);
 }
@@ -199,9 +206,7 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
 // 16 lanes from the address's on: r[2 n + i] from row lane / 4 + 8 i, column 4 n + lane % 4.
 template <int N>
 __device__ __forceinline__ void tmem_ld_16x128b(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 4 || N == 8 || N == 16, "registers of one load");
-  if constexpr (N == 4)
-    asm volatile("tcgen05.ld.sync.aligned.16x128b.x2.b32 {%0, %1, %2, %3}, [%4];" : EXATTN_R4(r, 0) : "r"(taddr));
+  static_assert(N == 8 || N == 16, "registers of one load");
   if constexpr (N == 8)
     asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : EXATTN_R4(r, 0), EXATTN_R4(r, 4)
@@ -224,7 +229,7 @@ __device__ __forceinline__ int tree_tiles(const ReqShape& s) { return max(1, (s.
 
 // On the line of tiles that the CTAs share a unit counts `extra` more than it has, at its front: queries, first
 // reference, sums and outputs take the time of that many tiles (64 requests of 500 to 8192 keys, up to 64 rows: 187 us with
-// 0, XXX with 4).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
+// 0, 160 with 4).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
 // have few tiles each, spreading them is worth more.  Units that are not split count 1.
 __device__ __forceinline__ int tree_extra(const Kv4Args& a, long long tiles) {
   return !a.whole_tiles && tiles >= 16ll * gridDim.x ? 4 : 0;
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
         --left_s;
         if (elect_one()) {
           const uint64_t qd = q_desc + (u_s & 1) * (G::kQBytes >> 4);
-          const uint32_t k = tmem + G::kK + (t & 1) * (D / 2), s = tmem + (t & 1) * G::kCols;
+          const uint32_t k = tmem + G::kK + (t & 1) * (D / 2), s = tmem + (t & 1) * N;
           mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 0u, k, qd);
           if constexpr (D == 128)
             mma_chain_ts_off<4, 0, 2, 8, 16, 24, 32, 40, 48, 56>(s, G::kIdescS, 1u, k + 32, qd + (N * 128 >> 4));
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       // ============================================================ queries, masks and places of a unit's rows
       // The rows come as they are, by 16 bytes to where the row's operand lies, and are turned into it in place.
       TreeWalk w = tree_walk<N>(a, ctl);
-      constexpr int kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = (N + 31) / 32;
+      constexpr int kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = N / 32;
       for (int u = 0;; ++u) {
         if (u >= 2 && !wait(ctl->q_empty[u & 1], (u >> 1) - 1)) break;
         TreeRows<N>& rows = ctl->rows[u & 1];
@@ -580,9 +585,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           for (int x = 0; x < kOffsets; ++x) {
             const int row = x * 32 + lane, at = w.s.block * N + row;
             const int node = at / a.group, head = w.s.head * a.group + at - node * a.group, token = w.s.req.q0 + node;
-            const bool live = row < N && at < w.s.req.q_len * a.group;
+            const bool live = at < w.s.req.q_len * a.group;
             from[x] = live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1;
-            if (row < N) rows.out[row] = live ? token * a.hq + head : -1;
+            rows.out[row] = live ? token * a.hq + head : -1;
             // the lane's row of bits, a word at a time, becomes a bit of each node's word
 #pragma unroll 1
             for (int y = 0; 32 * y < min(w.s.req.queries, 32 * a.words); ++y) {
@@ -632,21 +637,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
           for (int row0 = 0; row0 < N; row0 += 32 / kLanes) {
             const int row = row0 + lane / kLanes;
             uint32_t h[4][4];
-            if (row < N) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float f[8];
-                unpack_bf16x8(*reinterpret_cast<const uint4*>(q + piece_at(row, x * kLanes + part)), f);
+            for (int x = 0; x < 4; ++x) {
+              float f[8];
+              unpack_bf16x8(*reinterpret_cast<const uint4*>(q + piece_at(row, x * kLanes + part)), f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
-              }
+              for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
             }
             __syncwarp();
-            if (row < N) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                st_shared_v4(smem_u32(q) + piece_at(row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
-            }
+            for (int e = 0; e < 4; ++e)
+              st_shared_v4(smem_u32(q) + piece_at(row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
           }
           fence_proxy_async_smem();  // the MMAs read the queries through the async proxy
         }
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       for (int j = 0; j < n; ++j, ++t) {
         ok = ok && wait(ctl->s_full[t & 1], t >> 1);
         tc_fence_after();
-        const uint32_t t_here = t_s + (t & 1) * G::kCols;
+        const uint32_t t_here = t_s + (t & 1) * N;
         float x[H];
         auto scores = [&]() {
           uint32_t r[H];
