@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       if (h == 0 || two) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
         float c;   // factor of the row's scores
+        float far = 0.f;  // TREE: not 0: their factor where they get it ahead of the softmax
         int sees;  // keys that the row sees, one behind the other
         const uint32_t* bits = nullptr;  // TREE: the tree's nodes that it sees
         {
@@ -607,6 +608,12 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
                          pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
                          pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
           }
+          // scaled queries are below 2 and keys up to 448 * 6: where scores may pass 2^26, what m is rounded by would
+          // leave f16's range in a fused multiplication and difference
+          if (TREE && __any_sync(0xffffffffu, c * (2.f * 448.f * 6.f * D) > 0x1p26f)) {
+            far = c;
+            c = 1.f;
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[h]));
@@ -631,6 +638,18 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           if (frees) {
             mbar_arrive(smem_u32(&ctl->kv_empty[t % G::kSlots]));
             if (j > 0) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
+          }
+          if (TREE && __any_sync(0xffffffffu, far != 0.f)) {
+            uint32_t r[32];
+#pragma unroll 1
+            for (int cb = 0; cb < 128; cb += 32) {
+              tmem_ld32(t_s + cb, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), far));
+              tmem_st32(t_s + cb, r);
+            }
+            tmem_st_wait();
           }
           // Twice over the row's scores, 64 at a time: the maximum, then the probabilities.  (All 128
           // in registers as one unrolled body did not fit the instruction cache beside the other

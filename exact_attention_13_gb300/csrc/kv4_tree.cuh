@@ -40,13 +40,14 @@
 // pieces.  The two issue orders that would overlap more (PV and S from warps of their own; three steps in
 // flight with 24 warps) were not faster.
 //
-// Measured (64 requests of 4096 keys, 8 key heads, d 128: 302 MB of cache, 44 us at 6.8 TB/s): 120 us for 32 rows of a
-// key head, 148 us for 64; 1800 to 2050 cycles a tile of 128 keys, of which the copies are
-// 800.  Bound by neither memory nor the tensor core (0.37, 0.25 of their rates with 32 and 64 rows) but by the hand-offs
-// copy - widen - S - softmax - PV of the tiles and, three to four times a CTA, of the units: with copies, widening,
-// exponentials and MMAs all left out the waits and the units' work alone take 71 and 97 us.  What was worth the
-// most on the way (64 rows, 269 us at first): masks by node in shared memory instead of by row (a word a
-// row and tile before), code small enough for the instruction cache, one exponent for all rows' queries.
+// Measured (64 requests of 4096 keys, 8 key heads, d 128: 302 MB of cache, 44 us at 6.8 TB/s): 123 us for 32 rows of a
+// key head, 141 us for 64; 1800 to 2000 cycles a tile of 128 keys, of which the copies are 800.  Bound by neither
+// memory (0.36 and 0.31 of its rate) nor the tensor core (0.15 and 0.25) but by the hand-offs copy - widen - S -
+// softmax - PV of the tiles and, three to four times a CTA, of the units: with copies, widening, exponentials and
+// MMAs all left out the waits and the units' work alone took 71 and 97 us.  What was worth the most on the way (64
+// rows, 269 us at first): masks by node in shared memory instead of by row (a word a row and tile before), one
+// exponent for all rows' queries, code small enough for the instruction cache (its placement alone moves the 32
+// rows between 123 and 131 us).
 //
 // Every mbarrier wait is bounded in time; one that runs out sets the CTA's abort flag and the status word, and
 // all roles leave.
@@ -103,6 +104,9 @@ template <int N>
 struct TreeRows {          // of one unit, written by the query warps
   TreeSeg seg;
   float c;                 // factor of the scores
+  int apart;               // rows have factors of their own, which every tile's scores get first
+  float row_c[N];
+  float most[N], down[N];  // of the queries: the rows' largest values (the first unit's), what they are multiplied by
   int out[N];              // row of o and lse, -1: padding
   uint32_t seen[kTreeNodes][N / 32];  // rows that see a node
 };
@@ -192,7 +196,11 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32, "columns of one store");
+  static_assert(N == 8 || N == 16 || N == 32, "columns of one store");
+  if constexpr (N == 8)  // (scores of rows apart)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 EXATTN_W4(r, 0), EXATTN_W4(r, 4)
+                 : "memory");
   if constexpr (N == 16) tmem_st16(taddr, r);
   if constexpr (N == 32) tmem_st32(taddr, r);
 }
@@ -229,10 +237,11 @@ __device__ __forceinline__ int tree_tiles(const ReqShape& s) { return max(1, (s.
 
 // On the line of tiles that the CTAs share a unit counts `extra` more than it has, at its front: queries, first
 // reference, sums and outputs take the time of that many tiles (64 requests of 500 to 8192 keys, up to 64 rows: 187 us with
-// 0, 160 with 4).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
+// 0, 160 with 4 or 6, 166 with 8; of 16 to 2048 keys 75 with 4, 67 with 6, 68 with 8; 32 rows: 47.5, 49.4, 51.3).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
 // have few tiles each, spreading them is worth more.  Units that are not split count 1.
+template <int N>
 __device__ __forceinline__ int tree_extra(const Kv4Args& a, long long tiles) {
-  return !a.whole_tiles && tiles >= 16ll * gridDim.x ? 4 : 0;
+  return !a.whole_tiles && tiles >= 16ll * gridDim.x ? (N == 64 ? 6 : 4) : 0;
 }
 // Tiles of the walk's unit that its share has, from s.tile on, after `skip` of the line in front of them.
 __device__ __forceinline__ void tree_take(const Kv4Args& a, TreeWalk& w, int skip) {
@@ -312,7 +321,7 @@ __device__ __forceinline__ int tree_my_range(const Kv4Args& a, TreeCtrl<N>* ctl)
   long long mine = 0, tiles = 0;
   for (int r = tid; r < a.b; r += kTrThreads) mine += tiles = cost(r);
   long long inc = scan(mine), total = all_sum();
-  extra = tree_extra(a, total);
+  extra = tree_extra<N>(a, total);
   if (extra > 0) {  // the line again, with what each unit counts more
     per += extra;
     tiles += extra * units;  // (up to one request a thread: the scan below is the line itself)
@@ -417,6 +426,89 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       }
     }
     return true;
+  };
+
+  // ---- a unit's queries: they come by 16 bytes to where the row's operand lies and are turned into it in place
+  constexpr int kPieces = D / 8, kRowsIt = 32 / kPieces, kLanes = D / 32;
+  auto piece_at = [&](int buffer, int row, int piece) {
+    return buffer * G::kQBytes + piece / 8 * (N * 128) + row * 128 + ((piece % 8 ^ (row & 7)) << 4);
+  };
+  auto fetch = [&](int buffer, int row0, long long at) {  // kRowsIt rows; at: the lane's row in q, -1: zeros
+    const int piece = lane % kPieces;
+    cp_async16(smem_u32(s_q) + piece_at(buffer, row0 + lane / kPieces, piece), a.q + (at < 0 ? 0 : at + piece * 8),
+               at < 0 ? 0u : 16u);
+  };
+  auto row_most = [&](int buffer, int row, int first, int step) {  // largest finite value of a row's pieces first, ...
+    __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+    for (int x = first; x < kPieces; x += step) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(s_q + piece_at(buffer, row, x));
+      const __nv_bfloat162* const v = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)  // (infinities and NaN: 0 x + |x| is NaN, and the maximum the other one)
+        top = __hmax2(top, __hfma2(v[e], __float2bfloat162_rn(0.f), __habs2(v[e])));
+    }
+    return fmaxf(__low2float(top), __high2float(top));
+  };
+  // A power of two brings the largest finite value of all rows into [2^14, 2^15), so that the softmax needs one factor
+  // for all of them.  Rows whose largest lies 2^13 below have a power of their own (f16 then holds bf16's 8 bits down to
+  // 2^-18 of any row's largest at least), and all rows' scores get their factors ahead of the softmax.  So they do
+  // where they may pass 2^26: what the reference of such a row is rounded by would leave f16's range in a
+  // fused multiplication and difference.
+  auto factors = [&](TreeRows<N>& rows, const float (&most)[N / 32]) {  // of rows lane, lane + 32
+    float amax = most[0];
+#pragma unroll
+    for (int x = 1; x < N / 32; ++x) amax = fmaxf(amax, most[x]);
+    amax = warp_max(amax);
+    const uint32_t all_ex = __float_as_uint(amax) >> 23, all_down = min(268u - all_ex, 253u);
+    constexpr float kMost = 448.f * 6.f * D;  // of a product with a vector of ones
+    bool apart = amax * a.c * kMost > 0x1p26f;
+#pragma unroll
+    for (int x = 0; x < N / 32; ++x) {
+      const uint32_t ex = __float_as_uint(most[x]) >> 23;
+      const bool own = most[x] > 0.f && ex + 13u < all_ex;
+      const uint32_t down = own ? min(268u - ex, 253u) : all_down;
+      apart |= own;
+      rows.down[x * 32 + lane] = __uint_as_float(down << 23);
+      rows.row_c[x * 32 + lane] = a.c * __uint_as_float((254u - down) << 23);
+    }
+    apart = __any_sync(0xffffffffu, apart);
+    if (lane == 0) {
+      rows.apart = apart;
+      rows.c = apart ? 1.f : a.c * __uint_as_float((254u - all_down) << 23);
+    }
+  };
+  // 32 / kLanes rows: a lane takes d/4 dims of a row, 8 of each quarter, which are four chunks of the operand
+  auto convert = [&](int buffer, const TreeRows<N>& rows, int row, bool mine) {
+    const int part = lane % kLanes;
+    uint32_t h[4][4];
+    if (mine) {
+      const float down = rows.down[row];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float f[8];
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(s_q + piece_at(buffer, row, x * kLanes + part)), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
+      }
+    }
+    __syncwarp();
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        st_shared_v4(smem_u32(s_q) + piece_at(buffer, row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
+    }
+  };
+  struct RowPlace {
+    long long from;  // in q, -1: padding
+    int token, out;
+  };
+  auto place = [&](const TreeSeg& seg, int row) {
+    const int at = seg.block * N + row, node = at / a.group;
+    const int head = seg.head * a.group + at - node * a.group, token = seg.req.q0 + node;
+    const bool live = at < seg.req.q_len * a.group;
+    return RowPlace{live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1, token,
+                    live ? token * a.hq + head : -1};
   };
 
   if (warp >= kTrMmaWarp) {
@@ -572,26 +664,28 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       cp_async_wait<0>();  // copies under way land before the CTA's shared memory goes away
     } else {
       // ============================================================ queries, masks and places of a unit's rows
-      // The rows come as they are, by 16 bytes to where the row's operand lies, and are turned into it in place.
       TreeWalk w = tree_walk<N>(a, ctl);
-      constexpr int kPieces = D / 8, kRowsIt = 32 / kPieces, kOffsets = N / 32;
+      constexpr int kOffsets = N / 32;
+      constexpr int kUnroll = N == 32 ? 2 : 1;  // (32 rows: 123 us with 2 and 131 with 1, 64 rows: 143 and 141)
       for (int u = 0;; ++u) {
+        if (u == 0) {  // (the first unit's are brought by the softmax warps)
+          tree_next<N>(a, ctl, w);
+          continue;
+        }
         if (u >= 2 && !wait(ctl->q_empty[u & 1], (u >> 1) - 1)) break;
         TreeRows<N>& rows = ctl->rows[u & 1];
         if (lane == 0) rows.seg = w.s;
         if (w.s.n > 0) {
-          long long from[kOffsets];  // of rows lane, lane + 32; -1: padding
+          long long from[kOffsets];  // of rows lane, lane + 32
 #pragma unroll
           for (int x = 0; x < kOffsets; ++x) {
-            const int row = x * 32 + lane, at = w.s.block * N + row;
-            const int node = at / a.group, head = w.s.head * a.group + at - node * a.group, token = w.s.req.q0 + node;
-            const bool live = at < w.s.req.q_len * a.group;
-            from[x] = live ? static_cast<long long>(token) * a.q_row + static_cast<long long>(head) * a.q_head : -1;
-            rows.out[row] = live ? token * a.hq + head : -1;
+            const RowPlace p = place(w.s, x * 32 + lane);
+            from[x] = p.from;
+            rows.out[x * 32 + lane] = p.out;
             // the lane's row of bits, a word at a time, becomes a bit of each node's word
 #pragma unroll 1
             for (int y = 0; 32 * y < min(w.s.req.queries, 32 * a.words); ++y) {
-              const uint32_t bits = live ? a.tree[static_cast<size_t>(token) * a.words + y] : 0u;
+              const uint32_t bits = p.out >= 0 ? a.tree[static_cast<size_t>(p.token) * a.words + y] : 0u;
               uint32_t mine = 0u;
 #pragma unroll 4
               for (int e = 0; e < 32; ++e) {
@@ -601,54 +695,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
               rows.seen[32 * y + lane][x] = mine;
             }
           }
-          uint8_t* const q = s_q + (u & 1) * G::kQBytes;
-          auto piece_at = [&](int row, int piece) {
-            return piece / 8 * (N * 128) + row * 128 + ((piece % 8 ^ (row & 7)) << 4);
-          };
 #pragma unroll 4
           for (int row0 = 0; row0 < N; row0 += kRowsIt) {
-            const int row = row0 + lane / kPieces, piece = lane % kPieces;
-            const long long at = __shfl_sync(0xffffffffu, kOffsets > 1 && row0 >= 32 ? from[kOffsets - 1] : from[0], row % 32);
-            cp_async16(smem_u32(q) + piece_at(row, piece), a.q + (at < 0 ? 0 : at + piece * 8), at < 0 ? 0u : 16u);
+            const int row = row0 + lane / kPieces;
+            fetch(u & 1, row0, __shfl_sync(0xffffffffu, kOffsets > 1 && row0 >= 32 ? from[kOffsets - 1] : from[0], row % 32));
           }
           cp_async_commit();
           cp_async_wait<0>();
           __syncwarp();
-          // One power of two for all rows brings the largest finite value into [2^14, 2^15): f16 then holds bf16's 8
-          // bits down to 2^-31 of it (2^-17 of a row's own largest, as long as that is not below 2^-14 of the
-          // unit's), and the softmax needs no factor for each row.
-          __nv_bfloat162 top = __float2bfloat162_rn(0.f);
-#pragma unroll 4
-          for (int row0 = 0; row0 < N; row0 += kRowsIt) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(q + piece_at(row0 + lane / kPieces, lane % kPieces));
-            const __nv_bfloat162* const v = reinterpret_cast<const __nv_bfloat162*>(&raw);
+          float most[kOffsets];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)  // (infinities and NaN: 0 x + |x| is NaN, and the maximum the other one)
-              top = __hmax2(top, __hfma2(v[e], __float2bfloat162_rn(0.f), __habs2(v[e])));
-          }
-          const float amax = warp_max(fmaxf(__low2float(top), __high2float(top)));
-          const uint32_t down_ex = min(268u - (__float_as_uint(amax) >> 23), 253u);
-          const float down = __uint_as_float(down_ex << 23);
-          if (lane == 0) rows.c = a.c * __uint_as_float((254u - down_ex) << 23);
-          // a lane takes d/4 dims of a row, 8 of each quarter, which are four chunks of the operand
-          constexpr int kLanes = D / 32;
-          const int part = lane % kLanes;
-#pragma unroll 1
-          for (int row0 = 0; row0 < N; row0 += 32 / kLanes) {
-            const int row = row0 + lane / kLanes;
-            uint32_t h[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float f[8];
-              unpack_bf16x8(*reinterpret_cast<const uint4*>(q + piece_at(row, x * kLanes + part)), f);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[x][e] = pack_f16x2(f[2 * e] * down, f[2 * e + 1] * down);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st_shared_v4(smem_u32(q) + piece_at(row, 4 * part + e), h[0][e], h[1][e], h[2][e], h[3][e]);
-          }
+          for (int x = 0; x < kOffsets; ++x) most[x] = row_most(u & 1, x * 32 + lane, 0, 1);
+          factors(rows, most);
+          __syncwarp();
+#pragma unroll(kUnroll)
+          for (int row0 = 0; row0 < N; row0 += 32 / kLanes) convert(u & 1, rows, row0 + lane / kLanes, true);
           fence_proxy_async_smem();  // the MMAs read the queries through the async proxy
         }
         __syncwarp();
@@ -803,6 +864,42 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
     const int bar = 1 + g;
     int t = 0, unit_no = 0;
     bool ok = true;
+    // ---- the first unit's queries, eight rows a warp: there is nothing else to do yet (64 rows, 4096 keys: 3 % of the
+    // time less than by one warp)
+    if (warp < N / 8) {
+      TreeRows<N>& rows = ctl->rows[0];
+      const TreeSeg seg = tree_walk<N>(a, ctl).s;
+      if (threadIdx.x == 0) rows.seg = seg;
+      const RowPlace p = place(seg, 8 * warp + lane % 8);
+      if (lane < 8) rows.out[8 * warp + lane] = p.out;
+#pragma unroll
+      for (int x = 0; x < 8; x += kRowsIt) fetch(0, 8 * warp + x, __shfl_sync(0xffffffffu, p.from, x + lane / kPieces));
+      cp_async_commit();
+#pragma unroll 1
+      for (int y = 0; 32 * y < min(seg.req.queries, 32 * a.words); ++y) {
+        const uint32_t bits = p.out >= 0 ? a.tree[static_cast<size_t>(p.token) * a.words + y] : 0u;
+        uint32_t mine = 0u;  // bit e: row e sees node 32 y + lane
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine |= (__shfl_sync(0xffffffffu, bits, e) >> lane & 1u) << e;
+        reinterpret_cast<uint8_t*>(rows.seen[32 * y + lane])[warp] = static_cast<uint8_t>(mine);
+      }
+      cp_async_wait<0>();
+      __syncwarp();
+      float here = row_most(0, 8 * warp + lane % 8, lane / 8, 4);
+      here = fmaxf(here, __shfl_xor_sync(0xffffffffu, here, 8));
+      here = fmaxf(here, __shfl_xor_sync(0xffffffffu, here, 16));
+      if (lane < 8) rows.most[8 * warp + lane] = here;
+      bar_wait(3, 4 * N);
+      float most[N / 32];
+#pragma unroll
+      for (int x = 0; x < N / 32; ++x) most[x] = rows.most[x * 32 + lane];
+      factors(rows, most);  // (every warp all of them)
+      __syncwarp();
+      convert(0, rows, 8 * warp + lane / kLanes, lane < 8 * kLanes);
+      fence_proxy_async_smem();
+      bar_wait(3, 4 * N);
+      if (threadIdx.x == 0) mbar_arrive(smem_u32(&ctl->q_full[0]));
+    }
     if (threadIdx.x == 0 && !a.whole_tiles) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     // The four warps of a half meet at barriers that no time limit ends, so they leave together: a warp whose wait
     // has run out goes on to the next vote.
@@ -814,7 +911,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
       const int n = rows.seg.n;
       if (n == 0) break;
       bool leave = false;
-      const float c = rows.c;
+      const float c = rows.c, lazy = rows.apart ? -INFINITY : kDecLazy;
       const int keys = rows.seg.req.keys, before = keys - rows.seg.req.queries, tile0 = rows.seg.tile;
       const int clean_tiles = before / kTrKeys - tile0;  // whose keys all rows see, if their pages are there
       float l[H], nm[H];
@@ -870,8 +967,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) kv4_tree_kernel(const Kv4Args a
 #pragma unroll
           for (int i = 1; i + 1 < H; i += 2) big = max3f(big, x[i], x[i + 1]);
           big = fmaxf(big, x[H - 1]);
-          if (moved || !bar_any(bar, 128, big > kDecLazy || !ok)) break;
+          if (moved || !bar_any(bar, 128, big > lazy || !ok)) break;
           // ---- some row's reference moves: maxima of all rows over the tile's keys
+          if (rows.apart) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < H; i0 += 8) {
+              uint32_t r[8];
+              tmem_ld_cols<8>(t_here + i0, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), rows.row_c[g * H + i0 + i]));
+              tmem_st_cols<8>(t_here + i0, r);
+            }
+            tmem_st_wait();
+          }
 #pragma unroll 1
           for (int i0 = 0; i0 < H; i0 += 8) {
             uint32_t r[8];

@@ -361,6 +361,21 @@ def test_far_scores_rescale_the_sums(d, max_q):
     check(down, cache, table, lens, offsets_of(nodes), trees_of(nodes), d, max_q=max_q, scale=0.5)
 
 
+@pytest.mark.parametrize("max_q", [1, 12, 20, 40, 200])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_all_magnitudes_share_a_pass(d, max_q):
+    """A row keeps its bits whatever the others of its request hold: as small as 2^-120 of them, or zero."""
+    lens, nodes = [300, 130], [40, 9]
+    cache, table = make(lens, 19, 16, 1, d)
+    off, seen = offsets_of(nodes), trees_of(nodes)
+    for up in (1e4, 1e8, 1e20, 1e36):
+        q = queries(49, 3, d).float()
+        q[5::17] *= up
+        q[3::11] = 0
+        q[7::13, 1] *= 2.0 ** -15
+        check(q.bfloat16(), cache, table, lens, off, seen, d, max_q=max_q, scale=0.5)
+
+
 @pytest.mark.parametrize("max_q", [2, 20, 64])
 @pytest.mark.parametrize("d", [64, 128])
 def test_not_a_number_reaches_the_rows_that_see_it(d, max_q):
