@@ -343,6 +343,70 @@ def test_many_short_requests():
     check(queries(sum(nodes), 2, 64), cache, table, lens, offsets_of(nodes), trees_of(nodes), 64, max_q=5)
 
 
+def on_gpu(q, cache, table, lens, offsets, seen, d):
+    """The attention of the 64-bit reference, one request and key head at a time on the GPU, with the tolerances' sums
+    of |q k|, of p |v| and of |v|."""
+    T, Hq, _ = q.shape
+    Hkv, page = cache.shape[1], cache.shape[3] * 16 // (9 * d)
+    o, lse = torch.zeros(T, Hq, d).double().cuda(), torch.full((T, Hq), -math.inf).double().cuda()
+    mass, total, dot = torch.zeros_like(o), torch.zeros_like(o), torch.zeros_like(lse)
+    G = Hq // Hkv
+    for b, n in enumerate(lens):
+        at, m = torch.arange(n).cuda(), offsets[b + 1] - offsets[b]
+        if n == 0 or m == 0:
+            continue
+        slots = (torch.as_tensor(table[b]).cuda()[at // page] * page + at % page).int()
+        k, v = (x.double() for x in ea.kv4_read(cache, slots, d))
+        rows = slice(offsets[b], offsets[b + 1])
+        live = torch.ones(m, n, dtype=torch.bool, device="cuda")
+        w = min(m, n)  # nodes that are cached: the last ones of the tree fill the cache
+        live[:, n - m if n >= m else 0:] = torch.as_tensor(seen[rows, max(0, m - n):m]).cuda()[:, :w]
+        for h in range(Hkv):
+            x = q[rows, h * G:(h + 1) * G].double()
+            s = torch.einsum("mgd,nd->mgn", x, k[:, h]) / math.sqrt(d)
+            s = s.masked_fill(~live[:, None], -math.inf)
+            top = s.amax(-1, keepdim=True)
+            p = torch.where(torch.isfinite(s), torch.exp(s - torch.where(torch.isfinite(top), top, 0)), 0)
+            sum_ = p.sum(-1, keepdim=True)
+            some = sum_ > 0
+            p = torch.where(some, p / torch.where(some, sum_, 1), 0)
+            cols = slice(h * G, (h + 1) * G)
+            lse[rows, cols] = torch.where(some, top + torch.log(sum_), -math.inf)[..., 0]
+            o[rows, cols] = torch.einsum("mgn,nd->mgd", p, v[:, h])
+            mass[rows, cols] = torch.einsum("mgn,nd->mgd", p, v[:, h].abs())
+            total[rows, cols] = v[:, h].abs().sum(0)
+            dot[rows, cols] = torch.einsum("mgd,nd->mgn", x.abs(), k[:, h].abs()).amax(-1)
+    return o, lse, mass, total, dot
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,most,nodes", [
+    (128, 16, 4, 8000, 16), (64, 16, 8, 9000, 16), (128, 32, 8, 7000, 7), (128, 8, 4, 8000, 60), (64, 12, 4, 9000, 50),
+    (128, 8, 8, 6000, 3), (128, 16, 8, 6000, 8),
+])
+def test_many_tiles_a_share(d, Hq, Hkv, most, nodes):
+    """Ragged requests, some short ones among them, with enough tiles that the shares count what units cost."""
+    rng = np.random.default_rng(nodes)
+    long = -(-2800 * 128 // (Hkv * most * 3 // 4))
+    lens = [n + nodes for n in rng.integers(most // 2, most, long).tolist() + rng.integers(0, 300, 10).tolist()]
+    lens = [lens[i] for i in rng.permutation(len(lens))] + [0, 1]
+    trees = rng.integers(1, nodes + 1, len(lens)).tolist()
+    tiles = sum(-(-n // 128) for n in lens) * Hkv
+    assert tiles > 16 * 152 or max(trees) * Hq // Hkv <= 16
+    cache, table = make(lens, -(-max(lens) // 64), 64, Hkv, d)
+    off, seen = offsets_of(trees), trees_of(trees)
+    q = queries(off[-1], Hq, d)
+    o64, lse64, mass, total, dot = on_gpu(q, cache, table, lens, off, seen, d)
+    ws = torch.full((ea.kv4_tree_workspace_bytes(Hq, Hkv, d, nodes, 64, table.shape[1]),), 255, dtype=torch.uint8).cuda()
+    o, lse = ea.kv4_tree_fwd(q, cache, ints(table), ints(lens), ints(off), ints(tree.bits(seen)), max_q=nodes,
+                             workspace=ws)
+    delta = 2.0 ** -18 * dot / math.sqrt(d)  # (as in `check`)
+    tol = 2.0 ** -8 * o64.abs() + (2 * delta[..., None] + 2.0 ** -10) * mass + 2.0 ** -32 * total
+    assert bool(((o.double() - o64).abs() <= tol).all())
+    some = torch.isfinite(lse64)
+    assert torch.equal(torch.isneginf(lse), ~some)
+    assert bool(((lse.double() - lse64).abs() <= delta + 2.0 ** -20 * (1 + lse64.abs()))[some].all())
+
+
 @pytest.mark.parametrize("max_q", [1, 12, 40, 200])
 @pytest.mark.parametrize("d", [64, 128])
 def test_far_scores_rescale_the_sums(d, max_q):
