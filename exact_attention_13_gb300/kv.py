@@ -323,11 +323,11 @@ def kv4_cache(num_pages: int, heads: int, page_size: int, d: int, device="cuda")
     return cache
 
 
-def _cache_shape(cache, d):
-    """(pages, heads, page size) of a cache of head dim d."""
-    if cache.dim() != 4 or d < 16:
+def _cache_shape(cache, d, dims=4):
+    """(pages, heads, page size) of a cache of head dim d (5 dims: of several in one tensor)."""
+    if cache.dim() != dims or d < 16:
         raise ValueError("cache must be as kv4_cache makes it")
-    pages, heads, two, block = cache.shape
+    pages, heads, two, block = cache.shape if dims == 4 else cache.shape[1:]
     page, rest = divmod(block * 16, 9 * d)
     if rest or two != 2 or cache.dtype is not torch.uint8 or not cache.is_contiguous():
         raise ValueError(f"cache must be a contiguous uint8 tensor as kv4_cache makes it for d = {d}")

@@ -18,7 +18,7 @@ last cached token).  A step that checks all of them at once, every length on the
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import functools
 import math
 from typing import NamedTuple
@@ -131,14 +131,13 @@ def kv4_move(caches, sources, slots, q_offsets, counts, d: int):
     source or a slot outside the cache are skipped.  No source may be the slot of an earlier row of its request
     or of any row of another one (``tree_accept`` gives none such)."""
     if isinstance(caches, torch.Tensor):
-        one = caches[0] if caches.dim() == 5 and caches.shape[0] else caches
-        index = caches.get_device()
-        pages, heads, page = _cache_shape(one, d)
-        n = caches.shape[0] if caches.dim() == 5 else 1
-        if index < 0 or not caches.is_contiguous() or n > 256:
-            raise ValueError("caches must be contiguous on a CUDA device, 256 layers at most")
-        base = caches.data_ptr()
-        addresses = range(base, base + n * one.numel(), one.numel()) if one.numel() else (base,) * n
+        index, layers = caches.get_device(), caches.dim() == 5
+        pages, heads, page = _cache_shape(caches, d, 5 if layers else 4)
+        n = caches.shape[0] if layers else 1
+        if index < 0 or not 1 <= n <= 256:
+            raise ValueError("caches must be on a CUDA device, 1 to 256 layers")
+        base, size = caches.data_ptr(), caches.numel() // n
+        addresses = range(base, base + n * size, size) if size else (base,) * n
     else:
         if not 1 <= len(caches) <= 256:
             raise ValueError("there must be 1 to 256 caches")
@@ -163,7 +162,8 @@ def kv4_move(caches, sources, slots, q_offsets, counts, d: int):
     _ints(counts, (B,), index, "counts")
     if T == 0 or B == 0:
         return
-    _run("fa_kv4_move", index, (ctypes.c_void_p * n)(*addresses), n, pages, page, heads, d, sources.data_ptr(),
+    addresses = array.array("Q", addresses)  # (64 of them 1.8 us, as a ctypes array 6.5)
+    _run("fa_kv4_move", index, addresses.buffer_info()[0], n, pages, page, heads, d, sources.data_ptr(),
          slots.data_ptr(), q_offsets.data_ptr(), counts.data_ptr(), T, B)
 
 
