@@ -55,22 +55,32 @@ int opt_in_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
   return set_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
-// Launch a kernel that may begin while the one before it on the stream still runs (grid_wait in each).
+// Launch a kernel that may begin while the one before it on the stream still runs (grid_wait in each), in clusters of
+// `cluster` CTAs.
 template <typename... Params, typename... Args>
-int launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+int launch_early_clusters(unsigned cluster, void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s,
+                          const Args&... args) {
   cudaLaunchConfig_t config{};
   config.gridDim = grid;
   config.blockDim = dim3(threads);
   config.dynamicSmemBytes = smem;
   config.stream = s;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &early;
-  config.numAttrs = 1;
+  cudaLaunchAttribute attrs[2]{};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = cluster;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  config.attrs = attrs;
+  config.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&config, kern, args...) == cudaSuccess) return FA_OK;
   (void)cudaGetLastError();
   return FA_ERR_CUDA;
+}
+
+template <typename... Params, typename... Args>
+int launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, const Args&... args) {
+  return launch_early_clusters(1, kern, grid, threads, smem, s, args...);
 }
 
 int cache_checks(const void* cache, int pages, int heads, int page, int d) {

@@ -125,6 +125,10 @@ int fa_tree_accept(const int* parents, const unsigned* seen, int words, const in
                          table,   queue,  queue_state, lens_out, counts, path,            next_tokens, sources,
                          queue_state_out, B,      T,      words,       table_width, queue_size, log2_of(page_size)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B <= kTreeGroups * kTreeCluster) {
+    const unsigned n = static_cast<unsigned>((B + kTreeGroups - 1) / kTreeGroups);
+    return launch_early_clusters(n, tree_accept_small_kernel, n, kTreeGroups * kTreeThreads, 0, s, a);
+  }
   if (int rc = launch_early(tree_accept_kernel, static_cast<unsigned>(B + 1), kTreeThreads, 0, s, a)) return rc;
   static std::atomic<uint64_t> done{0};
   if (int rc = opt_in_smem(tree_release_kernel, kPlanMaxBatch * 4, done)) return rc;

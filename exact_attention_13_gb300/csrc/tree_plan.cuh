@@ -15,8 +15,9 @@
 // that was chosen before, and is good; another one is good if its token is its parent's choice (of several
 // such children the first).  A node is accepted iff all of A(i) is good, that is, iff A(i) without the good
 // nodes is empty: no walk down the tree.  The accepted nodes are a path, and node i's place on it is
-// |A(i)| - 1.  A second kernel, launched while the first runs, gives back the pages behind the new lengths: it
-// needs the sums over all requests.
+// |A(i)| - 1.  The pages behind the new lengths are given back in the requests' order, which needs the sums over all
+// requests: up to kTreeGroups requests a CTA and eight CTAs do all of it in one cluster; larger batches take a
+// second kernel, launched while the first runs.
 //
 // Integers only: results do not depend on scheduling (the one atomic is a minimum).
 #pragma once
@@ -148,17 +149,30 @@ struct TreeAcceptArgs {
   int b, t, words, width, cap, page_shift;
 };
 
-__global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcceptArgs a) {
-  __shared__ int s_choice[kTreeNodes], s_slot[kTreeNodes], s_first[kTreeNodes], s_path[kTreeNodes];
-  __shared__ uint32_t s_good[kTreeWords];
-  grid_launch_dependents();
-  grid_wait();
-  const int tid = threadIdx.x, lane = tid % 32, r = blockIdx.x;
-  if (r >= a.b) {
-    const int from = min(max(a.offsets[a.b], 0), a.t), step = (gridDim.x - a.b) * kTreeThreads;
-    for (int t = from + (r - a.b) * kTreeThreads + tid; t < a.t; t += step) a.path[t] = a.sources[t] = -1;
-    return;
-  }
+// Barriers of 128 threads of the CTA.
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(group + 1), "n"(kTreeThreads) : "memory");
+}
+__device__ __forceinline__ int group_count(int group, bool yes) {
+  int n;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, %1, %2, p;\n\t}"
+               : "=r"(n)
+               : "r"(group + 1), "n"(kTreeThreads), "r"(static_cast<unsigned>(yes))
+               : "memory");
+  return n;
+}
+
+struct TreeAcceptGroup {
+  int choice[kTreeNodes], slot[kTreeNodes], first[kTreeNodes], path[kTreeNodes];
+  uint32_t good[kTreeWords];
+};
+
+// Request r, by a group of 128 threads of the CTA.
+__device__ __forceinline__ void accept_request(const TreeAcceptArgs& a, TreeAcceptGroup& g, int r, int group) {
+  int(&s_choice)[kTreeNodes] = g.choice, (&s_slot)[kTreeNodes] = g.slot, (&s_first)[kTreeNodes] = g.first,
+  (&s_path)[kTreeNodes] = g.path;
+  uint32_t(&s_good)[kTreeWords] = g.good;
+  const int tid = threadIdx.x % kTreeThreads, lane = tid % 32;
   const TreeShape s = tree_shape(a.offsets, r, a.t);
   const int before = a.lens[r], after = a.after[r];
   const int n = after > before ? min(s.n, 32 * a.words) : 0;  // a refused request has no places
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
         seen[x][w] = w < a.words ? a.seen[static_cast<size_t>(s.first + i) * a.words + w] : 0u;
     }
   }
-  __syncthreads();
+  group_sync(group);
   bool hit[kPer];
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
     hit[x] = i < n && parent[x] >= 0 && parent[x] < i && token[x] == s_choice[parent[x]];
     if (hit[x]) atomicMin(&s_first[parent[x]], i);
   }
-  __syncthreads();
+  group_sync(group);
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
     const int i = x * kTreeThreads + tid;
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
     const unsigned word = __ballot_sync(0xffffffffu, good);
     if (lane == 0) s_good[i / 32] = word;
   }
-  __syncthreads();
+  group_sync(group);
   int count = 0;
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
       }
       if (on && place >= 0) s_path[place] = i;
     }
-    count += __syncthreads_count(on);
+    count += group_count(group, on);
   }
   for (int i = tid; i < s.n; i += kTreeThreads) {
     const int node = i < count ? min(max(s_path[i], 0), n - 1) : -1;
@@ -225,6 +239,85 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcc
   }
 }
 
+// Rows behind the last request.
+__device__ __forceinline__ void accept_no_request(const TreeAcceptArgs& a, int thread, int threads) {
+  for (int t = min(max(a.offsets[a.b], 0), a.t) + thread; t < a.t; t += threads) a.path[t] = a.sources[t] = -1;
+}
+
+// Pages of a length, up to those of the table, and the ones that the request gives back.
+__device__ __forceinline__ int tree_pages(const TreeAcceptArgs& a, int tokens) {
+  return tokens > 0 ? ((min(tokens, a.width << a.page_shift) - 1) >> a.page_shift) + 1 : 0;  // (at most 2^30 tokens)
+}
+__device__ __forceinline__ int tree_back(const TreeAcceptArgs& a, int r) {
+  return max(tree_pages(a, a.after[r]) - tree_pages(a, __ldcg(a.lens_out + r)), 0);
+}
+// The ring's free pages before: from `head` on, `count` of them.
+struct TreeRing {
+  int head, count;
+};
+__device__ __forceinline__ TreeRing tree_ring(const TreeAcceptArgs& a) {
+  return {static_cast<int>(static_cast<unsigned>(a.state[0]) % static_cast<unsigned>(a.cap)), min(max(a.state[1], 0), a.cap)};
+}
+__device__ __forceinline__ void tree_ring_out(const TreeAcceptArgs& a, const TreeRing& ring, int total) {
+  a.state_out[0] = ring.head;
+  a.state_out[1] = ring.count + min(total, a.cap - ring.count);
+}
+// Request r's n pages, behind `before` ones of other requests (a warp).
+__device__ __forceinline__ void give_back(const TreeAcceptArgs& a, const TreeRing& ring, int r, int n, int before) {
+  const int* const row = a.table + static_cast<long long>(r) * a.width + tree_pages(a, __ldcg(a.lens_out + r));
+  for (int i = threadIdx.x % 32; i < n; i += 32) {
+    const long long at = static_cast<long long>(ring.count) + before + i;
+    if (at >= a.cap) continue;  // a ring without room for all keeps the first ones
+    const unsigned x = static_cast<unsigned>(ring.head) + static_cast<unsigned>(at), cap = static_cast<unsigned>(a.cap);
+    a.queue[x >= cap ? x - cap : x] = row[i];
+  }
+}
+
+// Up to kTreeGroups requests a CTA, all of the batch's in a cluster: acceptance and pages (8 requests: 3.4 us
+// against 4.0 by two kernels, 64: 4.2 and 4.1, and a call from Python 26 against 29).
+constexpr int kTreeGroups = 8, kTreeCluster = 8;
+__global__ void __launch_bounds__(kTreeGroups* kTreeThreads) tree_accept_small_kernel(const TreeAcceptArgs a) {
+  __shared__ TreeAcceptGroup groups[kTreeGroups];
+  grid_launch_dependents();
+  grid_wait();
+  const int group = threadIdx.x / kTreeThreads, r = blockIdx.x * kTreeGroups + group;
+  if (r < a.b) accept_request(a, groups[group], r, group);
+  const int threads = gridDim.x * kTreeGroups * kTreeThreads;
+  accept_no_request(a, blockIdx.x * kTreeGroups * kTreeThreads + threadIdx.x, threads);
+  // every CTA's lengths are there for all
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const TreeRing ring = tree_ring(a);
+  const int lane = threadIdx.x % 32, warp = blockIdx.x * (kTreeGroups * kTreeThreads / 32) + threadIdx.x / 32;
+  if (warp >= a.b) return;
+  // warp i has request i; pages of the ones before it, two requests a lane
+  static_assert(kTreeGroups * kTreeCluster <= 64, "requests of a cluster");
+  int mine = 0, before = 0, total = 0;
+#pragma unroll
+  for (int x = 0; x < 64; x += 32) {
+    const int q = x + lane, n = q < a.b ? tree_back(a, q) : 0;
+    total += n;
+    before += q < warp ? n : 0;
+    mine += q == warp ? n : 0;
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  before = __reduce_add_sync(0xffffffffu, before);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (warp == 0 && lane == 0) tree_ring_out(a, ring, total);
+  give_back(a, ring, warp, mine, before);
+}
+
+// Any batch: a request a CTA, one more for the rows behind the last request.
+__global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const TreeAcceptArgs a) {
+  __shared__ TreeAcceptGroup one;
+  grid_launch_dependents();
+  grid_wait();
+  if (static_cast<int>(blockIdx.x) < a.b)
+    accept_request(a, one, blockIdx.x, 0);
+  else
+    accept_no_request(a, threadIdx.x, kTreeThreads);
+}
+
 // The pages behind the new lengths go behind the free ones of the ring, in the requests' order (as in
 // page_plan_kernel: every CTA sums over all requests itself).
 __global__ void __launch_bounds__(kPlanThreads) tree_release_kernel(const TreeAcceptArgs a) {
@@ -233,37 +326,20 @@ __global__ void __launch_bounds__(kPlanThreads) tree_release_kernel(const TreeAc
   __shared__ int warp_sums[kPlanThreads / 32][3];
   grid_launch_dependents();
   grid_wait();
-  const int head = static_cast<int>(static_cast<unsigned>(a.state[0]) % static_cast<unsigned>(a.cap));
-  const int count = min(max(a.state[1], 0), a.cap);
-  const int limit = a.width << a.page_shift;  // at most 2^30
-  auto pages = [&](int tokens) { return tokens > 0 ? ((min(tokens, limit) - 1) >> a.page_shift) + 1 : 0; };
-  auto back = [&](int r) { return max(pages(a.after[r]) - pages(a.lens_out[r]), 0); };
+  const TreeRing ring = tree_ring(a);
   const int per = (a.b + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(a.b, static_cast<int>(threadIdx.x) * per), r1 = min(a.b, r0 + per);
   int v[3] = {0, 0, 0}, total[3];
-  for (int r = r0; r < r1; ++r) v[0] += back(r);
+  for (int r = r0; r < r1; ++r) v[0] += tree_back(a, r);
   block_scan3(v, total, warp_sums);
   for (int r = r0; r < r1; ++r) {
     s_back[r] = v[0];
-    v[0] += back(r);
+    v[0] += tree_back(a, r);
   }
   __syncthreads();
   const int gthread = blockIdx.x * kPlanThreads + threadIdx.x, gthreads = gridDim.x * kPlanThreads;
-  const int lane = threadIdx.x % 32;
-  if (gthread == 0) {
-    a.state_out[0] = head;
-    a.state_out[1] = count + min(total[0], a.cap - count);
-  }
-  for (int r = gthread / 32; r < a.b; r += gthreads / 32) {
-    const int n = back(r), keep = pages(a.lens_out[r]);
-    const int* const row = a.table + static_cast<long long>(r) * a.width;
-    for (int i = lane; i < n; i += 32) {
-      const long long at = static_cast<long long>(count) + s_back[r] + i;
-      if (at >= a.cap) continue;  // a ring without room for all keeps the first ones
-      const unsigned x = static_cast<unsigned>(head) + static_cast<unsigned>(at), cap = static_cast<unsigned>(a.cap);
-      a.queue[x >= cap ? x - cap : x] = row[keep + i];
-    }
-  }
+  if (gthread == 0) tree_ring_out(a, ring, total[0]);
+  for (int r = gthread / 32; r < a.b; r += gthreads / 32) give_back(a, ring, r, tree_back(a, r), s_back[r]);
 }
 
 }  // namespace exattn

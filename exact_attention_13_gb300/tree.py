@@ -84,7 +84,7 @@ def _seen(seen, T, index):
 
 def tree_accept(parents, seen, tokens, choices, lens, new_lens, q_offsets, slots, table, queue, queue_state,
                 page_size: int, out: TreeAccept | None = None) -> TreeAccept:
-    """What a step accepts of its trees (two launches).
+    """What a step accepts of its trees (one launch for up to 64 requests, else two).
 
     ``tokens`` int32 [T]: the token at each node; ``choices`` int32 [T]: the token that the model chose behind
     it (greedy or drawn).  Node 0 of a request is accepted, and so is every child of an accepted node that holds

@@ -123,6 +123,7 @@ def run_accept(c, page, words, T=None, seen=None):
 @pytest.mark.parametrize("nodes,page,words", [
     ([1], 16, 1), ([9] * 8, 64, 1), ([12, 0, 1, 33, 5, 0, 64, 2], 16, 2), ([256, 128, 129, 1, 255], 128, 8),
     ([20] * 600, 32, 1), ([300, 9, 270], 16, 8), ([40, 50], 32, 1), ([0, 0, 3], 16, 1), ([2] * 16384, 16, 1),
+    ([5, 1, 0] * 3, 16, 1), ([70, 3, 9, 0] * 9 + [256], 32, 8), ([6, 3] * 32, 16, 1), ([6] * 65, 16, 1),
 ])
 @pytest.mark.parametrize("wild", [False, True])
 def test_accept(nodes, page, words, wild):
