@@ -21,7 +21,8 @@
 //
 // Several axes (AXES): the tokens of images and video have a position on each of up to four axes (time,
 // height, width), and each pair turns by its own axis's: p is p_{axis(i)}.  A row's positions are loaded once
-// a thread, the eight pairs' axes as one word, and each pair selects its position.
+// a thread, the eight pairs' axes as one word, and each pair selects its position: 16 % more ALU instructions than
+// with one axis (51 % of their issue slots), 80.1 us instead of 78.8 for the 537 MB above.
 #pragma once
 
 #include <cuda_bf16.h>

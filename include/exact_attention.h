@@ -442,7 +442,7 @@ FA_API size_t fa_kv4_tree_fwd_workspace_bytes(int Hq, int Hkv, int d, int max_q,
  *   queue_state_out : {head, count} after the step
  *   sizes         : as fa_tree_plan; T = 0 is a step without nodes (arrays of T entries may be NULL)
  * All arrays are device int32.  No output may overlap an input or another output (lens_out and queue_state_out
- * are refused when they are the inputs; the ring is both).  Two launches, integers only.
+ * are refused when they are the inputs; the ring is both).  One launch for up to 64 requests, else two; integers only.
  */
 FA_API int fa_tree_accept(const int* parents, const unsigned* seen, int words, const int* tokens,
                           const int* choices, const int* lens, const int* new_lens,
