@@ -112,20 +112,45 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const TreePlanA
       }
     }
   }
-  for (int i = tid; i < s.n; i += kTreeThreads) {
-    // a node past the bits is seen by none: it takes those of the nodes above it that have some
-    int j = i, depth = -1;
-    while (j >= n) {
-      ++depth;
-      j = parent(j);
-    }
+  auto write = [&](int i, int depth, auto bits) {
     uint32_t* const out = a.seen + static_cast<size_t>(s.first + i) * a.words;
     for (int w = 0; w < a.words; ++w) {
-      const uint32_t bits = j >= 0 ? s_seen[j][w] : 0u;
-      depth += __popc(bits);
-      out[w] = bits;
+      out[w] = bits(w);
+      if (i < n) depth += __popc(out[w]);
     }
     a.positions[s.first + i] = static_cast<int>(static_cast<unsigned>(len) + static_cast<unsigned>(depth));
+  };
+  for (int i = tid; i < n; i += kTreeThreads) write(i, -1, [&](int w) { return s_seen[i][w]; });
+  // Nodes past the bits are seen by none: they take the bits of the nodes above them that have some.  128 at a time, their
+  // pointers double until they leave the 128 for a node that has its results, or for none.
+  int* const s_hops = reinterpret_cast<int*>(s_seen);  // [128] steps that the pointer stands for
+  for (int i0 = n; i0 < s.n; i0 += kTreeThreads) {
+    const int i = i0 + tid;
+    __syncthreads();
+    if (i < s.n) {
+      s_up[tid] = parent(i);
+      s_hops[tid] = 1;
+    }
+    for (int reach = 1; reach < kTreeThreads; reach *= 2) {
+      __syncthreads();
+      const int up = i < s.n ? s_up[tid] : -1;
+      int next = 0, hops = 0;
+      if (up >= i0) {
+        next = s_up[up - i0];
+        hops = s_hops[up - i0];
+      }
+      __syncthreads();
+      if (up >= i0) {
+        s_up[tid] = next;
+        s_hops[tid] += hops;
+      }
+    }
+    if (i < s.n) {
+      const int up = s_up[tid];
+      const uint32_t* const above = a.seen + static_cast<size_t>(s.first + max(up, 0)) * a.words;
+      const int depth = up < 0 ? -1 : a.positions[s.first + up] - len;
+      write(i, depth + s_hops[tid], [&](int w) { return up < 0 ? 0u : above[w]; });
+    }
   }
 }
 

@@ -45,6 +45,7 @@ def random_trees(rng, nodes, spread=6, wild=False):
 @pytest.mark.parametrize("nodes,max_nodes,spread", [
     ([1], 1, 1), ([9, 0, 5, 1, 32, 33], 33, 4), ([64] * 5, 64, 1), ([256, 255, 129, 1, 0, 200], 256, 1),
     ([256, 100], 256, 300), ([7] * 700, 7, 3), ([300, 40, 270, 1000], 256, 1), ([50, 3], 20, 5), ([0, 0, 0], 8, 1),
+    ([700, 2, 1700], 40, 1), ([900, 129, 33], 1, 200), ([1500], 256, 400),
 ])
 @pytest.mark.parametrize("wild", [False, True])
 def test_plan(nodes, max_nodes, spread, wild):
@@ -408,6 +409,24 @@ def test_many_tiles_a_share(d, Hq, Hkv, most, nodes):
     assert bool(((lse.double() - lse64).abs() <= delta + 2.0 ** -20 * (1 + lse64.abs()))[some].all())
 
 
+@pytest.mark.parametrize("max_q", [3, 8, 20])  # units of 32, 64 and 256 rows
+def test_more_requests_than_threads_with_many_tiles(max_q):
+    rng = np.random.default_rng(max_q)
+    lens, nodes = rng.integers(0, 70, 1400).tolist(), rng.integers(0, 6, 1400).tolist()
+    lens[700] = 900
+    cache, table = make(lens, 57, 16, 2, 64)
+    off, seen = offsets_of(nodes), trees_of(nodes)
+    q = queries(off[-1], 16, 64)
+    o64, lse64, mass, total, dot = on_gpu(q, cache, table, lens, off, seen, 64)
+    o, lse = ea.kv4_tree_fwd(q, cache, ints(table), ints(lens), ints(off), ints(tree.bits(seen)), max_q=max_q)
+    delta = 2.0 ** -18 * dot / math.sqrt(64)  # (as in `check`)
+    tol = 2.0 ** -8 * o64.abs() + (2 * delta[..., None] + 2.0 ** -10) * mass + 2.0 ** -32 * total
+    assert bool(((o.double() - o64).abs() <= tol).all())
+    some = torch.isfinite(lse64)
+    assert torch.equal(torch.isneginf(lse), ~some)
+    assert bool(((lse.double() - lse64).abs() <= delta + 2.0 ** -20 * (1 + lse64.abs()))[some].all())
+
+
 @pytest.mark.parametrize("max_q", [1, 12, 40, 200])
 @pytest.mark.parametrize("d", [64, 128])
 def test_far_scores_rescale_the_sums(d, max_q):
@@ -426,7 +445,7 @@ def test_far_scores_rescale_the_sums(d, max_q):
     check(down, cache, table, lens, offsets_of(nodes), trees_of(nodes), d, max_q=max_q, scale=0.5)
 
 
-@pytest.mark.parametrize("max_q", [1, 12, 20, 40, 200])
+@pytest.mark.parametrize("max_q", [1, 5, 7, 12, 20, 40, 200])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rows_of_all_magnitudes_share_a_pass(d, max_q):
     """A row keeps its bits whatever the others of its request hold: as small as 2^-120 of them, or zero."""
