@@ -590,6 +590,67 @@ def test_attention_refusals():
 
 
 # --------------------------------------------------------------------------------- all of them together
+@pytest.mark.parametrize("B,Hq", [(5, 4), (70, 16)])  # acceptance by one kernel and by two; 16 and 64 rows
+def test_a_captured_step_on_another_stream(B, Hq):
+    """Plan, rotation, append, attention, acceptance and moves of a step, captured once on a side stream and replayed with
+    other trees, tokens and lengths: the same bits as the calls one by one."""
+    d, page, Hkv, width, T = 64, 16, 1, 8, 4 * B + 3
+    turns, _ = ea.rope_turns(d)
+    axes = ea.rope_axis_pairs((8, 12, 12))
+    slots = [b * width + i for b in range(B) for i in range(width)]
+
+    def fresh(seed):
+        r = np.random.default_rng(seed)
+        nodes = r.integers(0, 5, B).tolist()
+        lens = r.integers(1, 90, B).tolist()
+        parents = random_trees(r, nodes) + [0] * (T - sum(nodes))
+        return dict(nodes=ints(nodes), lens=ints(lens), parents=ints(parents), tokens=ints(r.integers(0, 2, T)),
+                    choices=ints(r.integers(0, 2, T)), q=queries(T, Hq, d, seed), k=queries(T, Hkv, d, seed + 1),
+                    v=queries(T, Hkv, d, seed + 2), cache=torch.randint(0, 40, (B * width + 1, Hkv, 2, page * 9 * d // 16),
+                                                                        dtype=torch.uint8).cuda(),
+                    table=ints(slots).view(B, width), queue=ints(np.zeros(B * width)), state=ints([0, 0]))
+
+    def step(x):
+        new = torch.minimum(x["nodes"], x["lens"] * 0 + 4)
+        offsets = torch.cat([x["nodes"][:1] * 0, torch.cumsum(new, 0).int()])
+        tp = ea.tree_plan(x["parents"], offsets, x["lens"], 4)
+        after = x["lens"] + new
+        row = torch.arange(T, device="cuda", dtype=torch.int32)
+        req = torch.searchsorted(offsets[1:].contiguous(), row, right=True).clamp(max=B - 1)
+        at = x["lens"][req] + row - offsets[req]
+        place = torch.where(row < offsets[-1], x["table"].view(-1)[req * width + (at // page).clamp(0, width - 1)] * page
+                            + at % page, -1).int()
+        q, k = ea.rope_axes(x["q"], x["k"], tp.positions.expand(3, T).contiguous(), turns, axes)
+        ea.kv4_append(k, x["v"], x["cache"], place)
+        o, lse = ea.kv4_tree_fwd(q, x["cache"], x["table"], after, offsets, tp.seen, max_q=4)
+        got = ea.tree_accept(x["parents"], tp.seen, x["tokens"], x["choices"], x["lens"], after, offsets, place,
+                             x["table"], x["queue"], x["state"], page)
+        ea.kv4_move(x["cache"], got.sources, place, offsets, got.counts, d)
+        n = offsets[-1]
+        live = (row < n)[:, None]
+        return [tp.positions, tp.seen, torch.where(live[..., None], o, 0), torch.where(live, lse, 0), *got, x["cache"],
+                x["queue"]]
+
+    side = torch.cuda.Stream()
+    held = fresh(100)
+    with torch.cuda.stream(side):
+        step({k: v.clone() for k, v in held.items()})  # (lazy initialisations)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = step(held)
+    for seed in (1, 2, 3):
+        x = fresh(seed)
+        want = step({k: v.clone() for k, v in x.items()})
+        for k, v in x.items():
+            held[k].copy_(v)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(outs, want):
+            assert torch.equal(g, w)
+
+
 def test_steps_that_check_trees():
     """Four steps of three requests, each: pages, tree, positions, append, attention, acceptance, moves.  The cache
     must end up as if the accepted tokens had been written alone, one after the other, and lengths, pages and the
