@@ -24,8 +24,8 @@
 // cuBLAS bf16); four chunks of up to 512 tokens behind 4096 to 8192 keys, 32 heads over 8: 129.5 us for
 // 116 GFLOP, 897 TFLOP/s (0.46), 5 us of that the start, 18 the queries and outputs of the two or three
 // shares of units a CTA has, and 10 the merge.  Units of at most 128 rows have one row tile: the other's
-// warps and accumulators idle, and its chain S, softmax, P V, S runs alone (64 requests of 4096 keys with 36
-// to 128 rows a key head: 231 to 238 us, their bytes take 47 to 50).  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
+// warps and accumulators idle (of trees: take units in turn), and its chain S, softmax, P V, S runs alone (64 requests
+// of 4096 keys with 36 to 128 rows a key head: 227 to 233 us, of trees 216 to 222; their bytes take 47 to 50).  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
 // tiles 2048 of them: S reads Q and K from shared memory at its full rate, beside which V is read and the
 // next tiles are written, and S of a row tile waits for its own softmax (2100 cycles) and P V.
 //
@@ -90,8 +90,8 @@ struct ChunkSegment {
 // A warp's place on the line, in shared memory: registers are scarce in the loops.
 struct ChunkWalk {
   ChunkSegment s;
-  int blocks;
-  long long left;  // tiles of the share from s.tile on
+  int blocks, unit;  // blocks of the request; number of the segment in the share
+  long long left;    // tiles of the share from s.tile on
 };
 
 struct ChunkCtrl {
@@ -102,7 +102,7 @@ struct ChunkCtrl {
   int abort;
   long long sum[kChThreads / 32];
   long long total, first, last;
-  int extra, skip;  // what a unit counts more on the line, and how much of that the share begins with
+  int extra, skip;  // whether units count more on the line than their tiles, and how much of that the share begins with
   ChunkSegment start;
   ChunkWalk walk[kChThreads / 32];
 };
@@ -110,6 +110,16 @@ struct ChunkCtrl {
 template <int D>
 constexpr int chunk_smem_bytes() {
   return (2 + ChunkGeo<D>::kSlots) * ChunkGeo<D>::kTileBytes + static_cast<int>(sizeof(ChunkCtrl)) + 1024;
+}
+
+// Trees of drafted tokens (TREE): a unit counts more tiles than it has, at its front, where the CTAs have many tiles
+// each: queries and outputs take the time of that many, of two row tiles 7, of one, whose units overlap, 4.  A share
+// that ends among them leaves the whole unit to the next one.  64 requests of 500 to 8192 keys, 8 key heads, d 128, 256
+// rows each: 401 us with 0, 355 with 2, 317 with 4, 299 with 7, 309 with 12; of 16 to 2048 keys 216, 169, 139, 122, 132;
+// 128 rows of these: 102 with 2, 91 with 4, 95 with 7.
+constexpr int kChTreeExtra = 7, kChTreeExtraOne = 4;
+__device__ __forceinline__ int chunk_extra(const Kv4Args& a, const ReqShape& s, int block) {
+  return s.q_len * a.group - block * kChRows > 128 ? kChTreeExtra : kChTreeExtraOne;
 }
 
 // Tiles that the 256 rows of a block need: up to the last key that its last row sees.
@@ -131,6 +141,7 @@ __device__ __forceinline__ void walk_begin(const Kv4Args& a, ChunkWalk* w, const
   if (threadIdx.x % 32 == 0) {
     w->s = ctl->start;
     w->blocks = chunk_blocks(a, w->s.req);
+    w->unit = 0;
     w->left = ctl->last - ctl->first - ctl->skip;
     w->s.n = static_cast<int>(min(static_cast<long long>(w->s.tiles - w->s.tile), w->left));
   }
@@ -142,8 +153,8 @@ __device__ __forceinline__ bool walk_next(const Kv4Args& a, ChunkWalk* w, const 
   __syncwarp();
   if (threadIdx.x % 32 == 0) {
     w->left -= w->s.n;
+    ++w->unit;
     if (w->left > 0) {
-      w->left -= ctl->extra;
       w->s.tile = 0;
       if (++w->s.block == w->blocks) {
         w->s.block = 0;
@@ -157,6 +168,7 @@ __device__ __forceinline__ bool walk_next(const Kv4Args& a, ChunkWalk* w, const 
         }
       }
       w->s.tiles = chunk_tiles(a, w->s.req, w->s.block);
+      if (ctl->extra) w->left -= chunk_extra(a, w->s.req, w->s.block);
       w->s.n = static_cast<int>(min(static_cast<long long>(w->s.tiles), w->left));
     }
   }
@@ -172,20 +184,14 @@ __device__ __forceinline__ int walk_rows(const Kv4Args& a, const ChunkWalk* w) {
 // The CTA's share [first, last) of the line of `total` tiles; fills ctl->start.  Returns the number
 // of CTAs that have work.
 //
-// Trees of drafted tokens (TREE): a unit counts kChTreeExtra tiles more than it has, at its front, where the CTAs have
-// many tiles each: queries and outputs take the time of that many.  A share that ends among them leaves the
-// whole unit to the next one.  64 requests of 500 to 8192 keys, 8 key heads, d 128, 256 rows each: 401 us with 0, 355
-// with 2, 317 with 4, 299 with 7, 309 with 12; of 16 to 2048 keys 216, 169, 139, 122, 132; with 128 rows 5 is 1 % better
-// than 7 on the first and 7 % worse on the second.
-constexpr int kChTreeExtra = 7;
 template <bool TREE>
 __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, long long& total,
                                               long long& first, long long& last) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   ReqShape s{0, 0, 0, 0};
   long long per_head = 0;  // tiles of one key head of the thread's request
-  int extra = 0;
-  long long blocks_seen = 0;  // of the thread's requests
+  bool extra = false;      // whether units count what they cost besides
+  long long all_more = 0;  // of the thread's requests, a key head
   auto lane_request = [&](int l) {
     return ReqShape{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.q_len, l),
                     __shfl_sync(0xffffffffu, s.keys, l), __shfl_sync(0xffffffffu, s.queries, l)};
@@ -208,8 +214,9 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
       if (lane == l) per_head = sum;
     }
     if constexpr (TREE) {
-      per_head += static_cast<long long>(extra) * blocks;
-      blocks_seen += blocks;
+      const long long more = blocks > 0 ? (blocks - 1ll) * kChTreeExtra + chunk_extra(a, s, blocks - 1) : 0;
+      if (extra) per_head += more;
+      all_more += more;
     }
     return per_head * a.hk;
   };
@@ -231,12 +238,13 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
   for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
   if constexpr (TREE) {
     if (total >= 16ll * gridDim.x) {  // the line again (up to one request a thread; more: below)
-      extra = kChTreeExtra;
+      extra = true;
       const int blocks = chunk_blocks(a, s);
-      per_head += static_cast<long long>(extra) * blocks;
-      tiles += static_cast<long long>(extra) * blocks * a.hk;
+      const long long more = blocks > 0 ? (blocks - 1ll) * kChTreeExtra + chunk_extra(a, s, blocks - 1) : 0;
+      per_head += more;
+      tiles += more * a.hk;
       __syncthreads();
-      inc = scan(mine + extra * blocks_seen * a.hk);
+      inc = scan(mine + all_more * a.hk);
       total = 0;
       for (int w = 0; w < kChThreads / 32; ++w) total += ctl->sum[w];
     }
@@ -265,7 +273,8 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
       off -= head * head_tiles;
       // the block that holds tile `off` of the head, 32 blocks at a time
       for (int b0 = 0;; b0 += 32) {
-        const int own = b0 + lane < chunk_blocks(a, x) ? chunk_tiles(a, x, b0 + lane) + extra : 0;
+        const int more = extra ? chunk_extra(a, x, b0 + lane) : 0;
+        const int own = b0 + lane < chunk_blocks(a, x) ? chunk_tiles(a, x, b0 + lane) + more : 0;
         long long upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -281,10 +290,10 @@ __device__ __forceinline__ int chunk_my_range(const Kv4Args& a, ChunkCtrl* ctl, 
             c.head = head;
             c.block = b0 + lane;
             const int at = static_cast<int>(off - (upto - own));
-            c.tile = max(0, at - extra);
-            c.tiles = own - extra;
+            c.tile = max(0, at - more);
+            c.tiles = own - more;
             ctl->extra = extra;
-            ctl->skip = max(0, extra - at);
+            ctl->skip = max(0, more - at);
           }
           break;
         }
@@ -403,19 +412,20 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
     };
     do {
       const bool two = walk_rows(a, w) > 128;
-      const int n = w->s.n;
-      ok = wait(ctl->q_full[0], segs[0]++);
+      const int n = w->s.n, one = TREE ? w->unit & 1 : 0;  // the row tile of a unit of one
+      const int h0 = two ? 0 : one;
+      ok = wait(ctl->q_full[h0], segs[h0]++);
       if (two) ok = ok && wait(ctl->q_full[1], segs[1]++);
       ok = ok && wait(ctl->kv_full[t % G::kSlots], t / G::kSlots);
       if (!ok) break;
       tc_fence_after();
-      issue_s(0, t);
+      issue_s(h0, t);
       if (two) issue_s(1, t);
 #pragma unroll 1
       for (int i = 0; i < (two ? 2 * n : n) && ok; ++i) {  // one copy of the step's code
-        const int h = two ? i & 1 : 0, j = two ? i >> 1 : i;
+        const int h = two ? i & 1 : one, j = two ? i >> 1 : i;
         ok = step(h, j == 0, j + 1 < n);
-        if (h == (two ? 1 : 0)) t += 2;
+        if (!two || h == 1) t += 2;
       }
     } while (ok && walk_next(a, w, ctl));
     // nothing this warp issued may still run when the TMEM is released
@@ -560,14 +570,17 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
                                         2 * static_cast<int>(blockIdx.x) + (unit_no > 0 ? 1 : 0),
                                         share_of(total, n_cta, x) - static_cast<int>(blockIdx.x) + 1);
       }
-      if (h == 0 || two) {
+      // Trees of drafted tokens: units of one row tile take the two tiles' warps and accumulators in turn, so that one
+      // brings its queries while the other still runs, and writes its outputs while that one has begun (128 rows, 64
+      // requests of 4096 keys: 222 us instead of 237).
+      if (two || h == (TREE ? w->unit & 1 : 0)) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
         float c;   // factor of the row's scores
         float far = 0.f;  // TREE: not 0: their factor where they get it ahead of the softmax
         int sees;  // keys that the row sees, one behind the other
         const uint32_t* bits = nullptr;  // TREE: the tree's nodes that it sees
         {
-          const int row = h * 128 + r_tile, urow = w->s.block * kChRows + row;
+          const int row = (two ? h * 128 : 0) + r_tile, urow = w->s.block * kChRows + row;
           const bool live = row < walk_rows(a, w);
           const int qi = urow / a.group, qg = urow - qi * a.group;
           sees = w->s.req.keys;
@@ -768,7 +781,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         if (!ok) break;
         tc_fence_after();
         if (frees) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
-        const int row = h * 128 + r_tile, urow = w->s.block * kChRows + row;
+        const int row = (two ? h * 128 : 0) + r_tile, urow = w->s.block * kChRows + row;
         const bool live = row < walk_rows(a, w), whole = n == w->s.tiles;
         const int qi = urow / a.group, qg = urow - qi * a.group;
         const float inv = l == 0.f ? 0.f : a.v_descale / l;
