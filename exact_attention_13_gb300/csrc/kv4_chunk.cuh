@@ -25,7 +25,7 @@
 // 116 GFLOP, 897 TFLOP/s (0.46), 5 us of that the start, 18 the queries and outputs of the two or three
 // shares of units a CTA has, and 10 the merge.  Units of at most 128 rows have one row tile: the other's
 // warps and accumulators idle (of trees: take units in turn), and its chain S, softmax, P V, S runs alone (64 requests
-// of 4096 keys with 36 to 128 rows a key head: 227 to 233 us, of trees 216 to 222; their bytes take 47 to 50).  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
+// of 4096 keys with 36 to 128 rows a key head: 227 to 233 us, of trees 210 to 215; their bytes take 47 to 50).  Within a unit a key tile takes about 3400 cycles, the MMAs of its two row
 // tiles 2048 of them: S reads Q and K from shared memory at its full rate, beside which V is read and the
 // next tiles are written, and S of a row tile waits for its own softmax (2100 cycles) and P V.
 //
@@ -496,6 +496,22 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
         }
       }
     };
+    // Of trees: the same bytes to L2, a line a lane (codes of 16 keys, then their scales), while the tile before is
+    // widened (128 rows, 64 requests of 4096 keys: 214 us instead of 222; loading each piece's registers again as soon as
+    // it is widened takes twice the time).
+    auto touch = [&]() {
+      constexpr int kLines = 16 * kCode / 128;
+      const int g = lane < 2 * kLines ? lane / kLines : lane - 2 * kLines;
+      const int page = __shfl_sync(0xffffffffu, id[0], 0), page1 = __shfl_sync(0xffffffffu, id[1], 0);
+      const int mine = g ? page1 : page;
+      if (lane < 2 * kLines + 2 && static_cast<unsigned>(mine) < static_cast<unsigned>(a.pages)) {
+        const int row = (key + 16 * g) & (page_rows - 1);
+        const uint8_t* const at = head + static_cast<size_t>(static_cast<unsigned>(mine)) * page_bytes +
+                                  (values ? block_bytes : 0) +
+                                  (lane < 2 * kLines ? row * kCode + lane % kLines * 128 : page_rows * kCode + row * kScale);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      }
+    };
     // (test builds that inject a stall widen nothing: the first wait for a tile runs out)
     bool more = !EXATTN_INJECT_STALL;
     fetch_ids();
@@ -504,6 +520,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
 #pragma unroll 1
     for (long long i = -1;; ++i) {
       if (i >= 0) {
+        if (TREE && more) touch();
         const long long t = 2 * i + (values ? 1 : 0);
         const int slot = static_cast<int>(t % G::kSlots);
         if (t >= G::kSlots && !wait(ctl->kv_empty[slot], static_cast<uint32_t>(t / G::kSlots - 1))) break;

@@ -21,8 +21,8 @@ namespace {
 // The kernel for `rows` query rows of a key head: 8 or 16 (kv4_attn.cuh, every value widened in registers), units of 32
 // or 64 (kv4_tree.cuh) or of 256 (kv4_chunk.cuh).  Both sides of each border in us, the chosen one first, for 64
 // requests of 4096 keys, 8 key heads, d 128: 8 rows 67 by the 8s, 89 by the 16s; 16 rows 91, 118 by the 32s; 32 rows 123,
-// 142 by the 64s (two 16s: 169); 64 rows 141, 216 by 256; 128 rows 222 by 256, 271 by two 64s (with 500 to 8192 keys
-// 254 and 296).  Where three of four requests of such a call fit one 64 the two are alike: 40 to 128 rows 220 and 222.
+// 142 by the 64s (two 16s: 169); 64 rows 141, 210 by 256; 128 rows 214 by 256, 271 by two 64s (with 500 to 8192 keys
+// 248 and 296).  Where a third of the requests fits one 64 the two are alike: 40 to 128 rows 212 and 222.
 int tree_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256; }
 
 size_t tree_workspace(int n, int d) {
