@@ -237,8 +237,9 @@ __device__ __forceinline__ int tree_tiles(const ReqShape& s) { return max(1, (s.
 
 // On the line of tiles that the CTAs share a unit counts `extra` more than it has, at its front: queries, first
 // reference, sums and outputs take the time of that many tiles (64 requests of 500 to 8192 keys, up to 64 rows: 187 us with
-// 0, 160 with 4 or 6, 166 with 8; of 16 to 2048 keys 75 with 4, 67 with 6, 68 with 8; 32 rows: 47.5, 49.4, 51.3).  A share that ends among them leaves the whole unit to the next one.  Where the CTAs
-// have few tiles each, spreading them is worth more.  Units that are not split count 1.
+// 0, 160 with 4 or 6, 166 with 8; of 16 to 2048 keys 75 with 4, 67 with 6, 68 with 8; 32 rows: 47.5, 49.4, 51.3).  A share
+// that ends among them leaves the whole unit to the next one.  Where the CTAs have few tiles each, spreading them is
+// worth more.  Units that are not split count 1.
 template <int N>
 __device__ __forceinline__ int tree_extra(const Kv4Args& a, long long tiles) {
   return !a.whole_tiles && tiles >= 16ll * gridDim.x ? (N == 64 ? 6 : 4) : 0;

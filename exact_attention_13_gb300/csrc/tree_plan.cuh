@@ -20,7 +20,9 @@
 // requests: up to kTreeGroups requests a CTA and eight CTAs do all of it in one cluster; larger batches take a
 // second kernel, launched while the first runs.
 //
-// 1000 requests of 64 nodes take 6.0 us, the second kernel under the end of the first.  Integers only: results do not depend on scheduling (the one atomic is a minimum).
+// 1000 requests of 64 nodes take 6.0 us, the second kernel under the end of the first.
+//
+// Integers only: results do not depend on scheduling (the one atomic is a minimum).
 #pragma once
 
 #include <cstdint>
