@@ -33,7 +33,8 @@
 //   warps 8-15   widen K and V^T: two warps share 32 rows of both
 //   warp  16     issues the MMAs:  S(0) S(1) | PV(t) S(t + 2) | ...
 //   warps 17, 18 copy codes and scales of K and of V into a ring of tiles
-//   warp  19     queries, masks and places of the rows of the next unit, while this one runs
+//   warp  19     queries, masks and places of the rows of the next unit, while this one runs (the first unit's are
+//                brought by the softmax warps)
 // The split over CTAs and the merge of units that cross them are those of kv4_attn.cuh.
 //
 // Copies go by 16 bytes a lane: a bulk copy takes its issuer about 90 cycles whatever its size, and a tile has 32
