@@ -198,6 +198,7 @@ def prepare(case, seed):
         count = torch.randint(1, max(1, min(n // 3, 7)) + 1, (b,), generator=host)
         st["cache"] = torch.randint(0, 256, (c["layers"], c["pages"], c["h"], 2, _page_bytes(page, c["d"])),
                                     device=DEV, generator=g, dtype=torch.uint8)
+        st["layers"] = list(st["cache"].unbind(0))
         # each request's n rows lie in consecutive places of its pages, from anywhere in the first one
         width = -(-n // page) + 1
         pages = torch.randperm(c["pages"], device=DEV, generator=g)[:b * width].view(b, width)
@@ -431,7 +432,7 @@ def run(st):
                                st["lens_after"], st["q_offsets"], st["slots"], st["table"], st["queue"],
                                st["queue_state"], page_size=c["page"])
             return [a.lens, a.counts, a.path, a.next_tokens, a.sources, a.queue_state, st["queue"]]
-        ea.kv4_move(st["cache"], st["sources"], st["slots"], st["q_offsets"], st["counts"], c["d"])
+        ea.kv4_move(st["layers"], st["sources"], st["slots"], st["q_offsets"], st["counts"], c["d"])
         return st["cache"]
     if op == "axes":
         return (_plain_axes(st["q"], st), _plain_axes(st["k"], st))
