@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
       if (two || h == (TREE ? w->unit & 1 : 0)) {
         const bool frees = threadIdx.x % 128 == 0 && (h == 1 || !two);
         float c;   // factor of the row's scores
-        float far = 0.f;  // TREE: not 0: their factor where they get it ahead of the softmax
+        float far = 0.f;  // not 0: their factor where they get it ahead of the softmax
         int sees;  // keys that the row sees, one behind the other
         const uint32_t* bits = nullptr;  // TREE: the tree's nodes that it sees
         {
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
           }
           // scaled queries are below 2 and keys up to 448 * 6: where scores may pass 2^26, what m is rounded by would
           // leave f16's range in a fused multiplication and difference
-          if (TREE && __any_sync(0xffffffffu, c * (2.f * 448.f * 6.f * D) > 0x1p26f)) {
+          if (__any_sync(0xffffffffu, c * (2.f * 448.f * 6.f * D) > 0x1p26f)) {
             far = c;
             c = 1.f;
           }
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
             mbar_arrive(smem_u32(&ctl->kv_empty[t % G::kSlots]));
             if (j > 0) mbar_arrive(smem_u32(&ctl->kv_empty[(t - 1) % G::kSlots]));
           }
-          if (TREE && __any_sync(0xffffffffu, far != 0.f)) {
+          if (__any_sync(0xffffffffu, far != 0.f)) {
             uint32_t r[32];
 #pragma unroll 1
             for (int cb = 0; cb < 128; cb += 32) {

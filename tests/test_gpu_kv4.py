@@ -836,3 +836,18 @@ def test_a_batch_cut_short_keeps_its_rows_places(d, max_q, qlens, T):
     q = queries(offsets[-1], 4, d)
     check(q[:T].contiguous(), cache, table, lens, offsets, d, max_q=max_q)
     check(q, cache, table, lens, offsets, d, max_q=max_q)
+
+
+@pytest.mark.parametrize("max_q", [1, 5, 9, 12, 40, 200])  # blocks of 8, 16, 32 and 256 rows
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_rows_of_all_magnitudes(d, max_q, causal):
+    """Scores of any size: a row keeps its bits beside others 2^120 times as large, and those stay finite."""
+    lens, qlens = [300, 130], [40, 9]
+    cache, table = make(lens, 19, 16, 1, d)
+    for up in (1e4, 1e8, 1e20, 1e36):
+        q = queries(49, 3, d).float()
+        q[5::17] *= up
+        q[3::11] = 0
+        q[7::13, 1] *= 2.0 ** -15
+        check(q.bfloat16(), cache, table, lens, [0, 40, 49], d, causal=causal, max_q=max_q, scale=0.5)
