@@ -53,8 +53,10 @@ def tree_plan(parents, q_offsets, lens, max_nodes: int, out: TreePlan | None = N
 
     ``parents`` int32 [T]: each node's parent, a smaller number among its request's nodes, or -1 (any other
     value counts as -1); ``q_offsets`` int32 [B + 1]: first node of each request; ``lens`` int32 [B]: cached
-    tokens before the step.  ``max_nodes`` (1 to 256): nodes of a request that have a bit; nodes past them
-    are seen by none, themselves included.  Rows past the last request get position 0 and no bits."""
+    tokens before the step.  ``max_nodes`` (1 to 256) is rounded up to a multiple of 32: that many nodes of a
+    request have a bit, nodes past them are seen by none, themselves included, and are not accepted.  It makes
+    room for the nodes there are; to check fewer of them, bring fewer.  Rows past the last request get position 0
+    and no bits."""
     index = parents.get_device()
     if index < 0 or parents.dim() != 1 or lens.dim() != 1 or not 1 <= max_nodes <= _most_nodes:
         raise ValueError("parents and lens must be int32 CUDA vectors, max_nodes in [1, 256]")

@@ -80,6 +80,23 @@ def test_plan_bad_offsets_and_refusals():
     assert ea.tree_plan(p[:0], ints([0, 0, 0]), lens, 4).positions.shape == (0,)
 
 
+@pytest.mark.parametrize("max_nodes,room", [(1, 32), (5, 32), (20, 32), (32, 32), (33, 64), (250, 256)])
+def test_max_nodes_counts_whole_words(max_nodes, room):
+    """A chain longer than `max_nodes`: nodes up to the next multiple of 32 have bits and can be accepted, no others."""
+    n = room + 9
+    parents, off, lens = ints(range(-1, n - 1)), ints([0, n]), ints([7])
+    got = ea.tree_plan(parents, off, lens, max_nodes)
+    assert got.seen.shape == (n, room // 32) and got.positions.tolist() == list(range(7, 7 + n))
+    whole = ea.tree_plan(parents, off, lens, room)
+    assert torch.equal(got.seen, whole.seen)
+    bits = (got.seen.cpu().numpy().view(np.uint32)[:, :, None] >> np.arange(32, dtype=np.uint32) & 1).reshape(n, -1)
+    assert np.array_equal(bits, np.tril(np.ones((n, n), dtype=int))[:, :room])
+    one = ints([1] * n)
+    step = ea.tree_accept(parents, got.seen, one, one, lens, ints([7 + n]), off, ints(range(7, 7 + n)),
+                          ints(np.zeros((1, 30))), ints([0] * 30), ints([0, 0]), 16)
+    assert step.counts.tolist() == [room] and step.lens.tolist() == [7 + room]
+
+
 # --------------------------------------------------------------------------------- acceptance
 def accept_case(rng, nodes, page, wild=False, refuse=0.1, end=0.1, vocabulary=3):
     B, off = len(nodes), offsets_of(nodes)
