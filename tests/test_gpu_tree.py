@@ -507,6 +507,35 @@ def test_not_a_number_reaches_the_rows_that_see_it(d, max_q):
     assert bool(torch.isfinite(o[:20][~hit[:20]]).all()) and bool(torch.isfinite(lse[:20][~hit[:20]]).all())
 
 
+@pytest.mark.parametrize("max_q", [1, 8, 16, 20, 64])  # units of 8, 16, 32, 64 and 256 rows
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_do_not_see_it_lie_within_the_reference(d, max_q):
+    """Rows that share tiles with NaN keys and values of their own tree, and do not see them: the 64-bit reference of the
+    cache without them, within the tolerances of `check`."""
+    lens, nodes = [200, 150, 64], [20, 9, 20]
+    cache, table = make(lens, 7, 32, 1, d)
+    seen, off = trees_of(nodes), offsets_of(nodes)
+    q = queries(off[-1], 2, d)
+    o64, lse64, mass, total, dot = tree.kv4_tree_attention(numpy64(q), cache.cpu().numpy(), table, lens, off, seen, d,
+                                                           1 / math.sqrt(d))
+    bad = torch.full((1, 1, d), math.nan).bfloat16().cuda()
+    fine = normal(1, 1, d, seed=3).bfloat16().cuda() * 8
+    for b, node, key in ((0, 7, True), (0, 11, False), (2, 13, True)):
+        j = lens[b] - nodes[b] + node
+        ea.kv4_append(*((bad, fine) if key else (fine, bad)), cache, ints([table[b, j // 32] * 32 + j % 32]))
+    o, lse = (numpy64(t) for t in ea.kv4_tree_fwd(q, cache, ints(table), ints(lens), ints(off), ints(tree.bits(seen)),
+                                                  max_q=max_q))
+    free = np.ones(off[-1], dtype=bool)
+    free[:20] = ~(seen[:20, 7] | seen[:20, 11])
+    free[off[2]:] = ~seen[off[2]:, 13]
+    assert 3 <= free[:20].sum() < 20 and free[off[2]:].sum() < 20
+    assert np.isnan(o[~free]).all() and np.isnan(lse[~free]).all()
+    delta = 2.0 ** -18 / math.sqrt(d) * dot
+    tol = 2.0 ** -8 * np.abs(o64) + (2 * delta[..., None] + 2.0 ** -10) * mass + 2.0 ** -32 * total
+    assert (np.abs(o - o64) <= tol)[free].all()
+    assert (np.abs(lse - lse64) <= delta + 2.0 ** -20 * (1 + np.abs(lse64)))[free].all()
+
+
 @pytest.mark.parametrize("nodes", [3, 20, 50])
 def test_missing_pages_bad_lengths_and_cut_batches(nodes):
     d, page = 128, 16
