@@ -635,6 +635,65 @@ def test_attention_refusals():
     assert empty[0].shape == (0, 4, 128)
 
 
+# --------------------------------------------------------------------------------- offsets that make no sense
+ODD_OFFSETS = [[0, -3, 900, 2], [5, 1, 4, 9], [2 ** 31 - 1, 0, 2, 4], [-2 ** 31, 3, 3, 2 ** 31 - 1], [4, 60, 61, 70]]
+
+
+def guarded(*shape, dtype=torch.int32, guard=1 << 16):
+    """A tensor of 7s in the middle of a larger one, and whether what lies on its two sides is still all 7s."""
+    n = math.prod(shape)
+    whole = torch.full((n + 2 * guard,), 7, dtype=dtype, device="cuda")
+    return whole[guard:guard + n].view(shape), lambda: bool((whole[:guard] == 7).all() and (whole[guard + n:] == 7).all())
+
+
+@pytest.mark.parametrize("off", ODD_OFFSETS)
+@pytest.mark.parametrize("T", [1, 4, 60, 700])
+def test_odd_offsets_write_plans_and_acceptances_nowhere_else(off, T):
+    """... and nothing of a request that the offsets leave without rows."""
+    lens, new, words = ints([5, 6, 90]), ints([9, 6, 95]), 2
+    p = ints(random_trees(np.random.default_rng(T), [T]))
+    (positions, safe_p), (seen, safe_s) = guarded(T), guarded(T, words)
+    ea.tree_plan(p, ints(off), lens, 64, out=ea.TreePlan(positions, seen))
+    assert safe_p() and safe_s()
+    outs, safe = zip(*(guarded(n) for n in (3, 3, T, 3, T, 2)))
+    queue, safe_q = guarded(40)
+    ea.tree_accept(p, seen, ints([1] * T), ints([1] * T), lens, new, ints(off), ints(range(T)), ints(np.zeros((3, 6))),
+                   queue, ints([38, 1]), 16, out=ea.TreeAccept(*outs))
+    assert all(f() for f in safe) and safe_q()
+    rows = np.zeros(T, dtype=bool)  # of some request, or behind the last one
+    for first, last in [*zip(off, off[1:]), (off[-1], T)]:
+        rows[max(0, min(first, T)):max(0, min(last, T))] = True
+    for t in (positions, seen, outs[2], outs[4]):
+        assert bool((t.cpu()[~torch.from_numpy(rows)] == 7).all())
+    for b in range(3):
+        n = max(0, min(off[b + 1], T) - max(0, min(off[b], T)))
+        assert 0 <= int(outs[1][b]) <= n
+    cache, safe_c = guarded(50, 2, 2, 16 * 36, dtype=torch.uint8)
+    ea.kv4_move(cache, ints(range(T)[::-1]), ints(range(T)), ints(off), ints([2 ** 31 - 1, -1, 3]), 64)
+    assert safe_c()
+
+
+@pytest.mark.parametrize("off", ODD_OFFSETS)
+@pytest.mark.parametrize("nodes", [1, 8, 16, 20, 50])  # units of 8, 16, 32, 64 and 256 rows
+@pytest.mark.parametrize("T", [4, 60])
+def test_odd_offsets_write_attention_nowhere_else(off, nodes, T):
+    d, lens = 128, [300, 170, 90]
+    cache, table = make(lens, 19, 16, 2, d)
+    q, seen = queries(T, 4, d), ints(np.full((T, 2), -1))
+    (o, safe_o), (lse, safe_l) = guarded(T, 4, d, dtype=torch.bfloat16), guarded(T, 4, dtype=torch.float32)
+    size = ea.kv4_tree_workspace_bytes(4, 2, d, nodes, 16, 19)
+    ws, safe_w = guarded(size, dtype=torch.uint8)
+    ea.kv4_tree_fwd(q, cache, ints(table), ints(lens), ints(off), seen, max_q=nodes, out=o, lse=lse,
+                    workspace=ws if size else None)
+    assert safe_o() and safe_l() and safe_w()
+    rows = torch.zeros(T, dtype=torch.bool)
+    for first, last in zip(off, off[1:]):
+        rows[max(0, min(first, T)):max(0, min(last, T))] = True
+    assert bool((o.cpu()[~rows] == 7).all()) and bool((lse.cpu()[~rows] == 7).all())
+    # (offsets of 900 nodes before 170 keys: the keys are nodes 730 and later, which have no bits, and no row sees any)
+    assert bool(torch.isfinite(o.cpu()[rows]).all()) and bool((lse.cpu()[rows] < 1e3).all())
+
+
 # --------------------------------------------------------------------------------- all of them together
 @pytest.mark.parametrize("B,Hq", [(5, 4), (70, 16)])  # acceptance by one kernel and by two; 16 and 64 rows
 def test_a_captured_step_on_another_stream(B, Hq):
