@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Rows a) 
 // nodes, whose sources rise and lie at or behind their destinations, no source is then written before it is
 // read.  Bound by latency (count, slots, row: 2.2 us for 8 requests and 4 layers), for large steps by short pieces
 // of lines: 64 requests, 64 layers, 20 MB of rows take 15.3 us; their 64 + 8 bytes at random places are 96 of
-// 32-byte sectors to read, 47.5 MB from DRAM (3.3 TB/s), and as much again to write.
+// 32-byte sectors to read, 26.9 MB, and as much again to write.  47.5 MB are read from DRAM (3.3 TB/s); the counters do
+// not show what the others are (fills of partly written sectors, perhaps, and a DRAM granule of two).
 constexpr int kMoveLayers = 256;  // caches of one launch (their addresses are the kernel's arguments)
 constexpr int kMoveAhead = 8;
 

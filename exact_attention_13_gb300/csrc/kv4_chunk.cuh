@@ -25,7 +25,7 @@
 // 116 GFLOP, 897 TFLOP/s (0.46), 5 us of that the start, 18 the queries and outputs of the two or three
 // shares of units a CTA has, and 10 the merge.  Units of at most 128 rows have one row tile: the other's
 // warps and accumulators idle (of trees: take units in turn), and its chain S, softmax, P V, S runs alone (64 requests
-// of 4096 keys with 36 to 128 rows a key head: 227 to 233 us, of trees 210 to 215; their bytes take 47 to 50).
+// of 4096 keys with 36 to 128 rows a key head: 227 to 235 us, of trees 210 to 215; their bytes take 47 to 50).
 // Within a unit a key tile takes about 3400 cycles, the MMAs of its two row tiles 2048 of them: S reads Q and K from
 // shared memory at its full rate, beside which V is read and the next tiles are written, and S of a row tile waits
 // for its own softmax (2100 cycles) and P V.

@@ -22,7 +22,8 @@ namespace {
 // or 64 (kv4_tree.cuh) or of 256 (kv4_chunk.cuh).  Both sides of each border in us, the chosen one first, for 64
 // requests of 4096 keys, 8 key heads, d 128: 8 rows 67 by the 8s, 89 by the 16s; 16 rows 91, 118 by the 32s; 32 rows 123,
 // 142 by the 64s (two 16s: 169); 64 rows 141, 210 by 256; 128 rows 214 by 256, 271 by two 64s (with 500 to 8192 keys
-// 248 and 296).  Where a third of the requests fits one 64 the two are alike: 40 to 128 rows 212 and 222.
+// 248 and 296).  Where a third of the requests fits one 64 the two are alike: 40 to 128 rows 212 and 222.  Only this
+// load and d 128 have both sides measured; for few requests or d 64 the rule is the same and its borders are not shown.
 int tree_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256; }
 
 size_t tree_workspace(int n, int d) {

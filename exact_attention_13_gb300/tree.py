@@ -10,7 +10,7 @@ last cached token).  A step that checks all of them at once, every length on the
     q, k = ea.rope(q, k, tree.positions, turns)                       # for each layer:
     ea.kv4_append(k, v, cache, plan.slots)
     o, lse = ea.kv4_tree_fwd(q, cache, table, plan.lens, plan.q_offsets, tree.seen, max_q=...)
-    # the model's choice at each node: choices [T]
+    # the model's choice at each node: choices [T]; caches: a list, one of each layer
     got = ea.tree_accept(parents, tree.seen, tokens, choices, lens, plan.lens, plan.q_offsets, plan.slots,
                          table, queue, plan.queue_state, page_size=64)
     ea.kv4_move(caches, got.sources, plan.slots, plan.q_offsets, got.counts, d)   # all layers at once
@@ -128,9 +128,11 @@ def kv4_move(caches, sources, slots, q_offsets, counts, d: int):
     """Move cached rows: of each request, row ``sources[i]`` to ``slots[i]`` for its first ``counts[b]``
     rows i from ``q_offsets[b]`` on, in all of ``caches`` (one launch).
 
-    ``caches``: a cache, several of one shape stacked in a tensor [layers, ...], or a list of separate ones (256 at
-    most); ``sources`` and ``slots`` int32 [T], ``q_offsets`` int32 [B + 1], ``counts`` int32 [B].  Rows with a
-    source or a slot outside the cache are skipped.  No source may be the slot of an earlier row of its request
+    ``caches``: a cache, a list of them (256 at most, of one shape, each from ``kv4_cache``; checking them takes
+    the host 0.8 us each), or one tensor [layers, ...] of the same bytes, which the caller allocates; that and its
+    slices do not remember a head dim, so ``d`` has to be the one that they are used with everywhere.  ``sources`` and ``slots``
+    int32 [T], ``q_offsets`` int32 [B + 1], ``counts`` int32 [B].  Rows with a source or a slot outside the cache are
+    skipped.  No source may be the slot of an earlier row of its request
     or of any row of another one (``tree_accept`` gives none such)."""
     if isinstance(caches, torch.Tensor):
         index, layers = caches.get_device(), caches.dim() == 5
