@@ -404,10 +404,10 @@ def kv4_fwd(q, cache, table, lens, q_offsets=None, max_q: int | None = None, cau
     are; request b's queries are rows q_offsets[b] .. q_offsets[b + 1) (int32 [B + 1]), or T / B rows
     each without ``q_offsets``.  ``causal``: the queries are the last tokens of the cache.
     ``max_q``: about the most queries of a request (default T / B, rounded up); it only picks the
-    kernel (how many rows share a pass over the cache), one for all requests of the call.  Several requests' drafts with 17 to 128
-    query rows a key head take less time at d = 128 as chains through ``kv4_tree_fwd`` (64 requests of 4096 keys: 123
-    us instead of 163 for 32 rows, 141 instead of 229 for 64).  Rows of ``out`` and ``lse`` past
-    the last request's are left as they are (not initialised in tensors made here).  Rows of
+    kernel (how many rows share a pass over the cache), one for all requests of the call.  Drafts of several
+    requests with 17 to 128 query rows a key head take less time at d = 128 as chains through ``kv4_tree_fwd`` (64
+    requests of 4096 keys: 123 us instead of 163 for 32 rows, 141 instead of 229 for 64).  Rows of ``out`` and
+    ``lse`` past the last request's are left as they are (not initialised in tensors made here).  Rows of
     tokens without a slot, such as those of a request that ``page_plan`` refused, mean nothing: their keys are
     not in the cache, and they see what it held before.
     ``workspace``: a CUDA tensor of kv4_workspace_bytes(...) bytes or more, not shared by calls that may run
