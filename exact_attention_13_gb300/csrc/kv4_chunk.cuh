@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const Kv4Args 
                          pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
           }
           // scaled queries are below 2 and keys up to 448 * 6: where scores may pass 2^26, what m is rounded by would
-          // leave f16's range in a fused multiplication and difference
+          // leave f16's range in a fused multiplication and difference (NaN from about 2^27 on; what the test costs other
+          // rows is within 1 % either way: four chunks of 300 to 512 tokens 181.5 us, 180 without, 64 rows 229 and 229.4)
           if (__any_sync(0xffffffffu, c * (2.f * 448.f * 6.f * D) > 0x1p26f)) {
             far = c;
             c = 1.f;
